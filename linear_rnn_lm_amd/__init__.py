@@ -10,6 +10,10 @@ CPU fallback; if the library is missing, calls raise.
     WKV7.apply(r, w, k, v, a, b, h0)                   # autograd op -> (y, hT)
     WKV7.apply(r, w, k, v, a, b, h0, False)            # the same, chunk operands not kept
 
+    o, ckpt, hT = gdr_fwd(q, k, v, g, beta, h0)        # the gated delta rule, see gdr.py
+    o = gdr_step(q, k, v, g, beta, state, slots=slots) # its recurrent step over a pool
+    y, mean, rstd = ln_fwd(x, weight, bias, groups=H)  # layer norm, see lnorm.py
+
 The recurrence (rwkv-mlx page, section "Metal kernel architecture"): per
 head a 64x64 fp32 state S; per token sa = S a, S = S diag(w) + v k^T + sa b^T,
 y = S r.  Inputs r, w, k, v, a, b are fp32 or bf16; all outputs are fp32.
@@ -21,7 +25,8 @@ import os
 
 __all__ = ["lib", "fwd", "fwd_sequential", "fwd_scan", "chunk_prepare", "chunk_inverse", "bwd", "bwd_scan",
            "bwd_inputs", "step", "WKV7", "Wkv7Error",
-           "num_chunks", "workspace_bytes", "chunk_ops_bytes", "CHUNK", "HEAD_SIZE"]
+           "num_chunks", "workspace_bytes", "chunk_ops_bytes", "CHUNK", "HEAD_SIZE",
+           "gdr_fwd", "gdr_bwd", "gdr_step", "GDR", "GDR_CHUNK", "ln_fwd", "ln_bwd", "LN"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libwkv7.so")
@@ -522,3 +527,20 @@ class _LazyOp:
 
 WKV7 = _LazyOp(0)
 WKV7Proj = _LazyOp(1)
+
+
+class _LazyOpOf:
+    """An autograd op made by `make` on first use (torch is imported only then)."""
+
+    def __init__(self, make):
+        self._make, self._op = make, None
+
+    def __getattr__(self, name):
+        if self._op is None:
+            self._op = self._make()
+        return getattr(self._op, name)
+
+
+# The operators beside the recurrence; their modules use the helpers above.
+from .gdr import GDR, GDR_CHUNK, gdr_bwd, gdr_fwd, gdr_step  # noqa: E402
+from .lnorm import LN, ln_bwd, ln_fwd  # noqa: E402

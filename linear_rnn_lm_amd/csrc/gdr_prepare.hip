@@ -1,0 +1,212 @@
+// gdr_prepare.hip -- per-chunk operands of the gated delta rule (gfx950): what a
+// chunk of 64 tokens of one head needs apart from the state.
+//
+//     T = (I + A)^-1,  A = strict_lower(b_t Lam K K^T);   M = lower(Lam Q K^T)
+//
+// as bf16 planes, with the chunk's gates (see gdr_device.h).  All chunks of all
+// heads run at once, one workgroup of four waves each.
+#include "gdr_device.h"
+#include "gdr_internal.h"
+#include "wkv7_internal.h"
+
+namespace gdr {
+namespace {
+
+constexpr int LDA = 68;  // row stride (floats) of the fp32 64 x 64 matrices
+
+// fp32 values to three bf16 planes (24 bits), for fp32 inputs.
+__global__ __launch_bounds__(256) void split_kernel(const float* x, uint16_t* o, int64_t n) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;   // n is a multiple of 64
+    if (i >= n) return;
+    const f32x4 v = *reinterpret_cast<const f32x4*>(x + i);
+    bf16x2 a[3], b[3];
+    planes2<3>(wkv7::f32x2{v[0], v[1]}, a);
+    planes2<3>(wkv7::f32x2{v[2], v[3]}, b);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+        *reinterpret_cast<bf16x4*>(o + p * n + i) = bf16x4{a[p][0], a[p][1], b[p][0], b[p][1]};
+}
+
+// Rows outside every sequence; one workgroup in x per share of them, y = tensor.
+__global__ __launch_bounds__(256) void zero_outside_kernel(ZeroArgs p) {
+    const int64_t a = min(max(p.cu[0], 0), p.T), b = min(max(p.cu[p.N], (int)a), p.T), w = p.words[blockIdx.y];
+    const int64_t n = (a + (p.T - b)) * w, head = a * w, skip = (b - a) * w;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        p.p[blockIdx.y][i < head ? i : i + skip] = 0u;
+}
+
+// Operand rows straight from memory: lane (g, r) gets X[row][32 ks + 8g .. + 7].
+template <int NX>
+__device__ __forceinline__ PF<NX> frag_mem(const Planes& x, int64_t row, int stride, int ks, int lane) {
+    PF<NX> f;
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+        f.p[i] = *reinterpret_cast<const bf16x8*>(x.p + i * x.plane + row * stride + 32 * ks + 8 * (lane >> 4));
+    return f;
+}
+
+// T = (I + A)^-1 for the strictly lower 64 x 64 matrix A.
+// Diagonal 16 x 16 blocks by forward substitution (one wave each, one column
+// per lane), then [[X, 0], [Z, Y]]^-1 = [[X', 0], [-Y' Z X', Y']] for blocks of
+// 16 and of 32 with fp32 MFMA products: stable for any A, unlike a series in
+// powers of A.
+__device__ __forceinline__ void block_product(const float* X, const float* Y, float* Z, int kn, float sign, int lane) {
+    // Z (16 x 16) = sign * X (16 x kn) Y (kn x 16), all with row stride LDA
+    const int r = lane & 15, g = lane >> 4;
+    f32x4 acc = zero4();
+    for (int k0 = 0; k0 < kn; k0 += 4) acc = wkv7::mfma_f32(X[r * LDA + k0 + g], Y[(k0 + g) * LDA + r], acc);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) Z[(4 * g + q) * LDA + r] = sign * acc[q];
+}
+
+template <int NX, int K>
+__global__ __launch_bounds__(256) void prepare_kernel(Args p) {
+    __shared__ __attribute__((aligned(16))) float As[C * LDA];
+    __shared__ __attribute__((aligned(16))) float Ts[C * LDA];
+    __shared__ __attribute__((aligned(16))) float Ms[C * LDA];
+    __shared__ double Gs[C];
+    __shared__ float bs[C];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int g4 = lane >> 4, r16 = lane & 15;
+    const int slot = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const Seqs seqs{p.cu, p.N, p.T, p.NC};
+    int n, len;
+    int64_t tok;
+    if (!slot_chunk(seqs, slot, n, tok, len)) return;
+    const int hk = h / (p.H / p.Hk);
+    const int64_t block = (int64_t)slot * p.H + h;
+
+    if (w == 0) {
+        float g = 0.f, b = 0.f;
+        if (lane < len) {
+            g = p.g[(tok + lane) * p.H + h];
+            b = p.beta[(tok + lane) * p.H + h];
+            g = g < kMinLogDecay ? kMinLogDecay : g;
+            b = fabsf(b) < kBetaMin ? kBetaMin : b;
+        }
+        double G = g;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double o = __shfl_up(G, d);
+            if (lane >= d) G += o;
+        }
+        const double Gc = __shfl(G, 63);
+        Gs[lane] = G;
+        bs[lane] = b;
+        float* gt = p.gates + block * kGateFloats;
+        gt[kGateEG + lane] = exp_d(G);
+        gt[kGateToEnd + lane] = lane < len ? exp_d(Gc - G) : 0.f;
+        gt[kGateBeta + lane] = b;
+        reinterpret_cast<double*>(gt + kGateG)[lane] = G;
+    }
+    for (int e = tid; e < C * LDA; e += 256) Ts[e] = 0.f;
+
+    // row tile w of K K^T and Q K^T (lower 32 x 32 blocks)
+    constexpr int KS = K / 32;
+    const int stride = p.Hk * K;
+    Planes kp = p.kp, qp = p.qp;
+    kp.p += tok * stride + hk * K;
+    qp.p += tok * stride + hk * K;
+    auto row = [&](int t) { return min(t, len - 1); };   // tokens past the end: masked below
+    PF<NX> ka[KS], qa[KS];
+    const int ra = row(idx(w, r16));
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        ka[ks] = frag_mem<NX>(kp, ra, stride, ks, lane);
+        qa[ks] = frag_mem<NX>(qp, ra, stride, ks, lane);
+    }
+    __syncthreads();
+    for (int nt = 0; nt < (w < 2 ? 2 : 4); ++nt) {
+        f32x4 kk = zero4(), qk = zero4();
+        const int s = idx(nt, r16);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const PF<NX> kb = frag_mem<NX>(kp, row(s), stride, ks, lane);
+            kk = pmma<NX>(kk, ka[ks], kb);
+            qk = pmma<NX>(qk, qa[ks], kb);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int t = idx(w, 4 * g4 + q);
+            const bool on = s <= t && t < len;
+            const float lam = on ? exp_d(Gs[t] - Gs[s]) : 0.f;
+            As[t * LDA + s] = on && s < t ? bs[t] * lam * kk[q] : 0.f;
+            Ms[t * LDA + s] = on ? lam * qk[q] : 0.f;
+        }
+    }
+    __syncthreads();
+
+    if (lane < 16) {
+        const int o = 16 * w;
+        float x[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) x[t] = t == lane ? 1.f : 0.f;
+#pragma unroll
+        for (int s = 0; s < 15; ++s)
+#pragma unroll
+            for (int t = s + 1; t < 16; ++t) x[t] = fmaf(-As[(o + t) * LDA + o + s], x[s], x[t]);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) Ts[(o + t) * LDA + o + lane] = x[t];
+    }
+    __syncthreads();
+    // blocks of 16: the scratch products lie in the unused upper part of As
+    if (w < 2) {
+        const int o = 32 * w;
+        float* scr = As + o * LDA + o + 16;
+        block_product(As + (o + 16) * LDA + o, Ts + o * LDA + o, scr, 16, 1.f, lane);
+        wkv7::wave_lds_sync();
+        block_product(Ts + (o + 16) * LDA + o + 16, scr, Ts + (o + 16) * LDA + o, 16, -1.f, lane);
+    }
+    __syncthreads();
+    // blocks of 32
+    const int mr = 16 * (w >> 1), mc = 16 * (w & 1);
+    block_product(As + (32 + mr) * LDA, Ts + mc, As + mr * LDA + 32 + mc, 32, 1.f, lane);
+    __syncthreads();
+    block_product(Ts + (32 + mr) * LDA + 32, As + 32 + mc, Ts + (32 + mr) * LDA + mc, 32, -1.f, lane);
+    __syncthreads();
+
+    // to planes; the upper right 32 x 32 block of both is zero and never read
+    char* ops = p.ops + block * kOpsBytes;
+    const int t = tid >> 2, c0 = 16 * (tid & 3);
+    if (t >= 32 || c0 < 32) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const float* src = (m ? Ms : Ts) + t * LDA + c0;
+            char* dst = ops + m * kPlanes * kMatBytes + (t * C + c0) * 2;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const PF<kPlanes> f = pf_acc<kPlanes>(*reinterpret_cast<const f32x4*>(src + 8 * u),
+                                                      *reinterpret_cast<const f32x4*>(src + 8 * u + 4));
+#pragma unroll
+                for (int i = 0; i < kPlanes; ++i)
+                    *reinterpret_cast<bf16x8*>(dst + i * kMatBytes + 16 * u) = f.p[i];
+            }
+        }
+    }
+}
+
+template <int NX>
+hipError_t launch_k(const Args& a, hipStream_t s) {
+    const dim3 grid((uint32_t)a.slots * a.H);
+    if (a.K == 64) hipLaunchKernelGGL((prepare_kernel<NX, 64>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((prepare_kernel<NX, 128>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_zero_outside(const ZeroArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(zero_outside_kernel, dim3(64, (uint32_t)a.n), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_split(const float* x, uint16_t* planes, int64_t n, hipStream_t s) {
+    hipLaunchKernelGGL(split_kernel, dim3((uint32_t)((n / 4 + 255) / 256)), dim3(256), 0, s, x, planes, n);
+    return hipGetLastError();
+}
+
+hipError_t launch_prepare(const Args& a, bool bf16, hipStream_t s) {
+    return bf16 ? launch_k<1>(a, s) : launch_k<3>(a, s);
+}
+
+}  // namespace gdr

@@ -1,0 +1,248 @@
+"""The gated delta rule (C ABI in ``include/gdr.h``): a linear-RNN time mix with
+one decay per head and token.
+
+    o, ckpt, hT = gdr_fwd(q, k, v, g, beta, h0, cu_seqlens=cu)
+    dq, dk, dv, dg, dbeta, dh0 = gdr_bwd(do, q, k, v, g, beta, ckpt, dhT, cu_seqlens=cu)
+    o = gdr_step(q, k, v, g, beta, state, slots=slots)     # state updated in place
+    o, hT = GDR.apply(q, k, v, g, beta, h0, cu, scale)     # autograd op
+
+Per value head a V x K fp32 state S; per token S = e^g S, u = beta (v - S k),
+S = S + u k^T, o = scale S q.  q, k: (B, T, Hk, K); v: (B, T, H, V), H a multiple
+of Hk; K and V 64 or 128; fp32 or bf16.  g, beta: (B, T, H) fp32.  Outputs and
+token gradients have the inputs' type; states and the gradients of g and beta
+are fp32.  ``scale`` defaults to K ** -0.5.
+
+``cu_seqlens`` (int32, N + 1 offsets on the GPU, B = 1) packs N sequences of any
+lengths, empty ones included, along T; states are then (N, H, V, K).  The
+offsets stay on the GPU: nothing waits for them, and a call can be captured into
+a graph and replayed with other offsets.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+from . import BF16, F32, _check, _check_bytes, _check_f32, _dense_on, _LazyOpOf, _ptr, _stream, _where, lib
+
+GDR_CHUNK = 64
+
+
+@functools.lru_cache(maxsize=None)
+def _lib():
+    L = lib()
+    vp, i, i64, sz, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    dims = [i] * 6
+    L.gdr_slots.argtypes, L.gdr_slots.restype = [i] * 4, i64
+    L.gdr_ckpt_bytes.argtypes, L.gdr_ckpt_bytes.restype = dims + [i] * 2, sz
+    for n in ("gdr_fwd_workspace_bytes", "gdr_bwd_workspace_bytes"):
+        getattr(L, n).argtypes, getattr(L, n).restype = dims + [i] * 3, sz
+    L.gdr_fwd.argtypes = dims + [i] + [vp] * 6 + [i, f] + [vp] * 4 + [vp, sz, vp]
+    L.gdr_bwd.argtypes = dims + [i] + [vp] * 8 + [i, f] + [vp] * 7 + [vp, sz, vp]
+    L.gdr_step.argtypes = dims + [i] + [vp] * 6 + [i, f] + [vp] * 4
+    L.gdr_zero_outside.argtypes = [i, i, vp, i, vp, vp, vp]
+    for n in ("gdr_fwd", "gdr_bwd", "gdr_step", "gdr_zero_outside"):
+        getattr(L, n).restype = i
+    return L
+
+
+def _check_inputs(fn, q, k, v, g, beta):
+    """(B, T, Hk, H, K, V) of the five token inputs, checked."""
+    import torch
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"{fn}: q must be (B, T, Hk, K) and v (B, T, H, V), got {tuple(q.shape)} and {tuple(v.shape)}")
+    B, T, Hk, K = q.shape
+    H, V = v.shape[2:]
+    if K not in (64, 128) or V not in (64, 128):
+        raise ValueError(f"{fn}: K and V must be 64 or 128, got {K} and {V}")
+    if min(B, T, Hk, H) < 1 or H % Hk:
+        raise ValueError(f"{fn}: B, T and heads must be at least 1 and H a multiple of Hk, got q {tuple(q.shape)}, "
+                         f"v {tuple(v.shape)}")
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{fn}: q must be float32 or bfloat16, got {q.dtype}")
+    for n, t, shape, dt in (("q", q, (B, T, Hk, K), q.dtype), ("k", k, (B, T, Hk, K), q.dtype),
+                            ("v", v, (B, T, H, V), q.dtype), ("g", g, (B, T, H), torch.float32),
+                            ("beta", beta, (B, T, H), torch.float32)):
+        _check_tensor(fn, n, t, shape, dt, q.device)
+    return B, T, Hk, H, K, V
+
+
+def _check_tensor(fn, name, t, shape, dtype, dev):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} is {_where(t)}, expected {tuple(shape)} {dtype}")
+    _dense_on(fn, name, t, dev)
+
+
+def _check_cu(fn, cu, B, dev):
+    """Number of packed sequences (0: none)."""
+    import torch
+    if cu is None:
+        return 0
+    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 2:
+        raise ValueError(f"{fn}: cu_seqlens is {_where(cu)}, expected (N + 1,) torch.int32")
+    if B != 1:
+        raise ValueError(f"{fn}: packed sequences need B = 1, got B = {B}")
+    _dense_on(fn, "cu_seqlens", cu, dev)
+    return cu.numel() - 1
+
+
+def _code(dtype):
+    import torch
+    return BF16 if dtype == torch.bfloat16 else F32
+
+
+def _workspace(fn, workspace, need, dev):
+    import torch
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check_bytes(fn, "workspace", workspace, need, dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _zero_outside(cu, N, T, fresh, stream):
+    """Zero the rows of freshly made token tensors that no sequence covers."""
+    n = len(fresh)
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in fresh])
+    rows = (ctypes.c_int64 * n)(*[t.numel() // T * t.element_size() for t in fresh])
+    _check("gdr_zero_outside", _lib().gdr_zero_outside(T, N, _ptr(cu), n, ptrs, rows, stream))
+
+
+def gdr_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, scale=None, want_o=True, want_ckpt=True, want_hT=True,
+            o=None, ckpt=None, hT=None, workspace=None):
+    """Forward.  Returns (o, ckpt, hT); entries not wanted are None.  Pre-allocated
+    outputs may be passed; hT may be h0 (in-place update).  ``ckpt`` is what
+    ``gdr_bwd`` needs, a flat fp32 tensor: not wanted for inference."""
+    import torch
+    fn = "gdr_fwd"
+    B, T, Hk, H, K, V = _check_inputs(fn, q, k, v, g, beta)
+    dev = q.device
+    N = _check_cu(fn, cu_seqlens, B, dev)
+    L, packed, states = _lib(), int(N > 0), (N or B, H, V, K)
+    dims = (B, T, Hk, H, K, V)
+    _check_f32(fn, "h0", h0, states, dev, required=False)
+    fresh = []
+    if o is not None:
+        _check_tensor(fn, "o", o, v.shape, v.dtype, dev)
+    elif want_o:
+        o = torch.empty_like(v)
+        fresh.append(o)
+    nck = L.gdr_ckpt_bytes(*dims, N, packed)
+    if ckpt is not None:
+        _check_f32(fn, "ckpt", ckpt, (nck // 4,), dev)
+    elif want_ckpt:
+        ckpt = torch.empty(nck // 4, dtype=torch.float32, device=dev)
+    if hT is not None:
+        _check_f32(fn, "hT", hT, states, dev)
+    elif want_hT:
+        hT = torch.empty(states, dtype=torch.float32, device=dev)
+    code = _code(q.dtype)
+    workspace, wsb = _workspace(fn, workspace, L.gdr_fwd_workspace_bytes(*dims, code, N, packed), dev)
+    stream = _stream(dev)
+    with torch.cuda.device(dev):
+        if packed and fresh:
+            _zero_outside(cu_seqlens, N, T, fresh, stream)
+        st = L.gdr_fwd(*dims, code, *map(_ptr, (q, k, v, g, beta, cu_seqlens)), N, K ** -0.5 if scale is None else scale,
+                       *map(_ptr, (h0, o, ckpt, hT, workspace)), wsb, stream)
+    _check(fn, st)
+    return o, ckpt, hT
+
+
+def gdr_bwd(do, q, k, v, g, beta, ckpt, dhT=None, *, cu_seqlens=None, scale=None, want_dh0=True, workspace=None,
+            out=None):
+    """Backward.  Returns (dq, dk, dv, dg, dbeta, dh0); ``out`` may hold the first five."""
+    import torch
+    fn = "gdr_bwd"
+    B, T, Hk, H, K, V = _check_inputs(fn, q, k, v, g, beta)
+    dev = q.device
+    N = _check_cu(fn, cu_seqlens, B, dev)
+    L, packed, states = _lib(), int(N > 0), (N or B, H, V, K)
+    dims = (B, T, Hk, H, K, V)
+    _check_tensor(fn, "do", do, v.shape, v.dtype, dev)
+    _check_f32(fn, "ckpt", ckpt, (L.gdr_ckpt_bytes(*dims, N, packed) // 4,), dev)
+    _check_f32(fn, "dhT", dhT, states, dev, required=False)
+    fresh = []
+    if out is None:
+        out = fresh = [torch.empty_like(x) for x in (q, k, v, g, beta)]
+    if len(out) != 5:
+        raise ValueError(f"{fn}: out must hold 5 tensors, got {len(out)}")
+    for n, x, like in zip(("dq", "dk", "dv", "dg", "dbeta"), out, (q, k, v, g, beta)):
+        _check_tensor(fn, n, x, like.shape, like.dtype, dev)
+    dh0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dh0 else None
+    code = _code(q.dtype)
+    workspace, wsb = _workspace(fn, workspace, L.gdr_bwd_workspace_bytes(*dims, code, N, packed), dev)
+    stream = _stream(dev)
+    with torch.cuda.device(dev):
+        if packed and fresh:
+            _zero_outside(cu_seqlens, N, T, fresh, stream)
+        st = L.gdr_bwd(*dims, code, *map(_ptr, (do, dhT, q, k, v, g, beta, cu_seqlens)), N,
+                       K ** -0.5 if scale is None else scale, *map(_ptr, (ckpt, *out, dh0, workspace)), wsb, stream)
+    _check(fn, st)
+    return (*out, dh0)
+
+
+def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, state_out=None, o=None):
+    """B rows of T new tokens, token by token; returns o.
+
+    ``state`` (P, H, V, K) fp32 is updated in place, or into ``state_out`` (a
+    tensor of the same shape, of which only the states worked on are written).
+    ``slots`` (B,) int32 picks each row's state (row b uses state b without it);
+    a row whose slot is outside 0 .. P - 1 is padding: its o is 0.  Rows with the
+    same slot are consecutive tokens of one sequence, in row order."""
+    import torch
+    fn = "gdr_step"
+    B, T, Hk, H, K, V = _check_inputs(fn, q, k, v, g, beta)
+    dev = q.device
+    if state.dim() != 4 or state.shape[0] < 1:
+        raise ValueError(f"{fn}: state must be (P, H, V, K), got {tuple(state.shape)}")
+    P = state.shape[0]
+    if slots is None:
+        if P < B:
+            raise ValueError(f"{fn}: state holds {P} states for {B} rows")
+    else:
+        _check_tensor(fn, "slots", slots, (B,), torch.int32, dev)
+    _check_f32(fn, "state", state, (P, H, V, K), dev)
+    if state_out is None:
+        state_out = state
+    _check_f32(fn, "state_out", state_out, (P, H, V, K), dev)
+    if o is None:
+        o = torch.empty_like(v)
+    _check_tensor(fn, "o", o, v.shape, v.dtype, dev)
+    stream = _stream(dev)
+    with torch.cuda.device(dev):
+        st = _lib().gdr_step(B, T, Hk, H, K, V, _code(q.dtype), *map(_ptr, (q, k, v, g, beta, slots)), P,
+                             K ** -0.5 if scale is None else scale, *map(_ptr, (state, state_out, o)), stream)
+    _check(fn, st)
+    return o
+
+
+def _make_autograd():
+    import torch
+
+    class GDR(torch.autograd.Function):
+        """Differentiable op: (q, k, v, g, beta, h0, cu_seqlens, scale) -> (o, hT),
+        gradients by gdr_bwd in the inputs' types.  Rows that no packed sequence
+        covers have o = 0 and zero gradients."""
+
+        @staticmethod
+        def forward(ctx, q, k, v, g, beta, h0=None, cu_seqlens=None, scale=None):
+            ins = [q.contiguous(), k.contiguous(), v.contiguous(), g.contiguous().float(), beta.contiguous().float()]
+            h0c = None if h0 is None else h0.contiguous().float()
+            need = any(ctx.needs_input_grad)
+            o, ckpt, hT = gdr_fwd(*ins, h0c, cu_seqlens=cu_seqlens, scale=scale, want_ckpt=need)
+            ctx.save_for_backward(*ins, ckpt, cu_seqlens)
+            ctx.scale, ctx.types = scale, (g.dtype, beta.dtype, None if h0 is None else h0.dtype)
+            return o, hT
+
+        @staticmethod
+        def backward(ctx, do, dhT):
+            *ins, ckpt, cu = ctx.saved_tensors
+            do = torch.zeros_like(ins[2]) if do is None else do.to(ins[2].dtype).contiguous()
+            dhT = None if dhT is None else dhT.contiguous().float()
+            tg, tb, th = ctx.types
+            dq, dk, dv, dg, dbeta, dh0 = gdr_bwd(do, *ins, ckpt, dhT, cu_seqlens=cu, scale=ctx.scale,
+                                                 want_dh0=th is not None)
+            return dq, dk, dv, dg.to(tg), dbeta.to(tb), None if th is None else dh0.to(th), None, None
+
+    return GDR
+
+
+GDR = _LazyOpOf(_make_autograd)

@@ -1,0 +1,165 @@
+"""Layer norm (C ABI in ``include/lnorm.h``): the norm in front of a time mix and,
+with ``groups`` = heads, the per-head norm of its output.
+
+    y, mean, rstd = ln_fwd(x, weight, bias, groups=H)
+    dx, dweight, dbias = ln_bwd(dy, x, weight, mean, rstd, groups=H)
+    y = LN.apply(x, weight, bias, groups, eps, out_dtype)     # autograd op
+
+Each of ``groups`` equal parts of a row's C channels is normalised by itself:
+y = (x - mean) / sqrt(var + eps) * weight + bias.  x: (..., C) fp32 or bf16; y has
+x's type, or bf16 for an fp32 x with ``out_dtype=torch.bfloat16`` (the
+recurrence's fp32 output into a bf16 layer).  weight, bias: (C,) fp32 or bf16, or
+None.  mean, rstd: (rows, groups) fp32.  dx has x's type, dweight and dbias are fp32.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+from . import BF16, F32, _check, _check_bytes, _check_f32, _dense_on, _LazyOpOf, _ptr, _stream, _where, lib
+
+
+@functools.lru_cache(maxsize=None)
+def _lib():
+    L = lib()
+    vp, i, i64, sz, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    L.ln_fwd.argtypes, L.ln_fwd.restype = [i64] + [i] * 5 + [vp] * 3 + [f] + [vp] * 4, i
+    L.ln_bwd.argtypes, L.ln_bwd.restype = [i64] + [i] * 5 + [vp] * 8 + [vp, sz, vp], i
+    L.ln_bwd_workspace_bytes.argtypes, L.ln_bwd_workspace_bytes.restype = [i64, i, i], sz
+    return L
+
+
+def _code(dtype):
+    import torch
+    return BF16 if dtype == torch.bfloat16 else F32
+
+
+def _check_x(fn, x, weight, bias, groups):
+    """(rows, C) of x, with the weights' type code."""
+    import torch
+    types = (torch.float32, torch.bfloat16)
+    if x.dim() < 1 or x.shape[-1] < 1 or x.numel() < 1:
+        raise ValueError(f"{fn}: x must be (..., C) and not empty, got {tuple(x.shape)}")
+    if x.dtype not in types:
+        raise TypeError(f"{fn}: x must be float32 or bfloat16, got {x.dtype}")
+    C = x.shape[-1]
+    if groups < 1 or C % groups or C // groups > 16384:
+        raise ValueError(f"{fn}: groups must divide C into parts of at most 16384, got C = {C}, groups = {groups}")
+    _dense_on(fn, "x", x, x.device)
+    wd = None
+    for n, w in (("weight", weight), ("bias", bias)):
+        if w is None:
+            continue
+        if w.dtype not in types or (wd is not None and w.dtype != wd) or tuple(w.shape) != (C,):
+            raise ValueError(f"{fn}: {n} is {_where(w)}, expected ({C},) float32 or bfloat16, both of one type")
+        _dense_on(fn, n, w, x.device)
+        wd = w.dtype
+    return x.numel() // C, C, _code(wd)
+
+
+def _check_like(fn, name, t, shape, dtype, dev):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} is {_where(t)}, expected {tuple(shape)} {dtype}")
+    _dense_on(fn, name, t, dev)
+
+
+def _out_dtype(fn, x, out_dtype):
+    import torch
+    out_dtype = out_dtype or x.dtype
+    if out_dtype != x.dtype and not (x.dtype == torch.float32 and out_dtype == torch.bfloat16):
+        raise TypeError(f"{fn}: {x.dtype} rows cannot give {out_dtype}")
+    return out_dtype
+
+
+def ln_fwd(x, weight=None, bias=None, *, groups=1, eps=1e-5, out_dtype=None, want_stats=True, y=None, mean=None,
+           rstd=None):
+    """Forward.  Returns (y, mean, rstd); the statistics are None if not wanted."""
+    import torch
+    fn = "ln_fwd"
+    rows, C, wcode = _check_x(fn, x, weight, bias, groups)
+    dev = x.device
+    out_dtype = _out_dtype(fn, x, out_dtype if y is None else y.dtype)
+    if y is None:
+        y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    _check_like(fn, "y", y, x.shape, out_dtype, dev)
+    if (mean is None) != (rstd is None):
+        raise ValueError(f"{fn}: mean and rstd go together")
+    if mean is None and want_stats:
+        mean, rstd = (torch.empty((rows, groups), dtype=torch.float32, device=dev) for _ in range(2))
+    _check_f32(fn, "mean", mean, (rows, groups), dev, required=False)
+    _check_f32(fn, "rstd", rstd, (rows, groups), dev, required=False)
+    stream = _stream(dev)
+    with torch.cuda.device(dev):
+        st = _lib().ln_fwd(rows, C, groups, _code(x.dtype), _code(out_dtype), wcode, *map(_ptr, (x, weight, bias)), eps,
+                           *map(_ptr, (y, mean, rstd)), stream)
+    _check(fn, st)
+    return y, mean, rstd
+
+
+def ln_bwd(dy, x, weight, mean, rstd, *, groups=1, want_dx=True, want_dw=True, workspace=None, out=None):
+    """Backward of ``ln_fwd``: (dx, dweight, dbias); entries not wanted are None.
+    ``out`` may hold the three (None for one not wanted)."""
+    import torch
+    fn = "ln_bwd"
+    rows, C, wcode = _check_x(fn, x, weight, None, groups)
+    dev = x.device
+    _check_like(fn, "dy", dy, x.shape, _out_dtype(fn, x, dy.dtype), dev)
+    _check_f32(fn, "mean", mean, (rows, groups), dev)
+    _check_f32(fn, "rstd", rstd, (rows, groups), dev)
+    if out is None:
+        f32 = dict(dtype=torch.float32, device=dev)
+        out = (torch.empty_like(x) if want_dx else None, torch.empty(C, **f32) if want_dw else None,
+               torch.empty(C, **f32) if want_dw else None)
+    if len(out) != 3:
+        raise ValueError(f"{fn}: out must hold 3 entries, got {len(out)}")
+    dx, dw, db = out
+    if (dw is None) != (db is None) or (dx is None and dw is None):
+        raise ValueError(f"{fn}: dx, or dweight and dbias together, must be wanted")
+    if dx is not None:
+        _check_like(fn, "dx", dx, x.shape, x.dtype, dev)
+    _check_f32(fn, "dweight", dw, (C,), dev, required=False)
+    _check_f32(fn, "dbias", db, (C,), dev, required=False)
+    need = _lib().ln_bwd_workspace_bytes(rows, C, groups) if dw is not None else 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check_bytes(fn, "workspace", workspace, need, dev)
+    stream = _stream(dev)
+    with torch.cuda.device(dev):
+        st = _lib().ln_bwd(rows, C, groups, _code(x.dtype), _code(dy.dtype), wcode,
+                           *map(_ptr, (dy, x, weight, mean, rstd, dx, dw, db)), _ptr(workspace),
+                           workspace.numel() * workspace.element_size(), stream)
+    _check(fn, st)
+    return dx, dw, db
+
+
+def _make_autograd():
+    import torch
+
+    class LN(torch.autograd.Function):
+        """Differentiable op: (x, weight, bias, groups, eps, out_dtype) -> y, gradients by
+        ln_bwd in the inputs' types."""
+
+        @staticmethod
+        def forward(ctx, x, weight=None, bias=None, groups=1, eps=1e-5, out_dtype=None):
+            x = x.contiguous()
+            weight = None if weight is None else weight.contiguous()
+            y, mean, rstd = ln_fwd(x, weight, None if bias is None else bias.contiguous(), groups=groups, eps=eps,
+                                   out_dtype=out_dtype)
+            ctx.save_for_backward(x, weight, mean, rstd)
+            ctx.groups, ctx.out, ctx.tb = groups, y.dtype, None if bias is None else bias.dtype
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, weight, mean, rstd = ctx.saved_tensors
+            nx, nw, nb = (*ctx.needs_input_grad, False, False)[:3]     # only what was passed is listed
+            if not (nx or nw or nb):
+                return (None,) * 6
+            dx, dw, db = ln_bwd(dy.to(ctx.out).contiguous(), x, weight, mean, rstd, groups=ctx.groups, want_dx=nx,
+                                want_dw=nw or nb)
+            return dx, dw.to(weight.dtype) if nw else None, db.to(ctx.tb) if nb else None, None, None, None
+
+    return LN
+
+
+LN = _LazyOpOf(_make_autograd)

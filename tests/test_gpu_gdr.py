@@ -1,0 +1,406 @@
+"""The gated delta rule on the GPU against its definition in 64 bits."""
+import pytest
+import torch
+
+import linear_rnn_lm_amd as L
+from linear_rnn_lm_amd import gdr
+from tests.gdr_util import make, ref_norm, reference, rel, tol_bwd, tol_fwd
+from tests.gpu_util import note
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF, F32 = torch.bfloat16, torch.float32
+GRADS = ("dq", "dk", "dv", "dg", "dbeta", "dh0")
+
+
+def dev(*xs):
+    return [None if x is None else x.to(DEV) for x in xs]
+
+
+def cu_of(cu):
+    return None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV)
+
+
+def check_all(got, want, K, V, dtype):
+    for n, x in got.items():
+        low = x.dtype == BF
+        tol = (tol_bwd(K, V, BF if low else F32) if n in GRADS else tol_fwd(K, BF if low else F32))
+        e = rel(x, want[n])
+        assert e <= tol, f"{n}: {e:.3e} over {tol:.3e}"
+
+
+def run(x, cu=None, scale=None, **kw):
+    q, k, v, g, beta, h0, do, dhT = dev(*x)
+    c = cu_of(cu)
+    o, ck, hT = L.gdr_fwd(q, k, v, g, beta, h0, cu_seqlens=c, scale=scale, **kw)
+    out = L.gdr_bwd(do, q, k, v, g, beta, ck, dhT, cu_seqlens=c, scale=scale)
+    torch.cuda.synchronize()
+    return {"o": o, "hT": hT, **dict(zip(GRADS, out))}
+
+
+HEADS = [(64, 64), (64, 128), (128, 64), (128, 128)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K,V", HEADS)
+@pytest.mark.parametrize("B,T,Hk,H,h0", [(1, 1, 1, 1, True), (2, 63, 1, 2, False), (1, 64, 2, 2, True),
+                                         (2, 65, 1, 3, True), (1, 200, 3, 6, True), (3, 129, 2, 2, False)])
+def test_dense(B, T, Hk, H, h0, K, V, dtype):
+    note(f"gdr dense B{B} T{T} Hk{Hk} H{H} K{K} V{V} {dtype}")
+    x = make(B, T, Hk, H, K, V, dtype, seed=T, h0=h0)
+    check_all(run(x), reference(*x), K, V, dtype)
+
+
+PACKED = [([0, 70], 70), ([0, 1, 1, 65, 193], 193), ([0, 0, 64, 64, 128, 130, 130], 130), ([3, 67, 140], 150),
+          ([5, 5], 9), ([0, 1, 2, 3, 4, 5, 6, 7], 8), ([64, 128, 129], 200)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("cu,T", PACKED)
+def test_packed(cu, T, K, V, dtype):
+    note(f"gdr packed {cu} T{T} K{K} V{V} {dtype}")
+    x = make(1, T, 1, 2, K, V, dtype, seed=len(cu), N=len(cu) - 1)
+    check_all(run(x, cu), reference(*x, cu=cu), K, V, dtype)
+
+
+@pytest.mark.parametrize("B,Hk,H,V", [(2, 2, 2, 64), (33, 1, 4, 64), (40, 4, 8, 128), (70, 2, 8, 64)])
+def test_head_counts(B, Hk, H, V):
+    """From a few heads to more than there are compute units: every launch shape of the scans."""
+    note(f"gdr heads B{B} Hk{Hk} H{H} V{V}")
+    for K in (64, 128):
+        x = make(B, 70, Hk, H, K, V, BF, seed=B)
+        check_all(run(x), reference(*x), K, V, BF)
+
+
+def test_scale_and_long():
+    note("gdr scale, 700 tokens")
+    x = make(1, 700, 1, 1, 64, 64, F32, seed=4)
+    check_all(run(x, scale=0.7), reference(*x, scale=0.7), 64, 64, F32)
+
+
+@pytest.mark.parametrize("kind", ["g_zero", "g_inf", "g_large", "beta_zero", "beta_one_same_keys", "beta_small"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_edges(kind, dtype):
+    note(f"gdr edge {kind} {dtype}")
+    q, k, v, g, beta, h0, do, dhT = make(1, 150, 1, 2, 64, 64, dtype, seed=9)
+    if kind == "g_zero":
+        g = torch.zeros_like(g)
+    elif kind == "g_inf":          # the state is cleared before tokens 0, 40 and 64 .. 66
+        g[:, [0, 40, 64, 65, 66]] = -float("inf")
+    elif kind == "g_large":
+        g = -30 * torch.rand(g.shape, generator=torch.Generator().manual_seed(1))
+    elif kind == "beta_zero":
+        beta[:, 20:90] = 0
+    elif kind == "beta_small":
+        beta = 1e-6 * beta
+    else:                          # (I + A) as far from I as it gets
+        beta, g = torch.ones_like(beta), torch.zeros_like(g)
+        k = k[:, :1].expand_as(k).contiguous()
+    x = (q, k, v, g, beta, h0, do, dhT)
+    want = reference(q, k, v, g.clamp(min=-1e4), beta, h0, do, dhT)
+    got = run(x)
+    # |k| is 1 up to its rounding: with one key throughout, a token's error along k is
+    # replaced, not added to, so the tolerances hold as they are.  dg under decays of e^-30
+    # is a difference of row sums that all but cancel: it is held to the size of those
+    # sums (dg's own plus q dq and k dk).
+    for n, t in got.items():
+        tol = tol_bwd(64, 64, t.dtype) if n in GRADS else tol_fwd(64, t.dtype)
+        d = (t.double().cpu() - want[n]).norm().item()
+        size = want[n].norm().item()
+        if n == "dg":
+            rows = (q.double() * want["dq"]).sum(-1).norm() + (k.double() * want["dk"]).sum(-1).norm()
+            size += rows.item()
+        assert torch.isfinite(t).all() and d <= tol * size, f"{n}: {d / size:.3e} over {tol:.3e}"
+
+
+def test_nan_stays_in_its_sequence():
+    note("gdr NaN in one packed sequence")
+    cu, T = [0, 70, 130, 200], 200
+    x = list(make(1, T, 1, 2, 64, 64, BF, seed=2, N=3))
+    clean = run(x, cu)
+    x[2] = x[2].clone()
+    x[2][0, 100] = float("nan")
+    x[0] = x[0].clone()
+    x[0][0, 129] = float("inf")    # the last token of the sequence, beside the next one's first
+    got = run(x, cu)
+    for n in ("o", "dq", "dk", "dv", "dg", "dbeta"):
+        for a, b in ((0, 70), (130, 200)):
+            assert torch.equal(got[n][0, a:b], clean[n][0, a:b]), n
+    for n in ("hT", "dh0"):
+        for s in (0, 2):
+            assert torch.equal(got[n][s], clean[n][s]), n
+    assert torch.isnan(got["o"][0, 100]).all()   # its chunk's other tokens are unspecified
+
+
+def test_rows_outside_the_sequences():
+    note("gdr rows outside")
+    cu, T = [10, 80], 100
+    q, k, v, g, beta, h0, do, dhT = dev(*make(1, T, 1, 2, 64, 64, BF, seed=3, N=1))
+    c = cu_of(cu)
+    o = torch.full_like(v, 7.0)
+    _, ck, _ = L.gdr_fwd(q, k, v, g, beta, h0, cu_seqlens=c, o=o)
+    out = [torch.full_like(t, 7.0) for t in (q, k, v, g, beta)]
+    L.gdr_bwd(do, q, k, v, g, beta, ck, dhT, cu_seqlens=c, out=out)
+    fresh = L.gdr_fwd(q, k, v, g, beta, h0, cu_seqlens=c)[0]
+    fresh_g = L.gdr_bwd(do, q, k, v, g, beta, ck, dhT, cu_seqlens=c)[:5]
+    torch.cuda.synchronize()
+    for kept, new in zip([o, *out], [fresh, *fresh_g]):
+        assert torch.equal(kept[:, 10:80], new[:, 10:80])
+        for a, b in ((0, 10), (80, T)):
+            assert (kept[:, a:b] == 7).all() and (new[:, a:b] == 0).all()
+
+
+def test_bad_offsets_only_give_bad_results():
+    """Offsets out of range or decreasing: clamped, nothing outside the tensors is touched
+    (the arithmetic is checked on the CPU in test_gdr_checks)."""
+    note("gdr bad offsets")
+    T = 130
+    q, k, v, g, beta, h0, do, dhT = dev(*make(1, T, 1, 2, 64, 64, BF, seed=3, N=3))
+    for cu in ([0, 500, 90, 130], [-5, 20, 2 ** 31 - 1, 130], [130, 100, 50, 0]):
+        c = cu_of(cu)
+        guard = torch.full((3, T, 2, 64), 7.0, dtype=BF, device=DEV)
+        _, ck, _ = L.gdr_fwd(q, k, v, g, beta, h0, cu_seqlens=c, o=guard[1:2])
+        L.gdr_bwd(do, q, k, v, g, beta, ck, dhT, cu_seqlens=c)
+        torch.cuda.synchronize()
+        assert (guard[0] == 7).all() and (guard[2] == 7).all()
+
+
+def test_outputs_are_fully_written_and_repeat():
+    note("gdr prefilled outputs, two runs")
+    q, k, v, g, beta, h0, do, dhT = dev(*make(2, 70, 2, 4, 128, 64, BF, seed=5))
+    nan = float("nan")
+    runs = []
+    for fill in (nan, 3.0):
+        full = lambda t: torch.full_like(t, fill)  # noqa: E731
+        hT = torch.full((2, 4, 64, 128), fill, device=DEV)
+        ws = torch.full((gdr._lib().gdr_fwd_workspace_bytes(2, 70, 2, 4, 128, 64, 1, 0, 0) // 4,), fill, device=DEV)
+        o, ck, hT = L.gdr_fwd(q, k, v, g, beta, h0, o=full(v), hT=hT, workspace=ws)
+        out = [full(t) for t in (q, k, v, g, beta)]
+        wb = torch.full((gdr._lib().gdr_bwd_workspace_bytes(2, 70, 2, 4, 128, 64, 1, 0, 0) // 4,), fill, device=DEV)
+        dh0 = L.gdr_bwd(do, q, k, v, g, beta, ck, dhT, out=out, workspace=wb)[5]
+        runs.append([o, hT, ck, *out, dh0])
+    torch.cuda.synchronize()
+    for a, b in zip(*runs):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+def test_in_place_state_and_wanted_outputs():
+    note("gdr hT in place of h0")
+    q, k, v, g, beta, h0, *_ = dev(*make(2, 90, 2, 2, 64, 64, BF, seed=6))
+    o, ck, hT = L.gdr_fwd(q, k, v, g, beta, h0)
+    s = h0.clone()
+    o2, ck2, hT2 = L.gdr_fwd(q, k, v, g, beta, s, hT=s, want_ckpt=False)
+    o3, ck3, hT3 = L.gdr_fwd(q, k, v, g, beta, h0, want_o=False, want_ckpt=False)
+    torch.cuda.synchronize()
+    assert ck2 is None and ck3 is None and o3 is None and hT2 is s
+    assert torch.equal(o, o2) and torch.equal(hT, s) and torch.equal(hT, hT3)
+
+
+def test_differences():
+    """A directional derivative from the forward itself (fp32 inputs) against the backward:
+    the central difference over +-h is off by the rounding of o and hT over h (about
+    2^-22 |L| / h) and by h^2 / 6 of the third derivative."""
+    note("gdr central differences")
+    x = make(1, 130, 1, 2, 64, 64, F32, seed=8)
+    q, k, v, g, beta, h0, do, dhT = dev(*x)
+    got = run(x)
+    gen = torch.Generator().manual_seed(3)
+    h = 2.0 ** -6
+    for i, (t, n) in enumerate(zip((q, k, v, g, beta, h0), GRADS)):
+        d = torch.randn(t.shape, generator=gen).to(DEV)
+        d = d / d.norm() * t.norm() * 0.25
+
+        def loss(sign):
+            ins = [q, k, v, g, beta, h0]
+            ins[i] = t + sign * h * d
+            o, _, hT = L.gdr_fwd(*ins, want_ckpt=False)
+            return ((o.double() * do.double()).sum() + (hT.double() * dhT.double()).sum()).item()
+
+        num, ana = (loss(1) - loss(-1)) / (2 * h), (got[n].double() * d.double()).sum().item()
+        size = got[n].double().norm().item() * d.double().norm().item()
+        assert abs(num - ana) <= 2e-3 * size + 1e-3 * abs(ana), (n, num, ana, size)
+
+
+def test_other_stream_and_graph():
+    """A forward and backward captured once and replayed with other offsets and inputs, against eager calls."""
+    note("gdr stream and graph")
+    T, N = 200, 4
+    x = make(1, T, 1, 2, 64, 64, BF, seed=11, N=N)
+    q, k, v, g, beta, h0, do, dhT = dev(*x)
+    offsets = [[0, 64, 64, 130, 200], [0, 1, 2, 3, 150], [0, 200, 200, 200, 200]]
+    c = cu_of(offsets[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def both():
+        o, ck, hT = L.gdr_fwd(q, k, v, g, beta, h0, cu_seqlens=c)
+        return [o, hT, *L.gdr_bwd(do, q, k, v, g, beta, ck, dhT, cu_seqlens=c)]
+
+    with torch.cuda.stream(side):
+        first = both()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both()
+    for i in range(6):
+        c.copy_(cu_of(offsets[i % 3]))
+        v.mul_(1.25)
+        graph.replay()
+        got = [t.clone() for t in outs]
+        torch.cuda.synchronize()
+        want = both()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+    assert all(torch.isfinite(t).all() for t in first)
+
+
+def test_autograd_op_and_norm():
+    """The layer as it is used: a norm before, the rule, a per-head norm after it; every gradient
+    against 64-bit autograd on the definitions."""
+    note("GDR + LN autograd")
+    B, T, Hk, H, K, V = 2, 75, 2, 4, 64, 64
+    q, k, v, g, beta, h0, *_ = make(B, T, Hk, H, K, V, F32, seed=12)
+    gen = torch.Generator().manual_seed(2)
+    w1, b1, w2 = (torch.randn(n, generator=gen) for n in (H * V, H * V, H * V))
+    cot = torch.randn(B, T, H * V, generator=gen)
+    leaves = [t.to(DEV).requires_grad_() for t in (q, k, v, g, beta, h0, w1, b1, w2)]
+    Q, Kk, Vv, G, Bt, S0, W1, B1, W2 = leaves
+    xn = L.LN.apply(Vv.reshape(B, T, H * V), W1, B1)
+    o, hT = L.GDR.apply(Q, Kk, xn.view(B, T, H, V), G, Bt, S0)
+    y = L.LN.apply(o.reshape(B, T, H * V), W2, None, H)
+    loss = (y * cot.to(DEV)).sum() + hT.square().sum()
+    got = torch.autograd.grad(loss, leaves)
+
+    ref = [t.detach().double().cpu().requires_grad_() for t in leaves]
+    rq, rk, rv, rg, rb, rs, rw1, rb1, rw2 = ref
+
+    def norm(z, w, b, n):
+        p = z.reshape(B, T, n, -1)
+        c = p - p.mean(-1, keepdim=True)
+        return (c / (c.square().mean(-1, keepdim=True) + 1e-5).sqrt()).reshape(B, T, -1) * w + b
+
+    from tests.gdr_util import ref_dense
+    ro, rhT = ref_dense(rq, rk, norm(rv, rw1, rb1, 1).view(B, T, H, V), rg, rb, rs, K ** -0.5)
+    ry = norm(ro, rw2, 0.0, H)
+    want = torch.autograd.grad((ry * cot.double()).sum() + rhT.square().sum(), ref)
+    # the norms add a sum over H V channels forward and backward, and divide by the
+    # spread of o's parts, which amplifies o's error by |o| / spread (about 1 here)
+    tol = 2 * tol_bwd(K, V, F32) + 2 * H * V * 2.0 ** -24
+    for n, a, b in zip("q k v g beta h0 w1 b1 w2".split(), got, want):
+        assert rel(a, b) <= tol, (n, rel(a, b), tol)
+
+
+def test_autograd_types_and_missing_gradients():
+    note("GDR autograd, bf16, unused hT, packed tail")
+    q, k, v, g, beta, h0, *_ = dev(*make(1, 40, 1, 2, 64, 64, BF, seed=13, N=1))
+    for t in (q, k, v):
+        t.requires_grad_()
+    gb = g.to(BF).requires_grad_()
+    o, hT = L.GDR.apply(q, k, v, gb, beta, None, cu_of([0, 30]), 0.5)
+    o.float().square().sum().backward()
+    assert q.grad.dtype == BF and gb.grad.dtype == BF and (q.grad[:, 30:] == 0).all() and (gb.grad[:, 30:] == 0).all()
+    assert (o[:, 30:] == 0).all() and torch.isfinite(k.grad).all()
+    with torch.no_grad():
+        o2, _ = L.GDR.apply(q, k, v, gb, beta, None, cu_of([0, 30]), 0.5)
+    assert torch.equal(o, o2)
+    q.grad = None
+    o, hT = L.GDR.apply(q, k, v, g, beta)
+    hT.sum().backward()                                    # o unused
+    assert (q.grad == 0).all() and k.grad.abs().sum() > 0
+
+
+# ---------------------------------------------------------------------------- the recurrent step
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K,V", HEADS)
+@pytest.mark.parametrize("B,T,Hk,H", [(1, 1, 1, 1), (3, 1, 2, 6), (2, 4, 1, 2), (70, 1, 2, 2)])
+def test_step(B, T, Hk, H, K, V, dtype):
+    note(f"gdr step B{B} T{T} Hk{Hk} H{H} K{K} V{V} {dtype}")
+    q, k, v, g, beta, h0, *_ = make(B, T, Hk, H, K, V, dtype, seed=B)
+    want = reference(q, k, v, g, beta, h0)
+    dq = dev(q, k, v, g, beta)
+    s = h0.to(DEV)
+    o = L.gdr_step(*dq, s)
+    out = torch.full_like(s, 5.0)
+    o2 = L.gdr_step(*dq, h0.to(DEV), state_out=out)
+    torch.cuda.synchronize()
+    assert rel(o, want["o"]) <= tol_fwd(K, dtype) and rel(s, want["hT"]) <= tol_fwd(K, F32)
+    assert torch.equal(o, o2) and torch.equal(s, out)
+
+
+def test_step_slots():
+    """Slots in any order, padding rows, and rows that share a slot: consecutive tokens of one sequence."""
+    note("gdr step slots")
+    B, T, Hk, H, K, V, P = 8, 2, 1, 2, 64, 128, 9
+    q, k, v, g, beta, h0, *_ = make(B, T, Hk, H, K, V, BF, seed=1, N=P)
+    slots = [4, -1, 0, 4, P, 8, 0, 4]
+    state = h0.to(DEV)
+    o = L.gdr_step(*dev(q, k, v, g, beta), state, slots=torch.tensor(slots, dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    want, wo = h0.double().clone(), torch.zeros(B, T, H, V, dtype=torch.float64)
+    for b, s in enumerate(slots):
+        if 0 <= s < P:
+            r = reference(*[x[b:b + 1] for x in (q, k, v, g, beta)], want[s:s + 1])
+            wo[b], want[s] = r["o"][0], r["hT"][0]
+    assert rel(o, wo) <= tol_fwd(K, BF) and rel(state, want) <= tol_fwd(K, F32)
+    assert (o[1] == 0).all() and (o[4] == 0).all()
+    for s in (1, 2, 3, 5, 6, 7):
+        assert torch.equal(state[s].cpu(), h0[s])
+
+
+def test_step_edges_and_graph():
+    note("gdr step, g = -inf, beta = 0, graph")
+    B, H = 3, 2
+    q, k, v, g, beta, h0, *_ = make(B, 1, H, H, 64, 64, BF, seed=21)
+    g[0], beta[1] = -float("inf"), 0.0
+    want = reference(q, k, v, g.clamp(min=-1e4), beta, h0)
+    ins, s = dev(q, k, v, g, beta), h0.to(DEV)
+    slots = torch.tensor([2, 0, 1], dtype=torch.int32, device=DEV)
+    pool = h0[[1, 2, 0]].to(DEV)
+    o = L.gdr_step(*ins, s)
+    assert rel(o, want["o"]) <= tol_fwd(64, BF) and rel(s, want["hT"]) <= tol_fwd(64, F32)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        og = L.gdr_step(*ins, pool, slots=slots)
+    eager = pool.clone()
+    for i in range(4):
+        slots.copy_(torch.tensor([[2, 0, 1], [1, 1, -1], [0, 2, 2], [7, 0, 1]][i], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        oe = L.gdr_step(*ins, eager, slots=slots)
+        torch.cuda.synchronize()
+        assert torch.equal(og, oe) and torch.equal(pool, eager), i
+
+
+def test_prompt_then_steps_then_norm():
+    """Serving as a whole: packed prompts fill a pool, tokens follow one at a time, each output goes
+    through the per-head norm."""
+    note("gdr prompt + steps + norm")
+    Hk, H, K, V, P = 1, 2, 128, 128, 5
+    lens, new = [65, 1, 0, 130], 5
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    q, k, v, g, beta, *_ = make(1, cu[-1], Hk, H, K, V, BF, seed=31, N=4)
+    nq, nk, nv, ng, nb, *_ = make(4, new, Hk, H, K, V, BF, seed=32)
+    w = torch.randn(H * V, generator=torch.Generator().manual_seed(5))
+    pool = torch.zeros(P, H, V, K, device=DEV)
+    slots = torch.tensor([3, 0, 4, 1], dtype=torch.int32, device=DEV)
+    _, _, hT = L.gdr_fwd(*dev(q, k, v, g, beta), cu_seqlens=cu_of(cu), want_ckpt=False)
+    pool[slots.long()] = hT
+    ys, os_ = [], []
+    for t in range(new):
+        o = L.gdr_step(*dev(*[x[:, t:t + 1].contiguous() for x in (nq, nk, nv, ng, nb)]), pool, slots=slots)
+        os_.append(o)
+        ys.append(L.ln_fwd(o.view(4, H * V), w.to(DEV), groups=H, want_stats=False)[0])
+    torch.cuda.synchronize()
+    for n in range(4):
+        a, b = cu[n], cu[n + 1]
+        full = [torch.cat([x[:, a:b], y[n:n + 1]], 1) for x, y in zip((q, k, v, g, beta), (nq, nk, nv, ng, nb))]
+        r = reference(*full)
+        o = torch.cat([x[n:n + 1] for x in os_], 1)
+        assert rel(o, r["o"][:, b - a:]) <= tol_fwd(K, BF)
+        assert rel(pool[slots[n].item()], r["hT"][0]) <= tol_fwd(K, F32)
+        for t in range(new):
+            want = ref_norm(os_[t][n].reshape(1, -1).cpu(), w, None, H, 1e-5)["y"]
+            assert rel(ys[t][n:n + 1], want) <= 2.0 ** -8 + 2 * V * 2.0 ** -24
