@@ -140,6 +140,33 @@ __device__ __forceinline__ PF<NP> frag_col(const char* X, int plane, int tile, i
     return f;
 }
 
+// T and M are lower triangular: only their three lower 32 x 32 blocks exist, in
+// the order (0, 0), (1, 0), (1, 1), each with rows of four units, unit u of row t
+// in slot u ^ (t / 8).  Rows and columns as above (ks <= tile / 2, ks >= tile / 2).
+constexpr int kTriBytes = 3 * 32 * 64;   // one plane
+__device__ __forceinline__ int tri_block(int br, int bc) { return (br + bc) * 2048; }
+template <int NP>
+__device__ __forceinline__ PF<NP> tri_row(const char* X, int tile, int ks, int lane) {
+    const int row = idx(tile & 1, lane & 15);
+    const char* p = X + tri_block(tile >> 1, ks) + (row * 4 + ((lane >> 4) ^ (row >> 3))) * 16;
+    PF<NP> f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) f.p[i] = *reinterpret_cast<const bf16x8*>(p + i * kTriBytes);
+    return f;
+}
+template <int NP>
+__device__ __forceinline__ PF<NP> tri_col(const char* X, int tile, int ks, int lane) {
+    const int row = 8 * (lane >> 4) + ((lane & 15) >> 2);
+    const char* p = X + tri_block(ks, tile >> 1) + (row * 4 + ((lane & 3) ^ (lane >> 4))) * 16 + 8 * (tile & 1);
+    PF<NP> f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+        f.p[i] = wkv7::cat8(
+            wkv7::as_bf16x4(__builtin_amdgcn_ds_read_tr16_b64_v4i16((wkv7::lds_i16x4*)(p + i * kTriBytes))),
+            wkv7::as_bf16x4(__builtin_amdgcn_ds_read_tr16_b64_v4i16((wkv7::lds_i16x4*)(p + 256 + i * kTriBytes))));
+    return f;
+}
+
 // Eight consecutive values of a row into the planes of an LDS matrix.
 template <int U, int NP>
 __device__ __forceinline__ void put8(char* X, int plane, int row, int unit, const PF<NP>& f) {
@@ -148,9 +175,12 @@ __device__ __forceinline__ void put8(char* X, int plane, int row, int unit, cons
     for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x8*>(p + i * plane) = f.p[i];
 }
 
-// One value of a token tensor.
-__device__ __forceinline__ float ld(const float* p) { return *p; }
-__device__ __forceinline__ float ld(const uint16_t* p) { return __uint_as_float((uint32_t)(*p) << 16); }
+// One value of a token tensor.  widen() is apart from the load, so that a load
+// ahead of its use does not wait where it is issued.
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+template <typename T>
+__device__ __forceinline__ float ld(const T* p) { return widen(*p); }
 __device__ __forceinline__ void st(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 

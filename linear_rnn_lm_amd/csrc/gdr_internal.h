@@ -33,9 +33,10 @@ struct Args {
 
 // bf16 planes of a derived value, and of an input, by input type.
 constexpr int kPlanes = 3;
-// Bytes of T and M of one chunk of one head: row-major 64 x 64 planes.
+// Bytes of T and M of one chunk of one head: planes of three 32 x 32 blocks.
+constexpr int kOpsBytes = 2 * kPlanes * 3 * 32 * 64;
+// Bytes of one plane of a row-major 64 x 64 matrix.
 constexpr int kMatBytes = 64 * 64 * 2;
-constexpr int kOpsBytes = 2 * kPlanes * kMatBytes;
 
 struct StepArgs {
     const void *q, *k, *v;

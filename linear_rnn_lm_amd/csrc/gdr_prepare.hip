@@ -165,23 +165,16 @@ __global__ __launch_bounds__(256) void prepare_kernel(Args p) {
     block_product(Ts + (32 + mr) * LDA + 32, As + 32 + mc, Ts + (32 + mr) * LDA + mc, 32, -1.f, lane);
     __syncthreads();
 
-    // to planes; the upper right 32 x 32 block of both is zero and never read
+    // The three lower 32 x 32 blocks to planes, as the scans' LDS holds them.
     char* ops = p.ops + block * kOpsBytes;
-    const int t = tid >> 2, c0 = 16 * (tid & 3);
-    if (t >= 32 || c0 < 32) {
+    for (int e = tid; e < 2 * 3 * 128; e += 256) {       // matrix, block, row, unit
+        const int m = e / 384, blk = (e >> 7) % 3, row = (e >> 2) & 31, u = e & 3;
+        const float* src = (m ? Ms : Ts) + ((blk ? 32 : 0) + row) * LDA + (blk == 2 ? 32 : 0) + 8 * u;
+        const PF<kPlanes> f =
+            pf_acc<kPlanes>(*reinterpret_cast<const f32x4*>(src), *reinterpret_cast<const f32x4*>(src + 4));
+        char* dst = ops + m * kPlanes * kTriBytes + blk * 2048 + (row * 4 + (u ^ (row >> 3))) * 16;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const float* src = (m ? Ms : Ts) + t * LDA + c0;
-            char* dst = ops + m * kPlanes * kMatBytes + (t * C + c0) * 2;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const PF<kPlanes> f = pf_acc<kPlanes>(*reinterpret_cast<const f32x4*>(src + 8 * u),
-                                                      *reinterpret_cast<const f32x4*>(src + 8 * u + 4));
-#pragma unroll
-                for (int i = 0; i < kPlanes; ++i)
-                    *reinterpret_cast<bf16x8*>(dst + i * kMatBytes + 16 * u) = f.p[i];
-            }
-        }
+        for (int i = 0; i < kPlanes; ++i) *reinterpret_cast<bf16x8*>(dst + i * kTriBytes) = f.p[i];
     }
 }
 

@@ -20,8 +20,8 @@ constexpr int NP = kPlanes;
 template <int NX, int K>
 struct Buf {
     static constexpr int XB = C * K * 2;                  // one plane of K or Q rows
-    static constexpr int Kr = 0, Qr = Kr + NX * XB, T = Qr + NX * XB, M = T + NP * kMatBytes;
-    static constexpr int G = M + NP * kMatBytes;          // e^G, e^(G_C - G), b, unused
+    static constexpr int Kr = 0, Qr = Kr + NX * XB, T = Qr + NX * XB, M = T + NP * kTriBytes;
+    static constexpr int G = M + NP * kTriBytes;          // e^G, e^(G_C - G), b, unused
     static constexpr int bytes = G + 1024;
     static constexpr int NBUF = 2 * bytes <= 160 * 1024 ? 2 : 1;
 };
@@ -46,14 +46,10 @@ __device__ __forceinline__ void stage(const Args& p, char* buf, int64_t tok, int
                       buf + (m ? B::Qr : B::Kr) + i * B::XB + pc * 1024);
             }
     }
-    const char* ops = p.ops + block * kOpsBytes;
+    const char* ops = p.ops + block * kOpsBytes;          // as the LDS holds it
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i)
-#pragma unroll
-        for (int u = 0; u < 8 / NMW; ++u) {
-            const int pc = u * NMW + mw, row = pc * 8 + lane / 8;
-            dma16(ops + i * kMatBytes + row * 128 + 16 * ((lane % 8) ^ swz<8>(row)), buf + B::T + i * kMatBytes + pc * 1024);
-        }
+    for (int u = 0; u < kOpsBytes / 1024 / NMW; ++u)
+        dma16(ops + (u * NMW + mw) * 1024 + 16 * lane, buf + B::T + (u * NMW + mw) * 1024);
     if (mw == 0) dma16(reinterpret_cast<const char*>(p.gates + block * kGateFloats) + 16 * lane, buf + B::G);
 }
 
@@ -109,16 +105,15 @@ __global__ __launch_bounds__(64 * (NCW + NMW)) void scan_kernel(Args p, int nsub
     const InT* x = static_cast<const InT*>(BWD ? p.dout : p.v);
     InT* y = static_cast<InT*>(BWD ? p.dv : p.o);
     const int64_t xstride = (int64_t)p.H * p.V, xoff = tok0 * xstride + (int64_t)h * p.V + i;
-    // column i of a chunk's v or dout rows, in accumulator order (0 past the end)
-    auto load_x = [&](float (&r)[16], int it) {
+    // column i of a chunk's v or dout rows, in accumulator order, as stored; rows past the
+    // end repeat the last one and are cleared at their use
+    auto load_x = [&](InT (&r)[16], int it) {
         const int c = chunk_of(min(it, nc - 1));
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int t = c * C + idx(e >> 2, 4 * g4 + (e & 3));
-            r[e] = t < len ? ld(x + xoff + t * xstride) : 0.f;
-        }
+        for (int e = 0; e < 16; ++e)
+            r[e] = x[xoff + min(c * C + idx(e >> 2, 4 * g4 + (e & 3)), len - 1) * xstride];
     };
-    float xr[16];
+    InT xr[16];
     if (nc > 0) load_x(xr, 0);
     lds_barrier();
     for (int it = 0; it < nc; ++it) {
@@ -126,7 +121,7 @@ __global__ __launch_bounds__(64 * (NCW + NMW)) void scan_kernel(Args p, int nsub
         const int64_t block = block_of(c);
         const char* buf = smem + (it % B::NBUF) * B::bytes;
         const float* gates = reinterpret_cast<const float*>(buf + B::G);
-        float xn[16];
+        InT xn[16];
         load_x(xn, it + 1);
         // the state entering the chunk, or the gradient at its end
         float* keep = BWD ? p.dend : p.ckpt;
@@ -140,7 +135,9 @@ __global__ __launch_bounds__(64 * (NCW + NMW)) void scan_kernel(Args p, int nsub
         auto gate = [&](int which, int t) { return *reinterpret_cast<const f32x4*>(gates + which + idx(t, 4 * g4)); };
         f32x4 xa[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) xa[t] = f32x4{xr[4 * t], xr[4 * t + 1], xr[4 * t + 2], xr[4 * t + 3]};
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) xa[t][q] = c * C + idx(t, 4 * g4 + q) < len ? widen(xr[4 * t + q]) : 0.f;
         const float eGC = gates[kGateEG + C - 1];
 
         f32x4 a[4], b[4];
@@ -167,7 +164,7 @@ __global__ __launch_bounds__(64 * (NCW + NMW)) void scan_kernel(Args p, int nsub
                 u[t] = zero4();
 #pragma unroll
                 for (int ks = 0; ks <= (t >> 1); ++ks)
-                    u[t] = pmma<NP>(u[t], frag_row<8, NP>(buf + B::T, kMatBytes, idx(t, r16), ks, lane), rf[ks]);
+                    u[t] = pmma<NP>(u[t], tri_row<NP>(buf + B::T, t, ks, lane), rf[ks]);
             }
             if (keep) {
                 float* ku = keep + block * kblock + (int64_t)p.V * K + i;
@@ -182,7 +179,7 @@ __global__ __launch_bounds__(64 * (NCW + NMW)) void scan_kernel(Args p, int nsub
                 f32x4 o = gate(kGateEG, t) * b[t];
 #pragma unroll
                 for (int ks = 0; ks <= (t >> 1); ++ks)
-                    o = pmma<NP>(o, frag_row<8, NP>(buf + B::M, kMatBytes, idx(t, r16), ks, lane), uf[ks]);
+                    o = pmma<NP>(o, tri_row<NP>(buf + B::M, t, ks, lane), uf[ks]);
                 if (y) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -211,7 +208,7 @@ __global__ __launch_bounds__(64 * (NCW + NMW)) void scan_kernel(Args p, int nsub
                 f32x4 m = zero4();
 #pragma unroll
                 for (int ks = (t >> 1); ks < 2; ++ks)
-                    m = pmma<NP>(m, frag_col<8, NP>(buf + B::M, kMatBytes, t, ks, lane), df[ks]);
+                    m = pmma<NP>(m, tri_col<NP>(buf + B::M, t, ks, lane), df[ks]);
                 du[t] = gate(kGateToEnd, t) * a[t] + p.scale * m;
             }
             const PF<NP> uf[2] = {pf_acc<NP>(du[0], du[1]), pf_acc<NP>(du[2], du[3])};
@@ -220,7 +217,7 @@ __global__ __launch_bounds__(64 * (NCW + NMW)) void scan_kernel(Args p, int nsub
                 z[t] = zero4();
 #pragma unroll
                 for (int ks = (t >> 1); ks < 2; ++ks)
-                    z[t] = pmma<NP>(z[t], frag_col<8, NP>(buf + B::T, kMatBytes, t, ks, lane), uf[ks]);
+                    z[t] = pmma<NP>(z[t], tri_col<NP>(buf + B::T, t, ks, lane), uf[ks]);
             }
             float* kz = p.z + block * (int64_t)C * p.V + i;
             f32x4 zg[4], xg[4];
