@@ -529,6 +529,28 @@ WKV7 = _LazyOp(0)
 WKV7Proj = _LazyOp(1)
 
 
+def _fits(t, shape, dtype, dev):
+    """Whether a tensor is what a call wants: one test for the good case, its
+    reason for failing is worked out only then (by the checks above)."""
+    return t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous()
+
+
+def _launch(fn, entry, dev, *args):
+    """Call a library entry point on the current stream of `dev` with that device
+    current, and raise its error."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError(f"libwkv7 works on GPU tensors; got tensors on {dev}")
+    i = torch.cuda.current_device() if dev.index is None else dev.index
+    if torch.cuda.current_device() == i:
+        st = entry(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            st = entry(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != 0:
+        _check(fn, st)
+
+
 class _LazyOpOf:
     """An autograd op made by `make` on first use (torch is imported only then)."""
 

@@ -10,6 +10,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "abi_checks.h"
 #include "lnorm.h"
 #include "wkv7_device.h"
@@ -20,6 +22,7 @@ namespace {
 
 using wkv7::bf16x8;
 using wkv7::f32x4;
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 struct Args {
     const void *x, *dy, *weight, *bias;
@@ -30,35 +33,41 @@ struct Args {
     int64_t rows;
     int C, G, D, teams;  // teams: a multiple of G
     int parts;           // row count of `part`
+    bool combine;        // backward: a workgroup adds up its teams of one group
     bool wbf16;
 };
 
-template <int VEC>
-__device__ __forceinline__ void loadv(const float* p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+// VEC values as stored, widened only at their use, so that the next row's loads
+// do not wait where they are issued.
+template <typename T, int VEC>
+struct Raw {
+    typename std::conditional<VEC == 8, typename std::conditional<sizeof(T) == 2, u32x4, f32x4>::type, T>::type v[VEC == 8 ? sizeof(T) / 2 : 1];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = a[e];
-            v[e + 4] = b[e];
-        }
-    } else {
-        v[0] = *p;
+        for (size_t i = 0; i < sizeof(v) / sizeof(v[0]); ++i) v[i] = reinterpret_cast<const std::remove_reference_t<decltype(v[0])>*>(p)[i];
     }
-}
-template <int VEC>
-__device__ __forceinline__ void loadv(const uint16_t* p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    __device__ __forceinline__ void widen(float (&o)[VEC]) const {
+        if constexpr (VEC == 8 && sizeof(T) == 2) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(w[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            for (int e = 0; e < 4; ++e) {
+                o[2 * e] = __uint_as_float(v[0][e] << 16);
+                o[2 * e + 1] = __uint_as_float(v[0][e] & 0xffff0000u);
+            }
+        } else if constexpr (VEC == 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = v[e / 4][e % 4];
+        } else if constexpr (sizeof(T) == 2) {
+            o[0] = __uint_as_float((uint32_t)v[0] << 16);
+        } else {
+            o[0] = v[0];
         }
-    } else {
-        v[0] = __uint_as_float((uint32_t)*p << 16);
     }
+};
+template <int VEC, typename T>
+__device__ __forceinline__ void loadv(const T* p, float (&v)[VEC]) {
+    Raw<T, VEC> r;
+    r.load(p);
+    r.widen(v);
 }
 template <int VEC>
 __device__ __forceinline__ void storev(float* p, const float (&v)[VEC]) {
@@ -162,12 +171,21 @@ __global__ __launch_bounds__(threads<L>()) void fwd_kernel(Args p) {
             load_w<VEC>(p, p.weight, t.g * p.D + t.d(i), 1.f, w[i]);
             load_w<VEC>(p, p.bias, t.g * p.D + t.d(i), 0.f, b[i]);
         }
+    Raw<InT, VEC> next[NV];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (t.d(i) < p.D) next[i].load(x + row * p.C + t.d(i));
+    };
+    if (t.row < p.rows) fetch(t.row);
     for (int64_t row = t.row; row < p.rows; row += t.step) {
         float v[NV][VEC], s = 0.f;
 #pragma unroll
+        for (int i = 0; i < NV; ++i) next[i].widen(v[i]);
+        if (row + t.step < p.rows) fetch(row + t.step);
+#pragma unroll
         for (int i = 0; i < NV; ++i)
             if (t.d(i) < p.D) {
-                loadv<VEC>(x + row * p.C + t.d(i), v[i]);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) s += v[i][e];
             }
@@ -215,15 +233,33 @@ __global__ __launch_bounds__(threads<L>()) void bwd_kernel(Args p) {
         for (int e = 0; e < VEC; ++e) w[i][e] = dw[i][e] = db[i][e] = 0.f;
         if (t.on && t.d(i) < p.D) load_w<VEC>(p, p.weight, t.g * p.D + t.d(i), 1.f, w[i]);
     }
-    int flip = 0;
-    for (int64_t row = t.on ? t.row : p.rows; row < p.rows; row += t.step, flip ^= 2) {
-        const float mean = p.mean[row * p.G + t.g], rstd = p.rstd[row * p.G + t.g];
-        float xh[NV][VEC], e[NV][VEC], s1 = 0.f, s2 = 0.f;
+    Raw<InT, VEC> nx[NV];
+    Raw<OutT, VEC> ny[NV];
+    float nmean = 0.f, nrstd = 0.f;
+    auto fetch = [&](int64_t row) {
+        nmean = p.mean[row * p.G + t.g];
+        nrstd = p.rstd[row * p.G + t.g];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (t.d(i) < p.D) {
-                loadv<VEC>(x + row * p.C + t.d(i), xh[i]);
-                loadv<VEC>(dy + row * p.C + t.d(i), e[i]);
+                nx[i].load(x + row * p.C + t.d(i));
+                ny[i].load(dy + row * p.C + t.d(i));
+            }
+    };
+    if (t.on && t.row < p.rows) fetch(t.row);
+    int flip = 0;
+    for (int64_t row = t.on ? t.row : p.rows; row < p.rows; row += t.step, flip ^= 2) {
+        const float mean = nmean, rstd = nrstd;
+        float xh[NV][VEC], e[NV][VEC], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            nx[i].widen(xh[i]);
+            ny[i].widen(e[i]);
+        }
+        if (row + t.step < p.rows) fetch(row + t.step);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (t.d(i) < p.D) {
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
                     xh[i][k] = (xh[i][k] - mean) * rstd;
@@ -245,7 +281,31 @@ __global__ __launch_bounds__(threads<L>()) void bwd_kernel(Args p) {
                 storev<VEC>(dx + row * p.C + t.d(i), e[i]);
             }
     }
-    if (!p.part || !t.on) return;
+    if (!p.part) return;
+    if constexpr (L <= 64) {
+        if (p.combine) {          // the workgroup holds whole rows of teams: one row of sums
+            constexpr int S = threads<L>() / L;
+            __shared__ float sum[threads<L>() * NV * VEC];
+            const int team = threadIdx.x / L, W = p.G * p.D;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (t.d(i) < p.D)
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) sum[team * p.D + t.d(i) + k] = m ? db[i][k] : dw[i][k];
+                __syncthreads();
+                for (int c = threadIdx.x; c < W; c += threads<L>()) {
+                    float s = 0.f;
+                    for (int j = 0; j < S / p.G; ++j) s += sum[j * W + c];
+                    p.part[((int64_t)m * p.parts + blockIdx.x) * p.C + c] = s;
+                }
+            }
+            return;
+        }
+    }
+    if (!t.on) return;
     float* pw = p.part + t.row * p.C + c0;
     float* pb = pw + (int64_t)p.parts * p.C;
 #pragma unroll
@@ -256,21 +316,24 @@ __global__ __launch_bounds__(threads<L>()) void bwd_kernel(Args p) {
         }
 }
 
-// Column sums of the (parts, C) sums: 32 columns by 8 rows of threads.
-__global__ __launch_bounds__(256) void reduce_kernel(const float* part, int parts, int C, float* dweight, float* dbias) {
-    __shared__ float red[8][32];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), r0 = threadIdx.x >> 5;
-    const float* src = part + (blockIdx.y ? (int64_t)parts * C : 0);
-    float s = 0.f;
-    if (c < C)
-        for (int r = r0; r < parts; r += 8) s += src[(int64_t)r * C + c];
-    red[r0][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (r0 == 0 && c < C) {
+// Column sums of the (parts, C) sums: 32 columns by 32 rows of threads, four rows each in flight.
+__global__ __launch_bounds__(1024) void reduce_kernel(const float* part, int parts, int C, float* dweight, float* dbias) {
+    __shared__ float red[32][33];
+    const int cl = threadIdx.x & 31, c = blockIdx.x * 32 + cl, r0 = threadIdx.x >> 5;
+    const float* src = part + (blockIdx.y ? (int64_t)parts * C : 0) + min(c, C - 1);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r = r0; r < parts; r += 128) {
 #pragma unroll
-        for (int r = 1; r < 8; ++r) s += red[r][threadIdx.x];
-        (blockIdx.y ? dbias : dweight)[c] = s;
+        for (int u = 0; u < 4; ++u) {
+            const float x = src[(int64_t)min(r + 32 * u, parts - 1) * C];
+            s[u] += r + 32 * u < parts ? x : 0.f;
+        }
     }
+    red[r0][cl] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    // the wave of rows 2c, 2c + 1 adds up columns 2c, 2c + 1
+    float x = wave_sum<32>(red[threadIdx.x & 31][r0]);
+    if ((threadIdx.x & 31) == 0 && blockIdx.x * 32 + r0 < C) (blockIdx.y ? dbias : dweight)[blockIdx.x * 32 + r0] = x;
 }
 
 // Lanes per team and vectors per lane for D channels.
@@ -300,12 +363,23 @@ int teams_of(int64_t rows, int G, int L, int n_cu, int waves_per_cu) {
     return (int)(r * G);
 }
 
-// Rows of the partial sums: enough teams to fill the chip, but at least 16 rows each.
-constexpr int kRowsPerTeam = 16;
-int bwd_parts(int64_t rows, int D, int G) {
+// How the backward's rows are shared out.  Where a workgroup of 256 holds the teams of one or
+// more whole rows (combine), each workgroup leaves one row of sums; otherwise each team
+// leaves its own.  At least two (eight) rows to a team, so that the sums
+// stay small beside x, dy and dx, and at most what fills the chip.
+struct Share {
+    bool combine;
+    int parts;
+};
+Share bwd_share(int64_t rows, int D, int G) {
     const Plan pl = plan_of(D);
-    const int64_t most = (int64_t)256 * 16 * 64 / pl.L / G + 1, few = (rows + kRowsPerTeam - 1) / kRowsPerTeam;
-    return (int)(few < most ? few : most);
+    const int S = 256 / pl.L;
+    if (pl.L <= 64 && S % G == 0) {
+        const int64_t per = S / G, few = (rows + 2 * per - 1) / (2 * per);
+        return {true, (int)(few < 1024 ? few : 1024)};
+    }
+    const int64_t most = (int64_t)256 * 16 * 64 / pl.L / G + 1, few = (rows + 7) / 8;
+    return {false, (int)(few < most ? few : most)};
 }
 
 template <typename InT, typename OutT, int VEC, int L, int NV>
@@ -314,7 +388,7 @@ hipError_t run(Args a, bool bwd, hipStream_t s) {
     int n_cu = 0;
     const hipError_t e = wkv7::device_cus(&n_cu);
     if (e != hipSuccess) return e;
-    a.teams = bwd ? a.parts * a.G : teams_of(a.rows, a.G, L, n_cu, 32);
+    a.teams = !bwd ? teams_of(a.rows, a.G, L, n_cu, 32) : a.combine ? a.parts * (nt / L) : a.parts * a.G;
     const dim3 grid((uint32_t)(((int64_t)a.teams * L + nt - 1) / nt));
     if (bwd) hipLaunchKernelGGL((bwd_kernel<InT, OutT, VEC, L, NV>), grid, dim3(nt), 0, s, a);
     else hipLaunchKernelGGL((fwd_kernel<InT, OutT, VEC, L, NV>), grid, dim3(nt), 0, s, a);
@@ -379,7 +453,7 @@ wkv7_status ln_fwd(int64_t rows, int C, int groups, wkv7_dtype x_dtype, wkv7_dty
     const int64_t n = rows * C, wb = C * lnorm::esz(w_dtype), sb = rows * groups * 4;
     const abi::Buf bufs[] = {{x, n * lnorm::esz(x_dtype), true, false, 16}, {weight, wb, false, false, 16},
                              {bias, wb, false, false, 16}, {y, n * lnorm::esz(y_dtype), true, true, 16},
-                             {mean, sb, false, true, 16}, {rstd, sb, false, true, 16}};
+                             {mean, sb, false, true, 4}, {rstd, sb, false, true, 4}};
     st = abi::check(bufs);
     if (st != WKV7_OK) return st;
     lnorm::Args a = {};
@@ -391,7 +465,7 @@ wkv7_status ln_fwd(int64_t rows, int C, int groups, wkv7_dtype x_dtype, wkv7_dty
 
 size_t ln_bwd_workspace_bytes(int64_t rows, int C, int groups) {
     if (lnorm::check_shape(rows, C, groups, WKV7_F32, WKV7_F32, WKV7_F32) != WKV7_OK) return 0;
-    return (size_t)lnorm::bwd_parts(rows, C / groups, groups) * C * 2 * 4;
+    return (size_t)lnorm::bwd_share(rows, C / groups, groups).parts * C * 2 * 4;
 }
 
 wkv7_status ln_bwd(int64_t rows, int C, int groups, wkv7_dtype x_dtype, wkv7_dtype y_dtype, wkv7_dtype w_dtype,
@@ -403,8 +477,8 @@ wkv7_status ln_bwd(int64_t rows, int C, int groups, wkv7_dtype x_dtype, wkv7_dty
     const int64_t n = rows * C, sb = rows * groups * 4;
     const int64_t need = dweight ? (int64_t)ln_bwd_workspace_bytes(rows, C, groups) : 0;
     const abi::Buf bufs[] = {{dy, n * lnorm::esz(y_dtype), true, false, 16}, {x, n * lnorm::esz(x_dtype), true, false, 16},
-                             {weight, C * lnorm::esz(w_dtype), false, false, 16}, {mean, sb, true, false, 16},
-                             {rstd, sb, true, false, 16}, {dx, n * lnorm::esz(x_dtype), false, true, 16},
+                             {weight, C * lnorm::esz(w_dtype), false, false, 16}, {mean, sb, true, false, 4},
+                             {rstd, sb, true, false, 4}, {dx, n * lnorm::esz(x_dtype), false, true, 16},
                              {dweight, C * 4LL, false, true, 16}, {dbias, C * 4LL, false, true, 16},
                              {workspace, need, false, true, 16}};
     st = abi::check(bufs);
@@ -414,12 +488,13 @@ wkv7_status ln_bwd(int64_t rows, int C, int groups, wkv7_dtype x_dtype, wkv7_dty
     a.x = x; a.dy = dy; a.weight = weight; a.dx = dx; a.mean = const_cast<float*>(mean);
     a.rstd = const_cast<float*>(rstd); a.rows = rows; a.C = C; a.G = groups; a.D = C / groups;
     a.wbf16 = w_dtype == WKV7_BF16;
-    a.parts = lnorm::bwd_parts(rows, a.D, groups);
+    const lnorm::Share share = lnorm::bwd_share(rows, a.D, groups);
+    a.parts = share.parts; a.combine = share.combine;
     a.part = dweight ? static_cast<float*>(workspace) : nullptr;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     hipError_t e = lnorm::launch(a, x_dtype, y_dtype, true, hs);
     if (e == hipSuccess && dweight) {
-        hipLaunchKernelGGL(lnorm::reduce_kernel, dim3((uint32_t)((C + 31) / 32), 2), dim3(256), 0, hs, a.part, a.parts, C,
+        hipLaunchKernelGGL(lnorm::reduce_kernel, dim3((uint32_t)((C + 31) / 32), 2), dim3(1024), 0, hs, a.part, a.parts, C,
                            dweight, dbias);
         e = hipGetLastError();
     }

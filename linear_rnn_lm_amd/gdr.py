@@ -22,7 +22,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import BF16, F32, _check, _check_bytes, _check_f32, _dense_on, _LazyOpOf, _ptr, _stream, _where, lib
+from . import BF16, F32, _check_bytes, _dense_on, _fits, _launch, _LazyOpOf, _ptr, _where, lib
 
 GDR_CHUNK = 64
 
@@ -59,17 +59,27 @@ def _check_inputs(fn, q, k, v, g, beta):
                          f"v {tuple(v.shape)}")
     if q.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"{fn}: q must be float32 or bfloat16, got {q.dtype}")
-    for n, t, shape, dt in (("q", q, (B, T, Hk, K), q.dtype), ("k", k, (B, T, Hk, K), q.dtype),
-                            ("v", v, (B, T, H, V), q.dtype), ("g", g, (B, T, H), torch.float32),
-                            ("beta", beta, (B, T, H), torch.float32)):
-        _check_tensor(fn, n, t, shape, dt, q.device)
+    dev, dt, f32, qs, gs = q.device, q.dtype, torch.float32, (B, T, Hk, K), (B, T, H)
+    if not (_fits(q, qs, dt, dev) and _fits(k, qs, dt, dev) and _fits(v, (B, T, H, V), dt, dev)
+            and _fits(g, gs, f32, dev) and _fits(beta, gs, f32, dev)):
+        for n, t, shape, d in (("q", q, qs, dt), ("k", k, qs, dt), ("v", v, (B, T, H, V), dt), ("g", g, gs, f32),
+                               ("beta", beta, gs, f32)):
+            _check_tensor(fn, n, t, shape, d, dev)
     return B, T, Hk, H, K, V
 
 
 def _check_tensor(fn, name, t, shape, dtype, dev):
+    if _fits(t, shape, dtype, dev):
+        return
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
         raise ValueError(f"{fn}: {name} is {_where(t)}, expected {tuple(shape)} {dtype}")
     _dense_on(fn, name, t, dev)
+
+
+def _check_state(fn, name, t, shape, dev):
+    import torch
+    if t is not None:
+        _check_tensor(fn, name, t, shape, torch.float32, dev)
 
 
 def _check_cu(fn, cu, B, dev):
@@ -93,17 +103,17 @@ def _code(dtype):
 def _workspace(fn, workspace, need, dev):
     import torch
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
     _check_bytes(fn, "workspace", workspace, need, dev)
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _zero_outside(cu, N, T, fresh, stream):
+def _zero_outside(cu, N, T, fresh):
     """Zero the rows of freshly made token tensors that no sequence covers."""
     n = len(fresh)
     ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in fresh])
     rows = (ctypes.c_int64 * n)(*[t.numel() // T * t.element_size() for t in fresh])
-    _check("gdr_zero_outside", _lib().gdr_zero_outside(T, N, _ptr(cu), n, ptrs, rows, stream))
+    _launch("gdr_zero_outside", _lib().gdr_zero_outside, cu.device, T, N, cu.data_ptr(), n, ptrs, rows)
 
 
 def gdr_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, scale=None, want_o=True, want_ckpt=True, want_hT=True,
@@ -118,7 +128,7 @@ def gdr_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, scale=None, want_o=Tr
     N = _check_cu(fn, cu_seqlens, B, dev)
     L, packed, states = _lib(), int(N > 0), (N or B, H, V, K)
     dims = (B, T, Hk, H, K, V)
-    _check_f32(fn, "h0", h0, states, dev, required=False)
+    _check_state(fn, "h0", h0, states, dev)
     fresh = []
     if o is not None:
         _check_tensor(fn, "o", o, v.shape, v.dtype, dev)
@@ -127,22 +137,20 @@ def gdr_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, scale=None, want_o=Tr
         fresh.append(o)
     nck = L.gdr_ckpt_bytes(*dims, N, packed)
     if ckpt is not None:
-        _check_f32(fn, "ckpt", ckpt, (nck // 4,), dev)
+        _check_state(fn, "ckpt", ckpt, (nck // 4,), dev)
     elif want_ckpt:
         ckpt = torch.empty(nck // 4, dtype=torch.float32, device=dev)
     if hT is not None:
-        _check_f32(fn, "hT", hT, states, dev)
+        _check_state(fn, "hT", hT, states, dev)
     elif want_hT:
         hT = torch.empty(states, dtype=torch.float32, device=dev)
     code = _code(q.dtype)
     workspace, wsb = _workspace(fn, workspace, L.gdr_fwd_workspace_bytes(*dims, code, N, packed), dev)
-    stream = _stream(dev)
-    with torch.cuda.device(dev):
-        if packed and fresh:
-            _zero_outside(cu_seqlens, N, T, fresh, stream)
-        st = L.gdr_fwd(*dims, code, *map(_ptr, (q, k, v, g, beta, cu_seqlens)), N, K ** -0.5 if scale is None else scale,
-                       *map(_ptr, (h0, o, ckpt, hT, workspace)), wsb, stream)
-    _check(fn, st)
+    _launch(fn, L.gdr_fwd, dev, *dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+            _ptr(cu_seqlens), N, K ** -0.5 if scale is None else scale, _ptr(h0), _ptr(o), _ptr(ckpt), _ptr(hT),
+            workspace.data_ptr(), wsb)
+    if packed and fresh:
+        _zero_outside(cu_seqlens, N, T, fresh)
     return o, ckpt, hT
 
 
@@ -157,8 +165,8 @@ def gdr_bwd(do, q, k, v, g, beta, ckpt, dhT=None, *, cu_seqlens=None, scale=None
     L, packed, states = _lib(), int(N > 0), (N or B, H, V, K)
     dims = (B, T, Hk, H, K, V)
     _check_tensor(fn, "do", do, v.shape, v.dtype, dev)
-    _check_f32(fn, "ckpt", ckpt, (L.gdr_ckpt_bytes(*dims, N, packed) // 4,), dev)
-    _check_f32(fn, "dhT", dhT, states, dev, required=False)
+    _check_state(fn, "ckpt", ckpt, (L.gdr_ckpt_bytes(*dims, N, packed) // 4,), dev)
+    _check_state(fn, "dhT", dhT, states, dev)
     fresh = []
     if out is None:
         out = fresh = [torch.empty_like(x) for x in (q, k, v, g, beta)]
@@ -169,13 +177,10 @@ def gdr_bwd(do, q, k, v, g, beta, ckpt, dhT=None, *, cu_seqlens=None, scale=None
     dh0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dh0 else None
     code = _code(q.dtype)
     workspace, wsb = _workspace(fn, workspace, L.gdr_bwd_workspace_bytes(*dims, code, N, packed), dev)
-    stream = _stream(dev)
-    with torch.cuda.device(dev):
-        if packed and fresh:
-            _zero_outside(cu_seqlens, N, T, fresh, stream)
-        st = L.gdr_bwd(*dims, code, *map(_ptr, (do, dhT, q, k, v, g, beta, cu_seqlens)), N,
-                       K ** -0.5 if scale is None else scale, *map(_ptr, (ckpt, *out, dh0, workspace)), wsb, stream)
-    _check(fn, st)
+    _launch(fn, L.gdr_bwd, dev, *dims, code, *map(_ptr, (do, dhT, q, k, v, g, beta, cu_seqlens)), N,
+            K ** -0.5 if scale is None else scale, *map(_ptr, (ckpt, *out, dh0, workspace)), wsb)
+    if packed and fresh:
+        _zero_outside(cu_seqlens, N, T, fresh)
     return (*out, dh0)
 
 
@@ -199,18 +204,18 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, state_out=None,
             raise ValueError(f"{fn}: state holds {P} states for {B} rows")
     else:
         _check_tensor(fn, "slots", slots, (B,), torch.int32, dev)
-    _check_f32(fn, "state", state, (P, H, V, K), dev)
+    _check_state(fn, "state", state, (P, H, V, K), dev)
     if state_out is None:
         state_out = state
-    _check_f32(fn, "state_out", state_out, (P, H, V, K), dev)
+    else:
+        _check_state(fn, "state_out", state_out, (P, H, V, K), dev)
     if o is None:
         o = torch.empty_like(v)
-    _check_tensor(fn, "o", o, v.shape, v.dtype, dev)
-    stream = _stream(dev)
-    with torch.cuda.device(dev):
-        st = _lib().gdr_step(B, T, Hk, H, K, V, _code(q.dtype), *map(_ptr, (q, k, v, g, beta, slots)), P,
-                             K ** -0.5 if scale is None else scale, *map(_ptr, (state, state_out, o)), stream)
-    _check(fn, st)
+    else:
+        _check_tensor(fn, "o", o, v.shape, v.dtype, dev)
+    _launch(fn, _lib().gdr_step, dev, B, T, Hk, H, K, V, _code(q.dtype), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            g.data_ptr(), beta.data_ptr(), _ptr(slots), P, K ** -0.5 if scale is None else scale, state.data_ptr(),
+            state_out.data_ptr(), o.data_ptr())
     return o
 
 

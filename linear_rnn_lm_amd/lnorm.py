@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import BF16, F32, _check, _check_bytes, _check_f32, _dense_on, _LazyOpOf, _ptr, _stream, _where, lib
+from . import BF16, F32, _check_bytes, _dense_on, _fits, _launch, _LazyOpOf, _ptr, _where, lib
 
 
 @functools.lru_cache(maxsize=None)
@@ -45,7 +45,12 @@ def _check_x(fn, x, weight, bias, groups):
     C = x.shape[-1]
     if groups < 1 or C % groups or C // groups > 16384:
         raise ValueError(f"{fn}: groups must divide C into parts of at most 16384, got C = {C}, groups = {groups}")
-    _dense_on(fn, "x", x, x.device)
+    if not x.is_contiguous():
+        _dense_on(fn, "x", x, x.device)
+    if weight is not None and bias is not None:
+        wd = weight.dtype
+        if wd in types and _fits(weight, (C,), wd, x.device) and _fits(bias, (C,), wd, x.device):
+            return x.numel() // C, C, _code(wd)
     wd = None
     for n, w in (("weight", weight), ("bias", bias)):
         if w is None:
@@ -58,6 +63,8 @@ def _check_x(fn, x, weight, bias, groups):
 
 
 def _check_like(fn, name, t, shape, dtype, dev):
+    if _fits(t, shape, dtype, dev):
+        return
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
         raise ValueError(f"{fn}: {name} is {_where(t)}, expected {tuple(shape)} {dtype}")
     _dense_on(fn, name, t, dev)
@@ -78,21 +85,21 @@ def ln_fwd(x, weight=None, bias=None, *, groups=1, eps=1e-5, out_dtype=None, wan
     fn = "ln_fwd"
     rows, C, wcode = _check_x(fn, x, weight, bias, groups)
     dev = x.device
-    out_dtype = _out_dtype(fn, x, out_dtype if y is None else y.dtype)
     if y is None:
+        out_dtype = x.dtype if out_dtype is None else _out_dtype(fn, x, out_dtype)
         y = torch.empty(x.shape, dtype=out_dtype, device=dev)
-    _check_like(fn, "y", y, x.shape, out_dtype, dev)
+    else:
+        out_dtype = _out_dtype(fn, x, y.dtype)
+        _check_like(fn, "y", y, x.shape, out_dtype, dev)
     if (mean is None) != (rstd is None):
         raise ValueError(f"{fn}: mean and rstd go together")
     if mean is None and want_stats:
-        mean, rstd = (torch.empty((rows, groups), dtype=torch.float32, device=dev) for _ in range(2))
-    _check_f32(fn, "mean", mean, (rows, groups), dev, required=False)
-    _check_f32(fn, "rstd", rstd, (rows, groups), dev, required=False)
-    stream = _stream(dev)
-    with torch.cuda.device(dev):
-        st = _lib().ln_fwd(rows, C, groups, _code(x.dtype), _code(out_dtype), wcode, *map(_ptr, (x, weight, bias)), eps,
-                           *map(_ptr, (y, mean, rstd)), stream)
-    _check(fn, st)
+        mean, rstd = torch.empty((2, rows, groups), dtype=torch.float32, device=dev)
+    elif mean is not None:
+        _check_like(fn, "mean", mean, (rows, groups), torch.float32, dev)
+        _check_like(fn, "rstd", rstd, (rows, groups), torch.float32, dev)
+    _launch(fn, _lib().ln_fwd, dev, rows, C, groups, _code(x.dtype), _code(out_dtype), wcode, x.data_ptr(), _ptr(weight),
+            _ptr(bias), eps, y.data_ptr(), _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
 
@@ -104,31 +111,30 @@ def ln_bwd(dy, x, weight, mean, rstd, *, groups=1, want_dx=True, want_dw=True, w
     rows, C, wcode = _check_x(fn, x, weight, None, groups)
     dev = x.device
     _check_like(fn, "dy", dy, x.shape, _out_dtype(fn, x, dy.dtype), dev)
-    _check_f32(fn, "mean", mean, (rows, groups), dev)
-    _check_f32(fn, "rstd", rstd, (rows, groups), dev)
+    _check_like(fn, "mean", mean, (rows, groups), torch.float32, dev)
+    _check_like(fn, "rstd", rstd, (rows, groups), torch.float32, dev)
     if out is None:
         f32 = dict(dtype=torch.float32, device=dev)
         out = (torch.empty_like(x) if want_dx else None, torch.empty(C, **f32) if want_dw else None,
                torch.empty(C, **f32) if want_dw else None)
-    if len(out) != 3:
+    elif len(out) != 3:
         raise ValueError(f"{fn}: out must hold 3 entries, got {len(out)}")
     dx, dw, db = out
     if (dw is None) != (db is None) or (dx is None and dw is None):
         raise ValueError(f"{fn}: dx, or dweight and dbias together, must be wanted")
-    if dx is not None:
-        _check_like(fn, "dx", dx, x.shape, x.dtype, dev)
-    _check_f32(fn, "dweight", dw, (C,), dev, required=False)
-    _check_f32(fn, "dbias", db, (C,), dev, required=False)
+    for n, t, shape, dt in (("dx", dx, x.shape, x.dtype), ("dweight", dw, (C,), torch.float32),
+                            ("dbias", db, (C,), torch.float32)):
+        if t is not None:
+            _check_like(fn, n, t, shape, dt, dev)
     need = _lib().ln_bwd_workspace_bytes(rows, C, groups) if dw is not None else 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check_bytes(fn, "workspace", workspace, need, dev)
-    stream = _stream(dev)
-    with torch.cuda.device(dev):
-        st = _lib().ln_bwd(rows, C, groups, _code(x.dtype), _code(dy.dtype), wcode,
-                           *map(_ptr, (dy, x, weight, mean, rstd, dx, dw, db)), _ptr(workspace),
-                           workspace.numel() * workspace.element_size(), stream)
-    _check(fn, st)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _check_bytes(fn, "workspace", workspace, need, dev)
+    _launch(fn, _lib().ln_bwd, dev, rows, C, groups, _code(x.dtype), _code(dy.dtype), wcode, dy.data_ptr(), x.data_ptr(),
+            _ptr(weight), mean.data_ptr(), rstd.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
     return dx, dw, db
 
 
