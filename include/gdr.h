@@ -54,8 +54,8 @@ extern "C" {
 int64_t gdr_slots(int B, int T, int N, int packed);
 
 /* Bytes of what gdr_fwd leaves for gdr_bwd: slots * H * (K + 64) * V fp32, per
- * chunk and head the state entering the chunk (V x K), then the chunk's rows
- * u (64 x V).  0 for invalid shapes. */
+ * chunk and head the state entering the chunk (V x K), then the chunk's u of
+ * every token (V x 64).  0 for invalid shapes. */
 size_t gdr_ckpt_bytes(int B, int T, int Hk, int H, int K, int V, int N, int packed);
 
 /* Device workspace of gdr_fwd and gdr_bwd.  0 for invalid shapes. */

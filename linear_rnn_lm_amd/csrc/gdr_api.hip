@@ -42,6 +42,7 @@ wkv7_status shape(int B, int T, int Hk, int H, int K, int V, int dt, int N, bool
     // one workgroup per chunk and head, and up to V / 16 per sequence and head
     if (s->slots > INT32_MAX / H || (int64_t)s->N * 8 > INT32_MAX / H) return WKV7_ERR_SHAPE;
     if (s->tokens > (int64_t(1) << 40) / ((int64_t)H * 128)) return WKV7_ERR_SHAPE;
+    if ((int64_t)kChunk * H * V * 4 > INT32_MAX) return WKV7_ERR_SHAPE;   // 32-bit offsets inside a chunk
     s->q_elems = s->tokens * Hk * K;
     s->v_elems = s->tokens * H * V;
     s->gate_elems = s->tokens * H;
@@ -86,14 +87,14 @@ gdr::Args args_of(int B, int T, int Hk, int H, int K, int V, const Shape& s, con
     return a;
 }
 
-hipError_t prepare(const gdr::Args& a, const Shape& s, hipStream_t st) {
+hipError_t prepare(const gdr::Args& a, const Shape& s, bool bwd, hipStream_t st) {
     if (!s.bf16) {
         hipError_t e = gdr::launch_split(static_cast<const float*>(a.q), const_cast<uint16_t*>(a.qp.p), s.q_elems, st);
         if (e == hipSuccess)
             e = gdr::launch_split(static_cast<const float*>(a.k), const_cast<uint16_t*>(a.kp.p), s.q_elems, st);
         if (e != hipSuccess) return e;
     }
-    return gdr::launch_prepare(a, s.bf16, st);
+    return gdr::launch_prepare(a, s.bf16, bwd, st);
 }
 
 }  // namespace
@@ -140,7 +141,7 @@ wkv7_status gdr_fwd(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dty
     gdr::Args a = args_of(B, T, Hk, H, K, V, s, q, k, v, g, beta, cu_seqlens, scale, workspace);
     a.h0 = h0; a.o = o; a.ckpt = ckpt; a.hT = hT;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t e = prepare(a, s, hs);
+    hipError_t e = prepare(a, s, false, hs);
     if (e == hipSuccess) e = gdr::launch_fwd_scan(a, s.bf16, hs);
     return status_of(e);
 }
@@ -166,7 +167,7 @@ wkv7_status gdr_bwd(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dty
     a.dout = dout; a.dhT = dhT; a.ckpt = const_cast<float*>(ckpt);
     a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t e = prepare(a, s, hs);
+    hipError_t e = prepare(a, s, true, hs);
     if (e == hipSuccess) e = gdr::launch_bwd_scan(a, s.bf16, hs);
     if (e == hipSuccess) e = gdr::launch_grad(a, s.bf16, hs);
     return status_of(e);

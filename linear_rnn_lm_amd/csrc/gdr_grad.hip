@@ -139,8 +139,8 @@ __global__ __launch_bounds__(NT) void grad_kernel(Args p) {
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) dos[hh] = zs[hh] = ug[hh] = pa[hh] = na[hh] = zero4();
             for (int is = 0; is < V / 64; ++is) {
-                const F8 u = load8(Um + (int64_t)row8 * V + 64 * is + 8 * u8);
-                const F8 z = load8(Zm + (int64_t)row8 * V + 64 * is + 8 * u8);
+                const F8 u = load8(Um + (64 * is + row8) * C + 8 * u8);      // rows i, columns t
+                const F8 z = load8(Zm + (64 * is + row8) * C + 8 * u8);
                 const F8 s = load8(S + (int64_t)(64 * is + row8) * K + 64 * js + 8 * u8);
                 const F8 g = load8(G1 + (int64_t)(64 * is + row8) * K + 64 * js + 8 * u8);
                 PF<NX> d;
@@ -167,8 +167,8 @@ __global__ __launch_bounds__(NT) void grad_kernel(Args p) {
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     const PF<NX> df = frag_row<8, NX>(smem + L::DO, kMatBytes, t, ks, lane);
-                    const PF<NP> zf = frag_row<8, NP>(smem + L::Z, kMatBytes, t, ks, lane);
-                    const PF<NP> uf = frag_row<8, NP>(smem + L::U, kMatBytes, t, ks, lane);
+                    const PF<NP> zf = frag_col<8, NP>(smem + L::Z, kMatBytes, tt, ks, lane);
+                    const PF<NP> uf = frag_col<8, NP>(smem + L::U, kMatBytes, tt, ks, lane);
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         const PF<NP> sf = frag_col<8, NP>(smem + L::S, kMatBytes, 2 * c + hh, ks, lane);
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(NT) void grad_kernel(Args p) {
                         zs[hh] = pmma<NP>(zs[hh], sf, zf);
                         ug[hh] = pmma<NP>(ug[hh], gf, uf);
                         if (c <= (tt >> 1)) {
-                            const PF<NP> us = frag_row<8, NP>(smem + L::U, kMatBytes, idx(2 * c + hh, r16), ks, lane);
+                            const PF<NP> us = frag_col<8, NP>(smem + L::U, kMatBytes, 2 * c + hh, ks, lane);
                             pa[hh] = pmma<NP>(pa[hh], us, df);
                             na[hh] = pmma<NP>(na[hh], us, zf);
                         }

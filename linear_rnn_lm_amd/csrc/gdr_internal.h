@@ -26,7 +26,7 @@ struct Args {
     Planes qp, kp;                      // set by the launcher
     char* ops;                          // (slots, H, ops_bytes): T, M
     float* gates;                       // (slots, H, kGateFloats)
-    float *dend, *z;                    // backward: (slots, H, V, K), (slots, H, 64, V)
+    float *dend, *z;                    // backward: (slots, H, V, K), (slots, H, V, 64)
     float scale;
     int B, T, Hk, H, K, V, N, NC, slots;
 };
@@ -58,7 +58,7 @@ struct ZeroArgs {
 
 hipError_t launch_zero_outside(const ZeroArgs& a, hipStream_t s);
 hipError_t launch_split(const float* x, uint16_t* planes, int64_t n, hipStream_t s);
-hipError_t launch_prepare(const Args& a, bool bf16, hipStream_t s);
+hipError_t launch_prepare(const Args& a, bool bf16, bool bwd, hipStream_t s);
 hipError_t launch_fwd_scan(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_bwd_scan(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_grad(const Args& a, bool bf16, hipStream_t s);

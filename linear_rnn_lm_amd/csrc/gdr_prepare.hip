@@ -59,7 +59,7 @@ __device__ __forceinline__ void block_product(const float* X, const float* Y, fl
     for (int q = 0; q < 4; ++q) Z[(4 * g + q) * LDA + r] = sign * acc[q];
 }
 
-template <int NX, int K>
+template <int NX, int K, bool BWD>
 __global__ __launch_bounds__(256) void prepare_kernel(Args p) {
     __shared__ __attribute__((aligned(16))) float As[C * LDA];
     __shared__ __attribute__((aligned(16))) float Ts[C * LDA];
@@ -165,24 +165,40 @@ __global__ __launch_bounds__(256) void prepare_kernel(Args p) {
     block_product(Ts + (32 + mr) * LDA + 32, As + 32 + mc, Ts + (32 + mr) * LDA + mc, 32, -1.f, lane);
     __syncthreads();
 
-    // The three lower 32 x 32 blocks to planes, as the scans' LDS holds them.
+    // To planes, the three lower 32 x 32 blocks only.  T: as the scans' LDS holds it.  M: as
+    // operand fragments (M in the forward, M^T in the backward), six 32-deep steps
+    // of 64 lanes, which the scans' helper waves load straight into registers.
     char* ops = p.ops + block * kOpsBytes;
-    for (int e = tid; e < 2 * 3 * 128; e += 256) {       // matrix, block, row, unit
-        const int m = e / 384, blk = (e >> 7) % 3, row = (e >> 2) & 31, u = e & 3;
-        const float* src = (m ? Ms : Ts) + ((blk ? 32 : 0) + row) * LDA + (blk == 2 ? 32 : 0) + 8 * u;
+    for (int e = tid; e < 384; e += 256) {
+        const int blk = e >> 7, row = (e >> 2) & 31, u = e & 3;
+        const float* src = Ts + ((blk ? 32 : 0) + row) * LDA + (blk == 2 ? 32 : 0) + 8 * u;
         const PF<kPlanes> f =
             pf_acc<kPlanes>(*reinterpret_cast<const f32x4*>(src), *reinterpret_cast<const f32x4*>(src + 4));
-        char* dst = ops + m * kPlanes * kTriBytes + blk * 2048 + (row * 4 + (u ^ (row >> 3))) * 16;
+        char* dst = ops + blk * 2048 + (row * 4 + (u ^ (row >> 3))) * 16;
 #pragma unroll
         for (int i = 0; i < kPlanes; ++i) *reinterpret_cast<bf16x8*>(dst + i * kTriBytes) = f.p[i];
     }
+    for (int e = tid; e < 384; e += 256) {
+        const int f = e >> 6, l = e & 63;
+        // tile and step of fragment f: forward 00 10 20 21 30 31, backward 00 01 10 11 21 31
+        const int tile = BWD ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : (f + 2) >> 1);
+        const int ks = BWD ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1);
+        const int a = idx(tile, l & 15), b = 32 * ks + 8 * (l >> 4);
+        f32x4 x[2];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q >> 2][q & 3] = BWD ? Ms[(b + q) * LDA + a] : Ms[a * LDA + b + q];
+        const PF<kPlanes> v = pf_acc<kPlanes>(x[0], x[1]);
+#pragma unroll
+        for (int i = 0; i < kPlanes; ++i)
+            *reinterpret_cast<bf16x8*>(ops + (kPlanes + i) * kTriBytes + e * 16) = v.p[i];
+    }
 }
 
-template <int NX>
+template <int NX, bool BWD>
 hipError_t launch_k(const Args& a, hipStream_t s) {
     const dim3 grid((uint32_t)a.slots * a.H);
-    if (a.K == 64) hipLaunchKernelGGL((prepare_kernel<NX, 64>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((prepare_kernel<NX, 128>), grid, dim3(256), 0, s, a);
+    if (a.K == 64) hipLaunchKernelGGL((prepare_kernel<NX, 64, BWD>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((prepare_kernel<NX, 128, BWD>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -198,8 +214,9 @@ hipError_t launch_split(const float* x, uint16_t* planes, int64_t n, hipStream_t
     return hipGetLastError();
 }
 
-hipError_t launch_prepare(const Args& a, bool bf16, hipStream_t s) {
-    return bf16 ? launch_k<1>(a, s) : launch_k<3>(a, s);
+hipError_t launch_prepare(const Args& a, bool bf16, bool bwd, hipStream_t s) {
+    if (bwd) return bf16 ? launch_k<1, true>(a, s) : launch_k<3, true>(a, s);
+    return bf16 ? launch_k<1, false>(a, s) : launch_k<3, false>(a, s);
 }
 
 }  // namespace gdr
