@@ -53,9 +53,10 @@ extern "C" {
  * ignored).  0 for invalid sizes. */
 int64_t gdr_slots(int B, int T, int N, int packed);
 
-/* Bytes of what gdr_fwd leaves for gdr_bwd: slots * H * (K + 64) * V fp32, per
- * chunk and head the state entering the chunk (V x K), then the chunk's u of
- * every token (V x 64).  0 for invalid shapes. */
+/* Bytes of what gdr_fwd leaves for gdr_bwd: slots * H blocks of
+ * (K + 64) * V + 6464 fp32, per chunk and head the state entering the chunk
+ * (V x K), the chunk's u (V x 64), and in a library-internal format its two
+ * triangular matrices and its gates.  0 for invalid shapes. */
 size_t gdr_ckpt_bytes(int B, int T, int Hk, int H, int K, int V, int N, int packed);
 
 /* Device workspace of gdr_fwd and gdr_bwd.  0 for invalid shapes. */

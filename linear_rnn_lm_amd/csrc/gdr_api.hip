@@ -11,11 +11,11 @@ namespace {
 using abi::Buf;
 
 constexpr int kChunk = 64;
-constexpr int kGateFloats = 384;   // per chunk and head, as the kernels lay them out
+constexpr int kGateFloats = 320;   // per chunk and head, as the kernels lay them out
 
 struct Shape {
     int64_t slots, tokens, q_elems, v_elems, gate_elems, state_elems, ckpt_elems;
-    int64_t ops_bytes, gates_bytes, split_bytes, dend_bytes, z_bytes;
+    int64_t ckpt_stride, tri_stride, tri_bytes, split_bytes, dend_bytes, z_bytes;
     int N;
     bool bf16;
     int64_t e() const { return bf16 ? 2 : 4; }
@@ -47,54 +47,55 @@ wkv7_status shape(int B, int T, int Hk, int H, int K, int V, int dt, int N, bool
     s->v_elems = s->tokens * H * V;
     s->gate_elems = s->tokens * H;
     s->state_elems = (int64_t)s->N * H * V * K;
-    s->ckpt_elems = s->slots * H * (int64_t)(K + kChunk) * V;
-    s->ops_bytes = s->slots * H * gdr::kOpsBytes;
-    s->gates_bytes = s->slots * H * kGateFloats * 4;
+    s->tri_stride = gdr::kTriFloats + kGateFloats;
+    s->ckpt_stride = (int64_t)(K + kChunk) * V + gdr::kTriFloats + s->tri_stride;
+    s->ckpt_elems = s->slots * H * s->ckpt_stride;
+    s->tri_bytes = s->slots * H * s->tri_stride * 4;
     s->split_bytes = s->bf16 ? 0 : 2 * 3 * s->q_elems * 2;
     s->dend_bytes = s->slots * H * (int64_t)V * K * 4;
     s->z_bytes = s->slots * H * (int64_t)V * kChunk * 4;
     return WKV7_OK;
 }
 
-int64_t fwd_ws(const Shape& s) { return s.ops_bytes + s.gates_bytes + s.split_bytes; }
-int64_t bwd_ws(const Shape& s) { return fwd_ws(s) + s.dend_bytes + s.z_bytes; }
+// T and gates of a forward without checkpoints (or 0 bytes), planes of fp32 inputs;
+// the backward's state gradients and Z, and those planes.
+int64_t fwd_ws(const Shape& s) { return s.tri_bytes + s.split_bytes; }
+int64_t bwd_ws(const Shape& s) { return s.dend_bytes + s.z_bytes + s.split_bytes; }
 
 wkv7_status status_of(hipError_t e) { return e == hipSuccess ? WKV7_OK : WKV7_ERR_HIP; }
 
-// Arguments shared by both directions; the workspace is laid out here: operands,
-// gates, planes of fp32 inputs, then the backward's own parts.
+// Arguments shared by both directions.  `planes`: where the planes of fp32 q and k go.
 gdr::Args args_of(int B, int T, int Hk, int H, int K, int V, const Shape& s, const void* q, const void* k,
-                  const void* v, const float* g, const float* beta, const int32_t* cu, float scale, void* ws) {
+                  const void* v, const float* g, const float* beta, const int32_t* cu, float scale, char* planes) {
     gdr::Args a = {};
     a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.cu = cu; a.scale = scale;
     a.B = B; a.T = T; a.Hk = Hk; a.H = H; a.K = K; a.V = V; a.N = s.N;
     a.slots = (int)s.slots;
     a.NC = cu ? (int)s.slots : (T + kChunk - 1) / kChunk;
-    char* w = static_cast<char*>(ws);
-    a.ops = w; w += s.ops_bytes;
-    a.gates = reinterpret_cast<float*>(w); w += s.gates_bytes;
+    a.ckpt_stride = s.ckpt_stride;
     if (s.bf16) {
         a.qp = {static_cast<const uint16_t*>(q), 0};
         a.kp = {static_cast<const uint16_t*>(k), 0};
     } else {
-        uint16_t* p = reinterpret_cast<uint16_t*>(w);
+        uint16_t* p = reinterpret_cast<uint16_t*>(planes);
         a.qp = {p, s.q_elems};
         a.kp = {p + 3 * s.q_elems, s.q_elems};
-        w += s.split_bytes;
     }
-    a.dend = reinterpret_cast<float*>(w); w += s.dend_bytes;
-    a.z = reinterpret_cast<float*>(w);
     return a;
 }
 
-hipError_t prepare(const gdr::Args& a, const Shape& s, bool bwd, hipStream_t st) {
-    if (!s.bf16) {
-        hipError_t e = gdr::launch_split(static_cast<const float*>(a.q), const_cast<uint16_t*>(a.qp.p), s.q_elems, st);
-        if (e == hipSuccess)
-            e = gdr::launch_split(static_cast<const float*>(a.k), const_cast<uint16_t*>(a.kp.p), s.q_elems, st);
-        if (e != hipSuccess) return e;
-    }
-    return gdr::launch_prepare(a, s.bf16, bwd, st);
+// T and gates behind the rest of each checkpoint block.
+void tri_in_ckpt(gdr::Args* a) {
+    a->tri = a->ckpt + (int64_t)(a->K + kChunk) * a->V + gdr::kTriFloats;
+    a->tri_stride = a->ckpt_stride;
+}
+
+hipError_t split(const gdr::Args& a, const Shape& s, hipStream_t st) {
+    if (s.bf16) return hipSuccess;
+    hipError_t e = gdr::launch_split(static_cast<const float*>(a.q), const_cast<uint16_t*>(a.qp.p), s.q_elems, st);
+    if (e == hipSuccess)
+        e = gdr::launch_split(static_cast<const float*>(a.k), const_cast<uint16_t*>(a.kp.p), s.q_elems, st);
+    return e;
 }
 
 }  // namespace
@@ -138,10 +139,18 @@ wkv7_status gdr_fwd(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dty
     st = abi::check(bufs, h0 == hT ? h0 : nullptr);
     if (st != WKV7_OK) return st;
     if (!workspace || workspace_bytes < (size_t)fwd_ws(s)) return WKV7_ERR_WORKSPACE;
-    gdr::Args a = args_of(B, T, Hk, H, K, V, s, q, k, v, g, beta, cu_seqlens, scale, workspace);
+    char* ws = static_cast<char*>(workspace);
+    gdr::Args a = args_of(B, T, Hk, H, K, V, s, q, k, v, g, beta, cu_seqlens, scale, ws + s.tri_bytes);
     a.h0 = h0; a.o = o; a.ckpt = ckpt; a.hT = hT;
+    if (ckpt) {
+        tri_in_ckpt(&a);
+    } else {
+        a.tri = reinterpret_cast<float*>(ws);
+        a.tri_stride = s.tri_stride;
+    }
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t e = prepare(a, s, false, hs);
+    hipError_t e = split(a, s, hs);
+    if (e == hipSuccess) e = gdr::launch_prepare(a, s.bf16, hs);
     if (e == hipSuccess) e = gdr::launch_fwd_scan(a, s.bf16, hs);
     return status_of(e);
 }
@@ -163,11 +172,15 @@ wkv7_status gdr_bwd(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dty
     st = abi::check(bufs);
     if (st != WKV7_OK) return st;
     if (!workspace || workspace_bytes < (size_t)bwd_ws(s)) return WKV7_ERR_WORKSPACE;
-    gdr::Args a = args_of(B, T, Hk, H, K, V, s, q, k, v, g, beta, cu_seqlens, scale, workspace);
+    char* ws = static_cast<char*>(workspace);
+    gdr::Args a = args_of(B, T, Hk, H, K, V, s, q, k, v, g, beta, cu_seqlens, scale, ws + s.dend_bytes + s.z_bytes);
     a.dout = dout; a.dhT = dhT; a.ckpt = const_cast<float*>(ckpt);
+    a.dend = reinterpret_cast<float*>(ws);
+    a.z = reinterpret_cast<float*>(ws + s.dend_bytes);
+    tri_in_ckpt(&a);
     a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t e = prepare(a, s, true, hs);
+    hipError_t e = split(a, s, hs);
     if (e == hipSuccess) e = gdr::launch_bwd_scan(a, s.bf16, hs);
     if (e == hipSuccess) e = gdr::launch_grad(a, s.bf16, hs);
     return status_of(e);

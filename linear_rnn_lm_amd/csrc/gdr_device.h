@@ -46,10 +46,11 @@ using wkv7::zero4;
 constexpr int C = 64;  // chunk length
 
 // Gates of one chunk of one head, written by the prepare kernel: e^G, e^(G_C -
-// G) and b as fp32 (b and e^(G_C - G) are 0 for tokens past the sequence's end),
-// 64 unused floats, then G in 64 bits.
-constexpr int kGateFloats = 384;
-constexpr int kGateEG = 0, kGateToEnd = 64, kGateBeta = 128, kGateG = 256;
+// G), b (the last two 0 for tokens past the sequence's end), then G log2(e) as a
+// whole number n and a rest f in +-1/2, so that e^(G_t - G_s) = 2^(n_t - n_s)
+// 2^(f_t - f_s) is good to fp32 however large the sums are.
+constexpr int kGateFloats = 320;
+constexpr int kGateEG = 0, kGateToEnd = 64, kGateBeta = 128, kGateN = 192, kGateF = 256;
 
 // A write strength of 0 is taken as 2^-60: the token's u then holds b times
 // the error v - S k it would have written, which no fp32 sum notices, and the
@@ -184,12 +185,15 @@ __device__ __forceinline__ float ld(const T* p) { return widen(*p); }
 __device__ __forceinline__ void st(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// e^x of a difference of 64-bit sums, good to fp32: 2^y with the integer part
-// of y = x log2(e) taken off in 64 bits.
+// e^x for a 64-bit x, good to fp32: the whole part of x log2(e) is taken off in 64 bits.
 __device__ __forceinline__ float exp_d(double x) {
     const double y = x * 1.4426950408889634074;
     const double n = __builtin_rint(y);
     return __builtin_ldexpf(__builtin_amdgcn_exp2f((float)(y - n)), (int)n);
+}
+// e^(G_t - G_s) from two tokens' whole and remaining parts
+__device__ __forceinline__ float decay(float nt, float ft, float ns, float fs) {
+    return __builtin_ldexpf(__builtin_amdgcn_exp2f(ft - fs), (int)(nt - ns));
 }
 
 // Where the sequences lie.  Dense: sequence n is row n of (B, T), its chunks

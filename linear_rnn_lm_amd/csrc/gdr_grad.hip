@@ -36,7 +36,7 @@ struct Lds {
     static constexpr bool apart = NX == 1;                // K, Q beside S, G or in their place
     static constexpr int Kr = apart ? after : S, Qr = Kr + NX * MB;
     static constexpr int small = apart ? Qr + NX * MB : after;
-    static constexpr int bytes = small + 64 * 8 + 5 * 64 * 4 + 2 * 128 * 4 + 64;
+    static constexpr int bytes = small + 7 * 64 * 4 + 2 * 128 * 4;
 };
 
 // Eight consecutive fp32 values.
@@ -79,8 +79,9 @@ __global__ __launch_bounds__(NT) void grad_kernel(Args p) {
     using L = Lds<NX>;
     constexpr int KJ = K / 64;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    double* Gd = reinterpret_cast<double*>(smem + L::small);
-    float* eG = reinterpret_cast<float*>(Gd + 64);
+    float* Gn = reinterpret_cast<float*>(smem + L::small);
+    float* Gf = Gn + 64;
+    float* eG = Gf + 64;
     float* toEnd = eG + 64;
     float* beta = toEnd + 64;
     float* dbeta = beta + 64;
@@ -107,14 +108,15 @@ __global__ __launch_bounds__(NT) void grad_kernel(Args p) {
     for (int hr = 0; hr < rep; ++hr) {
         const int h = hk * rep + hr;
         const int64_t block = (int64_t)slot * p.H + h;
-        const float* S = p.ckpt + block * (int64_t)V * (K + C);
+        const float* S = p.ckpt + block * p.ckpt_stride;
         const float* Um = S + (int64_t)V * K;
         const float* G1 = p.dend + block * (int64_t)V * K;
         const float* Zm = p.z + block * (int64_t)C * V;
-        const float* gates = p.gates + block * kGateFloats;
+        const float* gates = p.tri + block * p.tri_stride + kTriFloats;
         __syncthreads();
         if (tid < 64) {
-            Gd[tid] = reinterpret_cast<const double*>(gates + kGateG)[tid];
+            Gn[tid] = gates[kGateN + tid];
+            Gf[tid] = gates[kGateF + tid];
             eG[tid] = gates[kGateEG + tid];
             toEnd[tid] = gates[kGateToEnd + tid];
             beta[tid] = gates[kGateBeta + tid];
@@ -184,13 +186,13 @@ __global__ __launch_bounds__(NT) void grad_kernel(Args p) {
                     }
                 }
             }
-            const float bt = beta[t], egt = eG[t], tet = toEnd[t];
+            const float bt = beta[t], egt = eG[t], tet = toEnd[t], nt = Gn[t], ft = Gf[t];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int s = 32 * c + 8 * g4 + 4 * hh + q;
-                    const float lam = s <= t ? exp_d(Gd[t] - Gd[s]) : 0.f;
+                    const float lam = s <= t ? decay(nt, ft, Gn[s], Gf[s]) : 0.f;
                     if (s == t) dbeta[t] = t < len ? na[hh][q] / bt : 0.f;
                     pa[hh][q] = s <= t ? p.scale * lam * pa[hh][q] : 0.f;
                     na[hh][q] = s < t ? -bt * lam * na[hh][q] : 0.f;

@@ -22,10 +22,14 @@ struct Args {
     void *o, *dq, *dk, *dv;             // token outputs, in_dtype
     float *dg, *dbeta;                  // (tokens, H)
     float *hT, *dh0;                    // (N, H, V, K) or NULL
-    float* ckpt;                        // (slots, H, (K + 64) V) or NULL
+    // Per (slot, head), `stride` floats apart: what the forward leaves for the backward
+    // (state entering the chunk V x K, u V x 64, M^T), or NULL; then T and the gates,
+    // in the same blocks or, without them, in the workspace.
+    float* ckpt;
+    int64_t ckpt_stride;
+    float* tri;
+    int64_t tri_stride;
     Planes qp, kp;                      // set by the launcher
-    char* ops;                          // (slots, H, ops_bytes): T, M
-    float* gates;                       // (slots, H, kGateFloats)
     float *dend, *z;                    // backward: (slots, H, V, K), (slots, H, V, 64)
     float scale;
     int B, T, Hk, H, K, V, N, NC, slots;
@@ -33,8 +37,8 @@ struct Args {
 
 // bf16 planes of a derived value, and of an input, by input type.
 constexpr int kPlanes = 3;
-// Bytes of T and M of one chunk of one head: planes of three 32 x 32 blocks.
-constexpr int kOpsBytes = 2 * kPlanes * 3 * 32 * 64;
+// T and M^T of one chunk of one head: three 32 x 32 blocks in fp32.
+constexpr int kTriFloats = 3 * 32 * 32;
 // Bytes of one plane of a row-major 64 x 64 matrix.
 constexpr int kMatBytes = 64 * 64 * 2;
 
@@ -58,7 +62,7 @@ struct ZeroArgs {
 
 hipError_t launch_zero_outside(const ZeroArgs& a, hipStream_t s);
 hipError_t launch_split(const float* x, uint16_t* planes, int64_t n, hipStream_t s);
-hipError_t launch_prepare(const Args& a, bool bf16, bool bwd, hipStream_t s);
+hipError_t launch_prepare(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_fwd_scan(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_bwd_scan(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_grad(const Args& a, bool bf16, hipStream_t s);

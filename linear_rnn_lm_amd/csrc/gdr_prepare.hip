@@ -1,10 +1,10 @@
-// gdr_prepare.hip -- per-chunk operands of the gated delta rule (gfx950): what a
-// chunk of 64 tokens of one head needs apart from the state.
+// gdr_prepare.hip -- per-chunk operands of the gated delta rule (gfx950): what the
+// chain of states needs of a chunk of 64 tokens of one head apart from the state.
 //
-//     T = (I + A)^-1,  A = strict_lower(b_t Lam K K^T);   M = lower(Lam Q K^T)
+//     T = (I + A)^-1,  A = strict_lower(b_t Lam K K^T)
 //
-// as bf16 planes, with the chunk's gates (see gdr_device.h).  All chunks of all
-// heads run at once, one workgroup of four waves each.
+// with the chunk's gates (see gdr_device.h).  All chunks of all heads run at
+// once, one workgroup of four waves each.
 #include "gdr_device.h"
 #include "gdr_internal.h"
 #include "wkv7_internal.h"
@@ -59,11 +59,10 @@ __device__ __forceinline__ void block_product(const float* X, const float* Y, fl
     for (int q = 0; q < 4; ++q) Z[(4 * g + q) * LDA + r] = sign * acc[q];
 }
 
-template <int NX, int K, bool BWD>
+template <int NX, int K>
 __global__ __launch_bounds__(256) void prepare_kernel(Args p) {
     __shared__ __attribute__((aligned(16))) float As[C * LDA];
     __shared__ __attribute__((aligned(16))) float Ts[C * LDA];
-    __shared__ __attribute__((aligned(16))) float Ms[C * LDA];
     __shared__ double Gs[C];
     __shared__ float bs[C];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -93,45 +92,36 @@ __global__ __launch_bounds__(256) void prepare_kernel(Args p) {
         const double Gc = __shfl(G, 63);
         Gs[lane] = G;
         bs[lane] = b;
-        float* gt = p.gates + block * kGateFloats;
+        float* gt = p.tri + block * p.tri_stride + kTriFloats;
         gt[kGateEG + lane] = exp_d(G);
         gt[kGateToEnd + lane] = lane < len ? exp_d(Gc - G) : 0.f;
         gt[kGateBeta + lane] = b;
-        reinterpret_cast<double*>(gt + kGateG)[lane] = G;
+        const double y = G * 1.4426950408889634074, n2 = __builtin_rint(y);
+        gt[kGateN + lane] = (float)n2;
+        gt[kGateF + lane] = (float)(y - n2);
     }
     for (int e = tid; e < C * LDA; e += 256) Ts[e] = 0.f;
 
-    // row tile w of K K^T and Q K^T (lower 32 x 32 blocks)
+    // row tile w of K K^T (lower 32 x 32 blocks)
     constexpr int KS = K / 32;
     const int stride = p.Hk * K;
-    Planes kp = p.kp, qp = p.qp;
+    Planes kp = p.kp;
     kp.p += tok * stride + hk * K;
-    qp.p += tok * stride + hk * K;
     auto row = [&](int t) { return min(t, len - 1); };   // tokens past the end: masked below
-    PF<NX> ka[KS], qa[KS];
+    PF<NX> ka[KS];
     const int ra = row(idx(w, r16));
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        ka[ks] = frag_mem<NX>(kp, ra, stride, ks, lane);
-        qa[ks] = frag_mem<NX>(qp, ra, stride, ks, lane);
-    }
+    for (int ks = 0; ks < KS; ++ks) ka[ks] = frag_mem<NX>(kp, ra, stride, ks, lane);
     __syncthreads();
     for (int nt = 0; nt < (w < 2 ? 2 : 4); ++nt) {
-        f32x4 kk = zero4(), qk = zero4();
+        f32x4 kk = zero4();
         const int s = idx(nt, r16);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const PF<NX> kb = frag_mem<NX>(kp, row(s), stride, ks, lane);
-            kk = pmma<NX>(kk, ka[ks], kb);
-            qk = pmma<NX>(qk, qa[ks], kb);
-        }
+        for (int ks = 0; ks < KS; ++ks) kk = pmma<NX>(kk, ka[ks], frag_mem<NX>(kp, row(s), stride, ks, lane));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int t = idx(w, 4 * g4 + q);
-            const bool on = s <= t && t < len;
-            const float lam = on ? exp_d(Gs[t] - Gs[s]) : 0.f;
-            As[t * LDA + s] = on && s < t ? bs[t] * lam * kk[q] : 0.f;
-            Ms[t * LDA + s] = on ? lam * qk[q] : 0.f;
+            As[t * LDA + s] = s < t && t < len ? bs[t] * exp_d(Gs[t] - Gs[s]) * kk[q] : 0.f;
         }
     }
     __syncthreads();
@@ -165,40 +155,20 @@ __global__ __launch_bounds__(256) void prepare_kernel(Args p) {
     block_product(Ts + (32 + mr) * LDA + 32, As + 32 + mc, Ts + (32 + mr) * LDA + mc, 32, -1.f, lane);
     __syncthreads();
 
-    // To planes, the three lower 32 x 32 blocks only.  T: as the scans' LDS holds it.  M: as
-    // operand fragments (M in the forward, M^T in the backward), six 32-deep steps
-    // of 64 lanes, which the scans' helper waves load straight into registers.
-    char* ops = p.ops + block * kOpsBytes;
-    for (int e = tid; e < 384; e += 256) {
-        const int blk = e >> 7, row = (e >> 2) & 31, u = e & 3;
-        const float* src = Ts + ((blk ? 32 : 0) + row) * LDA + (blk == 2 ? 32 : 0) + 8 * u;
-        const PF<kPlanes> f =
-            pf_acc<kPlanes>(*reinterpret_cast<const f32x4*>(src), *reinterpret_cast<const f32x4*>(src + 4));
-        char* dst = ops + blk * 2048 + (row * 4 + (u ^ (row >> 3))) * 16;
-#pragma unroll
-        for (int i = 0; i < kPlanes; ++i) *reinterpret_cast<bf16x8*>(dst + i * kTriBytes) = f.p[i];
-    }
-    for (int e = tid; e < 384; e += 256) {
-        const int f = e >> 6, l = e & 63;
-        // tile and step of fragment f: forward 00 10 20 21 30 31, backward 00 01 10 11 21 31
-        const int tile = BWD ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : (f + 2) >> 1);
-        const int ks = BWD ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1);
-        const int a = idx(tile, l & 15), b = 32 * ks + 8 * (l >> 4);
-        f32x4 x[2];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[q >> 2][q & 3] = BWD ? Ms[(b + q) * LDA + a] : Ms[a * LDA + b + q];
-        const PF<kPlanes> v = pf_acc<kPlanes>(x[0], x[1]);
-#pragma unroll
-        for (int i = 0; i < kPlanes; ++i)
-            *reinterpret_cast<bf16x8*>(ops + (kPlanes + i) * kTriBytes + e * 16) = v.p[i];
+    // the three lower 32 x 32 blocks, in pieces of eight values: block, row, eight columns
+    float* out = p.tri + block * p.tri_stride;
+    for (int e = tid; e < 768; e += 256) {
+        const int blk = e >> 8, row = (e >> 3) & 31, u = e & 7;
+        *reinterpret_cast<f32x4*>(out + 4 * e) =
+            *reinterpret_cast<const f32x4*>(Ts + ((blk ? 32 : 0) + row) * LDA + (blk == 2 ? 32 : 0) + 4 * u);
     }
 }
 
-template <int NX, bool BWD>
+template <int NX>
 hipError_t launch_k(const Args& a, hipStream_t s) {
     const dim3 grid((uint32_t)a.slots * a.H);
-    if (a.K == 64) hipLaunchKernelGGL((prepare_kernel<NX, 64, BWD>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((prepare_kernel<NX, 128, BWD>), grid, dim3(256), 0, s, a);
+    if (a.K == 64) hipLaunchKernelGGL((prepare_kernel<NX, 64>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((prepare_kernel<NX, 128>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -214,9 +184,8 @@ hipError_t launch_split(const float* x, uint16_t* planes, int64_t n, hipStream_t
     return hipGetLastError();
 }
 
-hipError_t launch_prepare(const Args& a, bool bf16, bool bwd, hipStream_t s) {
-    if (bwd) return bf16 ? launch_k<1, true>(a, s) : launch_k<3, true>(a, s);
-    return bf16 ? launch_k<1, false>(a, s) : launch_k<3, false>(a, s);
+hipError_t launch_prepare(const Args& a, bool bf16, hipStream_t s) {
+    return bf16 ? launch_k<1>(a, s) : launch_k<3>(a, s);
 }
 
 }  // namespace gdr

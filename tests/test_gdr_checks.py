@@ -34,12 +34,13 @@ def test_size_queries():
     assert [lib.gdr_slots(2, t, 0, 0) for t in (1, 64, 65)] == [2, 2, 4]
     assert lib.gdr_slots(1, 200, 5, 1) == 200 // 64 + 5
     assert lib.gdr_slots(2, 200, 5, 1) == 0 and lib.gdr_slots(1, 0, 1, 0) == 0
-    assert lib.gdr_ckpt_bytes(2, 65, 2, 4, 64, 128, 0, 0) == 4 * 4 * (64 + 64) * 128 * 4
+    assert lib.gdr_ckpt_bytes(2, 65, 2, 4, 64, 128, 0, 0) == 4 * 4 * ((64 + 64) * 128 + 6464) * 4
     assert lib.gdr_ckpt_bytes(2, 65, 3, 4, 64, 128, 0, 0) == 0          # H not a multiple of Hk
     assert lib.gdr_ckpt_bytes(2, 65, 2, 4, 96, 128, 0, 0) == 0
     f = [lib.gdr_fwd_workspace_bytes(2, 65, 2, 4, 64, 128, dt, 0, 0) for dt in (0, 1)]
     assert f[0] == f[1] + 2 * 3 * 2 * (2 * 65 * 2 * 64)                 # planes of fp32 q and k
-    assert lib.gdr_bwd_workspace_bytes(2, 65, 2, 4, 64, 128, 1, 0, 0) == f[1] + 16 * 128 * (64 + 64) * 4
+    assert f[1] == 16 * 3392 * 4
+    assert lib.gdr_bwd_workspace_bytes(2, 65, 2, 4, 64, 128, 1, 0, 0) == 16 * 128 * (64 + 64) * 4
     assert lib.gdr_fwd_workspace_bytes(2, 65, 2, 4, 64, 128, 3, 0, 0) == 0
     ln = lnorm._lib()
     assert ln.ln_bwd_workspace_bytes(1, 8, 1) == 8 * 2 * 4
