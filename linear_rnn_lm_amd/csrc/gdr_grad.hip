@@ -25,18 +25,19 @@ namespace {
 constexpr int NP = kPlanes;
 constexpr int NT = 512;
 
+// LDS plan.  The rows i of U, Z (V x 64 each), S and G1 are taken 32 at a time, which
+// keeps a workgroup at half a compute unit's LDS for bf16 inputs, so that the loads,
+// the splitting and the products of two workgroups overlap.  P and N take
+// the place of U, Z, S, G1 once those are used up.
 template <int NX>
 struct Lds {
-    static constexpr int MB = kMatBytes;                  // one plane of a 64 x 64 matrix
-    static constexpr int U = 0, Z = U + NP * MB;          // then P, N
-    static constexpr int P = U, N = Z;
-    static constexpr int S = Z + NP * MB, G = S + NP * MB;
-    static constexpr int DO = G + NP * MB;
-    static constexpr int after = DO + NX * MB;
-    static constexpr bool apart = NX == 1;                // K, Q beside S, G or in their place
-    static constexpr int Kr = apart ? after : S, Qr = Kr + NX * MB;
-    static constexpr int small = apart ? Qr + NX * MB : after;
+    static constexpr int MB = kMatBytes, HB = kMatBytes / 2;   // one plane of 64 x 64, of 32 x 64
+    static constexpr int U = 0, Z = U + NP * HB, S = Z + NP * HB, G = S + NP * HB;
+    static constexpr int P = 0, N = P + NP * MB;
+    static constexpr int DO = G + NP * HB, Kr = DO + NX * MB, Qr = Kr + NX * MB;
+    static constexpr int small = Qr + NX * MB;
     static constexpr int bytes = small + 7 * 64 * 4 + 2 * 128 * 4;
+    static_assert(N + NP * MB <= DO, "P and N in place of U, Z, S, G1");
 };
 
 // Eight consecutive fp32 values.
@@ -74,8 +75,9 @@ __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
     return fmaf(a[0], b[0], fmaf(a[1], b[1], fmaf(a[2], b[2], a[3] * b[3])));
 }
 
-template <typename InT, int NX, int K>
-__global__ __launch_bounds__(NT) void grad_kernel(Args p) {
+// ONE: one value head to a key head, so nothing is summed over heads.
+template <typename InT, int NX, int K, bool ONE>
+__global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
     using L = Lds<NX>;
     constexpr int KJ = K / 64;
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -90,167 +92,187 @@ __global__ __launch_bounds__(NT) void grad_kernel(Args p) {
     float* ep = dGp + 128;               // [2][64]
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g4 = lane >> 4, r16 = lane & 15;
-    const int slot = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk, rep = p.H / p.Hk;
+    const int slot = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk, rep = ONE ? 1 : p.H / p.Hk;
     const Seqs seqs{p.cu, p.N, p.T, p.NC};
     int n, len;
     int64_t tok;
     if (!slot_chunk(seqs, slot, n, tok, len)) return;
 
-    const int c = wave & 1, tt = wave >> 1;          // index pair 32c .. + 31, token tile tt
-    const int t = idx(tt, r16);                      // this lane's token (as a column of an accumulator)
-    const int row8 = tid >> 3, u8 = tid & 7;         // staging: row and unit of a 64 x 64 matrix
+    // A wave takes one tile tt of 16 tokens (its lanes' columns) and 32 of a slice's 64
+    // columns j (its accumulators' rows).
+    const int c = wave & 1, tt = wave >> 1;
+    const int t = idx(tt, r16);
     const int V = p.V;
+    // staging: the first half of the threads moves U and Z, the second S and G1, one row of
+    // 32 and unit of eight values each; of 64 x 64 matrices every thread moves one unit
+    const bool second = tid >= 256;
+    const int row8 = (tid & 255) >> 3, u8 = tid & 7, row64 = tid >> 3;
 
-    F8 gq[KJ], gk[KJ];
+    F8 gq[KJ], gk[KJ];                               // sums over the heads of the group
+    auto store = [&](int js, const F8& q, const F8& k) {
+        if (t < len) {
+            const int64_t o = ((tok + t) * p.Hk + hk) * K + 64 * js + 32 * c + 8 * g4;
+            store8(static_cast<InT*>(p.dq) + o, q);
+            store8(static_cast<InT*>(p.dk) + o, k);
+        }
+    };
+    if constexpr (!ONE) {
 #pragma unroll
-    for (int j = 0; j < KJ; ++j) gq[j] = gk[j] = F8{zero4(), zero4()};
+        for (int j = 0; j < KJ; ++j) gq[j] = gk[j] = F8{zero4(), zero4()};
+    }
 
     for (int hr = 0; hr < rep; ++hr) {
         const int h = hk * rep + hr;
         const int64_t block = (int64_t)slot * p.H + h;
-        const float* S = p.ckpt + block * p.ckpt_stride;
-        const float* Um = S + (int64_t)V * K;
-        const float* G1 = p.dend + block * (int64_t)V * K;
-        const float* Zm = p.z + block * (int64_t)C * V;
+        const float* ck = p.ckpt + block * p.ckpt_stride;           // S (V x K), U (V x 64)
         const float* gates = p.tri + block * p.tri_stride + kTriFloats;
-        __syncthreads();
-        if (tid < 64) {
-            Gn[tid] = gates[kGateN + tid];
-            Gf[tid] = gates[kGateF + tid];
-            eG[tid] = gates[kGateEG + tid];
-            toEnd[tid] = gates[kGateToEnd + tid];
-            beta[tid] = gates[kGateBeta + tid];
-        }
-        if (tid < 128) dGp[tid] = ep[tid] = 0.f;
         float sg = 0.f;
 
 #pragma unroll
         for (int js = 0; js < KJ; ++js) {
-            auto put_kq = [&] {
-                const int64_t rowk = (tok + min(row8, len - 1)) * p.Hk + hk;
+            // this thread's two of the four matrices, and how far apart their rows are
+            const float* src0 = second ? ck + (int64_t)row8 * K + 64 * js + 8 * u8
+                                       : ck + (int64_t)V * K + row8 * C + 8 * u8;
+            const float* src1 = second ? p.dend + block * (int64_t)V * K + (int64_t)row8 * K + 64 * js + 8 * u8
+                                       : p.z + block * (int64_t)C * V + row8 * C + 8 * u8;
+            const int step = second ? K : C;
+            F8 x0 = load8(src0), x1 = load8(src1);    // the next 32 rows, on their way
+            PF<NX> kx, qx;
+            const int64_t rowk = ((tok + min(row64, len - 1)) * p.Hk + hk) * K + 64 * js + 8 * u8;
 #pragma unroll
-                for (int i = 0; i < NX; ++i) {
-                    const int64_t o = i * p.kp.plane + rowk * K + 64 * js + 8 * u8;
-                    const PF<1> fk{{*reinterpret_cast<const bf16x8*>(p.kp.p + o)}};
-                    const PF<1> fq{{*reinterpret_cast<const bf16x8*>(p.qp.p + o)}};
-                    put8<8, 1>(smem + L::Kr + i * kMatBytes, 0, row8, u8, fk);
-                    put8<8, 1>(smem + L::Qr + i * kMatBytes, 0, row8, u8, fq);
-                }
-            };
+            for (int i = 0; i < NX; ++i) {
+                kx.p[i] = *reinterpret_cast<const bf16x8*>(p.kp.p + i * p.kp.plane + rowk);
+                qx.p[i] = *reinterpret_cast<const bf16x8*>(p.qp.p + i * p.qp.plane + rowk);
+            }
+            float gate = 0.f;
+            if (js == 0 && tid < kGateFloats) gate = gates[tid];
             f32x4 dos[2], zs[2], ug[2], pa[2], na[2];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) dos[hh] = zs[hh] = ug[hh] = pa[hh] = na[hh] = zero4();
-            for (int is = 0; is < V / 64; ++is) {
-                const F8 u = load8(Um + (64 * is + row8) * C + 8 * u8);      // rows i, columns t
-                const F8 z = load8(Zm + (64 * is + row8) * C + 8 * u8);
-                const F8 s = load8(S + (int64_t)(64 * is + row8) * K + 64 * js + 8 * u8);
-                const F8 g = load8(G1 + (int64_t)(64 * is + row8) * K + 64 * js + 8 * u8);
+            for (int j = 0; j < 2; ++j) dos[j] = zs[j] = ug[j] = pa[j] = na[j] = zero4();
+            for (int i0 = 0; i0 < V; i0 += 32) {
                 PF<NX> d;
-                if constexpr (NX == 1) {
-                    d.p[0] = bf16x8{};
-                    if (row8 < len)
-                        d.p[0] = *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(p.dout) +
-                                                                  ((tok + row8) * p.H + h) * V + 64 * is + 8 * u8);
-                } else {
-                    F8 x{zero4(), zero4()};
-                    if (row8 < len)
-                        x = load8(static_cast<const float*>(p.dout) + ((tok + row8) * p.H + h) * V + 64 * is + 8 * u8);
-                    d = pf_acc<NX>(x.a, x.b);
-                }
-                sg += dot4(s.a, g.a) + dot4(s.b, g.b);
-                __syncthreads();                          // the readers of the last slices are done
-                put8<8, NP>(smem + L::U, kMatBytes, row8, u8, pf_acc<NP>(u.a, u.b));
-                put8<8, NP>(smem + L::Z, kMatBytes, row8, u8, pf_acc<NP>(z.a, z.b));
-                put8<8, NP>(smem + L::S, kMatBytes, row8, u8, pf_acc<NP>(s.a, s.b));
-                put8<8, NP>(smem + L::G, kMatBytes, row8, u8, pf_acc<NP>(g.a, g.b));
-                put8<8, NX>(smem + L::DO, kMatBytes, row8, u8, d);
-                if (L::apart && is == 0) put_kq();
-                __syncthreads();
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const PF<NX> df = frag_row<8, NX>(smem + L::DO, kMatBytes, t, ks, lane);
-                    const PF<NP> zf = frag_col<8, NP>(smem + L::Z, kMatBytes, tt, ks, lane);
-                    const PF<NP> uf = frag_col<8, NP>(smem + L::U, kMatBytes, tt, ks, lane);
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const PF<NP> sf = frag_col<8, NP>(smem + L::S, kMatBytes, 2 * c + hh, ks, lane);
-                        const PF<NP> gf = frag_col<8, NP>(smem + L::G, kMatBytes, 2 * c + hh, ks, lane);
-                        dos[hh] = pmma<NP>(dos[hh], sf, df);
-                        zs[hh] = pmma<NP>(zs[hh], sf, zf);
-                        ug[hh] = pmma<NP>(ug[hh], gf, uf);
-                        if (c <= (tt >> 1)) {
-                            const PF<NP> us = frag_col<8, NP>(smem + L::U, kMatBytes, 2 * c + hh, ks, lane);
-                            pa[hh] = pmma<NP>(pa[hh], us, df);
-                            na[hh] = pmma<NP>(na[hh], us, zf);
-                        }
+                if (i0 % 64 == 0) {                   // 64 columns of dout, for two rounds
+                    const int64_t o = ((tok + min(row64, len - 1)) * p.H + h) * V + i0 + 8 * u8;
+                    if constexpr (NX == 1) {
+                        d.p[0] = *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(p.dout) + o);
+                        if (row64 >= len) d.p[0] = bf16x8{};
+                    } else {
+                        F8 x = load8(static_cast<const float*>(p.dout) + o);
+                        if (row64 >= len) x = F8{zero4(), zero4()};
+                        d = pf_acc<NX>(x.a, x.b);
                     }
                 }
+                if (second) sg += dot4(x0.a, x1.a) + dot4(x0.b, x1.b);
+                __syncthreads();                      // the readers of what lay here are done
+                put8<8, NP>(smem + (second ? L::S : L::U), L::HB, row8, u8, pf_acc<NP>(x0.a, x0.b));
+                put8<8, NP>(smem + (second ? L::G : L::Z), L::HB, row8, u8, pf_acc<NP>(x1.a, x1.b));
+                if (i0 % 64 == 0) put8<8, NX>(smem + L::DO, L::MB, row64, u8, d);
+                if (i0 == 0) {
+                    put8<8, NX>(smem + L::Kr, L::MB, row64, u8, kx);
+                    put8<8, NX>(smem + L::Qr, L::MB, row64, u8, qx);
+                    if (js == 0 && tid < kGateFloats) {      // in the order e^G, e^(G_C - G), b, n, f
+                        float* to = tid < 64 ? eG : tid < 128 ? toEnd - 64 : tid < 192 ? beta - 128 : tid < 256 ? Gn - 192 : Gf - 256;
+                        to[tid] = gate;
+                    }
+                    if (js == 0 && tid < 128) dGp[tid] = ep[tid] = 0.f;
+                }
+                if (i0 + 32 < V) {
+                    x0 = load8(src0 + (int64_t)(i0 + 32) * step);
+                    x1 = load8(src1 + (int64_t)(i0 + 32) * step);
+                }
+                __syncthreads();
+                const PF<NX> df = frag_row<8, NX>(smem + L::DO, L::MB, t, (i0 >> 5) & 1, lane);
+                const PF<NP> zf = frag_col<8, NP>(smem + L::Z, L::HB, tt, 0, lane);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const PF<NP> sf = frag_col<8, NP>(smem + L::S, L::HB, 2 * c + j, 0, lane);
+                    dos[j] = pmma<NP>(dos[j], sf, df);
+                    zs[j] = pmma<NP>(zs[j], sf, zf);
+                }
+                if (c <= (tt >> 1)) {                 // tokens s of 32 c .. + 31 at or before t
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const PF<NP> us = frag_col<8, NP>(smem + L::U, L::HB, 2 * c + j, 0, lane);
+                        pa[j] = pmma<NP>(pa[j], us, df);
+                        na[j] = pmma<NP>(na[j], us, zf);
+                    }
+                }
+                const PF<NP> uf = frag_col<8, NP>(smem + L::U, L::HB, tt, 0, lane);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    ug[j] = pmma<NP>(ug[j], frag_col<8, NP>(smem + L::G, L::HB, 2 * c + j, 0, lane), uf);
             }
             const float bt = beta[t], egt = eG[t], tet = toEnd[t], nt = Gn[t], ft = Gf[t];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
+            for (int j = 0; j < 2; ++j) {
+                const int s0 = 32 * c + 8 * g4 + 4 * j;
+                const f32x4 ns = *reinterpret_cast<const f32x4*>(Gn + s0), fs = *reinterpret_cast<const f32x4*>(Gf + s0);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int s = 32 * c + 8 * g4 + 4 * hh + q;
-                    const float lam = s <= t ? decay(nt, ft, Gn[s], Gf[s]) : 0.f;
-                    if (s == t) dbeta[t] = t < len ? na[hh][q] / bt : 0.f;
-                    pa[hh][q] = s <= t ? p.scale * lam * pa[hh][q] : 0.f;
-                    na[hh][q] = s < t ? -bt * lam * na[hh][q] : 0.f;
+                    const int s = s0 + q;
+                    const float lam = s <= t ? decay(nt, ft, ns[q], fs[q]) : 0.f;
+                    if (s == t) dbeta[t] = t < len ? na[j][q] / bt : 0.f;
+                    pa[j][q] = s <= t ? p.scale * lam * pa[j][q] : 0.f;
+                    na[j][q] = s < t ? -bt * lam * na[j][q] : 0.f;
                 }
+            }
             __syncthreads();
-            put8<8, NP>(smem + L::P, kMatBytes, t, 4 * c + g4, pf_acc<NP>(pa[0], pa[1]));
-            put8<8, NP>(smem + L::N, kMatBytes, t, 4 * c + g4, pf_acc<NP>(na[0], na[1]));
-            if (!L::apart) put_kq();
+            put8<8, NP>(smem + L::P, L::MB, t, 4 * c + g4, pf_acc<NP>(pa[0], pa[1]));
+            put8<8, NP>(smem + L::N, L::MB, t, 4 * c + g4, pf_acc<NP>(na[0], na[1]));
             __syncthreads();
-            f32x4 pk[2], nk[2], pq[2];
+            f32x4 nk[2], pq[2];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) pk[hh] = nk[hh] = pq[hh] = zero4();
+            for (int j = 0; j < 2; ++j) {
+                dos[j] = p.scale * egt * dos[j];      // then + P K
+                nk[j] = pq[j] = zero4();
+            }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 if (ks <= (tt >> 1)) {
-                    const PF<NP> pr = frag_row<8, NP>(smem + L::P, kMatBytes, t, ks, lane);
-                    const PF<NP> nr = frag_row<8, NP>(smem + L::N, kMatBytes, t, ks, lane);
+                    const PF<NP> pr = frag_row<8, NP>(smem + L::P, L::MB, t, ks, lane);
+                    const PF<NP> nr = frag_row<8, NP>(smem + L::N, L::MB, t, ks, lane);
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const PF<NX> kf = frag_col<8, NX>(smem + L::Kr, kMatBytes, 2 * c + hh, ks, lane);
-                        pk[hh] = pmma<NP>(pk[hh], kf, pr);
-                        nk[hh] = pmma<NP>(nk[hh], kf, nr);
+                    for (int j = 0; j < 2; ++j) {
+                        const PF<NX> kf = frag_col<8, NX>(smem + L::Kr, L::MB, 2 * c + j, ks, lane);
+                        dos[j] = pmma<NP>(dos[j], kf, pr);
+                        nk[j] = pmma<NP>(nk[j], kf, nr);
                     }
                 }
                 if (ks >= (tt >> 1)) {
-                    const PF<NP> pc = frag_col<8, NP>(smem + L::P, kMatBytes, tt, ks, lane);
-                    const PF<NP> nc = frag_col<8, NP>(smem + L::N, kMatBytes, tt, ks, lane);
+                    const PF<NP> pc = frag_col<8, NP>(smem + L::P, L::MB, tt, ks, lane);
+                    const PF<NP> nc = frag_col<8, NP>(smem + L::N, L::MB, tt, ks, lane);
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        pq[hh] = pmma<NP>(pq[hh], frag_col<8, NX>(smem + L::Qr, kMatBytes, 2 * c + hh, ks, lane), pc);
-                        pq[hh] = pmma<NP>(pq[hh], frag_col<8, NX>(smem + L::Kr, kMatBytes, 2 * c + hh, ks, lane), nc);
+                    for (int j = 0; j < 2; ++j) {
+                        pq[j] = pmma<NP>(pq[j], frag_col<8, NX>(smem + L::Qr, L::MB, 2 * c + j, ks, lane), pc);
+                        pq[j] = pmma<NP>(pq[j], frag_col<8, NX>(smem + L::Kr, L::MB, 2 * c + j, ks, lane), nc);
                     }
                 }
             }
             const F8 kv = get8<NX>(smem + L::Kr, t, 4 * c + g4), qv = get8<NX>(smem + L::Qr, t, 4 * c + g4);
             float dG = 0.f, e = 0.f;
+            F8 oq, ok;
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const f32x4 k4 = hh ? kv.b : kv.a, q4 = hh ? qv.b : qv.a;
-                const f32x4 dq = p.scale * egt * dos[hh] + pk[hh];
-                const f32x4 plus = nk[hh] - egt * bt * zs[hh];
-                const f32x4 end = tet * ug[hh];
-                const f32x4 minus = pq[hh] + end;
-                dG += dot4(q4, dq) + dot4(k4, plus - minus);
+            for (int j = 0; j < 2; ++j) {
+                const f32x4 k4 = j ? kv.b : kv.a, q4 = j ? qv.b : qv.a;
+                const f32x4 plus = nk[j] - egt * bt * zs[j], end = tet * ug[j], minus = pq[j] + end;
+                dG += dot4(q4, dos[j]) + dot4(k4, plus - minus);
                 e += dot4(k4, end);
-                if (hh) {
-                    gq[js].b += dq;
-                    gk[js].b += plus + minus;
-                } else {
-                    gq[js].a += dq;
-                    gk[js].a += plus + minus;
-                }
+                (j ? oq.b : oq.a) = dos[j];
+                (j ? ok.b : ok.a) = plus + minus;
+            }
+            if constexpr (ONE) {
+                store(js, oq, ok);
+            } else {
+                gq[js].a += oq.a;
+                gq[js].b += oq.b;
+                gk[js].a += ok.a;
+                gk[js].b += ok.b;
             }
             dG += __shfl_xor(dG, 16);
             e += __shfl_xor(e, 16);
             dG += __shfl_xor(dG, 32);
             e += __shfl_xor(e, 32);
-            if (g4 == 0) {                                // one lane per (c, t)
+            if (g4 == 0) {                            // one lane per (c, t)
                 dGp[c * 64 + t] += dG;
                 ep[c * 64 + t] += e;
             }
@@ -280,21 +302,18 @@ __global__ __launch_bounds__(NT) void grad_kernel(Args p) {
                 p.dbeta[(tok + lane) * p.H + h] = dbeta[lane];
             }
         }
+        if constexpr (!ONE) __syncthreads();          // wave 0 reads what the next head overwrites
     }
-    if (t < len) {
+    if constexpr (!ONE) {
 #pragma unroll
-        for (int js = 0; js < KJ; ++js) {
-            const int64_t o = ((tok + t) * p.Hk + hk) * K + 64 * js + 32 * c + 8 * g4;
-            store8(static_cast<InT*>(p.dq) + o, gq[js]);
-            store8(static_cast<InT*>(p.dk) + o, gk[js]);
-        }
+        for (int js = 0; js < KJ; ++js) store(js, gq[js], gk[js]);
     }
 }
 
-template <typename InT, int NX, int K>
+template <typename InT, int NX, int K, bool ONE>
 hipError_t launch_typed(const Args& a, hipStream_t s) {
     static_assert(Lds<NX>::bytes <= 160 * 1024, "gradient LDS");
-    auto kern = grad_kernel<InT, NX, K>;
+    auto kern = grad_kernel<InT, NX, K, ONE>;
     static wkv7::PerDeviceOnce once;
     const hipError_t e = wkv7::set_smem_once(once, kern, Lds<NX>::bytes);
     if (e != hipSuccess) return e;
@@ -302,11 +321,16 @@ hipError_t launch_typed(const Args& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <bool ONE>
+hipError_t launch_k(const Args& a, bool bf16, hipStream_t s) {
+    if (bf16) return a.K == 64 ? launch_typed<uint16_t, 1, 64, ONE>(a, s) : launch_typed<uint16_t, 1, 128, ONE>(a, s);
+    return a.K == 64 ? launch_typed<float, 3, 64, ONE>(a, s) : launch_typed<float, 3, 128, ONE>(a, s);
+}
+
 }  // namespace
 
 hipError_t launch_grad(const Args& a, bool bf16, hipStream_t s) {
-    if (bf16) return a.K == 64 ? launch_typed<uint16_t, 1, 64>(a, s) : launch_typed<uint16_t, 1, 128>(a, s);
-    return a.K == 64 ? launch_typed<float, 3, 64>(a, s) : launch_typed<float, 3, 128>(a, s);
+    return a.H == a.Hk ? launch_k<true>(a, bf16, s) : launch_k<false>(a, bf16, s);
 }
 
 }  // namespace gdr
