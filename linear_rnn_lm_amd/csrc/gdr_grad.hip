@@ -90,8 +90,7 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
     float* red = dbeta + 64;             // 8 floats used
     float* dGp = red + 64;               // [2][64]
     float* ep = dGp + 128;               // [2][64]
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int g4 = lane >> 4, r16 = lane & 15;
+    const int tid0 = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid0 >> 6);
     const int slot = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk, rep = ONE ? 1 : p.H / p.Hk;
     const Seqs seqs{p.cu, p.N, p.T, p.NC};
     int n, len;
@@ -101,42 +100,42 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
     // A wave takes one tile tt of 16 tokens (its lanes' columns) and 32 of a slice's 64
     // columns j (its accumulators' rows).
     const int c = wave & 1, tt = wave >> 1;
-    const int t = idx(tt, r16);
     const int V = p.V;
-    // staging: the first half of the threads moves U and Z, the second S and G1, one row of
-    // 32 and unit of eight values each; of 64 x 64 matrices every thread moves one unit
-    const bool second = tid >= 256;
-    const int row8 = (tid & 255) >> 3, u8 = tid & 7, row64 = tid >> 3;
 
-    F8 gq[KJ], gk[KJ];                               // sums over the heads of the group
-    auto store = [&](int js, const F8& q, const F8& k) {
-        if (t < len) {
-            const int64_t o = ((tok + t) * p.Hk + hk) * K + 64 * js + 32 * c + 8 * g4;
-            store8(static_cast<InT*>(p.dq) + o, q);
-            store8(static_cast<InT*>(p.dk) + o, k);
-        }
-    };
-    if constexpr (!ONE) {
-#pragma unroll
-        for (int j = 0; j < KJ; ++j) gq[j] = gk[j] = F8{zero4(), zero4()};
-    }
-
+    // Slices outside, heads inside: the sums over the heads are those of one slice.  What
+    // dg has of the slices before is in memory, written by the same lanes.
+    for (int js = 0; js < KJ; ++js) {
+    F8 gq{zero4(), zero4()}, gk{zero4(), zero4()};
     for (int hr = 0; hr < rep; ++hr) {
+        // The thread's number is made opaque in every round, or the loops' many LDS
+        // addresses, all functions of it, are kept in registers that are not there.
+        int tid = tid0;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, g4 = lane >> 4, r16 = lane & 15, t = idx(tt, r16);
+        // staging: the first half of the threads moves U and Z, the second S and G1, one row of
+        // 32 and unit of eight values each; of 64 x 64 matrices every thread moves one unit
+        const bool second = wave >= 4;
+        const int row8 = (tid & 255) >> 3, u8 = tid & 7, row64 = tid >> 3;
+        auto store = [&](const F8& q, const F8& k) {
+            if (t < len) {
+                const int64_t o = ((tok + t) * p.Hk + hk) * K + 64 * js + 32 * c + 8 * g4;
+                store8(static_cast<InT*>(p.dq) + o, q);
+                store8(static_cast<InT*>(p.dk) + o, k);
+            }
+        };
         const int h = hk * rep + hr;
         const int64_t block = (int64_t)slot * p.H + h;
         const float* ck = p.ckpt + block * p.ckpt_stride;           // S (V x K), U (V x 64)
         const float* gates = p.tri + block * p.tri_stride + kTriFloats;
         float sg = 0.f;
-
-#pragma unroll
-        for (int js = 0; js < KJ; ++js) {
+        {
             // this thread's two of the four matrices, and how far apart their rows are
             const float* src0 = second ? ck + (int64_t)row8 * K + 64 * js + 8 * u8
                                        : ck + (int64_t)V * K + row8 * C + 8 * u8;
             const float* src1 = second ? p.dend + block * (int64_t)V * K + (int64_t)row8 * K + 64 * js + 8 * u8
                                        : p.z + block * (int64_t)C * V + row8 * C + 8 * u8;
             const int step = second ? K : C;
-            F8 x0 = load8(src0), x1 = load8(src1);    // the next 32 rows, on their way
+            F8 x0 = load8(src0), x1 = load8(src1);    // the next 32 rows, on their way (ONE; else no registers are left)
             PF<NX> kx, qx;
             const int64_t rowk = ((tok + min(row64, len - 1)) * p.Hk + hk) * K + 64 * js + 8 * u8;
 #pragma unroll
@@ -145,7 +144,7 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
                 qx.p[i] = *reinterpret_cast<const bf16x8*>(p.qp.p + i * p.qp.plane + rowk);
             }
             float gate = 0.f;
-            if (js == 0 && tid < kGateFloats) gate = gates[tid];
+            if (tid < kGateFloats) gate = gates[tid];
             f32x4 dos[2], zs[2], ug[2], pa[2], na[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) dos[j] = zs[j] = ug[j] = pa[j] = na[j] = zero4();
@@ -162,6 +161,10 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
                         d = pf_acc<NX>(x.a, x.b);
                     }
                 }
+                if (!ONE && i0 > 0) {
+                    x0 = load8(src0 + (int64_t)i0 * step);
+                    x1 = load8(src1 + (int64_t)i0 * step);
+                }
                 if (second) sg += dot4(x0.a, x1.a) + dot4(x0.b, x1.b);
                 __syncthreads();                      // the readers of what lay here are done
                 put8<8, NP>(smem + (second ? L::S : L::U), L::HB, row8, u8, pf_acc<NP>(x0.a, x0.b));
@@ -170,13 +173,12 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
                 if (i0 == 0) {
                     put8<8, NX>(smem + L::Kr, L::MB, row64, u8, kx);
                     put8<8, NX>(smem + L::Qr, L::MB, row64, u8, qx);
-                    if (js == 0 && tid < kGateFloats) {      // in the order e^G, e^(G_C - G), b, n, f
+                    if (tid < kGateFloats) {          // in the order e^G, e^(G_C - G), b, n, f
                         float* to = tid < 64 ? eG : tid < 128 ? toEnd - 64 : tid < 192 ? beta - 128 : tid < 256 ? Gn - 192 : Gf - 256;
                         to[tid] = gate;
                     }
-                    if (js == 0 && tid < 128) dGp[tid] = ep[tid] = 0.f;
                 }
-                if (i0 + 32 < V) {
+                if (ONE && i0 + 32 < V) {
                     x0 = load8(src0 + (int64_t)(i0 + 32) * step);
                     x1 = load8(src1 + (int64_t)(i0 + 32) * step);
                 }
@@ -261,20 +263,21 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
                 (j ? ok.b : ok.a) = plus + minus;
             }
             if constexpr (ONE) {
-                store(js, oq, ok);
+                store(oq, ok);
             } else {
-                gq[js].a += oq.a;
-                gq[js].b += oq.b;
-                gk[js].a += ok.a;
-                gk[js].b += ok.b;
+                gq.a += oq.a;
+                gq.b += oq.b;
+                gk.a += ok.a;
+                gk.b += ok.b;
+                if (hr == rep - 1) store(gq, gk);
             }
             dG += __shfl_xor(dG, 16);
             e += __shfl_xor(e, 16);
             dG += __shfl_xor(dG, 32);
             e += __shfl_xor(e, 32);
             if (g4 == 0) {                            // one lane per (c, t)
-                dGp[c * 64 + t] += dG;
-                ep[c * 64 + t] += e;
+                dGp[c * 64 + t] = dG;
+                ep[c * 64 + t] = e;
             }
         }
 #pragma unroll
@@ -298,15 +301,13 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
                 if (lane + d < 64) x += o;
             }
             if (lane < len) {
-                p.dg[(tok + lane) * p.H + h] = (float)x;
+                float* dg = p.dg + (tok + lane) * p.H + h;
+                *dg = (float)(js ? x + *dg : x);
                 p.dbeta[(tok + lane) * p.H + h] = dbeta[lane];
             }
         }
-        if constexpr (!ONE) __syncthreads();          // wave 0 reads what the next head overwrites
+        if (KJ > 1 || !ONE) __syncthreads();          // wave 0 reads what the next round overwrites
     }
-    if constexpr (!ONE) {
-#pragma unroll
-        for (int js = 0; js < KJ; ++js) store(js, gq[js], gk[js]);
     }
 }
 
