@@ -5,13 +5,17 @@
 // A state wave holds 16 rows i of S (or of its gradient) for all K columns in
 // its accumulators, as K / 16 tiles of S^T, and shares nothing with the other
 // state waves: every product of the chain has the form (operand from LDS) x
-// (that wave's registers).  What the chain does not wait for is done by a
-// helper wave beside each state wave, one chunk behind (forward: o and the
-// stores for the backward) or one chunk ahead (backward: the parts of dU and of the state
-// gradient that come from dout alone); the two pass fp32 tiles through LDS, in
-// accumulator order.  One wave copies the next chunks' K and gates into LDS, another
-// splits their T into planes there; in the forward, two more form M.  One barrier
-// per chunk.
+// (that wave's registers).  What the chain does not wait for is done by other
+// waves: in the forward four output waves, one tile of 16 tokens each, one chunk
+// behind (M, o, the stores for the backward); in the backward a helper beside
+// each state wave, one chunk ahead (the parts of dU and of the state gradient
+// that come from dout alone).  They pass fp32 tiles through LDS, in accumulator
+// order.  Of two memory waves one copies the next chunks' K, v and gates into
+// LDS, the other splits their T into planes there.  One barrier per chunk.
+//
+// Memory instructions are issued one wave at a time on a compute unit, 16 and more
+// cycles each, and a wave that issues one waits its turn; so token columns
+// go through LDS in 16-byte pieces, and the state waves of the forward issue none.
 #include "gdr_device.h"
 #include "gdr_internal.h"
 #include "wkv7_internal.h"
@@ -19,44 +23,47 @@
 namespace gdr {
 namespace {
 
-using wkv7::make_rsrc;
-using wkv7::Rsrc;
-
 constexpr int NP = kPlanes;
 constexpr int kLds = 160 * 1024;
 
-// LDS plan.  One chunk's K rows, T planes and gates; the backward also stages Q
-// rows, one chunk further ahead; the forward keeps M^T (NO planes) from one chunk
-// to the next; then the tiles that state and helper waves pass on, all of
-// these double-buffered by chunk parity.
-template <int NX, int K, int NCW, bool BWD>
+// LDS plan.  Of one chunk: K rows, T planes and gates, and in the forward the
+// workgroup's columns of v.  The backward stages Q rows and dout's columns one chunk
+// further ahead.  Then the tiles that waves pass on, double-buffered by chunk parity.
+template <typename InT, int NX, int K, int NCW, bool BWD>
 struct Plan {
-    // o leaves in in_dtype: for bf16 two planes (2^-17) in its own products lose nothing
-    // beside its rounding; the products of the state keep all three
-    static constexpr int NO = NX == 1 ? 2 : NP;
     static constexpr int XB = C * K * 2;                  // one plane of K or Q rows
-    static constexpr int Kr = 0, T = Kr + NX * XB, G = T + NP * kTriBytes, bytes = G + kGateFloats * 4;
-    static constexpr int QB = BWD ? NX * XB : 0, MB = BWD ? 0 : NO * kTriBytes;
+    static constexpr int RB = NCW * 16 * (int)sizeof(InT), VB = C * RB;   // a token's columns, a chunk's
+    static constexpr int Kr = 0, T = Kr + NX * XB, G = T + NP * kTriBytes, V = G + kGateFloats * 4;
+    static constexpr int bytes = V + (BWD ? 0 : VB);
+    static constexpr int QB = BWD ? NX * XB + VB : 0;
     static constexpr int ST = K / 16 * 1024, UT = 4 * 1024;   // state tiles, token tiles of one wave
-    static constexpr int pass = 2 * NCW * (ST + UT), rest = 2 * QB + 2 * MB + pass;
+    static constexpr int pass = 2 * NCW * (ST + UT), OB = BWD ? 0 : 4 * 16 * RB, rest = 2 * QB + pass + OB;
     static constexpr int NBUF = 3 * bytes + rest <= kLds ? 3 : 2 * bytes + rest <= kLds ? 2 : 1;
     static constexpr int NQ = NBUF > 1 ? 2 : 1;
-    static constexpr int Q0 = NBUF * bytes, M0 = Q0 + NQ * QB, P0 = M0 + 2 * MB, total = P0 + pass;
+    static constexpr int Q0 = NBUF * bytes, P0 = Q0 + NQ * QB, O0 = P0 + pass, total = O0 + OB;
     static_assert(total <= kLds, "scan LDS");
 };
 
-// A raw value of a token tensor by byte offset; 0 past the resource's end.
-__device__ __forceinline__ uint16_t bload(const uint16_t*, Rsrc r, int off) {
-    return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+// A row block of 16 token columns per wave, staged in LDS with RB bytes per token: the wave's
+// column in accumulator order (tokens idx(t, 4g + q)).
+template <int RB>
+__device__ __forceinline__ void column_tiles(f32x4 (&x)[4], const char* buf, int cw, int lane, uint16_t) {
+    const char* p = buf + (8 * (lane >> 4) + ((lane & 15) >> 2)) * RB + 32 * cw + 8 * (lane & 3);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const wkv7::i16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (wkv7::lds_i16x4*)(p + (32 * (t >> 1) + 4 * (t & 1)) * RB));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[t][q] = widen((uint16_t)v[q]);
+    }
 }
-__device__ __forceinline__ float bload(const float*, Rsrc r, int off) {
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-}
-__device__ __forceinline__ void bput(uint16_t*, Rsrc r, int off, float v) {
-    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), r, off, 0, 0);
-}
-__device__ __forceinline__ void bput(float*, Rsrc r, int off, float v) {
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, off, 0, 0);
+template <int RB>
+__device__ __forceinline__ void column_tiles(f32x4 (&x)[4], const char* buf, int cw, int lane, float) {
+    const char* p = buf + 64 * cw + 4 * (lane & 15);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[t][q] = *reinterpret_cast<const float*>(p + idx(t, 4 * (lane >> 4) + q) * RB);
 }
 
 // Rows of K or Q of one chunk into LDS, in 1 KiB pieces.
@@ -90,21 +97,17 @@ struct Where {
     __device__ __forceinline__ int64_t block(const Args& p, int c) const { return (int64_t)(slot0 + c) * p.H + h; }
 };
 
-// Byte offsets of a lane's 16 values of a chunk: tokens in accumulator order, one column.
-template <typename InT>
-__device__ __forceinline__ void token_offsets(int (&off)[16], const Args& p, int i, int g4) {
+// The workgroup's columns of a chunk of a (tokens, H, V) tensor into LDS.
+template <typename InT, int RB>
+__device__ __forceinline__ void stage_columns(const InT* x, char* buf, const Args& p, const Where& w, int c, int lane) {
+    constexpr int UPR = RB / 16, EPU = 16 / (int)sizeof(InT);
+    const int len = min(C, w.len - c * C);
+    const InT* src = x + ((w.tok0 + (int64_t)c * C) * p.H + w.h) * p.V + w.sub * (RB / (int)sizeof(InT));
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-        off[e] = (int)(((int64_t)idx(e >> 2, 4 * g4 + (e & 3)) * p.H * p.V + i) * (int64_t)sizeof(InT));
-}
-// Chunk c of a (tokens, H, V) tensor, ending with the sequence.
-template <typename T>
-__device__ __forceinline__ Rsrc chunk_rsrc(T* x, const Args& p, const Where& w, int c) {
-    const int64_t stride = (int64_t)p.H * p.V;
-    const bool on = x && c >= 0 && c < w.nc;
-    const int rows = on ? min(C, w.len - c * C) : 0;
-    return make_rsrc(on ? x + (w.tok0 + (int64_t)c * C) * stride + (int64_t)w.h * p.V : nullptr,
-                     on ? (uint32_t)(((rows - 1) * stride + p.V) * (int64_t)sizeof(T)) : 0u);
+    for (int pc = 0; pc < C * UPR / 64; ++pc) {
+        const int e = pc * 64 + lane;
+        dma16(src + (int64_t)min(e / UPR, len - 1) * p.H * p.V + (e % UPR) * EPU, buf + pc * 1024);
+    }
 }
 
 template <int KT>
@@ -144,9 +147,9 @@ __device__ __forceinline__ void pass_get(const char* p, int lane, f32x4 (&x)[N])
 
 // The two memory waves.  They work NBUF - 1 chunks ahead of the one in use (none
 // ahead, and two barriers per chunk, where a single buffer is all that fits).
-template <int NX, int K, int NCW, bool BWD>
+template <typename InT, int NX, int K, int NCW, bool BWD>
 __device__ __forceinline__ void memory_wave(const Args& p, const Where& w, char* smem, int mw, int lane) {
-    using L = Plan<NX, K, NCW, BWD>;
+    using L = Plan<InT, NX, K, NCW, BWD>;
     constexpr int ahead = L::NBUF - 1;
     const int64_t stride = (int64_t)p.Hk * K;
     auto chunk_of = [&](int it) { return BWD ? w.nc - 1 - it : it; };
@@ -207,12 +210,15 @@ __device__ __forceinline__ void memory_wave(const Args& p, const Where& w, char*
         const char* gates = reinterpret_cast<const char*>(tri(it) + kTriFloats) + 16 * lane;
         dma16(gates, buf(it) + L::G);
         if (lane < kGateFloats / 4 - 64) dma16(gates + 1024, buf(it) + L::G + 1024);
+        if constexpr (!BWD) stage_columns<InT, L::RB>(static_cast<const InT*>(p.v), buf(it) + L::V, p, w, c, lane);
     };
     auto fetch_q = [&](int it) {
         if constexpr (BWD) {
             if (it >= w.nc) return;                       // an empty sequence has no chunk 0
             const int c = chunk_of(it);
-            stage_rows<NX, K>(p.qp, smem + L::Q0 + (it % L::NQ) * L::QB, rows_of(c), stride, min(C, w.len - c * C), lane);
+            char* q = smem + L::Q0 + (it % L::NQ) * L::QB;
+            stage_rows<NX, K>(p.qp, q, rows_of(c), stride, min(C, w.len - c * C), lane);
+            stage_columns<InT, L::RB>(static_cast<const InT*>(p.dout), q + NX * L::XB, p, w, c, lane);
         }
     };
     if constexpr (L::NBUF == 1) {
@@ -241,7 +247,7 @@ __device__ __forceinline__ void memory_wave(const Args& p, const Where& w, char*
         fetch(it + ahead);
         // chunk it + 1 was fetched in the iteration before where ahead is 2: only this iteration's
         // chunk may be in flight (loads land in order)
-        constexpr int n = NX * C * K * 2 / 1024 + 2;
+        constexpr int n = NX * C * K * 2 / 1024 + 2 + (BWD ? 0 : L::VB / 1024);
         if (ahead == 2 && it + ahead < w.nc) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
         else landed();
         lds_barrier();
@@ -358,163 +364,27 @@ __device__ __forceinline__ void load_row(PF<NX> (&f)[KS], const Planes& x, const
         for (int j = 0; j < NX; ++j) f[ks].p[j] = *reinterpret_cast<const bf16x8*>(row + j * x.plane + 32 * ks);
 }
 
-// The two M waves of the forward: M^T = (Lam Q K^T)^T of chunk it in iteration it, in six
-// pieces of one tile of s by 32 tokens t (rows s of eight consecutive t per lane), as
-// planes in LDS for the helpers and in fp32 for the backward.  Wave 0 takes pieces
-// (0, 0), (1, 0), (0, 1), wave 1 pieces (1, 1), (2, 1), (3, 1) of (tile, 32 tokens).
-template <int NX, int K, int NCW, int MW>
-__device__ __forceinline__ void m_wave(const Args& p, const Where& w, char* smem, int lane) {
-    using L = Plan<NX, K, NCW, false>;
-    constexpr int U = K / 8, KS = K / 32, NO = L::NO, T0 = MW == 0 ? 0 : 2;
-    const int g4 = lane >> 4, r16 = lane & 15;
-    const bool want = p.o || p.ckpt;
-    PF<NX> qf[4 - T0][KS];
-    auto load = [&](int c) {
-        if (c >= w.nc || !want) return;
-#pragma unroll
-        for (int t = T0; t < 4; ++t) load_row<NX, KS>(qf[t - T0], p.qp, p, w, c, idx(t, r16), g4);
-    };
-    load(0);
-    lds_barrier();
-    for (int it = 0; it < w.nc; ++it) {
-        if constexpr (L::NBUF == 1) lds_barrier();
-        if (want) {
-            const char* buf = smem + (it % L::NBUF) * L::bytes;
-            const float* gates = reinterpret_cast<const float*>(buf + L::G);
-            char* m = smem + L::M0 + (it & 1) * L::MB;
-            f32x4 x[3][2];
-#pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const int ts = MW == 0 ? j & 1 : j + 1, ks = MW == 0 ? j >> 1 : 1;
-                x[j][0] = x[j][1] = zero4();
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const PF<NX> kf = frag_row<U, NX>(buf + L::Kr, L::XB, idx(ts, r16), k, lane);
-                    x[j][0] = pmma<NP>(x[j][0], qf[2 * ks - T0][k], kf);
-                    x[j][1] = pmma<NP>(x[j][1], qf[2 * ks + 1 - T0][k], kf);
-                }
-            }
-            load(it + 1);
-#pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const int ts = MW == 0 ? j & 1 : j + 1, ks = MW == 0 ? j >> 1 : 1, s = idx(ts, r16);
-                const float ns = gates[kGateN + s], fs = gates[kGateF + s];
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int t0 = 32 * ks + 8 * g4 + 4 * hh;
-                    const f32x4 nt = *reinterpret_cast<const f32x4*>(gates + kGateN + t0);
-                    const f32x4 ft = *reinterpret_cast<const f32x4*>(gates + kGateF + t0);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        x[j][hh][q] = s <= t0 + q ? x[j][hh][q] * decay(nt[q], ft[q], ns, fs) : 0.f;
-                }
-                const PF<NO> mf = pf_acc<NO>(x[j][0], x[j][1]);
-                const int row = idx(ts & 1, r16);
-                char* dst = m + tri_block(ts >> 1, ks) + (row * 4 + (g4 ^ (row >> 3))) * 16;
-#pragma unroll
-                for (int o = 0; o < NO; ++o) *reinterpret_cast<bf16x8*>(dst + o * kTriBytes) = mf.p[o];
-                if (p.ckpt && w.sub == 0) {
-                    float* mt = p.ckpt + w.block(p, it) * p.ckpt_stride + (int64_t)p.V * (K + C) +
-                                (64 * tri_at<true>(ts, ks) + lane) * 8;
-                    *reinterpret_cast<f32x4*>(mt) = x[j][0];
-                    *reinterpret_cast<f32x4*>(mt + 4) = x[j][1];
-                }
-            }
-        }
-        lds_barrier();
-    }
-}
-
-// v -> o, hT and what the backward needs (ckpt).
-template <typename InT, int NX, int K, int NCW>
-__global__ __launch_bounds__(64 * (2 * NCW + 4)) void fwd_kernel(Args p, int nsub) {
-    using L = Plan<NX, K, NCW, false>;
-    constexpr int U = K / 8, KS = K / 32, KT = K / 16, NO = L::NO;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int g4 = lane >> 4, r16 = lane & 15;
-    const Where w(p, nsub);
-    if (wave >= 2 * NCW) {
-        if (wave < 2 * NCW + 2) memory_wave<NX, K, NCW, false>(p, w, smem, wave - 2 * NCW, lane);
-        else if (wave == 2 * NCW + 2) m_wave<NX, K, NCW, 0>(p, w, smem, lane);
-        else m_wave<NX, K, NCW, 1>(p, w, smem, lane);
-        return;
-    }
-    const int cw = wave % NCW, i = 16 * (w.sub * NCW + cw) + r16;     // this lane's state row
-    auto pass = [&](int it) { return smem + L::P0 + ((it & 1) * NCW + cw) * (L::ST + L::UT); };
-    const int64_t soff = (((int64_t)w.n * p.H + w.h) * p.V + i) * K + 8 * g4;
-
-    if (wave < NCW) {
-        // ---- state wave
-        f32x4 s[KT];                                      // s[2c + hh][q] = S[i][32c + 8g + 4hh + q]
-        load_state(s, p.h0, soff);
-        const InT* v = static_cast<const InT*>(p.v);
-        int off[16];
-        token_offsets<InT>(off, p, i, g4);
-        InT xn[16];
-        auto load_v = [&](int c) {
-            const Rsrc r = chunk_rsrc(v, p, w, c);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) xn[e] = bload(v, r, off[e]);
-        };
-        load_v(0);
-        lds_barrier();
-        for (int it = 0; it < w.nc; ++it) {
-            if constexpr (L::NBUF == 1) lds_barrier();
-            const char* buf = smem + (it % L::NBUF) * L::bytes;
-            const float* gates = reinterpret_cast<const float*>(buf + L::G);
-            f32x4 bt[4], eg[4], te[4], a[4], u[4];
-            PF<NX> kf[KS][4];
-            read_rows<U, NX, KS>(kf, buf + L::Kr, L::XB, lane);
-            read_gate(bt, gates + kGateBeta, g4);
-            read_gate(eg, gates + kGateEG, g4);
-            const float eGC = gates[kGateEG + C - 1];
-            fence();
-            // a = K S^T;  R = V - e^G a;  U = T (b R)
-            pass_put(pass(it), lane, s);
-            rows_times_state<NX, KS, KT>(a, kf, s);
-            PF<NP> tf[6];
-            read_tri<false>(tf, buf + L::T, lane);
-            read_gate(te, gates + kGateToEnd, g4);
-            fence();
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) a[t][q] = bt[t][q] * (widen(xn[4 * t + q]) - eg[t][q] * a[t][q]);
-            load_v(it + 1);
-            const PF<NP> rf[2] = {pf_acc<NP>(a[0], a[1]), pf_acc<NP>(a[2], a[3])};
-            fence();
-            tri_times<false>(u, tf, rf);
-            fence();
-            PF<NX> kc[2][KT];
-            read_cols<U, NX, KT>(kc, buf + L::Kr, L::XB, lane);
-            fence();
-            // S1^T = e^(G_C) S0^T + K^T (e^(G_C - G) U)
-#pragma unroll
-            for (int t = 0; t < KT; ++t) s[t] = eGC * s[t];
-            pass_put(pass(it) + L::ST, lane, u);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) u[t] = te[t] * u[t];
-            const PF<NP> ue[2] = {pf_acc<NP>(u[0], u[1]), pf_acc<NP>(u[2], u[3])};
-            fence();
-            add_cols_times<NX, KT>(s, kc, ue);
-            lds_barrier();
-        }
-        if (p.hT) store_state(p.hT, soff, s);
-        return;
-    }
-
-    // ---- helper wave: chunk it - 1 in iteration it
+// An output wave of the forward: tokens of tile TT.  In iteration it it finishes chunk it - 1,
+//     O = scale (e^G Q S0^T + M U),
+// and forms its rows of M = Lam Q K^T of chunk it, as operand fragments that stay in its
+// registers.  For the backward it stores its share of S and U, and its rows of M as
+// fragments of M^T, which takes the product a second time, the other way round.
+template <typename InT, int NX, int K, int NCW, int TT>
+__device__ __forceinline__ void output_wave(const Args& p, const Where& w, char* smem, int lane) {
+    using L = Plan<InT, NX, K, NCW, false>;
+    // o leaves in in_dtype: for bf16 two planes (2^-17) in its own products lose nothing
+    // beside its rounding; the products of the state keep all three
+    constexpr int NO = NX == 1 ? 2 : NP;
+    constexpr int U = K / 8, KS = K / 32, KT = K / 16, MS = TT / 2 + 1;   // 32-token steps of M's rows
+    const int g4 = lane >> 4, r16 = lane & 15, t = idx(TT, r16);
     InT* o = static_cast<InT*>(p.o);
-    int off[16];
-    token_offsets<InT>(off, p, i, g4);
-    PF<NX> qf[4][KS];
-    f32x4 eg[4];
+    const bool want = o || p.ckpt;
+    char* stage = smem + L::O0 + TT * 16 * L::RB;
+    PF<NX> qn[KS], qf[KS];
+    PF<NO> mf[MS];
+    f32x4 eg = zero4();
     auto load = [&](int c) {
-        if (c >= w.nc || !o) return;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) load_row<NX, KS>(qf[t], p.qp, p, w, c, idx(t, r16), g4);
-        read_gate(eg, p.tri + w.block(p, c) * p.tri_stride + kTriFloats + kGateEG, g4);
+        if (c < w.nc && want) load_row<NX, KS>(qn, p.qp, p, w, c, t, g4);
     };
     load(0);
     lds_barrier();
@@ -522,48 +392,169 @@ __global__ __launch_bounds__(64 * (2 * NCW + 4)) void fwd_kernel(Args p, int nsu
         if constexpr (L::NBUF == 1) {
             if (it < w.nc) lds_barrier();
         }
-        if (it > 0) {
+        if (it > 0 && want) {
             const int c = it - 1;
-            f32x4 s[KT], u[4];
-            pass_get(pass(c), lane, s);
-            pass_get(pass(c) + L::ST, lane, u);
-            if (p.ckpt) {
-                float* ck = p.ckpt + w.block(p, c) * p.ckpt_stride;
-                store_state(ck, (int64_t)i * K + 8 * g4, s);
-                store_tokens(ck + (int64_t)p.V * K, i, g4, u);
+            const char* pass = smem + L::P0 + (c & 1) * NCW * (L::ST + L::UT);
+            float* ck = p.ckpt ? p.ckpt + w.block(p, c) * p.ckpt_stride : nullptr;
+#pragma unroll
+            for (int cs = 0; cs < NCW; ++cs) {
+                const int i = 16 * (w.sub * NCW + cs) + r16;
+                const char* ps = pass + cs * (L::ST + L::UT);
+                f32x4 s[KT], u[4], b = zero4();
+                pass_get(ps, lane, s);
+                pass_get(ps + L::ST, lane, u);
+                if (ck) {
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+                        if ((cs * KS + ks) % 4 == TT) {
+                            float* d = ck + (int64_t)i * K + 8 * g4 + 32 * ks;
+                            *reinterpret_cast<f32x4*>(d) = s[2 * ks];
+                            *reinterpret_cast<f32x4*>(d + 4) = s[2 * ks + 1];
+                        }
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks)
+                        if ((cs * 2 + ks) % 4 == 3 - TT) {
+                            float* d = ck + (int64_t)p.V * K + (int64_t)i * C + 8 * g4 + 32 * ks;
+                            *reinterpret_cast<f32x4*>(d) = u[2 * ks];
+                            *reinterpret_cast<f32x4*>(d + 4) = u[2 * ks + 1];
+                        }
+                }
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) b = pmma<NO>(b, qf[ks], pf_acc<NO>(s[2 * ks], s[2 * ks + 1]));
+                b = eg * b;
+#pragma unroll
+                for (int ks = 0; ks < MS; ++ks) b = pmma<NO>(b, mf[ks], pf_acc<NO>(u[2 * ks], u[2 * ks + 1]));
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    st(reinterpret_cast<InT*>(stage + (4 * g4 + q) * L::RB) + 16 * cs + r16, p.scale * b[q]);
             }
             if (o) {
-                // O = scale (e^G Q S0^T + M U)
-                const char* m = smem + L::M0 + (c & 1) * L::MB;
-                PF<NO> mf[6];
+                constexpr int UPR = L::RB / 16, EPU = 16 / (int)sizeof(InT);
+                wkv7::wave_lds_sync();
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int ks = 0; ks <= (t >> 1); ++ks) mf[tri_at<false>(t, ks)] = tri_col<NO>(m, t, ks, lane);
-                f32x4 b[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) b[t] = zero4();
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const PF<NO> sf = pf_acc<NO>(s[2 * ks], s[2 * ks + 1]);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) b[t] = pmma<NO>(b[t], qf[t][ks], sf);
+                for (int j = 0; j < 16 * UPR / 64; ++j) {
+                    const int e = 64 * j + lane, tt = c * C + idx(TT, e / UPR);
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(stage + 16 * e);
+                    if (tt < w.len)
+                        *reinterpret_cast<f32x4*>(o + ((w.tok0 + tt) * p.H + w.h) * p.V + w.sub * NCW * 16 + (e % UPR) * EPU) = v;
                 }
-                const PF<NO> uf[2] = {pf_acc<NO>(u[0], u[1]), pf_acc<NO>(u[2], u[3])};
-#pragma unroll
-                for (int t = 0; t < 4; ++t) b[t] = eg[t] * b[t];
-                load(it);
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int ks = 0; ks <= (t >> 1); ++ks) b[t] = pmma<NO>(b[t], mf[tri_at<false>(t, ks)], uf[ks]);
-                const Rsrc r = chunk_rsrc(o, p, w, c);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) bput(o, r, off[e], p.scale * b[e >> 2][e & 3]);
             }
         }
-        if (it < w.nc) lds_barrier();
+        if (it < w.nc) {
+            if (want) {
+                const char* buf = smem + (it % L::NBUF) * L::bytes;
+                const float* gates = reinterpret_cast<const float*>(buf + L::G);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) qf[ks] = qn[ks];
+                load(it + 1);
+                eg = *reinterpret_cast<const f32x4*>(gates + kGateEG + idx(TT, 4 * g4));
+                const float nt = gates[kGateN + t], ft = gates[kGateF + t];
+#pragma unroll
+                for (int m = 0; m < MS; ++m) {
+                    f32x4 x[2] = {zero4(), zero4()};      // rows s of 32 m .. + 31, column t
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                        for (int k = 0; k < KS; ++k)
+                            x[hh] = pmma<NP>(x[hh], frag_row<U, NX>(buf + L::Kr, L::XB, idx(2 * m + hh, r16), k, lane), qf[k]);
+                        const int s0 = 32 * m + 8 * g4 + 4 * hh;
+                        const f32x4 ns = *reinterpret_cast<const f32x4*>(gates + kGateN + s0);
+                        const f32x4 fs = *reinterpret_cast<const f32x4*>(gates + kGateF + s0);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) x[hh][q] = s0 + q <= t ? x[hh][q] * decay(nt, ft, ns[q], fs[q]) : 0.f;
+                    }
+                    mf[m] = pf_acc<NO>(x[0], x[1]);
+                }
+                if (p.ckpt && w.sub == 0) {
+                    // piece (tile ts of s, 32 tokens): this wave's half of each lane's eight tokens
+                    float* mt = p.ckpt + w.block(p, it) * p.ckpt_stride + (int64_t)p.V * (K + C) + 4 * (TT & 1);
+                    const f32x4 nq = *reinterpret_cast<const f32x4*>(gates + kGateN + idx(TT, 4 * g4));
+                    const f32x4 fq = *reinterpret_cast<const f32x4*>(gates + kGateF + idx(TT, 4 * g4));
+#pragma unroll
+                    for (int ts = 0; ts < 2 * MS; ++ts) {
+                        f32x4 x = zero4();                // rows t, column s
+                        const int s = idx(ts, r16);
+#pragma unroll
+                        for (int k = 0; k < KS; ++k)
+                            x = pmma<NP>(x, qf[k], frag_row<U, NX>(buf + L::Kr, L::XB, s, k, lane));
+                        const float ns = gates[kGateN + s], fs = gates[kGateF + s];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) x[q] = s <= idx(TT, 4 * g4) + q ? x[q] * decay(nq[q], fq[q], ns, fs) : 0.f;
+                        *reinterpret_cast<f32x4*>(mt + (64 * tri_at<true>(ts, TT / 2) + lane) * 8) = x;
+                    }
+                }
+            }
+            lds_barrier();
+        }
     }
+}
+
+// v -> o, hT and what the backward needs (ckpt).
+template <typename InT, int NX, int K, int NCW>
+__global__ __launch_bounds__(64 * (NCW + 6)) void fwd_kernel(Args p, int nsub) {
+    using L = Plan<InT, NX, K, NCW, false>;
+    constexpr int U = K / 8, KS = K / 32, KT = K / 16;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g4 = lane >> 4, r16 = lane & 15;
+    const Where w(p, nsub);
+    // Waves are dealt to the four SIMDs in turn: with two state waves, those share theirs with the memory
+    // waves, and the heavier output waves (more rows of M) with the lighter ones.
+    switch (wave - NCW) {
+        case 0: output_wave<InT, NX, K, NCW, 3>(p, w, smem, lane); return;
+        case 1: output_wave<InT, NX, K, NCW, 2>(p, w, smem, lane); return;
+        case 2: memory_wave<InT, NX, K, NCW, false>(p, w, smem, 1, lane); return;
+        case 3: memory_wave<InT, NX, K, NCW, false>(p, w, smem, 0, lane); return;
+        case 4: output_wave<InT, NX, K, NCW, 0>(p, w, smem, lane); return;
+        case 5: output_wave<InT, NX, K, NCW, 1>(p, w, smem, lane); return;
+        default: break;
+    }
+    const int i = 16 * (w.sub * NCW + wave) + r16;        // this lane's state row
+    auto pass = [&](int it) { return smem + L::P0 + ((it & 1) * NCW + wave) * (L::ST + L::UT); };
+    const int64_t soff = (((int64_t)w.n * p.H + w.h) * p.V + i) * K + 8 * g4;
+    f32x4 s[KT];                                          // s[2c + hh][q] = S[i][32c + 8g + 4hh + q]
+    load_state(s, p.h0, soff);
+    lds_barrier();
+    for (int it = 0; it < w.nc; ++it) {
+        if constexpr (L::NBUF == 1) lds_barrier();
+        const char* buf = smem + (it % L::NBUF) * L::bytes;
+        const float* gates = reinterpret_cast<const float*>(buf + L::G);
+        f32x4 bt[4], eg[4], te[4], a[4], u[4], v[4];
+        PF<NX> kf[KS][4];
+        read_rows<U, NX, KS>(kf, buf + L::Kr, L::XB, lane);
+        read_gate(bt, gates + kGateBeta, g4);
+        read_gate(eg, gates + kGateEG, g4);
+        const float eGC = gates[kGateEG + C - 1];
+        fence();
+        // a = K S^T;  R = V - e^G a;  U = T (b R)
+        pass_put(pass(it), lane, s);
+        rows_times_state<NX, KS, KT>(a, kf, s);
+        PF<NP> tf[6];
+        column_tiles<L::RB>(v, buf + L::V, wave, lane, InT());
+        read_tri<false>(tf, buf + L::T, lane);
+        read_gate(te, gates + kGateToEnd, g4);
+        fence();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) a[t] = bt[t] * (v[t] - eg[t] * a[t]);
+        const PF<NP> rf[2] = {pf_acc<NP>(a[0], a[1]), pf_acc<NP>(a[2], a[3])};
+        fence();
+        tri_times<false>(u, tf, rf);
+        fence();
+        PF<NX> kc[2][KT];
+        read_cols<U, NX, KT>(kc, buf + L::Kr, L::XB, lane);
+        fence();
+        // S1^T = e^(G_C) S0^T + K^T (e^(G_C - G) U)
+#pragma unroll
+        for (int t = 0; t < KT; ++t) s[t] = eGC * s[t];
+        pass_put(pass(it) + L::ST, lane, u);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) u[t] = te[t] * u[t];
+        const PF<NP> ue[2] = {pf_acc<NP>(u[0], u[1]), pf_acc<NP>(u[2], u[3])};
+        fence();
+        add_cols_times<NX, KT>(s, kc, ue);
+        lds_barrier();
+    }
+    if (p.hT) store_state(p.hT, soff, s);
 }
 
 // dout -> dv, the state gradients at the chunks' ends (dend), Z, dh0.
@@ -572,22 +563,20 @@ __global__ __launch_bounds__(64 * (2 * NCW + 4)) void fwd_kernel(Args p, int nsu
 //   G0 = e^(G_C) G1 + scale DO^T e^G Q - (b Z)^T e^G K
 template <typename InT, int NX, int K, int NCW>
 __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsub) {
-    using L = Plan<NX, K, NCW, true>;
+    using L = Plan<InT, NX, K, NCW, true>;
     constexpr int U = K / 8, KS = K / 32, KT = K / 16;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g4 = lane >> 4, r16 = lane & 15;
     const Where w(p, nsub);
     if (wave >= 2 * NCW) {
-        memory_wave<NX, K, NCW, true>(p, w, smem, wave - 2 * NCW, lane);
+        memory_wave<InT, NX, K, NCW, true>(p, w, smem, wave - 2 * NCW, lane);
         return;
     }
     const int cw = wave % NCW, i = 16 * (w.sub * NCW + cw) + r16;
     auto chunk_of = [&](int it) { return w.nc - 1 - it; };
     auto pass = [&](int it) { return smem + L::P0 + ((it & 1) * NCW + cw) * (L::ST + L::UT); };
     const int64_t soff = (((int64_t)w.n * p.H + w.h) * p.V + i) * K + 8 * g4;
-    int off[16];
-    token_offsets<InT>(off, p, i, g4);
 
     if (wave < NCW) {
         // ---- state wave
@@ -627,13 +616,24 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
             f32x4 g[KT];
             pass_get(pass(it), lane, g);
             store_tokens(p.z + block * (int64_t)C * p.V, i, g4, z);
-            const Rsrc r = chunk_rsrc(dv, p, w, c);
+            // dv: through the tiles just read, whose next writer comes after the barrier, to 16-byte pieces
+            char* stage = pass(it) + L::ST;
+            constexpr int SB = 16 * (int)sizeof(InT);     // a token's 16 columns
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 z[t] = bt[t] * z[t];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) bput(dv, r, off[4 * t + q], z[t][q]);
+                for (int q = 0; q < 4; ++q) st(reinterpret_cast<InT*>(stage + idx(t, 4 * g4 + q) * SB) + r16, z[t][q]);
                 z[t] = -eg[t] * z[t];
+            }
+            wkv7::wave_lds_sync();
+#pragma unroll
+            for (int j = 0; j < C * SB / 1024; ++j) {
+                const int e = 64 * j + lane, tt = c * C + e / (SB / 16);
+                const f32x4 v = *reinterpret_cast<const f32x4*>(stage + 16 * e);
+                if (tt < w.len)
+                    *reinterpret_cast<f32x4*>(dv + ((w.tok0 + tt) * p.H + w.h) * p.V + 16 * (w.sub * NCW + cw) +
+                                              (e % (SB / 16)) * (16 / (int)sizeof(InT))) = v;
             }
             const PF<NP> zf[2] = {pf_acc<NP>(z[0], z[1]), pf_acc<NP>(z[2], z[3])};
 #pragma unroll
@@ -647,15 +647,10 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
     }
 
     // ---- helper wave: chunk it + 1 in iteration it
-    const InT* dout = static_cast<const InT*>(p.dout);
-    InT xn[16];
     f32x4 mt[6][2];                                       // M^T: tiles 0, 1 (steps 0, 1), 2, 3 (step 1)
     f32x4 eg[4];
     auto load = [&](int it) {
         const int c = chunk_of(it);
-        const Rsrc r = chunk_rsrc(dout, p, w, c);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) xn[e] = bload(dout, r, off[e]);
         if (c < 0) return;
         const float* m = p.ckpt + w.block(p, c) * p.ckpt_stride + (int64_t)p.V * (K + C);
         read_gate(eg, m + 2 * kTriFloats + kGateEG, g4);
@@ -667,17 +662,17 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
     };
     auto work = [&](int it) {
         const char* q = smem + L::Q0 + (it % L::NQ) * L::QB;
-        f32x4 x[4], d[4];
+        const int c = chunk_of(it);
+        f32x4 x[4], y[4], d[4];
+        column_tiles<L::RB>(y, q + NX * L::XB, cw, lane, InT());
+        if (w.len - c * C < C) {                          // tokens past the end repeat the last one there
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][e] = p.scale * widen(xn[4 * t + e]);
+                for (int e = 0; e < 4; ++e)
+                    if (c * C + idx(t, 4 * g4 + e) >= w.len) y[t][e] = 0.f;
+        }
         // scale M^T DO: DO is exact in one plane for bf16 inputs, the scale is applied after
-        f32x4 y[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[t][e] = widen(xn[4 * t + e]);
         const PF<NX> df[2] = {pf_acc<NX>(y[0], y[1]), pf_acc<NX>(y[2], y[3])};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -688,7 +683,7 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
                 d[t] = pmma<NP>(d[t], pf_acc<NP>(m[0], m[1]), df[ks]);
             }
             d[t] = p.scale * d[t];
-            x[t] = eg[t] * x[t];
+            x[t] = p.scale * eg[t] * y[t];
         }
         load(it + 1);
         pass_put(pass(it) + L::ST, lane, d);
@@ -716,7 +711,7 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
 
 template <typename InT, int NX, int K, int NCW, bool BWD>
 hipError_t launch_typed(const Args& a, hipStream_t s) {
-    constexpr int lds = Plan<NX, K, NCW, BWD>::total;
+    constexpr int lds = Plan<InT, NX, K, NCW, BWD>::total;
     auto kern = [] {
         if constexpr (BWD) return bwd_kernel<InT, NX, K, NCW>;
         else return fwd_kernel<InT, NX, K, NCW>;
@@ -725,7 +720,7 @@ hipError_t launch_typed(const Args& a, hipStream_t s) {
     const hipError_t e = wkv7::set_smem_once(once, kern, lds);
     if (e != hipSuccess) return e;
     const int nsub = a.V / (16 * NCW);
-    hipLaunchKernelGGL(kern, dim3((uint32_t)a.N * a.H * nsub), dim3(64 * (2 * NCW + (BWD ? 2 : 4))), lds, s, a, nsub);
+    hipLaunchKernelGGL(kern, dim3((uint32_t)a.N * a.H * nsub), dim3(64 * (BWD ? 2 * NCW + 2 : NCW + 6)), lds, s, a, nsub);
     return hipGetLastError();
 }
 
