@@ -191,9 +191,10 @@ __device__ __forceinline__ float exp_d(double x) {
     const double n = __builtin_rint(y);
     return __builtin_ldexpf(__builtin_amdgcn_exp2f((float)(y - n)), (int)n);
 }
-// e^(G_t - G_s) from two tokens' whole and remaining parts
+// e^(G_t - G_s) from two tokens' whole and remaining parts.  The parts' differences are
+// exact to 2^-25; their sum y is rounded by 2^-24 |y|, which 2^y has where it is small.
 __device__ __forceinline__ float decay(float nt, float ft, float ns, float fs) {
-    return __builtin_ldexpf(__builtin_amdgcn_exp2f(ft - fs), (int)(nt - ns));
+    return __builtin_amdgcn_exp2f((nt - ns) + (ft - fs));
 }
 
 // Where the sequences lie.  Dense: sequence n is row n of (B, T), its chunks

@@ -300,12 +300,20 @@ __device__ __forceinline__ void read_tri(PF<NP> (&f)[6], const char* X, int lane
             }
 }
 
-// a[t] = X S^T over all K columns, S split on the way
+// a[t] = X S^T over all K columns, S split on the way; its leading two planes go to `pass` if given
 template <int NX, int KS, int KT>
-__device__ __forceinline__ void rows_times_state(f32x4 (&a)[4], const PF<NX> (&f)[KS][4], const f32x4 (&s)[KT]) {
+__device__ __forceinline__ void rows_times_state(f32x4 (&a)[4], const PF<NX> (&f)[KS][4], const f32x4 (&s)[KT],
+                                                 char* pass = nullptr) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) a[t] = zero4();
     PF<NP> sf = pf_acc<NP>(s[0], s[1]);
+    auto hand = [&](int ks) {
+        if (pass) {
+            *reinterpret_cast<bf16x8*>(pass + 2048 * ks) = sf.p[0];
+            *reinterpret_cast<bf16x8*>(pass + 2048 * ks + 1024) = sf.p[1];
+        }
+    };
+    hand(0);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         fence();
@@ -319,6 +327,8 @@ __device__ __forceinline__ void rows_times_state(f32x4 (&a)[4], const PF<NX> (&f
         if (ks + 1 < KS) {
             sf = pf_acc<NP>(s[2 * ks + 2], s[2 * ks + 3]);
             interleave<4 * (NX == 1 ? 3 : 6), 4>();
+            fence();
+            hand(ks + 1);
         }
     }
     fence();
@@ -367,7 +377,7 @@ __device__ __forceinline__ void load_row(PF<NX> (&f)[KS], const Planes& x, const
 // An output wave of the forward: tokens of tile TT.  In iteration it it finishes chunk it - 1,
 //     O = scale (e^G Q S0^T + M U),
 // and forms its rows of M = Lam Q K^T of chunk it, as operand fragments that stay in its
-// registers.  For the backward it stores its share of S and U, and its rows of M as
+// registers.  For the backward it stores its share of U, and its rows of M as
 // fragments of M^T, which takes the product a second time, the other way round.
 template <typename InT, int NX, int K, int NCW, int TT>
 __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char* smem, int lane) {
@@ -395,38 +405,59 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
         if (it > 0 && want) {
             const int c = it - 1;
             const char* pass = smem + L::P0 + (c & 1) * NCW * (L::ST + L::UT);
-            float* ck = p.ckpt ? p.ckpt + w.block(p, c) * p.ckpt_stride : nullptr;
+            // S arrives as its leading two planes for bf16 inputs, as fp32 tiles otherwise
+            f32x4 s[NCW][NX == 1 ? 1 : KT], u[NCW][4];
+            PF<NO> sf[NCW][KS];
 #pragma unroll
             for (int cs = 0; cs < NCW; ++cs) {
-                const int i = 16 * (w.sub * NCW + cs) + r16;
                 const char* ps = pass + cs * (L::ST + L::UT);
-                f32x4 s[KT], u[4], b = zero4();
-                pass_get(ps, lane, s);
-                pass_get(ps + L::ST, lane, u);
-                if (ck) {
+                if constexpr (NX == 1) {
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
-                        if ((cs * KS + ks) % 4 == TT) {
+#pragma unroll
+                        for (int j = 0; j < NO; ++j)
+                            sf[cs][ks].p[j] = *reinterpret_cast<const bf16x8*>(ps + 2048 * ks + 1024 * j + 16 * lane);
+                } else {
+                    pass_get(ps, lane, s[cs]);
+                }
+                pass_get(ps + L::ST, lane, u[cs]);
+            }
+            fence();
+#pragma unroll
+            for (int cs = 0; cs < NCW; ++cs) {
+                f32x4 b = zero4();
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    if constexpr (NX > 1) sf[cs][ks] = pf_acc<NO>(s[cs][2 * ks], s[cs][2 * ks + 1]);
+                    b = pmma<NO>(b, qf[ks], sf[cs][ks]);
+                }
+                b = eg * b;
+#pragma unroll
+                for (int ks = 0; ks < MS; ++ks) b = pmma<NO>(b, mf[ks], pf_acc<NO>(u[cs][2 * ks], u[cs][2 * ks + 1]));
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    st(reinterpret_cast<InT*>(stage + (4 * g4 + q) * L::RB) + 16 * cs + r16, p.scale * b[q]);
+            }
+            if (p.ckpt) {
+                float* ck = p.ckpt + w.block(p, c) * p.ckpt_stride;
+#pragma unroll
+                for (int cs = 0; cs < NCW; ++cs) {
+                    const int i = 16 * (w.sub * NCW + cs) + r16;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+                        if (NX > 1 && (cs * KS + ks) % 4 == TT) {
                             float* d = ck + (int64_t)i * K + 8 * g4 + 32 * ks;
-                            *reinterpret_cast<f32x4*>(d) = s[2 * ks];
-                            *reinterpret_cast<f32x4*>(d + 4) = s[2 * ks + 1];
+                            *reinterpret_cast<f32x4*>(d) = s[cs][NX > 1 ? 2 * ks : 0];
+                            *reinterpret_cast<f32x4*>(d + 4) = s[cs][NX > 1 ? 2 * ks + 1 : 0];
                         }
 #pragma unroll
                     for (int ks = 0; ks < 2; ++ks)
                         if ((cs * 2 + ks) % 4 == 3 - TT) {
                             float* d = ck + (int64_t)p.V * K + (int64_t)i * C + 8 * g4 + 32 * ks;
-                            *reinterpret_cast<f32x4*>(d) = u[2 * ks];
-                            *reinterpret_cast<f32x4*>(d + 4) = u[2 * ks + 1];
+                            *reinterpret_cast<f32x4*>(d) = u[cs][2 * ks];
+                            *reinterpret_cast<f32x4*>(d + 4) = u[cs][2 * ks + 1];
                         }
                 }
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) b = pmma<NO>(b, qf[ks], pf_acc<NO>(s[2 * ks], s[2 * ks + 1]));
-                b = eg * b;
-#pragma unroll
-                for (int ks = 0; ks < MS; ++ks) b = pmma<NO>(b, mf[ks], pf_acc<NO>(u[2 * ks], u[2 * ks + 1]));
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    st(reinterpret_cast<InT*>(stage + (4 * g4 + q) * L::RB) + 16 * cs + r16, p.scale * b[q]);
             }
             if (o) {
                 constexpr int UPR = L::RB / 16, EPU = 16 / (int)sizeof(InT);
@@ -449,22 +480,33 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
                 load(it + 1);
                 eg = *reinterpret_cast<const f32x4*>(gates + kGateEG + idx(TT, 4 * g4));
                 const float nt = gates[kGateN + t], ft = gates[kGateF + t];
+                PF<NX> kf[2 * MS][KS];
+                for (int k = 0; k < KS; ++k) {
 #pragma unroll
-                for (int m = 0; m < MS; ++m) {
-                    f32x4 x[2] = {zero4(), zero4()};      // rows s of 32 m .. + 31, column t
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-                        for (int k = 0; k < KS; ++k)
-                            x[hh] = pmma<NP>(x[hh], frag_row<U, NX>(buf + L::Kr, L::XB, idx(2 * m + hh, r16), k, lane), qf[k]);
-                        const int s0 = 32 * m + 8 * g4 + 4 * hh;
-                        const f32x4 ns = *reinterpret_cast<const f32x4*>(gates + kGateN + s0);
-                        const f32x4 fs = *reinterpret_cast<const f32x4*>(gates + kGateF + s0);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) x[hh][q] = s0 + q <= t ? x[hh][q] * decay(nt, ft, ns[q], fs[q]) : 0.f;
-                    }
-                    mf[m] = pf_acc<NO>(x[0], x[1]);
+                    for (int ts = 0; ts < 2 * MS; ++ts)
+                        kf[ts][k] = frag_row<U, NX>(buf + L::Kr, L::XB, idx(ts, r16), k, lane);
                 }
+                fence();
+                f32x4 x[2 * MS];                          // rows s of tile ts, column t
+#pragma unroll
+                for (int ts = 0; ts < 2 * MS; ++ts) {
+                    x[ts] = zero4();
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) x[ts] = pmma<NP>(x[ts], kf[ts][k], qf[k]);
+                }
+#pragma unroll
+                for (int ts = 0; ts < 2 * MS; ++ts) {
+                    const int s0 = 32 * (ts >> 1) + 8 * g4 + 4 * (ts & 1);
+                    const f32x4 ns = *reinterpret_cast<const f32x4*>(gates + kGateN + s0);
+                    const f32x4 fs = *reinterpret_cast<const f32x4*>(gates + kGateF + s0);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        x[ts][q] *= decay(nt, ft, ns[q], fs[q]);
+                        if (ts / 2 == TT / 2 && s0 + q > t) x[ts][q] = 0.f;   // other tiles lie below the diagonal
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < MS; ++m) mf[m] = pf_acc<NO>(x[2 * m], x[2 * m + 1]);
                 if (p.ckpt && w.sub == 0) {
                     // piece (tile ts of s, 32 tokens): this wave's half of each lane's eight tokens
                     float* mt = p.ckpt + w.block(p, it) * p.ckpt_stride + (int64_t)p.V * (K + C) + 4 * (TT & 1);
@@ -472,15 +514,17 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
                     const f32x4 fq = *reinterpret_cast<const f32x4*>(gates + kGateF + idx(TT, 4 * g4));
 #pragma unroll
                     for (int ts = 0; ts < 2 * MS; ++ts) {
-                        f32x4 x = zero4();                // rows t, column s
+                        f32x4 y = zero4();                // rows t, column s
                         const int s = idx(ts, r16);
 #pragma unroll
-                        for (int k = 0; k < KS; ++k)
-                            x = pmma<NP>(x, qf[k], frag_row<U, NX>(buf + L::Kr, L::XB, s, k, lane));
+                        for (int k = 0; k < KS; ++k) y = pmma<NP>(y, qf[k], kf[ts][k]);
                         const float ns = gates[kGateN + s], fs = gates[kGateF + s];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) x[q] = s <= idx(TT, 4 * g4) + q ? x[q] * decay(nq[q], fq[q], ns, fs) : 0.f;
-                        *reinterpret_cast<f32x4*>(mt + (64 * tri_at<true>(ts, TT / 2) + lane) * 8) = x;
+                        for (int q = 0; q < 4; ++q) {
+                            y[q] *= decay(nq[q], fq[q], ns, fs);
+                            if (ts / 2 == TT / 2 && s > idx(TT, 4 * g4) + q) y[q] = 0.f;
+                        }
+                        *reinterpret_cast<f32x4*>(mt + (64 * tri_at<true>(ts, TT / 2) + lane) * 8) = y;
                     }
                 }
             }
@@ -514,6 +558,7 @@ __global__ __launch_bounds__(64 * (NCW + 6)) void fwd_kernel(Args p, int nsub) {
     const int64_t soff = (((int64_t)w.n * p.H + w.h) * p.V + i) * K + 8 * g4;
     f32x4 s[KT];                                          // s[2c + hh][q] = S[i][32c + 8g + 4hh + q]
     load_state(s, p.h0, soff);
+    __builtin_amdgcn_s_setprio(3);                        // the chain goes first on its SIMD
     lds_barrier();
     for (int it = 0; it < w.nc; ++it) {
         if constexpr (L::NBUF == 1) lds_barrier();
@@ -527,8 +572,13 @@ __global__ __launch_bounds__(64 * (NCW + 6)) void fwd_kernel(Args p, int nsub) {
         const float eGC = gates[kGateEG + C - 1];
         fence();
         // a = K S^T;  R = V - e^G a;  U = T (b R)
-        pass_put(pass(it), lane, s);
-        rows_times_state<NX, KS, KT>(a, kf, s);
+        if constexpr (NX == 1) {
+            if (p.ckpt) store_state(p.ckpt + w.block(p, it) * p.ckpt_stride, (int64_t)i * K + 8 * g4, s);
+            rows_times_state<NX, KS, KT>(a, kf, s, pass(it) + 16 * lane);
+        } else {
+            pass_put(pass(it), lane, s);
+            rows_times_state<NX, KS, KT>(a, kf, s);
+        }
         PF<NP> tf[6];
         column_tiles<L::RB>(v, buf + L::V, wave, lane, InT());
         read_tri<false>(tf, buf + L::T, lane);
@@ -582,6 +632,7 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
         // ---- state wave
         f32x4 s[KT];
         load_state(s, p.dhT, soff);
+        __builtin_amdgcn_s_setprio(3);                    // the chain goes first on its SIMD
         InT* dv = static_cast<InT*>(p.dv);
         lds_barrier();
         lds_barrier();
@@ -685,6 +736,8 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
             d[t] = p.scale * d[t];
             x[t] = p.scale * eg[t] * y[t];
         }
+        PF<NX> qc[2][KT];
+        read_cols<U, NX, KT>(qc, q, L::XB, lane);
         load(it + 1);
         pass_put(pass(it) + L::ST, lane, d);
         // Q^T (scale e^G DO)
@@ -694,7 +747,7 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
         for (int t = 0; t < KT; ++t) {
             g[t] = zero4();
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) g[t] = pmma<NP>(g[t], frag_col<U, NX>(q, L::XB, t, ks, lane), xf[ks]);
+            for (int ks = 0; ks < 2; ++ks) g[t] = pmma<NP>(g[t], qc[ks][t], xf[ks]);
         }
         pass_put(pass(it), lane, g);
     };
