@@ -45,26 +45,26 @@ __device__ __forceinline__ PF<NX> frag_mem(const Planes& x, int64_t row, int str
     return f;
 }
 
-// T = (I + A)^-1 for the strictly lower 64 x 64 matrix A.
-// Diagonal 16 x 16 blocks by forward substitution (one wave each, one column
-// per lane), then [[X, 0], [Z, Y]]^-1 = [[X', 0], [-Y' Z X', Y']] for blocks of
+// T = (I + A)^-1 for the strictly lower 64 x 64 matrix A, held transposed (At[s][t] =
+// A[t][s]).  Diagonal 16 x 16 blocks by forward substitution (one wave each, one
+// column per lane), then [[X, 0], [Z, Y]]^-1 = [[X', 0], [-Y' Z X', Y']] for blocks of
 // 16 and of 32 with fp32 MFMA products: stable for any A, unlike a series in
-// powers of A.
+// powers of A.  Z (16 x 16) = sign X Y over kn; XT: X is given transposed.
+template <bool XT>
 __device__ __forceinline__ void block_product(const float* X, const float* Y, float* Z, int kn, float sign, int lane) {
-    // Z (16 x 16) = sign * X (16 x kn) Y (kn x 16), all with row stride LDA
     const int r = lane & 15, g = lane >> 4;
     f32x4 acc = zero4();
-    for (int k0 = 0; k0 < kn; k0 += 4) acc = wkv7::mfma_f32(X[r * LDA + k0 + g], Y[(k0 + g) * LDA + r], acc);
+    for (int k0 = 0; k0 < kn; k0 += 4)
+        acc = wkv7::mfma_f32(XT ? X[(k0 + g) * LDA + r] : X[r * LDA + k0 + g], Y[(k0 + g) * LDA + r], acc);
 #pragma unroll
     for (int q = 0; q < 4; ++q) Z[(4 * g + q) * LDA + r] = sign * acc[q];
 }
 
 template <int NX, int K>
-__global__ __launch_bounds__(256) void prepare_kernel(Args p) {
-    __shared__ __attribute__((aligned(16))) float As[C * LDA];
+__global__ __launch_bounds__(256, 4) void prepare_kernel(Args p) {
+    __shared__ __attribute__((aligned(16))) float At[C * LDA];
     __shared__ __attribute__((aligned(16))) float Ts[C * LDA];
-    __shared__ double Gs[C];
-    __shared__ float bs[C];
+    __shared__ float nf[2][C], bs[C];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int g4 = lane >> 4, r16 = lane & 15;
     const int slot = blockIdx.x / p.H, h = blockIdx.x % p.H;
@@ -75,7 +75,18 @@ __global__ __launch_bounds__(256) void prepare_kernel(Args p) {
     const int hk = h / (p.H / p.Hk);
     const int64_t block = (int64_t)slot * p.H + h;
 
-    if (w == 0) {
+    // row tile w of K K^T (lower 32 x 32 blocks), rows straight from memory
+    constexpr int KS = K / 32;
+    const int stride = p.Hk * K;
+    Planes kp = p.kp;
+    kp.p += tok * stride + hk * K;
+    auto row = [&](int t) { return min(t, len - 1); };   // tokens past the end: masked below
+    PF<NX> ka[KS];
+    const int ra = row(idx(w, r16));
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) ka[ks] = frag_mem<NX>(kp, ra, stride, ks, lane);
+
+    if (w == 3) {
         float g = 0.f, b = 0.f;
         if (lane < len) {
             g = p.g[(tok + lane) * p.H + h];
@@ -90,39 +101,42 @@ __global__ __launch_bounds__(256) void prepare_kernel(Args p) {
             if (lane >= d) G += o;
         }
         const double Gc = __shfl(G, 63);
-        Gs[lane] = G;
+        const double y = G * 1.4426950408889634074, n2 = __builtin_rint(y);
+        nf[0][lane] = (float)n2;
+        nf[1][lane] = (float)(y - n2);
         bs[lane] = b;
         float* gt = p.tri + block * p.tri_stride + kTriFloats;
         gt[kGateEG + lane] = exp_d(G);
         gt[kGateToEnd + lane] = lane < len ? exp_d(Gc - G) : 0.f;
         gt[kGateBeta + lane] = b;
-        const double y = G * 1.4426950408889634074, n2 = __builtin_rint(y);
         gt[kGateN + lane] = (float)n2;
         gt[kGateF + lane] = (float)(y - n2);
+    } else if (w < 2) {
+        // the zero 16 x 16 blocks of T's diagonal 32 x 32 blocks
+        *reinterpret_cast<f32x4*>(Ts + (32 * w + (lane >> 2)) * LDA + 32 * w + 16 + 4 * (lane & 3)) = zero4();
     }
-    for (int e = tid; e < C * LDA; e += 256) Ts[e] = 0.f;
-
-    // row tile w of K K^T (lower 32 x 32 blocks)
-    constexpr int KS = K / 32;
-    const int stride = p.Hk * K;
-    Planes kp = p.kp;
-    kp.p += tok * stride + hk * K;
-    auto row = [&](int t) { return min(t, len - 1); };   // tokens past the end: masked below
-    PF<NX> ka[KS];
-    const int ra = row(idx(w, r16));
+    f32x4 kk[4];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) ka[ks] = frag_mem<NX>(kp, ra, stride, ks, lane);
+    for (int nt = 0; nt < 4; ++nt) {
+        kk[nt] = zero4();
+        if (nt >= 2 && w < 2) continue;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            kk[nt] = pmma<NX>(kk[nt], ka[ks], frag_mem<NX>(kp, row(idx(nt, r16)), stride, ks, lane));
+    }
     __syncthreads();
-    for (int nt = 0; nt < (w < 2 ? 2 : 4); ++nt) {
-        f32x4 kk = zero4();
+    const int t0 = idx(w, 4 * g4);
+    const f32x4 nt4 = *reinterpret_cast<const f32x4*>(&nf[0][t0]), ft4 = *reinterpret_cast<const f32x4*>(&nf[1][t0]);
+    const f32x4 b4 = *reinterpret_cast<const f32x4*>(&bs[t0]);
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+        if (nt >= 2 && w < 2) continue;
         const int s = idx(nt, r16);
+        f32x4 a;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) kk = pmma<NX>(kk, ka[ks], frag_mem<NX>(kp, row(s), stride, ks, lane));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int t = idx(w, 4 * g4 + q);
-            As[t * LDA + s] = s < t && t < len ? bs[t] * exp_d(Gs[t] - Gs[s]) * kk[q] : 0.f;
-        }
+        for (int q = 0; q < 4; ++q)
+            a[q] = s < t0 + q && t0 + q < len ? b4[q] * decay(nt4[q], ft4[q], nf[0][s], nf[1][s]) * kk[nt][q] : 0.f;
+        *reinterpret_cast<f32x4*>(At + s * LDA + t0) = a;
     }
     __syncthreads();
 
@@ -131,28 +145,41 @@ __global__ __launch_bounds__(256) void prepare_kernel(Args p) {
         float x[16];
 #pragma unroll
         for (int t = 0; t < 16; ++t) x[t] = t == lane ? 1.f : 0.f;
+        // once x[s] is final every later row takes A[t][s] x[s]; column s of A is read in
+        // 16-byte pieces, five columns ahead of their use
 #pragma unroll
-        for (int s = 0; s < 15; ++s)
+        for (int s0 = 0; s0 < 15; s0 += 5) {
+            f32x4 col[5][4];
 #pragma unroll
-            for (int t = s + 1; t < 16; ++t) x[t] = fmaf(-As[(o + t) * LDA + o + s], x[s], x[t]);
+            for (int s = s0; s < s0 + 5; ++s)
+#pragma unroll
+                for (int c = (s + 1) / 4; c < 4; ++c)
+                    col[s - s0][c] = *reinterpret_cast<const f32x4*>(At + (o + s) * LDA + o + 4 * c);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = s0; s < s0 + 5; ++s)
+#pragma unroll
+                for (int t = s + 1; t < 16; ++t) x[t] = fmaf(-col[s - s0][t / 4][t % 4], x[s], x[t]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int t = 0; t < 16; ++t) Ts[(o + t) * LDA + o + lane] = x[t];
     }
     __syncthreads();
-    // blocks of 16: the scratch products lie in the unused upper part of As
+    // blocks of 16: the scratch products lie in At's part for t < s, which is unused
     if (w < 2) {
         const int o = 32 * w;
-        float* scr = As + o * LDA + o + 16;
-        block_product(As + (o + 16) * LDA + o, Ts + o * LDA + o, scr, 16, 1.f, lane);
+        float* scr = At + (o + 16) * LDA + o;
+        block_product<true>(At + o * LDA + o + 16, Ts + o * LDA + o, scr, 16, 1.f, lane);
         wkv7::wave_lds_sync();
-        block_product(Ts + (o + 16) * LDA + o + 16, scr, Ts + (o + 16) * LDA + o, 16, -1.f, lane);
+        block_product<false>(Ts + (o + 16) * LDA + o + 16, scr, Ts + (o + 16) * LDA + o, 16, -1.f, lane);
     }
     __syncthreads();
-    // blocks of 32
+    // blocks of 32: wave (mr, mc) forms one 16 x 16 tile of each product
     const int mr = 16 * (w >> 1), mc = 16 * (w & 1);
-    block_product(As + (32 + mr) * LDA, Ts + mc, As + mr * LDA + 32 + mc, 32, 1.f, lane);
+    block_product<true>(At + 32 + mr, Ts + mc, At + (32 + mr) * LDA + mc, 32, 1.f, lane);
     __syncthreads();
-    block_product(Ts + (32 + mr) * LDA + 32, As + 32 + mc, Ts + (32 + mr) * LDA + mc, 32, -1.f, lane);
+    block_product<false>(Ts + (32 + mr) * LDA + 32, At + 32 * LDA + mc, Ts + (32 + mr) * LDA + mc, 32, -1.f, lane);
     __syncthreads();
 
     // the three lower 32 x 32 blocks, in pieces of eight values: block, row, eight columns

@@ -405,58 +405,62 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
         if (it > 0 && want) {
             const int c = it - 1;
             const char* pass = smem + L::P0 + (c & 1) * NCW * (L::ST + L::UT);
-            // S arrives as its leading two planes for bf16 inputs, as fp32 tiles otherwise
-            f32x4 s[NCW][NX == 1 ? 1 : KT], u[NCW][4];
-            PF<NO> sf[NCW][KS];
+            float* ck = p.ckpt ? p.ckpt + w.block(p, c) * p.ckpt_stride : nullptr;
+            constexpr int TWO = NCW < 2 ? 1 : 2;          // slices at a time
 #pragma unroll
-            for (int cs = 0; cs < NCW; ++cs) {
-                const char* ps = pass + cs * (L::ST + L::UT);
-                if constexpr (NX == 1) {
+            for (int c0 = 0; c0 < NCW; c0 += TWO) {
+                // S arrives as its leading two planes for bf16 inputs, as fp32 tiles otherwise
+                f32x4 s[TWO][NX == 1 ? 1 : KT], u[TWO][4];
+                PF<NO> sf[TWO][KS];
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
+                for (int cs = 0; cs < TWO; ++cs) {
+                    const char* ps = pass + (c0 + cs) * (L::ST + L::UT);
+                    if constexpr (NX == 1) {
 #pragma unroll
-                        for (int j = 0; j < NO; ++j)
-                            sf[cs][ks].p[j] = *reinterpret_cast<const bf16x8*>(ps + 2048 * ks + 1024 * j + 16 * lane);
-                } else {
-                    pass_get(ps, lane, s[cs]);
+                        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                            for (int j = 0; j < NO; ++j)
+                                sf[cs][ks].p[j] = *reinterpret_cast<const bf16x8*>(ps + 2048 * ks + 1024 * j + 16 * lane);
+                    } else {
+                        pass_get(ps, lane, s[cs]);
+                    }
+                    pass_get(ps + L::ST, lane, u[cs]);
                 }
-                pass_get(ps + L::ST, lane, u[cs]);
-            }
-            fence();
+                fence();
 #pragma unroll
-            for (int cs = 0; cs < NCW; ++cs) {
-                f32x4 b = zero4();
+                for (int cs = 0; cs < TWO; ++cs) {
+                    f32x4 b = zero4();
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    if constexpr (NX > 1) sf[cs][ks] = pf_acc<NO>(s[cs][2 * ks], s[cs][2 * ks + 1]);
-                    b = pmma<NO>(b, qf[ks], sf[cs][ks]);
+                    for (int ks = 0; ks < KS; ++ks) {
+                        if constexpr (NX > 1) sf[cs][ks] = pf_acc<NO>(s[cs][2 * ks], s[cs][2 * ks + 1]);
+                        b = pmma<NO>(b, qf[ks], sf[cs][ks]);
+                    }
+                    b = eg * b;
+#pragma unroll
+                    for (int ks = 0; ks < MS; ++ks) b = pmma<NO>(b, mf[ks], pf_acc<NO>(u[cs][2 * ks], u[cs][2 * ks + 1]));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        st(reinterpret_cast<InT*>(stage + (4 * g4 + q) * L::RB) + 16 * (c0 + cs) + r16, p.scale * b[q]);
                 }
-                b = eg * b;
+                if (ck) {
 #pragma unroll
-                for (int ks = 0; ks < MS; ++ks) b = pmma<NO>(b, mf[ks], pf_acc<NO>(u[cs][2 * ks], u[cs][2 * ks + 1]));
+                    for (int cs = 0; cs < TWO; ++cs) {
+                        const int i = 16 * (w.sub * NCW + c0 + cs) + r16;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    st(reinterpret_cast<InT*>(stage + (4 * g4 + q) * L::RB) + 16 * cs + r16, p.scale * b[q]);
-            }
-            if (p.ckpt) {
-                float* ck = p.ckpt + w.block(p, c) * p.ckpt_stride;
+                        for (int ks = 0; ks < KS; ++ks)
+                            if (NX > 1 && ((c0 + cs) * KS + ks) % 4 == TT) {
+                                float* d = ck + (int64_t)i * K + 8 * g4 + 32 * ks;
+                                *reinterpret_cast<f32x4*>(d) = s[cs][NX > 1 ? 2 * ks : 0];
+                                *reinterpret_cast<f32x4*>(d + 4) = s[cs][NX > 1 ? 2 * ks + 1 : 0];
+                            }
 #pragma unroll
-                for (int cs = 0; cs < NCW; ++cs) {
-                    const int i = 16 * (w.sub * NCW + cs) + r16;
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-                        if (NX > 1 && (cs * KS + ks) % 4 == TT) {
-                            float* d = ck + (int64_t)i * K + 8 * g4 + 32 * ks;
-                            *reinterpret_cast<f32x4*>(d) = s[cs][NX > 1 ? 2 * ks : 0];
-                            *reinterpret_cast<f32x4*>(d + 4) = s[cs][NX > 1 ? 2 * ks + 1 : 0];
-                        }
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-                        if ((cs * 2 + ks) % 4 == 3 - TT) {
-                            float* d = ck + (int64_t)p.V * K + (int64_t)i * C + 8 * g4 + 32 * ks;
-                            *reinterpret_cast<f32x4*>(d) = u[cs][2 * ks];
-                            *reinterpret_cast<f32x4*>(d + 4) = u[cs][2 * ks + 1];
-                        }
+                        for (int ks = 0; ks < 2; ++ks)
+                            if (((c0 + cs) * 2 + ks) % 4 == 3 - TT) {
+                                float* d = ck + (int64_t)p.V * K + (int64_t)i * C + 8 * g4 + 32 * ks;
+                                *reinterpret_cast<f32x4*>(d) = u[cs][2 * ks];
+                                *reinterpret_cast<f32x4*>(d + 4) = u[cs][2 * ks + 1];
+                            }
+                    }
                 }
             }
             if (o) {
@@ -567,8 +571,6 @@ __global__ __launch_bounds__(64 * (NCW + 6)) void fwd_kernel(Args p, int nsub) {
         f32x4 bt[4], eg[4], te[4], a[4], u[4], v[4];
         PF<NX> kf[KS][4];
         read_rows<U, NX, KS>(kf, buf + L::Kr, L::XB, lane);
-        read_gate(bt, gates + kGateBeta, g4);
-        read_gate(eg, gates + kGateEG, g4);
         const float eGC = gates[kGateEG + C - 1];
         fence();
         // a = K S^T;  R = V - e^G a;  U = T (b R)
@@ -581,8 +583,9 @@ __global__ __launch_bounds__(64 * (NCW + 6)) void fwd_kernel(Args p, int nsub) {
         }
         PF<NP> tf[6];
         column_tiles<L::RB>(v, buf + L::V, wave, lane, InT());
+        read_gate(bt, gates + kGateBeta, g4);
+        read_gate(eg, gates + kGateEG, g4);
         read_tri<false>(tf, buf + L::T, lane);
-        read_gate(te, gates + kGateToEnd, g4);
         fence();
 #pragma unroll
         for (int t = 0; t < 4; ++t) a[t] = bt[t] * (v[t] - eg[t] * a[t]);
@@ -590,6 +593,7 @@ __global__ __launch_bounds__(64 * (NCW + 6)) void fwd_kernel(Args p, int nsub) {
         fence();
         tri_times<false>(u, tf, rf);
         fence();
+        read_gate(te, gates + kGateToEnd, g4);
         PF<NX> kc[2][KT];
         read_cols<U, NX, KT>(kc, buf + L::Kr, L::XB, lane);
         fence();
@@ -645,12 +649,12 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
             f32x4 bt[4], eg[4], te[4], a[4], z[4];
             PF<NX> kf[KS][4];
             read_rows<U, NX, KS>(kf, buf + L::Kr, L::XB, lane);
-            read_gate(te, gates + kGateToEnd, g4);
-            pass_get(pass(it) + L::ST, lane, z);          // scale M^T DO
             fence();
             store_state(p.dend + block * (int64_t)p.V * K, (int64_t)i * K + 8 * g4, s);
             rows_times_state<NX, KS, KT>(a, kf, s);
             PF<NP> tf[6];
+            read_gate(te, gates + kGateToEnd, g4);
+            pass_get(pass(it) + L::ST, lane, z);          // scale M^T DO
             read_tri<true>(tf, buf + L::T, lane);
             fence();
 #pragma unroll
@@ -779,7 +783,14 @@ hipError_t launch_typed(const Args& a, hipStream_t s) {
 
 template <bool BWD>
 hipError_t launch_scan(const Args& a, bool bf16, hipStream_t s) {
-    if (bf16) return a.K == 64 ? launch_typed<uint16_t, 1, 64, 2, BWD>(a, s) : launch_typed<uint16_t, 1, 128, 2, BWD>(a, s);
+    int n_cu = 0;
+    const hipError_t e = wkv7::device_cus(&n_cu);
+    if (e != hipSuccess) return e;
+    const bool many = (int64_t)a.N * a.H * (a.V / 64) >= n_cu;
+    if (bf16) {
+        if (a.K == 128) return launch_typed<uint16_t, 1, 128, 2, BWD>(a, s);
+        return many ? launch_typed<uint16_t, 1, 64, 4, BWD>(a, s) : launch_typed<uint16_t, 1, 64, 2, BWD>(a, s);
+    }
     return a.K == 64 ? launch_typed<float, 3, 64, 1, BWD>(a, s) : launch_typed<float, 3, 128, 1, BWD>(a, s);
 }
 
