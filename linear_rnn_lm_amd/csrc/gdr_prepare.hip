@@ -81,10 +81,19 @@ __global__ __launch_bounds__(256, 4) void prepare_kernel(Args p) {
     Planes kp = p.kp;
     kp.p += tok * stride + hk * K;
     auto row = [&](int t) { return min(t, len - 1); };   // tokens past the end: masked below
-    PF<NX> ka[KS];
+    PF<NX> ka[KS], kb[4][KS];
     const int ra = row(idx(w, r16));
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) ka[ks] = frag_mem<NX>(kp, ra, stride, ks, lane);
+    if constexpr (NX == 1) {                             // all rows at once: one wait for memory
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+            if (nt < 2 || w >= 2) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) kb[nt][ks] = frag_mem<NX>(kp, row(idx(nt, r16)), stride, ks, lane);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+    }
 
     if (w == 3) {
         float g = 0.f, b = 0.f;
@@ -121,8 +130,10 @@ __global__ __launch_bounds__(256, 4) void prepare_kernel(Args p) {
         kk[nt] = zero4();
         if (nt >= 2 && w < 2) continue;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-            kk[nt] = pmma<NX>(kk[nt], ka[ks], frag_mem<NX>(kp, row(idx(nt, r16)), stride, ks, lane));
+        for (int ks = 0; ks < KS; ++ks) {
+            if constexpr (NX > 1) kb[nt][ks] = frag_mem<NX>(kp, row(idx(nt, r16)), stride, ks, lane);
+            kk[nt] = pmma<NX>(kk[nt], ka[ks], kb[nt][ks]);
+        }
     }
     __syncthreads();
     const int t0 = idx(w, 4 * g4);
