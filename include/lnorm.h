@@ -19,7 +19,8 @@
  * - Statistics, sums and gradients are fp32 (the variance from the centred
  *   values); y and dx are rounded once.  NaN and Inf inputs propagate within their part.
  * - groups divides C, and D is at most 16384.
- * - Every pointer is a device pointer aligned to 16 bytes.
+ * - Every pointer is a device pointer aligned to 16 bytes (mean, rstd, dweight and
+ *   dbias: 4).
  * - Results do not vary from run to run: the sums over the rows go through
  *   per-workgroup parts in a fixed order, without atomics.
  */

@@ -21,6 +21,7 @@ y = S r.  Inputs r, w, k, v, a, b are fp32 or bf16; all outputs are fp32.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = ["lib", "fwd", "fwd_sequential", "fwd_scan", "chunk_prepare", "chunk_inverse", "bwd", "bwd_scan",
@@ -538,17 +539,24 @@ def _fits(t, shape, dtype, dev):
 def _launch(fn, entry, dev, *args):
     """Call a library entry point on the current stream of `dev` with that device
     current, and raise its error."""
-    import torch
+    c = _torch_c()
     if dev.type != "cuda":
         raise ValueError(f"libwkv7 works on GPU tensors; got tensors on {dev}")
-    i = torch.cuda.current_device() if dev.index is None else dev.index
-    if torch.cuda.current_device() == i:
-        st = entry(*args, torch._C._cuda_getCurrentRawStream(i))
+    now = c._cuda_getDevice()
+    if dev.index is None or dev.index == now:
+        st = entry(*args, c._cuda_getCurrentRawStream(now))
     else:
-        with torch.cuda.device(i):
-            st = entry(*args, torch._C._cuda_getCurrentRawStream(i))
+        import torch
+        with torch.cuda.device(dev.index):
+            st = entry(*args, c._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         _check(fn, st)
+
+
+@functools.lru_cache(maxsize=None)
+def _torch_c():
+    import torch
+    return torch._C
 
 
 class _LazyOpOf:

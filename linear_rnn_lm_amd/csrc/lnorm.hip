@@ -479,7 +479,7 @@ wkv7_status ln_bwd(int64_t rows, int C, int groups, wkv7_dtype x_dtype, wkv7_dty
     const abi::Buf bufs[] = {{dy, n * lnorm::esz(y_dtype), true, false, 16}, {x, n * lnorm::esz(x_dtype), true, false, 16},
                              {weight, C * lnorm::esz(w_dtype), false, false, 16}, {mean, sb, true, false, 4},
                              {rstd, sb, true, false, 4}, {dx, n * lnorm::esz(x_dtype), false, true, 16},
-                             {dweight, C * 4LL, false, true, 16}, {dbias, C * 4LL, false, true, 16},
+                             {dweight, C * 4LL, false, true, 4}, {dbias, C * 4LL, false, true, 4},
                              {workspace, need, false, true, 16}};
     st = abi::check(bufs);
     if (st != WKV7_OK) return st;

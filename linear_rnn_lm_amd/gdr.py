@@ -45,22 +45,38 @@ def _lib():
     return L
 
 
+@functools.lru_cache(maxsize=None)
+def _types():
+    """The input types and their codes, and the type of gates and states."""
+    import torch
+    return {torch.float32: F32, torch.bfloat16: BF16}, torch.float32
+
+
+@functools.lru_cache(maxsize=1024)
+def _sizes(dims, code, N):
+    """Bytes of the checkpoints and of both workspaces."""
+    L, packed = _lib(), int(N > 0)
+    return (L.gdr_ckpt_bytes(*dims, N, packed), L.gdr_fwd_workspace_bytes(*dims, code, N, packed),
+            L.gdr_bwd_workspace_bytes(*dims, code, N, packed))
+
+
 def _check_inputs(fn, q, k, v, g, beta):
     """(B, T, Hk, H, K, V) of the five token inputs, checked."""
-    import torch
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError(f"{fn}: q must be (B, T, Hk, K) and v (B, T, H, V), got {tuple(q.shape)} and {tuple(v.shape)}")
-    B, T, Hk, K = q.shape
-    H, V = v.shape[2:]
-    if K not in (64, 128) or V not in (64, 128):
+    qs, vs = q.shape, v.shape
+    if len(qs) != 4 or len(vs) != 4:
+        raise ValueError(f"{fn}: q must be (B, T, Hk, K) and v (B, T, H, V), got {tuple(qs)} and {tuple(vs)}")
+    B, T, Hk, K = qs
+    H, V = vs[2], vs[3]
+    if (K != 64 and K != 128) or (V != 64 and V != 128):
         raise ValueError(f"{fn}: K and V must be 64 or 128, got {K} and {V}")
-    if min(B, T, Hk, H) < 1 or H % Hk:
-        raise ValueError(f"{fn}: B, T and heads must be at least 1 and H a multiple of Hk, got q {tuple(q.shape)}, "
-                         f"v {tuple(v.shape)}")
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{fn}: q must be float32 or bfloat16, got {q.dtype}")
-    dev, dt, f32, qs, gs = q.device, q.dtype, torch.float32, (B, T, Hk, K), (B, T, H)
-    if not (_fits(q, qs, dt, dev) and _fits(k, qs, dt, dev) and _fits(v, (B, T, H, V), dt, dev)
+    if B < 1 or T < 1 or Hk < 1 or H < 1 or H % Hk:
+        raise ValueError(f"{fn}: B, T and heads must be at least 1 and H a multiple of Hk, got q {tuple(qs)}, "
+                         f"v {tuple(vs)}")
+    codes, f32 = _types()
+    dev, dt, gs = q.device, q.dtype, (B, T, H)
+    if dt not in codes:
+        raise TypeError(f"{fn}: q must be float32 or bfloat16, got {dt}")
+    if not (q.is_contiguous() and _fits(k, qs, dt, dev) and _fits(v, (B, T, H, V), dt, dev)
             and _fits(g, gs, f32, dev) and _fits(beta, gs, f32, dev)):
         for n, t, shape, d in (("q", q, qs, dt), ("k", k, qs, dt), ("v", v, (B, T, H, V), dt), ("g", g, gs, f32),
                                ("beta", beta, gs, f32)):
@@ -77,9 +93,8 @@ def _check_tensor(fn, name, t, shape, dtype, dev):
 
 
 def _check_state(fn, name, t, shape, dev):
-    import torch
     if t is not None:
-        _check_tensor(fn, name, t, shape, torch.float32, dev)
+        _check_tensor(fn, name, t, shape, _types()[1], dev)
 
 
 def _check_cu(fn, cu, B, dev):
@@ -96,8 +111,7 @@ def _check_cu(fn, cu, B, dev):
 
 
 def _code(dtype):
-    import torch
-    return BF16 if dtype == torch.bfloat16 else F32
+    return _types()[0][dtype]
 
 
 def _workspace(fn, workspace, need, dev):
@@ -135,7 +149,8 @@ def gdr_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, scale=None, want_o=Tr
     elif want_o:
         o = torch.empty_like(v)
         fresh.append(o)
-    nck = L.gdr_ckpt_bytes(*dims, N, packed)
+    code = _code(q.dtype)
+    nck, nws, _ = _sizes(dims, code, N)
     if ckpt is not None:
         _check_state(fn, "ckpt", ckpt, (nck // 4,), dev)
     elif want_ckpt:
@@ -144,8 +159,7 @@ def gdr_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, scale=None, want_o=Tr
         _check_state(fn, "hT", hT, states, dev)
     elif want_hT:
         hT = torch.empty(states, dtype=torch.float32, device=dev)
-    code = _code(q.dtype)
-    workspace, wsb = _workspace(fn, workspace, L.gdr_fwd_workspace_bytes(*dims, code, N, packed), dev)
+    workspace, wsb = _workspace(fn, workspace, nws, dev)
     _launch(fn, L.gdr_fwd, dev, *dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
             _ptr(cu_seqlens), N, K ** -0.5 if scale is None else scale, _ptr(h0), _ptr(o), _ptr(ckpt), _ptr(hT),
             workspace.data_ptr(), wsb)
@@ -165,7 +179,9 @@ def gdr_bwd(do, q, k, v, g, beta, ckpt, dhT=None, *, cu_seqlens=None, scale=None
     L, packed, states = _lib(), int(N > 0), (N or B, H, V, K)
     dims = (B, T, Hk, H, K, V)
     _check_tensor(fn, "do", do, v.shape, v.dtype, dev)
-    _check_state(fn, "ckpt", ckpt, (L.gdr_ckpt_bytes(*dims, N, packed) // 4,), dev)
+    code = _code(q.dtype)
+    nck, _, nws = _sizes(dims, code, N)
+    _check_state(fn, "ckpt", ckpt, (nck // 4,), dev)
     _check_state(fn, "dhT", dhT, states, dev)
     fresh = []
     if out is None:
@@ -175,8 +191,7 @@ def gdr_bwd(do, q, k, v, g, beta, ckpt, dhT=None, *, cu_seqlens=None, scale=None
     for n, x, like in zip(("dq", "dk", "dv", "dg", "dbeta"), out, (q, k, v, g, beta)):
         _check_tensor(fn, n, x, like.shape, like.dtype, dev)
     dh0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dh0 else None
-    code = _code(q.dtype)
-    workspace, wsb = _workspace(fn, workspace, L.gdr_bwd_workspace_bytes(*dims, code, N, packed), dev)
+    workspace, wsb = _workspace(fn, workspace, nws, dev)
     _launch(fn, L.gdr_bwd, dev, *dims, code, *map(_ptr, (do, dhT, q, k, v, g, beta, cu_seqlens)), N,
             K ** -0.5 if scale is None else scale, *map(_ptr, (ckpt, *out, dh0, workspace)), wsb)
     if packed and fresh:
@@ -192,17 +207,16 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, state_out=None,
     ``slots`` (B,) int32 picks each row's state (row b uses state b without it);
     a row whose slot is outside 0 .. P - 1 is padding: its o is 0.  Rows with the
     same slot are consecutive tokens of one sequence, in row order."""
-    import torch
     fn = "gdr_step"
     B, T, Hk, H, K, V = _check_inputs(fn, q, k, v, g, beta)
-    dev = q.device
-    if state.dim() != 4 or state.shape[0] < 1:
+    dev, P = q.device, state.shape[0] if state.dim() == 4 else 0
+    if P < 1:
         raise ValueError(f"{fn}: state must be (P, H, V, K), got {tuple(state.shape)}")
-    P = state.shape[0]
     if slots is None:
         if P < B:
             raise ValueError(f"{fn}: state holds {P} states for {B} rows")
     else:
+        import torch
         _check_tensor(fn, "slots", slots, (B,), torch.int32, dev)
     _check_state(fn, "state", state, (P, H, V, K), dev)
     if state_out is None:
@@ -210,7 +224,7 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, state_out=None,
     else:
         _check_state(fn, "state_out", state_out, (P, H, V, K), dev)
     if o is None:
-        o = torch.empty_like(v)
+        o = v.new_empty(v.shape)
     else:
         _check_tensor(fn, "o", o, v.shape, v.dtype, dev)
     _launch(fn, _lib().gdr_step, dev, B, T, Hk, H, K, V, _code(q.dtype), q.data_ptr(), k.data_ptr(), v.data_ptr(),

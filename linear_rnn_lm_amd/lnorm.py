@@ -29,37 +29,39 @@ def _lib():
     return L
 
 
-def _code(dtype):
+@functools.lru_cache(maxsize=None)
+def _types():
+    """The two types and their codes (None: no tensor, any code)."""
     import torch
-    return BF16 if dtype == torch.bfloat16 else F32
+    return {torch.float32: F32, torch.bfloat16: BF16, None: F32}
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(rows, C, groups):
+    return _lib().ln_bwd_workspace_bytes(rows, C, groups)
 
 
 def _check_x(fn, x, weight, bias, groups):
-    """(rows, C) of x, with the weights' type code."""
-    import torch
-    types = (torch.float32, torch.bfloat16)
-    if x.dim() < 1 or x.shape[-1] < 1 or x.numel() < 1:
-        raise ValueError(f"{fn}: x must be (..., C) and not empty, got {tuple(x.shape)}")
+    """(rows, C) of x, with the type codes of x and of the weights."""
+    types, dev, shape = _types(), x.device, x.shape
+    C, n = shape[-1] if shape else 0, x.numel()
+    if n < 1:
+        raise ValueError(f"{fn}: x must be (..., C) and not empty, got {tuple(shape)}")
     if x.dtype not in types:
         raise TypeError(f"{fn}: x must be float32 or bfloat16, got {x.dtype}")
-    C = x.shape[-1]
     if groups < 1 or C % groups or C // groups > 16384:
         raise ValueError(f"{fn}: groups must divide C into parts of at most 16384, got C = {C}, groups = {groups}")
     if not x.is_contiguous():
-        _dense_on(fn, "x", x, x.device)
-    if weight is not None and bias is not None:
-        wd = weight.dtype
-        if wd in types and _fits(weight, (C,), wd, x.device) and _fits(bias, (C,), wd, x.device):
-            return x.numel() // C, C, _code(wd)
+        _dense_on(fn, "x", x, dev)
     wd = None
-    for n, w in (("weight", weight), ("bias", bias)):
-        if w is None:
-            continue
-        if w.dtype not in types or (wd is not None and w.dtype != wd) or tuple(w.shape) != (C,):
-            raise ValueError(f"{fn}: {n} is {_where(w)}, expected ({C},) float32 or bfloat16, both of one type")
-        _dense_on(fn, n, w, x.device)
-        wd = w.dtype
-    return x.numel() // C, C, _code(wd)
+    for name, w in (("weight", weight), ("bias", bias)):
+        if w is not None:
+            if w.dtype not in types or (wd is not None and w.dtype != wd) or w.shape != (C,):
+                raise ValueError(f"{fn}: {name} is {_where(w)}, expected ({C},) float32 or bfloat16, both of one type")
+            if w.device != dev or not w.is_contiguous():
+                _dense_on(fn, name, w, dev)
+            wd = w.dtype
+    return n // C, C, types[x.dtype], types[wd]
 
 
 def _check_like(fn, name, t, shape, dtype, dev):
@@ -83,23 +85,25 @@ def ln_fwd(x, weight=None, bias=None, *, groups=1, eps=1e-5, out_dtype=None, wan
     """Forward.  Returns (y, mean, rstd); the statistics are None if not wanted."""
     import torch
     fn = "ln_fwd"
-    rows, C, wcode = _check_x(fn, x, weight, bias, groups)
-    dev = x.device
-    if y is None:
-        out_dtype = x.dtype if out_dtype is None else _out_dtype(fn, x, out_dtype)
-        y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    rows, C, xcode, wcode = _check_x(fn, x, weight, bias, groups)
+    dev, ycode = x.device, xcode
+    if y is None and (out_dtype is None or out_dtype == x.dtype):
+        y = torch.empty_like(x)
     else:
-        out_dtype = _out_dtype(fn, x, y.dtype)
+        out_dtype = _out_dtype(fn, x, out_dtype if y is None else y.dtype)
+        ycode = _types()[out_dtype]
+        if y is None:
+            y = torch.empty_like(x, dtype=out_dtype)
         _check_like(fn, "y", y, x.shape, out_dtype, dev)
     if (mean is None) != (rstd is None):
         raise ValueError(f"{fn}: mean and rstd go together")
     if mean is None and want_stats:
-        mean, rstd = torch.empty((2, rows, groups), dtype=torch.float32, device=dev)
+        mean, rstd = x.new_empty((2, rows, groups), dtype=torch.float32).unbind(0)
     elif mean is not None:
         _check_like(fn, "mean", mean, (rows, groups), torch.float32, dev)
         _check_like(fn, "rstd", rstd, (rows, groups), torch.float32, dev)
-    _launch(fn, _lib().ln_fwd, dev, rows, C, groups, _code(x.dtype), _code(out_dtype), wcode, x.data_ptr(), _ptr(weight),
-            _ptr(bias), eps, y.data_ptr(), _ptr(mean), _ptr(rstd))
+    _launch(fn, _lib().ln_fwd, dev, rows, C, groups, xcode, ycode, wcode, x.data_ptr(), _ptr(weight), _ptr(bias), eps,
+            y.data_ptr(), _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
 
@@ -108,33 +112,33 @@ def ln_bwd(dy, x, weight, mean, rstd, *, groups=1, want_dx=True, want_dw=True, w
     ``out`` may hold the three (None for one not wanted)."""
     import torch
     fn = "ln_bwd"
-    rows, C, wcode = _check_x(fn, x, weight, None, groups)
-    dev = x.device
-    _check_like(fn, "dy", dy, x.shape, _out_dtype(fn, x, dy.dtype), dev)
+    rows, C, xcode, wcode = _check_x(fn, x, weight, None, groups)
+    dev, ydt = x.device, dy.dtype
+    if ydt != x.dtype:
+        _out_dtype(fn, x, ydt)
+    _check_like(fn, "dy", dy, x.shape, ydt, dev)
     _check_like(fn, "mean", mean, (rows, groups), torch.float32, dev)
     _check_like(fn, "rstd", rstd, (rows, groups), torch.float32, dev)
     if out is None:
-        f32 = dict(dtype=torch.float32, device=dev)
-        out = (torch.empty_like(x) if want_dx else None, torch.empty(C, **f32) if want_dw else None,
-               torch.empty(C, **f32) if want_dw else None)
-    elif len(out) != 3:
-        raise ValueError(f"{fn}: out must hold 3 entries, got {len(out)}")
-    dx, dw, db = out
+        dx = torch.empty_like(x) if want_dx else None
+        dw, db = x.new_empty((2, C), dtype=torch.float32).unbind(0) if want_dw else (None, None)
+    else:
+        if len(out) != 3:
+            raise ValueError(f"{fn}: out must hold 3 entries, got {len(out)}")
+        dx, dw, db = out
+        for n, t, shape, dt in (("dx", dx, x.shape, x.dtype), ("dweight", dw, (C,), torch.float32),
+                                ("dbias", db, (C,), torch.float32)):
+            if t is not None:
+                _check_like(fn, n, t, shape, dt, dev)
     if (dw is None) != (db is None) or (dx is None and dw is None):
         raise ValueError(f"{fn}: dx, or dweight and dbias together, must be wanted")
-    for n, t, shape, dt in (("dx", dx, x.shape, x.dtype), ("dweight", dw, (C,), torch.float32),
-                            ("dbias", db, (C,), torch.float32)):
-        if t is not None:
-            _check_like(fn, n, t, shape, dt, dev)
-    need = _lib().ln_bwd_workspace_bytes(rows, C, groups) if dw is not None else 0
-    if workspace is None:
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    else:
+    need = 0 if dw is None else _workspace_bytes(rows, C, groups)
+    if workspace is not None:
         _check_bytes(fn, "workspace", workspace, need, dev)
-    _launch(fn, _lib().ln_bwd, dev, rows, C, groups, _code(x.dtype), _code(dy.dtype), wcode, dy.data_ptr(), x.data_ptr(),
-            _ptr(weight), mean.data_ptr(), rstd.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size())
+    elif need:
+        workspace = x.new_empty(need, dtype=torch.uint8)
+    _launch(fn, _lib().ln_bwd, dev, rows, C, groups, xcode, _types()[ydt], wcode, dy.data_ptr(), x.data_ptr(), _ptr(weight),
+            mean.data_ptr(), rstd.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace), need)
     return dx, dw, db
 
 
