@@ -45,12 +45,12 @@ struct Plan {
 };
 
 // A row block of 16 token columns per wave, staged in LDS with RB bytes per token: the wave's
-// column in accumulator order (tokens idx(t, 4g + q)).
+// column in accumulator order (tokens idx(t, 4g + q)), tiles t0 and t0 + 1.
 template <int RB>
-__device__ __forceinline__ void column_tiles(f32x4 (&x)[4], const char* buf, int cw, int lane, uint16_t) {
+__device__ __forceinline__ void column_tiles(f32x4 (&x)[4], const char* buf, int cw, int lane, uint16_t, int t0) {
     const char* p = buf + (8 * (lane >> 4) + ((lane & 15) >> 2)) * RB + 32 * cw + 8 * (lane & 3);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = t0; t < t0 + 2; ++t) {
         const wkv7::i16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (wkv7::lds_i16x4*)(p + (32 * (t >> 1) + 4 * (t & 1)) * RB));
 #pragma unroll
@@ -58,10 +58,10 @@ __device__ __forceinline__ void column_tiles(f32x4 (&x)[4], const char* buf, int
     }
 }
 template <int RB>
-__device__ __forceinline__ void column_tiles(f32x4 (&x)[4], const char* buf, int cw, int lane, float) {
+__device__ __forceinline__ void column_tiles(f32x4 (&x)[4], const char* buf, int cw, int lane, float, int t0) {
     const char* p = buf + 64 * cw + 4 * (lane & 15);
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = t0; t < t0 + 2; ++t)
 #pragma unroll
         for (int q = 0; q < 4; ++q) x[t][q] = *reinterpret_cast<const float*>(p + idx(t, 4 * (lane >> 4) + q) * RB);
 }
@@ -128,7 +128,11 @@ __device__ __forceinline__ void store_tokens(float* dst, int i, int g4, const f3
         *reinterpret_cast<f32x4*>(dst + (int64_t)i * C + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1)) = u[t];
 }
 
-// A gate's values for a lane's tokens, per tile.
+// A gate's values for a lane's tokens, per tile; of the tile pair t0 only.
+__device__ __forceinline__ void read_gate2(f32x4 (&x)[4], const float* gate, int g4, int t0) {
+    x[t0] = *reinterpret_cast<const f32x4*>(gate + idx(t0, 4 * g4));
+    x[t0 + 1] = *reinterpret_cast<const f32x4*>(gate + idx(t0 + 1, 4 * g4));
+}
 __device__ __forceinline__ void read_gate(f32x4 (&x)[4], const float* gate, int g4) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) x[t] = *reinterpret_cast<const f32x4*>(gate + idx(t, 4 * g4));
@@ -138,6 +142,15 @@ template <int N>
 __device__ __forceinline__ void pass_put(char* p, int lane, const f32x4 (&x)[N]) {
 #pragma unroll
     for (int t = 0; t < N; ++t) *reinterpret_cast<f32x4*>(p + t * 1024 + lane * 16) = x[t];
+}
+// tiles t, t + 1 only
+__device__ __forceinline__ void pass_put2(char* p, int lane, const f32x4 (&x)[4], int t) {
+    *reinterpret_cast<f32x4*>(p + t * 1024 + lane * 16) = x[t];
+    *reinterpret_cast<f32x4*>(p + (t + 1) * 1024 + lane * 16) = x[t + 1];
+}
+__device__ __forceinline__ void pass_get2(const char* p, int lane, f32x4 (&x)[4], int t) {
+    x[t] = *reinterpret_cast<const f32x4*>(p + t * 1024 + lane * 16);
+    x[t + 1] = *reinterpret_cast<const f32x4*>(p + (t + 1) * 1024 + lane * 16);
 }
 template <int N>
 __device__ __forceinline__ void pass_get(const char* p, int lane, f32x4 (&x)[N]) {
@@ -255,10 +268,11 @@ __device__ __forceinline__ void memory_wave(const Args& p, const Where& w, char*
 }
 
 // ---------------------------------------------------------------------------
-// The products of the chain, with every LDS operand read a step ahead of its
-// use: an MFMA that waits for its own operand loses about 120 cycles, eight
-// times its length.  fence() keeps the compiler from moving the reads back to
-// their uses; interleave() deals VALU work out between MFMAs, which run 16 cycles each.
+// The products of the chain.  One wave has a SIMD's matrix unit nearly to itself, and its
+// MFMAs (16 cycles each) and its VALU work (splitting values into planes, gates) take
+// about as long; so a chunk is cut into regions, each with the MFMAs of one step
+// and the VALU work of the next, dealt out between them by interleave().  LDS operands
+// are read a region ahead; fence() keeps the compiler from moving them back to their uses.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 template <int N, int VALU>
 __device__ __forceinline__ void interleave() {
@@ -267,7 +281,11 @@ __device__ __forceinline__ void interleave() {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // one MFMA
         __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);  // then VALU
     }
+    fence();
 }
+// plane products of an input (NX planes) and a derived value
+template <int NX>
+constexpr int products() { return NX == 1 ? NP : NP * (NP + 1) / 2; }
 
 template <int U, int NX, int KS>
 __device__ __forceinline__ void read_rows(PF<NX> (&f)[KS][4], const char* X, int XB, int lane) {
@@ -277,11 +295,9 @@ __device__ __forceinline__ void read_rows(PF<NX> (&f)[KS][4], const char* X, int
         for (int t = 0; t < 4; ++t) f[ks][t] = frag_row<U, NX>(X, XB, idx(t, lane & 15), ks, lane);
 }
 template <int U, int NX, int KT>
-__device__ __forceinline__ void read_cols(PF<NX> (&f)[2][KT], const char* X, int XB, int lane) {
+__device__ __forceinline__ void read_cols(PF<NX> (&f)[KT], const char* X, int XB, int ks, int lane) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-        for (int t = 0; t < KT; ++t) f[ks][t] = frag_col<U, NX>(X, XB, t, ks, lane);
+    for (int t = 0; t < KT; ++t) f[t] = frag_col<U, NX>(X, XB, t, ks, lane);
 }
 // Fragments of a lower triangular matrix's rows, or of its columns (TR), tile and step as numbered by tri_at.
 template <bool TR>
@@ -289,23 +305,31 @@ __device__ __forceinline__ constexpr int tri_at(int t, int ks) {
     return TR ? (t < 2 ? 2 * t + ks : t + 2) : (t < 2 ? t : 2 * t - 2 + ks);
 }
 template <bool TR>
-__device__ __forceinline__ void read_tri(PF<NP> (&f)[6], const char* X, int lane) {
+__device__ __forceinline__ void read_tri(PF<NP> (&f)[6], const char* X, int ks, int lane) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-            if (TR ? ks >= (t >> 1) : ks <= (t >> 1)) {
-                if constexpr (TR) f[tri_at<TR>(t, ks)] = tri_col<NP>(X, t, ks, lane);
-                else f[tri_at<TR>(t, ks)] = tri_row<NP>(X, t, ks, lane);
-            }
+        if (TR ? ks >= (t >> 1) : ks <= (t >> 1)) {
+            if constexpr (TR) f[tri_at<TR>(t, ks)] = tri_col<NP>(X, t, ks, lane);
+            else f[tri_at<TR>(t, ks)] = tri_row<NP>(X, t, ks, lane);
+        }
 }
 
-// a[t] = X S^T over all K columns, S split on the way; its leading two planes go to `pass` if given
-template <int NX, int KS, int KT>
-__device__ __forceinline__ void rows_times_state(f32x4 (&a)[4], const PF<NX> (&f)[KS][4], const f32x4 (&s)[KT],
-                                                 char* pass = nullptr) {
+// a[t] += X S^T over 32 columns, tiles T0 .. T0 + N - 1
+template <int NX, int T0, int N>
+__device__ __forceinline__ void rows_step(f32x4 (&a)[4], const PF<NX> (&f)[4], const PF<NP>& sf) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) a[t] = zero4();
+    for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+            if (o - i >= 0)
+#pragma unroll
+                for (int t = T0; t < T0 + N; ++t) a[t] = wkv7::mfma_bf16(f[t].p[i], sf.p[o - i], a[t]);
+}
+// a = X S^T over all columns but the last 32 (whose planes it returns), S split on the way; the
+// leading two planes go to `pass` if given
+template <int NX, int KS, int KT>
+__device__ __forceinline__ PF<NP> rows_times_state(f32x4 (&a)[4], const PF<NX> (&f)[KS][4], const f32x4 (&s)[KT],
+                                                   char* pass) {
     PF<NP> sf = pf_acc<NP>(s[0], s[1]);
     auto hand = [&](int ks) {
         if (pass) {
@@ -315,52 +339,40 @@ __device__ __forceinline__ void rows_times_state(f32x4 (&a)[4], const PF<NX> (&f
     };
     hand(0);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
+    for (int t = 0; t < 4; ++t) a[t] = zero4();
+#pragma unroll
+    for (int ks = 0; ks + 1 < KS; ++ks) {
         fence();
-#pragma unroll
-        for (int o = NP - 1; o >= 0; --o)
-#pragma unroll
-            for (int i = 0; i < NX; ++i)
-                if (o - i >= 0)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) a[t] = wkv7::mfma_bf16(f[ks][t].p[i], sf.p[o - i], a[t]);
-        if (ks + 1 < KS) {
-            sf = pf_acc<NP>(s[2 * ks + 2], s[2 * ks + 3]);
-            interleave<4 * (NX == 1 ? 3 : 6), 4>();
-            fence();
-            hand(ks + 1);
-        }
+        rows_step<NX, 0, 4>(a, f[ks], sf);
+        sf = pf_acc<NP>(s[2 * ks + 2], s[2 * ks + 3]);
+        interleave<4 * products<NX>(), 4>();
+        hand(ks + 1);
     }
     fence();
+    return sf;
 }
-// u[t] = (triangular) r
+// u[t] += (triangular) r over 32 tokens
 template <bool TR>
-__device__ __forceinline__ void tri_times(f32x4 (&u)[4], const PF<NP> (&f)[6], const PF<NP> (&r)[2]) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) u[t] = zero4();
+__device__ __forceinline__ void tri_step(f32x4 (&u)[4], const PF<NP> (&f)[6], int ks, const PF<NP>& r) {
 #pragma unroll
     for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
         for (int i = 0; i <= o; ++i)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    if (TR ? ks >= (t >> 1) : ks <= (t >> 1))
-                        u[t] = wkv7::mfma_bf16(f[tri_at<TR>(t, ks)].p[i], r[ks].p[o - i], u[t]);
+            for (int t = 0; t < 4; ++t)
+                if (TR ? ks >= (t >> 1) : ks <= (t >> 1))
+                    u[t] = wkv7::mfma_bf16(f[tri_at<TR>(t, ks)].p[i], r.p[o - i], u[t]);
 }
-// s[t] += X^T r
+// s[t] += X^T r over 32 tokens
 template <int NX, int KT>
-__device__ __forceinline__ void add_cols_times(f32x4 (&s)[KT], const PF<NX> (&f)[2][KT], const PF<NP> (&r)[2]) {
+__device__ __forceinline__ void cols_step(f32x4 (&s)[KT], const PF<NX> (&f)[KT], const PF<NP>& r) {
 #pragma unroll
     for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
         for (int i = 0; i < NX; ++i)
             if (o - i >= 0)
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                    for (int t = 0; t < KT; ++t) s[t] = wkv7::mfma_bf16(f[ks][t].p[i], r[ks].p[o - i], s[t]);
+                for (int t = 0; t < KT; ++t) s[t] = wkv7::mfma_bf16(f[t].p[i], r.p[o - i], s[t]);
 }
 
 // One token row of a chunk of q or k from memory, as operand fragments (a token past the end repeats the last one).
@@ -488,15 +500,20 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
                 for (int k = 0; k < KS; ++k) {
 #pragma unroll
                     for (int ts = 0; ts < 2 * MS; ++ts)
-                        kf[ts][k] = frag_row<U, NX>(buf + L::Kr, L::XB, idx(ts, r16), k, lane);
+                        if (NX == 1) kf[ts][k] = frag_row<U, NX>(buf + L::Kr, L::XB, idx(ts, r16), k, lane);
                 }
                 fence();
+                // three planes of them would not fit the registers: those are read at their use
+                auto kfrag = [&](int ts, int k) {
+                    if constexpr (NX == 1) return kf[ts][k];
+                    else return frag_row<U, NX>(buf + L::Kr, L::XB, idx(ts, r16), k, lane);
+                };
                 f32x4 x[2 * MS];                          // rows s of tile ts, column t
 #pragma unroll
                 for (int ts = 0; ts < 2 * MS; ++ts) {
                     x[ts] = zero4();
 #pragma unroll
-                    for (int k = 0; k < KS; ++k) x[ts] = pmma<NP>(x[ts], kf[ts][k], qf[k]);
+                    for (int k = 0; k < KS; ++k) x[ts] = pmma<NP>(x[ts], kfrag(ts, k), qf[k]);
                 }
 #pragma unroll
                 for (int ts = 0; ts < 2 * MS; ++ts) {
@@ -521,7 +538,7 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
                         f32x4 y = zero4();                // rows t, column s
                         const int s = idx(ts, r16);
 #pragma unroll
-                        for (int k = 0; k < KS; ++k) y = pmma<NP>(y, qf[k], kf[ts][k]);
+                        for (int k = 0; k < KS; ++k) y = pmma<NP>(y, qf[k], kfrag(ts, k));
                         const float ns = gates[kGateN + s], fs = gates[kGateF + s];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -573,39 +590,61 @@ __global__ __launch_bounds__(64 * (NCW + 6)) void fwd_kernel(Args p, int nsub) {
         read_rows<U, NX, KS>(kf, buf + L::Kr, L::XB, lane);
         const float eGC = gates[kGateEG + C - 1];
         fence();
-        // a = K S^T;  R = V - e^G a;  U = T (b R)
+        // a = K S^T
+        char* hand = nullptr;
         if constexpr (NX == 1) {
+            hand = pass(it) + 16 * lane;
             if (p.ckpt) store_state(p.ckpt + w.block(p, it) * p.ckpt_stride, (int64_t)i * K + 8 * g4, s);
-            rows_times_state<NX, KS, KT>(a, kf, s, pass(it) + 16 * lane);
         } else {
             pass_put(pass(it), lane, s);
-            rows_times_state<NX, KS, KT>(a, kf, s);
         }
+        const PF<NP> sl = rows_times_state<NX, KS, KT>(a, kf, s, hand);
+        column_tiles<L::RB>(v, buf + L::V, wave, lane, InT(), 0);
+        read_gate2(bt, gates + kGateBeta, g4, 0);
+        read_gate2(eg, gates + kGateEG, g4, 0);
         PF<NP> tf[6];
-        column_tiles<L::RB>(v, buf + L::V, wave, lane, InT());
-        read_gate(bt, gates + kGateBeta, g4);
-        read_gate(eg, gates + kGateEG, g4);
-        read_tri<false>(tf, buf + L::T, lane);
+        read_tri<false>(tf, buf + L::T, 0, lane);
+        fence();
+        rows_step<NX, 0, 2>(a, kf[KS - 1], sl);
+        fence();
+        // the last of a; b R = b (V - e^G a) of the first 32 tokens
+        rows_step<NX, 2, 2>(a, kf[KS - 1], sl);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) a[t] = bt[t] * (v[t] - eg[t] * a[t]);
+        const PF<NP> r0 = pf_acc<NP>(a[0], a[1]);
+        interleave<2 * products<NX>(), 12>();
+        // U = T (b R): what the first 32 tokens add; b R of the others; e^(G_C) S
+        column_tiles<L::RB>(v, buf + L::V, wave, lane, InT(), 2);
+        read_gate2(bt, gates + kGateBeta, g4, 2);
+        read_gate2(eg, gates + kGateEG, g4, 2);
         fence();
 #pragma unroll
-        for (int t = 0; t < 4; ++t) a[t] = bt[t] * (v[t] - eg[t] * a[t]);
-        const PF<NP> rf[2] = {pf_acc<NP>(a[0], a[1]), pf_acc<NP>(a[2], a[3])};
-        fence();
-        tri_times<false>(u, tf, rf);
-        fence();
-        read_gate(te, gates + kGateToEnd, g4);
-        PF<NX> kc[2][KT];
-        read_cols<U, NX, KT>(kc, buf + L::Kr, L::XB, lane);
-        fence();
-        // S1^T = e^(G_C) S0^T + K^T (e^(G_C - G) U)
+        for (int t = 0; t < 4; ++t) u[t] = zero4();
+        tri_step<false>(u, tf, 0, r0);
+#pragma unroll
+        for (int t = 2; t < 4; ++t) a[t] = bt[t] * (v[t] - eg[t] * a[t]);
+        const PF<NP> r1 = pf_acc<NP>(a[2], a[3]);
 #pragma unroll
         for (int t = 0; t < KT; ++t) s[t] = eGC * s[t];
-        pass_put(pass(it) + L::ST, lane, u);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) u[t] = te[t] * u[t];
-        const PF<NP> ue[2] = {pf_acc<NP>(u[0], u[1]), pf_acc<NP>(u[2], u[3])};
+        interleave<24, 4>();
+        // the rest of U; e^(G_C - G) U of the first 32 tokens
+        PF<NX> kc[KT], kd[KT];
+        read_tri<false>(tf, buf + L::T, 1, lane);
+        read_gate(te, gates + kGateToEnd, g4);
+        read_cols<U, NX, KT>(kc, buf + L::Kr, L::XB, 0, lane);
         fence();
-        add_cols_times<NX, KT>(s, kc, ue);
+        tri_step<false>(u, tf, 1, r1);
+        pass_put2(pass(it) + L::ST, lane, u, 0);
+        const PF<NP> e0 = pf_acc<NP>(te[0] * u[0], te[1] * u[1]);
+        interleave<12, 4>();
+        // S1^T = e^(G_C) S0^T + K^T (e^(G_C - G) U)
+        read_cols<U, NX, KT>(kd, buf + L::Kr, L::XB, 1, lane);
+        fence();
+        cols_step<NX, KT>(s, kc, e0);
+        pass_put2(pass(it) + L::ST, lane, u, 2);
+        const PF<NP> e1 = pf_acc<NP>(te[2] * u[2], te[3] * u[3]);
+        interleave<KT * products<NX>(), 3>();
+        cols_step<NX, KT>(s, kd, e1);
         lds_barrier();
     }
     if (p.hT) store_state(p.hT, soff, s);
@@ -638,63 +677,93 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
         load_state(s, p.dhT, soff);
         __builtin_amdgcn_s_setprio(3);                    // the chain goes first on its SIMD
         InT* dv = static_cast<InT*>(p.dv);
+        const int lane0 = lane, i0 = i;
         lds_barrier();
         lds_barrier();
         for (int it = 0; it < w.nc; ++it) {
+            // opaque in every chunk, or the LDS addresses, all functions of these, stay in registers
+            int lane = lane0, i = i0;
+            asm volatile("" : "+v"(lane), "+v"(i));
+            const int g4 = lane >> 4, r16 = lane & 15;
             if constexpr (L::NBUF == 1) lds_barrier();
             const int c = chunk_of(it);
             const int64_t block = w.block(p, c);
             const char* buf = smem + (it % L::NBUF) * L::bytes;
             const float* gates = reinterpret_cast<const float*>(buf + L::G);
-            f32x4 bt[4], eg[4], te[4], a[4], z[4];
+            f32x4 bt[4], eg[4], te[4], a[4], d[4], z[4], g[KT];
             PF<NX> kf[KS][4];
             read_rows<U, NX, KS>(kf, buf + L::Kr, L::XB, lane);
-            fence();
-            store_state(p.dend + block * (int64_t)p.V * K, (int64_t)i * K + 8 * g4, s);
-            rows_times_state<NX, KS, KT>(a, kf, s);
-            PF<NP> tf[6];
-            read_gate(te, gates + kGateToEnd, g4);
-            pass_get(pass(it) + L::ST, lane, z);          // scale M^T DO
-            read_tri<true>(tf, buf + L::T, lane);
-            fence();
-#pragma unroll
-            for (int t = 0; t < 4; ++t) a[t] = te[t] * a[t] + z[t];
-            const PF<NP> uf[2] = {pf_acc<NP>(a[0], a[1]), pf_acc<NP>(a[2], a[3])};
-            fence();
-            tri_times<true>(z, tf, uf);
-            read_gate(bt, gates + kGateBeta, g4);
-            read_gate(eg, gates + kGateEG, g4);
             const float eGC = gates[kGateEG + C - 1];
             fence();
-            PF<NX> kc[2][KT];
-            read_cols<U, NX, KT>(kc, buf + L::Kr, L::XB, lane);
-            f32x4 g[KT];
+            // a = K G1^T
+            store_state(p.dend + block * (int64_t)p.V * K, (int64_t)i * K + 8 * g4, s);
+            const PF<NP> sl = rows_times_state<NX, KS, KT>(a, kf, s, nullptr);
+            read_gate2(te, gates + kGateToEnd, g4, 2);
+            pass_get2(pass(it) + L::ST, lane, d, 2);      // scale M^T DO
+            PF<NP> tf[6];
+            read_tri<true>(tf, buf + L::T, 1, lane);
+            fence();
+            rows_step<NX, 2, 2>(a, kf[KS - 1], sl);
+            fence();
+            // the last of a; dU = e^(G_C - G) a + scale M^T DO of the last 32 tokens
+            rows_step<NX, 0, 2>(a, kf[KS - 1], sl);
+            const PF<NP> u1 = pf_acc<NP>(te[2] * a[2] + d[2], te[3] * a[3] + d[3]);
+            interleave<2 * products<NX>(), 10>();
+            // Z = T^T dU: what the last 32 tokens add; dU of the others; e^(G_C) G1 and dout's part
+            read_gate2(te, gates + kGateToEnd, g4, 0);
+            pass_get2(pass(it) + L::ST, lane, d, 0);
             pass_get(pass(it), lane, g);
-            store_tokens(p.z + block * (int64_t)C * p.V, i, g4, z);
+            fence();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) z[t] = zero4();
+            tri_step<true>(z, tf, 1, u1);
+            const PF<NP> u0 = pf_acc<NP>(te[0] * a[0] + d[0], te[1] * a[1] + d[1]);
+#pragma unroll
+            for (int t = 0; t < KT; ++t) s[t] = eGC * s[t] + g[t];
+            interleave<24, 4>();
+            // the rest of Z; dv = b Z and -e^G dv of the last 32 tokens
+            read_tri<true>(tf, buf + L::T, 0, lane);
+            read_gate2(bt, gates + kGateBeta, g4, 2);
+            read_gate2(eg, gates + kGateEG, g4, 2);
+            PF<NX> kc[KT], kd[KT];
+            read_cols<U, NX, KT>(kd, buf + L::Kr, L::XB, 1, lane);
+            fence();
             // dv: through the tiles just read, whose next writer comes after the barrier, to 16-byte pieces
             char* stage = pass(it) + L::ST;
             constexpr int SB = 16 * (int)sizeof(InT);     // a token's 16 columns
+            f32x4 e[4];
+            auto finish = [&](int t) {
+                const f32x4 x = bt[t] * z[t];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                z[t] = bt[t] * z[t];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) st(reinterpret_cast<InT*>(stage + idx(t, 4 * g4 + q) * SB) + r16, z[t][q]);
-                z[t] = -eg[t] * z[t];
-            }
+                for (int q = 0; q < 4; ++q) st(reinterpret_cast<InT*>(stage + idx(t, 4 * g4 + q) * SB) + r16, x[q]);
+                e[t] = -eg[t] * x;
+            };
+            tri_step<true>(z, tf, 0, u0);
+            finish(2);
+            finish(3);
+            const PF<NP> z1 = pf_acc<NP>(e[2], e[3]);
+            interleave<12, 6>();
+            // G0^T = e^(G_C) G1^T + ... - K^T (e^G dv)
+            read_gate2(bt, gates + kGateBeta, g4, 0);
+            read_gate2(eg, gates + kGateEG, g4, 0);
+            read_cols<U, NX, KT>(kc, buf + L::Kr, L::XB, 0, lane);
+            fence();
+            cols_step<NX, KT>(s, kd, z1);
+            finish(0);
+            finish(1);
+            const PF<NP> z0 = pf_acc<NP>(e[0], e[1]);
+            interleave<KT * products<NX>(), 4>();
+            cols_step<NX, KT>(s, kc, z0);
+            store_tokens(p.z + block * (int64_t)C * p.V, i, g4, z);
             wkv7::wave_lds_sync();
 #pragma unroll
             for (int j = 0; j < C * SB / 1024; ++j) {
-                const int e = 64 * j + lane, tt = c * C + e / (SB / 16);
-                const f32x4 v = *reinterpret_cast<const f32x4*>(stage + 16 * e);
+                const int n = 64 * j + lane, tt = c * C + n / (SB / 16);
+                const f32x4 x = *reinterpret_cast<const f32x4*>(stage + 16 * n);
                 if (tt < w.len)
                     *reinterpret_cast<f32x4*>(dv + ((w.tok0 + tt) * p.H + w.h) * p.V + 16 * (w.sub * NCW + cw) +
-                                              (e % (SB / 16)) * (16 / (int)sizeof(InT))) = v;
+                                              (n % (SB / 16)) * (16 / (int)sizeof(InT))) = x;
             }
-            const PF<NP> zf[2] = {pf_acc<NP>(z[0], z[1]), pf_acc<NP>(z[2], z[3])};
-#pragma unroll
-            for (int t = 0; t < KT; ++t) s[t] = eGC * s[t] + g[t];
-            fence();
-            add_cols_times<NX, KT>(s, kc, zf);
             lds_barrier();
         }
         if (p.dh0) store_state(p.dh0, soff, s);
@@ -719,7 +788,8 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
         const char* q = smem + L::Q0 + (it % L::NQ) * L::QB;
         const int c = chunk_of(it);
         f32x4 x[4], y[4], d[4];
-        column_tiles<L::RB>(y, q + NX * L::XB, cw, lane, InT());
+        column_tiles<L::RB>(y, q + NX * L::XB, cw, lane, InT(), 0);
+        column_tiles<L::RB>(y, q + NX * L::XB, cw, lane, InT(), 2);
         if (w.len - c * C < C) {                          // tokens past the end repeat the last one there
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -740,19 +810,18 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
             d[t] = p.scale * d[t];
             x[t] = p.scale * eg[t] * y[t];
         }
-        PF<NX> qc[2][KT];
-        read_cols<U, NX, KT>(qc, q, L::XB, lane);
-        load(it + 1);
+        PF<NX> qc[KT];
+        read_cols<U, NX, KT>(qc, q, L::XB, 0, lane);
         pass_put(pass(it) + L::ST, lane, d);
         // Q^T (scale e^G DO)
         const PF<NP> xf[2] = {pf_acc<NP>(x[0], x[1]), pf_acc<NP>(x[2], x[3])};
+        load(it + 1);
         f32x4 g[KT];
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            g[t] = zero4();
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) g[t] = pmma<NP>(g[t], qc[ks][t], xf[ks]);
-        }
+        for (int t = 0; t < KT; ++t) g[t] = zero4();
+        cols_step<NX, KT>(g, qc, xf[0]);
+        read_cols<U, NX, KT>(qc, q, L::XB, 1, lane);
+        cols_step<NX, KT>(g, qc, xf[1]);
         pass_put(pass(it), lane, g);
     };
     load(0);
