@@ -172,9 +172,8 @@ __device__ __forceinline__ void memory_wave(const Args& p, const Where& w, char*
     auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
 
     if (mw == 1) {
-        // T: fp32 pieces of eight values, one chunk ahead in registers, into planes
-        f32x4 x[6][2];
-        auto load = [&](int it) {
+        // T: fp32 pieces of eight values, two chunks ahead in two register sets, into planes
+        auto load = [&](f32x4 (&x)[6][2], int it) {
             if (it >= w.nc) return;
             const float* src = tri(it) + 8 * lane;
 #pragma unroll
@@ -183,7 +182,7 @@ __device__ __forceinline__ void memory_wave(const Args& p, const Where& w, char*
                 x[j][1] = *reinterpret_cast<const f32x4*>(src + 512 * j + 4);
             }
         };
-        auto put = [&](int it) {
+        auto put = [&](f32x4 (&x)[6][2], int it) {
             if (it >= w.nc) return;
 #pragma unroll
             for (int j = 0; j < 6; ++j) {
@@ -193,25 +192,25 @@ __device__ __forceinline__ void memory_wave(const Args& p, const Where& w, char*
 #pragma unroll
                 for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x8*>(dst + i * kTriBytes) = f.p[i];
             }
-            load(it + 1);
+            load(x, it + 2);
         };
-        load(0);
-        if constexpr (L::NBUF == 1) {
+        f32x4 even[6][2], odd[6][2];                      // chunks of even and odd number
+        load(even, 0);
+        load(odd, 1);
+        if constexpr (ahead > 0) put(even, 0);
+        if constexpr (ahead > 1) put(odd, 1);
+        lds_barrier();
+        if constexpr (BWD) lds_barrier();
+        for (int it = 0; it < w.nc; it += 2) {
+            if constexpr (ahead == 1) put(odd, it + ahead);
+            else put(even, it + ahead);
             lds_barrier();
-            if constexpr (BWD) lds_barrier();
-            for (int it = 0; it < w.nc; ++it) {
-                put(it);
-                lds_barrier();
-                lds_barrier();
-            }
-        } else {
-            for (int it = 0; it < ahead; ++it) put(it);
+            if constexpr (L::NBUF == 1) lds_barrier();
+            if (it + 1 == w.nc) break;
+            if constexpr (ahead == 1) put(even, it + 1 + ahead);
+            else put(odd, it + 1 + ahead);
             lds_barrier();
-            if constexpr (BWD) lds_barrier();
-            for (int it = 0; it < w.nc; ++it) {
-                put(it + ahead);
-                lds_barrier();
-            }
+            if constexpr (L::NBUF == 1) lds_barrier();
         }
         return;
     }
@@ -479,8 +478,9 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
                 constexpr int UPR = L::RB / 16, EPU = 16 / (int)sizeof(InT);
                 wkv7::wave_lds_sync();
 #pragma unroll
-                for (int j = 0; j < 16 * UPR / 64; ++j) {
+                for (int j = 0; j < (16 * UPR + 63) / 64; ++j) {
                     const int e = 64 * j + lane, tt = c * C + idx(TT, e / UPR);
+                    if (16 * UPR < 64 && e >= 16 * UPR) continue;
                     const f32x4 v = *reinterpret_cast<const f32x4*>(stage + 16 * e);
                     if (tt < w.len)
                         *reinterpret_cast<f32x4*>(o + ((w.tok0 + tt) * p.H + w.h) * p.V + w.sub * NCW * 16 + (e % UPR) * EPU) = v;
@@ -810,12 +810,12 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
             d[t] = p.scale * d[t];
             x[t] = p.scale * eg[t] * y[t];
         }
+        load(it + 1);
         PF<NX> qc[KT];
         read_cols<U, NX, KT>(qc, q, L::XB, 0, lane);
         pass_put(pass(it) + L::ST, lane, d);
         // Q^T (scale e^G DO)
         const PF<NP> xf[2] = {pf_acc<NP>(x[0], x[1]), pf_acc<NP>(x[2], x[3])};
-        load(it + 1);
         f32x4 g[KT];
 #pragma unroll
         for (int t = 0; t < KT; ++t) g[t] = zero4();
@@ -855,10 +855,16 @@ hipError_t launch_scan(const Args& a, bool bf16, hipStream_t s) {
     int n_cu = 0;
     const hipError_t e = wkv7::device_cus(&n_cu);
     if (e != hipSuccess) return e;
-    const bool many = (int64_t)a.N * a.H * (a.V / 64) >= n_cu;
+    // 16 rows to a workgroup where that leaves none waiting for a compute unit: a unit's issue slots are
+    // what bounds a chunk, and with one slice they serve one chain
+    const int64_t slices = (int64_t)a.N * a.H * (a.V / 16);
     if (bf16) {
-        if (a.K == 128) return launch_typed<uint16_t, 1, 128, 2, BWD>(a, s);
-        return many ? launch_typed<uint16_t, 1, 64, 4, BWD>(a, s) : launch_typed<uint16_t, 1, 64, 2, BWD>(a, s);
+        if (a.K == 128)
+            return slices <= n_cu ? launch_typed<uint16_t, 1, 128, 1, BWD>(a, s)
+                                  : launch_typed<uint16_t, 1, 128, 2, BWD>(a, s);
+        if (slices <= n_cu) return launch_typed<uint16_t, 1, 64, 1, BWD>(a, s);
+        return slices >= 4 * n_cu ? launch_typed<uint16_t, 1, 64, 4, BWD>(a, s)
+                                  : launch_typed<uint16_t, 1, 64, 2, BWD>(a, s);
     }
     return a.K == 64 ? launch_typed<float, 3, 64, 1, BWD>(a, s) : launch_typed<float, 3, 128, 1, BWD>(a, s);
 }
