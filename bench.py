@@ -73,8 +73,9 @@ OPS_BYTES = 36864      # transition operands P, M, E, F of one chunk of one head
 
 
 def source_digest() -> str:
+    """Of the recurrence's sources (wkv7_*), the ones the recorded counters are of."""
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
+    for name in sorted(n for n in os.listdir(CSRC) if n.startswith("wkv7_")):
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]
