@@ -18,7 +18,7 @@
  *   mean, rstd: (rows, groups) fp32.  dweight, dbias: (C) fp32.
  * - Statistics, sums and gradients are fp32 (the variance from the centred
  *   values); y and dx are rounded once.  NaN and Inf inputs propagate within their part.
- * - groups divides C, and D is at most 16384.
+ * - groups divides C, and D is at most 16384; C is at most 2^26, groups 2^20.
  * - Every pointer is a device pointer aligned to 16 bytes (mean, rstd, dweight and
  *   dbias: 4).
  * - Results do not vary from run to run: the sums over the rows go through

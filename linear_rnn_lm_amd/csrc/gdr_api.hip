@@ -39,8 +39,9 @@ wkv7_status shape(int B, int T, int Hk, int H, int K, int V, int dt, int N, bool
     s->N = packed ? N : B;
     s->slots = slots_of(B, T, N, packed);
     s->tokens = (int64_t)B * T;
-    // one workgroup per chunk and head, and up to V / 16 per sequence and head
-    if (s->slots > INT32_MAX / H || (int64_t)s->N * 8 > INT32_MAX / H) return WKV7_ERR_SHAPE;
+    // a launch takes fewer than 2^32 threads: at most 512 for each chunk and head, and 8 x 448 for each sequence
+    // and head
+    if (s->slots > ((1 << 23) - 1) / H || s->N > (1 << 20) / H) return WKV7_ERR_SHAPE;
     if (s->tokens > (int64_t(1) << 40) / ((int64_t)H * 128)) return WKV7_ERR_SHAPE;
     if ((int64_t)kChunk * H * V * 4 > INT32_MAX) return WKV7_ERR_SHAPE;   // 32-bit offsets inside a chunk
     s->q_elems = s->tokens * Hk * K;
@@ -92,10 +93,8 @@ void tri_in_ckpt(gdr::Args* a) {
 
 hipError_t split(const gdr::Args& a, const Shape& s, hipStream_t st) {
     if (s.bf16) return hipSuccess;
-    hipError_t e = gdr::launch_split(static_cast<const float*>(a.q), const_cast<uint16_t*>(a.qp.p), s.q_elems, st);
-    if (e == hipSuccess)
-        e = gdr::launch_split(static_cast<const float*>(a.k), const_cast<uint16_t*>(a.kp.p), s.q_elems, st);
-    return e;
+    return gdr::launch_split(static_cast<const float*>(a.q), static_cast<const float*>(a.k),
+                             const_cast<uint16_t*>(a.qp.p), const_cast<uint16_t*>(a.kp.p), s.q_elems, st);
 }
 
 }  // namespace
@@ -209,7 +208,7 @@ wkv7_status gdr_step(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dt
     wkv7_status st = heads_ok(B, T, Hk, H, K, V);
     if (st != WKV7_OK) return st;
     if (P < 1 || (!slots && P < B)) return WKV7_ERR_SHAPE;
-    if ((int64_t)B * 8 > INT32_MAX / H) return WKV7_ERR_SHAPE;
+    if (B > ((1 << 22) - 1) / H) return WKV7_ERR_SHAPE;           // at most 4 x 256 threads for each row and head
     const int64_t tokens = (int64_t)B * T, lim = (int64_t(1) << 40) / ((int64_t)H * 128);
     if (tokens > lim || (int64_t)P * 128 > lim) return WKV7_ERR_SHAPE;
     const int64_t e = in_dtype == WKV7_BF16 ? 2 : 4, qb = tokens * Hk * K * e, vb = tokens * H * V * e;

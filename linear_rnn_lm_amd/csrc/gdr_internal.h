@@ -61,7 +61,7 @@ struct ZeroArgs {
 };
 
 hipError_t launch_zero_outside(const ZeroArgs& a, hipStream_t s);
-hipError_t launch_split(const float* x, uint16_t* planes, int64_t n, hipStream_t s);
+hipError_t launch_split(const float* q, const float* k, uint16_t* qp, uint16_t* kp, int64_t n, hipStream_t s);
 hipError_t launch_prepare(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_fwd_scan(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_bwd_scan(const Args& a, bool bf16, hipStream_t s);

@@ -14,8 +14,10 @@ namespace {
 
 constexpr int LDA = 68;  // row stride (floats) of the fp32 64 x 64 matrices
 
-// fp32 values to three bf16 planes (24 bits), for fp32 inputs.
-__global__ __launch_bounds__(256) void split_kernel(const float* x, uint16_t* o, int64_t n) {
+// fp32 q (y = 0) and k (y = 1) to three bf16 planes (24 bits).
+__global__ __launch_bounds__(256) void split_kernel(const float* q, const float* k, uint16_t* qp, uint16_t* kp, int64_t n) {
+    const float* x = blockIdx.y ? k : q;
+    uint16_t* o = blockIdx.y ? kp : qp;
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;   // n is a multiple of 64
     if (i >= n) return;
     const f32x4 v = *reinterpret_cast<const f32x4*>(x + i);
@@ -217,8 +219,8 @@ hipError_t launch_zero_outside(const ZeroArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_split(const float* x, uint16_t* planes, int64_t n, hipStream_t s) {
-    hipLaunchKernelGGL(split_kernel, dim3((uint32_t)((n / 4 + 255) / 256)), dim3(256), 0, s, x, planes, n);
+hipError_t launch_split(const float* q, const float* k, uint16_t* qp, uint16_t* kp, int64_t n, hipStream_t s) {
+    hipLaunchKernelGGL(split_kernel, dim3((uint32_t)((n / 4 + 255) / 256), 2), dim3(256), 0, s, q, k, qp, kp, n);
     return hipGetLastError();
 }
 

@@ -433,6 +433,7 @@ bool is_dtype(int d) { return d == WKV7_F32 || d == WKV7_BF16; }
 wkv7_status check_shape(int64_t rows, int C, int groups, int xd, int yd, int wd) {
     if (!is_dtype(xd) || !is_dtype(yd) || !is_dtype(wd) || (xd == WKV7_BF16 && yd != WKV7_BF16)) return WKV7_ERR_DTYPE;
     if (rows < 1 || C < 1 || groups < 1 || C % groups || C / groups > 16384) return WKV7_ERR_SHAPE;
+    if (C > (1 << 26) || groups > (1 << 20)) return WKV7_ERR_SHAPE;   // a launch takes fewer than 2^32 threads
     if (rows > (int64_t(1) << 40) / C) return WKV7_ERR_SHAPE;
     return WKV7_OK;
 }

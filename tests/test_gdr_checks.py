@@ -288,3 +288,18 @@ def test_bad_offsets_stay_inside():
             x = _slot_chunk(cu, s, T)
             if x:
                 assert 0 <= x[1] and 1 <= x[2] <= 64 and x[1] + x[2] <= T
+
+
+@needs_no_gpu
+def test_sizes_that_no_launch_takes_are_refused():
+    """A launch holds fewer than 2^32 threads."""
+    assert _fwd(T=2 ** 23, H=64, Hk=1, B=1) == ERR_SHAPE                # 2^17 chunks of 64 heads
+    assert _fwd(B=2 ** 20, T=1, H=2) == ERR_SHAPE                       # sequences times heads
+    assert _fwd(T=1, H=2 ** 17, Hk=1) == ERR_SHAPE                      # a chunk's rows past 31 bits
+    s = gdr._lib().gdr_step
+    assert s(2 ** 20, 1, 1, 4, 64, 64, 1, *map(fake, range(5)), fake(5), 1, 0.1, fake(6), fake(7), fake(8),
+             None) == ERR_SHAPE
+    ln = lnorm._lib().ln_fwd
+    for C, G in ((2 ** 27, 2 ** 17), (2 ** 21, 2 ** 21)):
+        assert ln(1, C, G, 0, 0, 0, fake(0), None, None, 1e-5, fake(1), None, None, None) == ERR_SHAPE
+    assert gdr._lib().gdr_ckpt_bytes(1, 2 ** 23, 1, 64, 64, 64, 0, 0) == 0
