@@ -48,7 +48,7 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
     const InT* v = static_cast<const InT*>(p.v);
     InT* o = static_cast<InT*>(p.o);
 
-    int slot = b;
+    int slot = b, end = b + 1;                             // rows b .. end - 1 are looked through
     if (p.slots) {
         slot = p.slots[b];
         if (slot < 0 || slot >= p.P) {
@@ -57,20 +57,25 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
                     for (int i = 0; i < RT; ++i) st(o + (((int64_t)b * p.T + t) * p.H + h) * p.V + r0 + i, 0.f);
             return;
         }
-        int earlier = 0;
-        for (int e = tid; e < b; e += NT) earlier |= p.slots[e] == slot;
-        if (__syncthreads_or(earlier)) return;
     }
     const int64_t soff = (((int64_t)slot * p.H + h) * p.V + r0) * K + c0;
     f32x4 s[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
         s[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p.state + soff + i * K));
-    for (int row = b; row < p.B; ++row) {
-        if (row != b && (!p.slots || p.slots[row] != slot)) {
-            if (!p.slots) break;
-            continue;
+    if (p.slots) {                                         // while the state is on its way; every wave for itself
+        bool before = false, after = false;                // whether other rows have this slot
+#pragma unroll 4
+        for (int e = tid & 63; e < p.B; e += 64) {
+            const bool same = p.slots[e] == slot;
+            before |= same && e < b;
+            after |= same && e > b;
         }
+        if (__ballot(before)) return;
+        if (__ballot(after)) end = p.B;
+    }
+    for (int row = b; row < end; ++row) {
+        if (row != b && p.slots[row] != slot) continue;
         for (int t = 0; t < p.T; ++t) {
             const int64_t tok = (int64_t)row * p.T + t;
             const f32x4 q4 = load4(q + (tok * p.Hk + hk) * K + c0), k4 = load4(k + (tok * p.Hk + hk) * K + c0);

@@ -243,6 +243,7 @@ def _make_autograd():
 
         @staticmethod
         def forward(ctx, q, k, v, g, beta, h0=None, cu_seqlens=None, scale=None):
+            ctx.set_materialize_grads(False)               # a gradient that is not there costs nothing
             ins = [q.contiguous(), k.contiguous(), v.contiguous(), g.contiguous().float(), beta.contiguous().float()]
             h0c = None if h0 is None else h0.contiguous().float()
             need = any(ctx.needs_input_grad)

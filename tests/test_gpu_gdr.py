@@ -404,3 +404,81 @@ def test_prompt_then_steps_then_norm():
         for t in range(new):
             want = ref_norm(os_[t][n].reshape(1, -1).cpu(), w, None, H, 1e-5)["y"]
             assert rel(ys[t][n:n + 1], want) <= 2.0 ** -8 + 2 * V * 2.0 ** -24
+
+
+def test_step_many_rows_of_one_slot():
+    """More rows than a workgroup has threads, with the rows of a slot far apart and next to each other."""
+    note("gdr step, 600 rows, 300 slots")
+    B, H, P = 600, 1, 300
+    q, k, v, g, beta, h0, *_ = make(B, 1, 1, H, 64, 64, BF, seed=41, N=P)
+    slots = [b % P for b in range(B)]
+    slots[257], slots[258], slots[599] = 256, 256, 0
+    state = h0.to(DEV)
+    o = L.gdr_step(*dev(q, k, v, g, beta), state, slots=torch.tensor(slots, dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    want, wo = h0.double().clone(), torch.zeros(B, 1, H, 64, dtype=torch.float64)
+    for s in range(P):
+        rows = [b for b in range(B) if slots[b] == s]
+        if rows:
+            r = reference(*[x[rows].transpose(0, 1).contiguous() for x in (q, k, v, g, beta)], want[s:s + 1])
+            wo[rows], want[s] = r["o"].transpose(0, 1), r["hT"][0]
+    assert rel(o, wo) <= tol_fwd(64, BF) and rel(state, want) <= tol_fwd(64, F32)
+
+
+def test_two_streams_at_once():
+    """Two forwards and backwards in flight together, each on its own stream, against one after the other."""
+    note("gdr, two streams")
+    sets = [dev(*make(2, 300, 2, 4, 64, 128, BF, seed=s)) for s in (51, 52)]
+
+    def both(x):
+        q, k, v, g, beta, h0, do, dhT = x
+        o, ck, hT = L.gdr_fwd(q, k, v, g, beta, h0)
+        return [o, hT, *L.gdr_bwd(do, q, k, v, g, beta, ck, dhT)]
+
+    want = [both(x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = both(sets[i])
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_captured_training_step():
+    """Norm, rule and norm with their backward captured through autograd, on leaves that no eager graph
+    uses, replayed with other values and checked against eager passes on other leaves."""
+    note("gdr + ln autograd in a graph")
+    B, T, H, K = 2, 70, 2, 64
+    vals = [t.to(DEV) for t in make(B, T, H, H, K, K, BF, seed=61)[:5]] + [torch.ones(H * K, device=DEV)]
+    cot = torch.randn(B, T, H * K, generator=torch.Generator().manual_seed(3)).to(DEV, BF)
+
+    def grads(leaves):
+        q, k, v, g, beta, w = leaves
+        xn = L.LN.apply(v.reshape(B, T, H * K), w)
+        o, _ = L.GDR.apply(q, k, xn.view(B, T, H, K), g, beta)
+        y = L.LN.apply(o.reshape(B, T, H * K), w, None, H)
+        return torch.autograd.grad(y, leaves, cot)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        grads([x.clone().requires_grad_() for x in vals])
+    torch.cuda.current_stream().wait_stream(side)
+    leaves = [x.clone().requires_grad_() for x in vals]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = grads(leaves)
+    for i in range(4):
+        with torch.no_grad():
+            for x, y in zip(leaves, vals):
+                x.copy_(y)
+            leaves[2].mul_(1.0 + 0.5 * i)
+        graph.replay()
+        got = [t.clone() for t in outs]
+        want = grads([x.detach().clone().requires_grad_() for x in leaves])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
