@@ -47,25 +47,29 @@ __device__ __forceinline__ PF<NX> frag_mem(const Planes& x, int64_t row, int str
     return f;
 }
 
-// T = (I + A)^-1 for the strictly lower 64 x 64 matrix A, held transposed (At[s][t] =
-// A[t][s]).  Diagonal 16 x 16 blocks by forward substitution (one wave each, one
-// column per lane), then [[X, 0], [Z, Y]]^-1 = [[X', 0], [-Y' Z X', Y']] for blocks of
-// 16 and of 32 with fp32 MFMA products: stable for any A, unlike a series in
-// powers of A.  Z (16 x 16) = sign X Y over kn; XT: X is given transposed.
+// T = (I + A)^-1 for the strictly lower 64 x 64 matrix A.  Diagonal 16 x 16 blocks by
+// forward substitution (one wave each, one column per lane), then [[X, 0], [Z, Y]]^-1 =
+// [[X', 0], [-Y' Z X', Y']] for blocks of 16 and of 32 with fp32 MFMA products: stable
+// for any A, unlike a series in powers of A.  One LDS matrix holds both: A transposed in
+// its upper half, T in its lower (a diagonal block of T replaces A's once that is used
+// up).  18 KB to a workgroup instead of 35 lets more of them overlap their waits.
+// A 16 x 16 tile of X Y over kn; XT: X is given transposed.
 template <bool XT>
-__device__ __forceinline__ void block_product(const float* X, const float* Y, float* Z, int kn, float sign, int lane) {
+__device__ __forceinline__ f32x4 block_product(const float* X, const float* Y, int kn, int lane) {
     const int r = lane & 15, g = lane >> 4;
     f32x4 acc = zero4();
     for (int k0 = 0; k0 < kn; k0 += 4)
         acc = wkv7::mfma_f32(XT ? X[(k0 + g) * LDA + r] : X[r * LDA + k0 + g], Y[(k0 + g) * LDA + r], acc);
+    return acc;
+}
+__device__ __forceinline__ void put_tile(float* Z, f32x4 x, int lane) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) Z[(4 * g + q) * LDA + r] = sign * acc[q];
+    for (int q = 0; q < 4; ++q) Z[(4 * (lane >> 4) + q) * LDA + (lane & 15)] = x[q];
 }
 
 template <int NX, int K>
-__global__ __launch_bounds__(256, 4) void prepare_kernel(Args p) {
-    __shared__ __attribute__((aligned(16))) float At[C * LDA];
-    __shared__ __attribute__((aligned(16))) float Ts[C * LDA];
+__global__ __launch_bounds__(256, NX == 1 ? 7 : 4) void prepare_kernel(Args p) {
+    __shared__ __attribute__((aligned(16))) float X[C * LDA];   // X[s][t] = A[t][s] for s < t; X[t][s] = T[t][s]
     __shared__ float nf[2][C], bs[C];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int g4 = lane >> 4, r16 = lane & 15;
@@ -83,19 +87,21 @@ __global__ __launch_bounds__(256, 4) void prepare_kernel(Args p) {
     Planes kp = p.kp;
     kp.p += tok * stride + hk * K;
     auto row = [&](int t) { return min(t, len - 1); };   // tokens past the end: masked below
-    PF<NX> ka[KS], kb[4][KS];
+    // 64 columns of the rows at a time (32 of three planes): all of them at once, one wait for memory
+    constexpr int KB = NX == 1 ? 2 : 1;
+    PF<NX> ka[KB], kb[4][KB];
     const int ra = row(idx(w, r16));
+    auto fetch = [&](int k0) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) ka[ks] = frag_mem<NX>(kp, ra, stride, ks, lane);
-    if constexpr (NX == 1) {                             // all rows at once: one wait for memory
+        for (int ks = 0; ks < KB; ++ks) {
+            ka[ks] = frag_mem<NX>(kp, ra, stride, k0 + ks, lane);
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-            if (nt < 2 || w >= 2) {
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) kb[nt][ks] = frag_mem<NX>(kp, row(idx(nt, r16)), stride, ks, lane);
-            }
+            for (int nt = 0; nt < 4; ++nt)
+                if (nt < 2 || w >= 2) kb[nt][ks] = frag_mem<NX>(kp, row(idx(nt, r16)), stride, k0 + ks, lane);
+        }
         __builtin_amdgcn_sched_barrier(0);
-    }
+    };
+    fetch(0);
 
     if (w == 3) {
         float g = 0.f, b = 0.f;
@@ -122,20 +128,17 @@ __global__ __launch_bounds__(256, 4) void prepare_kernel(Args p) {
         gt[kGateBeta + lane] = b;
         gt[kGateN + lane] = (float)n2;
         gt[kGateF + lane] = (float)(y - n2);
-    } else if (w < 2) {
-        // the zero 16 x 16 blocks of T's diagonal 32 x 32 blocks
-        *reinterpret_cast<f32x4*>(Ts + (32 * w + (lane >> 2)) * LDA + 32 * w + 16 + 4 * (lane & 3)) = zero4();
     }
-    f32x4 kk[4];
+    f32x4 kk[4] = {zero4(), zero4(), zero4(), zero4()};
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-        kk[nt] = zero4();
-        if (nt >= 2 && w < 2) continue;
+    for (int k0 = 0; k0 < KS; k0 += KB) {
+        if (k0 > 0) fetch(k0);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            if constexpr (NX > 1) kb[nt][ks] = frag_mem<NX>(kp, row(idx(nt, r16)), stride, ks, lane);
-            kk[nt] = pmma<NX>(kk[nt], ka[ks], kb[nt][ks]);
-        }
+        for (int nt = 0; nt < 4; ++nt)
+            if (nt < 2 || w >= 2) {
+#pragma unroll
+                for (int ks = 0; ks < KB; ++ks) kk[nt] = pmma<NX>(kk[nt], ka[ks], kb[nt][ks]);
+            }
     }
     __syncthreads();
     const int t0 = idx(w, 4 * g4);
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(256, 4) void prepare_kernel(Args p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             a[q] = s < t0 + q && t0 + q < len ? b4[q] * decay(nt4[q], ft4[q], nf[0][s], nf[1][s]) * kk[nt][q] : 0.f;
-        *reinterpret_cast<f32x4*>(At + s * LDA + t0) = a;
+        *reinterpret_cast<f32x4*>(X + s * LDA + t0) = a;
     }
     __syncthreads();
 
@@ -161,38 +164,43 @@ __global__ __launch_bounds__(256, 4) void prepare_kernel(Args p) {
         // once x[s] is final every later row takes A[t][s] x[s]; column s of A is read in
         // 16-byte pieces, five columns ahead of their use
 #pragma unroll
-        for (int s0 = 0; s0 < 15; s0 += 5) {
-            f32x4 col[5][4];
+        for (int s0 = 0; s0 < 15; s0 += 3) {
+            f32x4 col[3][4];
 #pragma unroll
-            for (int s = s0; s < s0 + 5; ++s)
+            for (int s = s0; s < s0 + 3; ++s)
 #pragma unroll
                 for (int c = (s + 1) / 4; c < 4; ++c)
-                    col[s - s0][c] = *reinterpret_cast<const f32x4*>(At + (o + s) * LDA + o + 4 * c);
+                    col[s - s0][c] = *reinterpret_cast<const f32x4*>(X + (o + s) * LDA + o + 4 * c);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int s = s0; s < s0 + 5; ++s)
+            for (int s = s0; s < s0 + 3; ++s)
 #pragma unroll
                 for (int t = s + 1; t < 16; ++t) x[t] = fmaf(-col[s - s0][t / 4][t % 4], x[s], x[t]);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int t = 0; t < 16; ++t) Ts[(o + t) * LDA + o + lane] = x[t];
+        for (int t = 0; t < 16; ++t) X[(o + t) * LDA + o + lane] = x[t];
     }
     __syncthreads();
-    // blocks of 16: the scratch products lie in At's part for t < s, which is unused
+    // blocks of 16, Z X' in its result's place; A's block then becomes T's zero block
     if (w < 2) {
-        const int o = 32 * w;
-        float* scr = At + (o + 16) * LDA + o;
-        block_product<true>(At + o * LDA + o + 16, Ts + o * LDA + o, scr, 16, 1.f, lane);
+        float* d = X + 32 * w * (LDA + 1);
+        put_tile(d + 16 * LDA, block_product<true>(d + 16, d, 16, lane), lane);
         wkv7::wave_lds_sync();
-        block_product<false>(Ts + (o + 16) * LDA + o + 16, scr, Ts + (o + 16) * LDA + o, 16, -1.f, lane);
+        const f32x4 z = block_product<false>(d + 16 * LDA + 16, d + 16 * LDA, 16, lane);
+        wkv7::wave_lds_sync();
+        put_tile(d + 16 * LDA, -z, lane);
+        put_tile(d + 16, zero4(), lane);
     }
     __syncthreads();
     // blocks of 32: wave (mr, mc) forms one 16 x 16 tile of each product
     const int mr = 16 * (w >> 1), mc = 16 * (w & 1);
-    block_product<true>(At + 32 + mr, Ts + mc, At + (32 + mr) * LDA + mc, 32, 1.f, lane);
+    float* d = X + (32 + mr) * LDA + mc;
+    put_tile(d, block_product<true>(X + 32 + mr, X + mc, 32, lane), lane);
     __syncthreads();
-    block_product<false>(Ts + (32 + mr) * LDA + 32, At + 32 * LDA + mc, Ts + (32 + mr) * LDA + mc, 32, -1.f, lane);
+    const f32x4 z = block_product<false>(X + (32 + mr) * LDA + 32, X + 32 * LDA + mc, 32, lane);
+    __syncthreads();
+    put_tile(d, -z, lane);
     __syncthreads();
 
     // the three lower 32 x 32 blocks, in pieces of eight values: block, row, eight columns
@@ -200,7 +208,7 @@ __global__ __launch_bounds__(256, 4) void prepare_kernel(Args p) {
     for (int e = tid; e < 768; e += 256) {
         const int blk = e >> 8, row = (e >> 3) & 31, u = e & 7;
         *reinterpret_cast<f32x4*>(out + 4 * e) =
-            *reinterpret_cast<const f32x4*>(Ts + ((blk ? 32 : 0) + row) * LDA + (blk == 2 ? 32 : 0) + 4 * u);
+            *reinterpret_cast<const f32x4*>(X + ((blk ? 32 : 0) + row) * LDA + (blk == 2 ? 32 : 0) + 4 * u);
     }
 }
 
