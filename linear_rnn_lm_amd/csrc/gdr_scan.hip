@@ -86,8 +86,13 @@ struct Where {
     int n, h, hk, sub, len, slot0, nc;
     int64_t tok0;
     __device__ __forceinline__ Where(const Args& p, int nsub) {
-        sub = blockIdx.x % nsub;
-        const int nh = blockIdx.x / nsub;
+        // Workgroups go to the eight XCDs in turn; those that read the same q and k (the slices of the
+        // heads of a key head) are put on one, so that its L2 serves all but the first of them.
+        const uint32_t group = nsub * (p.H / p.Hk), round = 8 * group, whole = gridDim.x / round * round;
+        uint32_t id = blockIdx.x;
+        if (id < whole) id = id / round * round + id % 8 * group + id % round / 8;
+        sub = id % nsub;
+        const int nh = id / nsub;
         h = nh % p.H;
         n = nh / p.H;
         hk = h / (p.H / p.Hk);
