@@ -15,6 +15,12 @@
 // are row sums of terms that are there anyway).  q and k of one key head serve
 // H / Hk value heads: one workgroup does all of them in turn, so the sums over
 // the heads stay in registers and in one order.
+//
+// It reads S, U, G1, Z, q, k and dout and writes dq and dk: 1.73 GB at B8 T4096 H32 64 x 64,
+// 340 us at the rate of a large copy; it takes 445 to 480 (the splitting into planes
+// and the products overlap the loads of the other workgroup on the unit, not wholly).
+// With K = 128, 8200 packed tokens, 8 key and 16 value heads 232 us: U and Z are read
+// once for either half of the columns, and 1096 workgroups make 2.1 rounds of 512.
 #include "gdr_device.h"
 #include "gdr_internal.h"
 #include "wkv7_internal.h"

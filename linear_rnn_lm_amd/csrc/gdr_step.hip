@@ -3,7 +3,9 @@
 //
 // A thread holds RT consecutive rows of four columns of the state; the K / 4
 // threads of a row share a half wave or a DPP row, so the row sums S k and S q
-// need no LDS.  The state is read once and written once: bound by HBM.
+// need no LDS.  The state is read once and written once: bound by HBM (256 rows of
+// 64 heads of 64 x 64: 537 MB in 84 us, 6.4 TB/s; 100 us where slots say which state is
+// whose, since those loads wait for the slot).
 #include "gdr_device.h"
 #include "gdr_internal.h"
 #include "wkv7_internal.h"

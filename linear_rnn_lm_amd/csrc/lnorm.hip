@@ -1,7 +1,9 @@
 // lnorm.hip -- layer norm over the parts of a row, forward and backward (gfx950).
 //
 // Bound by HBM: x is read once and kept in registers for the mean, the centred
-// variance and the output; the backward reads x and dy once.  A part of D
+// variance and the output (32768 x 2048 in 32 parts, bf16: 48 us, 5.6 TB/s); the backward
+// reads x and dy once (the same: 84 us, 4.8 TB/s).  Small calls are bound by the launch
+// (256 x 4096: 4.6 us on the GPU, 11 us a call).  A part of D
 // channels belongs to a team of L lanes (part of a wave, a wave, or a
 // workgroup), NV vectors of VEC values per lane.  A team keeps one group index and walks
 // rows, so its weight and bias stay in registers, and in the backward so
@@ -316,7 +318,7 @@ __global__ __launch_bounds__(threads<L>()) void bwd_kernel(Args p) {
         }
 }
 
-// Column sums of the (parts, C) sums: 32 columns by 32 rows of threads, four rows each in flight.
+// Column sums of the (parts, C) sums, 3 to 5 us (a launch and one round trip): 32 columns by 32 rows of threads, four rows each in flight.
 __global__ __launch_bounds__(1024) void reduce_kernel(const float* part, int parts, int C, float* dweight, float* dbias) {
     __shared__ float red[32][33];
     const int cl = threadIdx.x & 31, c = blockIdx.x * 32 + cl, r0 = threadIdx.x >> 5;
@@ -336,7 +338,9 @@ __global__ __launch_bounds__(1024) void reduce_kernel(const float* part, int par
     if ((threadIdx.x & 31) == 0 && blockIdx.x * 32 + r0 < C) (blockIdx.y ? dbias : dweight)[blockIdx.x * 32 + r0] = x;
 }
 
-// Lanes per team and vectors per lane for D channels.
+// Lanes per team and vectors per lane for D channels: the fewest lanes that hold a part in
+// four 16-byte vectors each, so that a workgroup keeps many rows in flight and a sum takes
+// few exchanges; D that is no multiple of 8 goes by single values.
 struct Plan {
     int vec, L, NV;
 };
@@ -354,7 +358,8 @@ Plan plan_of(int D) {
     return {1, 1024, 16};
 }
 
-// Teams of a launch: a multiple of G, at most what the chip holds at once.
+// Teams of a launch: a multiple of G, at most what the chip holds at once (32 waves per
+// unit; 16 or 64 changed nothing from 12288 x 384 to 65536 x 768).
 int teams_of(int64_t rows, int G, int L, int n_cu, int waves_per_cu) {
     const int64_t most = (int64_t)n_cu * waves_per_cu * 64 / L;
     int64_t r = most / G;
@@ -365,8 +370,12 @@ int teams_of(int64_t rows, int G, int L, int n_cu, int waves_per_cu) {
 
 // How the backward's rows are shared out.  Where a workgroup of 256 holds the teams of one or
 // more whole rows (combine), each workgroup leaves one row of sums; otherwise each team
-// leaves its own.  At least two (eight) rows to a team, so that the sums
-// stay small beside x, dy and dx, and at most what fills the chip.
+// leaves its own.  At least two (eight) rows to a team, so that the sums stay small beside
+// x, dy and dx; from 256 workgroups on at least eight, and at most 512 of them: the sums
+// are written and read again, and more rows in flight no longer help (gradients of 65536
+// x 768: 53 us, with 1024 of them 60, with 256 53; 32768 x 2048 in 32 parts: 84, 86, 119;
+// 4096 x 2048: 22 with 256, 24 with 512).  Without combining: 65536 x 768 92 us,
+// 12288 x 384 20 instead of 14.
 struct Share {
     bool combine;
     int parts;
@@ -375,8 +384,9 @@ Share bwd_share(int64_t rows, int D, int G) {
     const Plan pl = plan_of(D);
     const int S = 256 / pl.L;
     if (pl.L <= 64 && S % G == 0) {
-        const int64_t per = S / G, few = (rows + 2 * per - 1) / (2 * per);
-        return {true, (int)(few < 1024 ? few : 1024)};
+        const int64_t per = S / G, few = (rows + 2 * per - 1) / (2 * per), good = rows / (8 * per);
+        const int64_t most = good < 256 ? 256 : good < 512 ? good : 512;
+        return {true, (int)(few < most ? few : most)};
     }
     const int64_t most = (int64_t)256 * 16 * 64 / pl.L / G + 1, few = (rows + 7) / 8;
     return {false, (int)(few < most ? few : most)};
