@@ -37,7 +37,7 @@
  *   three bf16 planes per fp32 value (24 bits), sums of log decays 64 bits.
  * - Chunks are 64 tokens, counted from each sequence's first.  A call has
  *   gdr_slots(...) chunk slots: N * ceil(T / 64) dense, T / 64 + N packed.  Chunk
- *   slots times H must stay below 2^23, and N * H at most 2^20 (gdr_step: B * H
+ *   slots times H must stay below 2^22 - 15, and N * H at most 2^20 (gdr_step: B * H
  *   below 2^22).
  * - Every pointer is a device pointer aligned to 16 bytes (cu_seqlens and slots: 4).
  * - Results do not vary from run to run.

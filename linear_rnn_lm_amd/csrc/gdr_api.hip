@@ -39,9 +39,9 @@ wkv7_status shape(int B, int T, int Hk, int H, int K, int V, int dt, int N, bool
     s->N = packed ? N : B;
     s->slots = slots_of(B, T, N, packed);
     s->tokens = (int64_t)B * T;
-    // a launch takes fewer than 2^32 threads: at most 512 for each chunk and head, and 8 x 448 for each sequence
-    // and head
-    if (s->slots > ((1 << 23) - 1) / H || s->N > (1 << 20) / H) return WKV7_ERR_SHAPE;
+    // a launch takes fewer than 2^32 threads: at most 2 x 512 for each chunk and head (and 15 workgroups more), 8 x
+    // 448 for each sequence and head
+    if (s->slots > ((1 << 22) - 16) / H || s->N > (1 << 20) / H) return WKV7_ERR_SHAPE;
     if (s->tokens > (int64_t(1) << 40) / ((int64_t)H * 128)) return WKV7_ERR_SHAPE;
     if ((int64_t)kChunk * H * V * 4 > INT32_MAX) return WKV7_ERR_SHAPE;   // 32-bit offsets inside a chunk
     s->q_elems = s->tokens * Hk * K;

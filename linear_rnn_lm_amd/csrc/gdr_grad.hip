@@ -19,8 +19,9 @@
 // It reads S, U, G1, Z, q, k and dout and writes dq and dk: 1.73 GB at B8 T4096 H32 64 x 64,
 // 340 us at the rate of a large copy; it takes 445 to 480 (the splitting into planes
 // and the products overlap the loads of the other workgroup on the unit, not wholly).
-// With K = 128, 8200 packed tokens, 8 key and 16 value heads 232 us: U and Z are read
-// once for either half of the columns, and 1096 workgroups make 2.1 rounds of 512.
+// K = 128 takes a workgroup for either half of the columns: with one for both, 8200 packed
+// tokens of 8 key and 16 value heads made 2.1 rounds of the chip's 512 and 232 us, now
+// 4.3 rounds of half the work and 207 us.
 #include "gdr_device.h"
 #include "gdr_internal.h"
 #include "wkv7_internal.h"
@@ -97,7 +98,11 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
     float* dGp = red + 64;               // [2][64]
     float* ep = dGp + 128;               // [2][64]
     const int tid0 = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid0 >> 6);
-    const int slot = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk, rep = ONE ? 1 : p.H / p.Hk;
+    // K = 128: two workgroups, one for either half js of the columns, eight apart in the launch's order, so
+    // that they are on one XCD and share U and Z in its L2
+    const int js = KJ == 1 ? 0 : blockIdx.x / 8 % KJ, work = KJ == 1 ? blockIdx.x : blockIdx.x / (8 * KJ) * 8 + blockIdx.x % 8;
+    const int slot = work / p.Hk, hk = work % p.Hk, rep = ONE ? 1 : p.H / p.Hk;
+    if (slot >= p.slots) return;
     const Seqs seqs{p.cu, p.N, p.T, p.NC};
     int n, len;
     int64_t tok;
@@ -108,9 +113,6 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
     const int c = wave & 1, tt = wave >> 1;
     const int V = p.V;
 
-    // Slices outside, heads inside: the sums over the heads are those of one slice.  What
-    // dg has of the slices before is in memory, written by the same lanes.
-    for (int js = 0; js < KJ; ++js) {
     F8 gq{zero4(), zero4()}, gk{zero4(), zero4()};
     for (int hr = 0; hr < rep; ++hr) {
         // The thread's number is made opaque in every round, or the loops' many LDS
@@ -308,12 +310,13 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
             }
             if (lane < len) {
                 float* dg = p.dg + (tok + lane) * p.H + h;
-                *dg = (float)(js ? x + *dg : x);
-                p.dbeta[(tok + lane) * p.H + h] = dbeta[lane];
+                // two halves, added to the zero that the scan left: the order makes no difference to a sum of two
+                if (KJ > 1) unsafeAtomicAdd(dg, (float)x);
+                else *dg = (float)x;
+                if (js == 0) p.dbeta[(tok + lane) * p.H + h] = dbeta[lane];
             }
         }
-        if (KJ > 1 || !ONE) __syncthreads();          // wave 0 reads what the next round overwrites
-    }
+        if (!ONE) __syncthreads();                    // wave 0 reads what the next round overwrites
     }
 }
 
@@ -324,7 +327,8 @@ hipError_t launch_typed(const Args& a, hipStream_t s) {
     static wkv7::PerDeviceOnce once;
     const hipError_t e = wkv7::set_smem_once(once, kern, Lds<NX>::bytes);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((uint32_t)a.slots * a.Hk), dim3(NT), Lds<NX>::bytes, s, a);
+    const uint32_t n = (uint32_t)a.slots * a.Hk;
+    hipLaunchKernelGGL(kern, dim3(K == 64 ? n : (n + 7) / 8 * 16), dim3(NT), Lds<NX>::bytes, s, a);
     return hipGetLastError();
 }
 

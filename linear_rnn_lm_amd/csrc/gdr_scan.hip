@@ -799,6 +799,8 @@ __global__ __launch_bounds__(64 * (2 * NCW + 2)) void bwd_kernel(Args p, int nsu
     auto work = [&](int it) {
         const char* q = smem + L::Q0 + (it % L::NQ) * L::QB;
         const int c = chunk_of(it);
+        // two workgroups of the gradient kernel add to dg where K = 128
+        if (K == 128 && w.sub == 0 && cw == 0 && c * C + lane < w.len) p.dg[(w.tok0 + c * C + lane) * p.H + w.h] = 0.f;
         f32x4 x[4], y[4], d[4];
         column_tiles<L::RB>(y, q + NX * L::XB, cw, lane, InT(), 0);
         column_tiles<L::RB>(y, q + NX * L::XB, cw, lane, InT(), 2);
