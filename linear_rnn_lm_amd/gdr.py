@@ -235,6 +235,7 @@ def gdr_step(q, k, v, g, beta, state, *, slots=None, scale=None, state_out=None,
 
 def _make_autograd():
     import torch
+    from torch.autograd.function import once_differentiable
 
     class GDR(torch.autograd.Function):
         """Differentiable op: (q, k, v, g, beta, h0, cu_seqlens, scale) -> (o, hT),
@@ -253,6 +254,7 @@ def _make_autograd():
             return o, hT
 
         @staticmethod
+        @once_differentiable                               # a gradient of the gradient is an error, not a zero
         def backward(ctx, do, dhT):
             *ins, ckpt, cu = ctx.saved_tensors
             do = torch.zeros_like(ins[2]) if do is None else do.to(ins[2].dtype).contiguous()

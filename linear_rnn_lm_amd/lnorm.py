@@ -144,6 +144,7 @@ def ln_bwd(dy, x, weight, mean, rstd, *, groups=1, want_dx=True, want_dw=True, w
 
 def _make_autograd():
     import torch
+    from torch.autograd.function import once_differentiable
 
     class LN(torch.autograd.Function):
         """Differentiable op: (x, weight, bias, groups, eps, out_dtype) -> y, gradients by
@@ -160,6 +161,7 @@ def _make_autograd():
             return y
 
         @staticmethod
+        @once_differentiable                               # a gradient of the gradient is an error, not a zero
         def backward(ctx, dy):
             x, weight, mean, rstd = ctx.saved_tensors
             nx, nw, nb = (*ctx.needs_input_grad, False, False)[:3]     # only what was passed is listed

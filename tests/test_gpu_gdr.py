@@ -482,3 +482,51 @@ def test_captured_training_step():
         want = grads([x.detach().clone().requires_grad_() for x in leaves])
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+
+
+def test_offsets_past_31_and_32_bits():
+    """A short sequence at the end of a row so long that token and checkpoint offsets pass 2^31 and 2^32, and a
+    step on the last states of a pool of more than 2^32 values, against the same calls on short tensors."""
+    note("gdr, long offsets")
+    H, K, V, n = 16, 64, 128, 100
+    T = (1 << 20) + 200
+    x = dev(*make(1, n, H, H, K, V, BF, seed=71, N=1))
+    q, k, v, g, beta, h0, do, dhT = x
+    o, ck, hT = L.gdr_fwd(q, k, v, g, beta, h0)
+    want = [o, *L.gdr_bwd(do, q, k, v, g, beta, ck, dhT)]
+
+    def tail(t):
+        big = torch.empty(1, T, *t.shape[2:], dtype=t.dtype, device=DEV)
+        big[:, T - n:] = t
+        return big
+
+    bq, bk, bv, bg, bb, bdo = [tail(t) for t in (q, k, v, g, beta, do)]
+    assert bv.numel() > 2 ** 31
+    cu = cu_of([T - n, T])
+    bo, bck, bhT = L.gdr_fwd(bq, bk, bv, bg, bb, h0, cu_seqlens=cu)
+    assert bck.numel() > 2 ** 32
+    got = [bo, *L.gdr_bwd(bdo, bq, bk, bv, bg, bb, bck, dhT, cu_seqlens=cu)]
+    torch.cuda.synchronize()
+    assert torch.equal(bhT, hT)
+    for a, b in zip(got[:-1], want):
+        assert torch.equal(a[:, T - n:], b) and not a[:, :T - n:4099].any()
+    assert torch.equal(got[-1], want[-1])
+    del bq, bk, bv, bg, bb, bdo, bo, bck, got
+
+    P = (1 << 32) // (H * V * K) + 2
+    pool = torch.empty(P, H, V, K, device=DEV)
+    pool[P - 1], pool[1] = h0[0], h0[0]
+    row = [t[:, :1].contiguous().expand(2, 1, *t.shape[2:]).contiguous() for t in (q, k, v, g, beta)]
+    os_ = L.gdr_step(*row, pool, slots=torch.tensor([P - 1, 1], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(os_[0], os_[1]) and torch.equal(pool[P - 1], pool[1]) and not torch.equal(pool[1], h0[0])
+
+
+def test_no_gradient_of_the_gradient():
+    note("gdr + ln, second derivative refused")
+    q, k, v, g, beta, *_ = dev(*make(1, 5, 1, 1, 64, 64, F32, seed=81))
+    v.requires_grad_()
+    for y in (L.GDR.apply(q, k, v, g, beta)[0], L.LN.apply(v.reshape(5, 64))):
+        dv, = torch.autograd.grad(y.square().sum(), v, create_graph=True)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(dv.sum(), v)

@@ -181,3 +181,24 @@ def test_norm_of_the_recurrences_output():
     z = L.ln_fwd(y.view(2, 40, 192), w.to(DEV), groups=3, eps=64e-5, out_dtype=BF, want_stats=False)[0]
     want = ref_norm(y.view(80, 192).cpu(), w, None, 3, 64e-5)["y"]
     assert z.dtype == BF and rel(z.view(80, 192), want) <= 2.0 ** -8 + 140 * EPS
+
+
+def test_offsets_past_31_bits():
+    """The last rows of a tensor of more than 2^31 values, against the same rows alone."""
+    note("ln, long offsets")
+    rows, C, n = (1 << 20) + 5, 2056, 7
+    gen = torch.Generator().manual_seed(9)
+    xs, ds = (torch.randn(n, C, generator=gen).to("cuda", torch.bfloat16) for _ in range(2))
+    x, dy = (torch.zeros(rows, C, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[-n:], dy[-n:] = xs, ds
+    assert x.numel() > 2 ** 31
+    y, mean, rstd = L.ln_fwd(x)
+    ys, ms, rs = L.ln_fwd(xs)
+    dx, dw, db = L.ln_bwd(dy, x, None, mean, rstd)
+    dxs, dws, dbs = L.ln_bwd(ds, xs, None, ms, rs)
+    torch.cuda.synchronize()
+    assert torch.equal(y[-n:], ys) and torch.equal(mean[-n:], ms) and torch.equal(dx[-n:], dxs)
+    # n terms of at most 5 max abs(dy) (xh stays below 5 here), summed in another order: n roundings of their
+    # total at most, on either side
+    for a, b in ((dw, dws), (db, dbs)):
+        assert (a - b).abs().max() <= 2 * n * 2.0 ** -24 * n * ds.abs().max().float() * 5
