@@ -5,10 +5,11 @@
 //
 // with the chunk's gates (see gdr_device.h).  All chunks of all heads run at
 // once, one workgroup of four waves each.  The data moved would take 57 us at B8
-// T4096 H32 K64 (16384 chunks of heads; 290 MB), the kernel takes 136: each workgroup is a row
+// T4096 H32 K64 (16384 chunks of heads; 290 MB), the kernel takes 124: each workgroup is a row
 // of dependent steps (loads, products, substitution, two levels of block products), so
 // what counts is how many of them a unit holds.  Seven fit 18 KB of LDS and 72 registers
-// each; four, with A and T apart and five columns of A ahead, took 171 us, six 140.
+// each; four, with A and T apart and five columns of A ahead, took 171 us, and eight, which
+// have to spill, 144 where seven took 129.  At K = 128 (B1 T32768 H32, 355 MB) 147 us.
 #include "gdr_device.h"
 #include "gdr_internal.h"
 #include "wkv7_internal.h"
@@ -52,7 +53,7 @@ __device__ __forceinline__ PF<NX> frag_mem(const Planes& x, int64_t row, int str
 }
 
 // T = (I + A)^-1 for the strictly lower 64 x 64 matrix A.  Diagonal 16 x 16 blocks by
-// forward substitution (one wave each, one column per lane), then [[X, 0], [Z, Y]]^-1 =
+// forward substitution (one column per lane), then [[X, 0], [Z, Y]]^-1 =
 // [[X', 0], [-Y' Z X', Y']] for blocks of 16 and of 32 with fp32 MFMA products: stable
 // for any A, unlike a series in powers of A.  One LDS matrix holds both: A transposed in
 // its upper half, T in its lower (a diagonal block of T replaces A's once that is used
@@ -93,15 +94,14 @@ __global__ __launch_bounds__(256, NX == 1 ? 7 : 4) void prepare_kernel(Args p) {
     auto row = [&](int t) { return min(t, len - 1); };   // tokens past the end: masked below
     // 64 columns of the rows at a time (32 of three planes): all of them at once, one wait for memory
     constexpr int KB = NX == 1 ? 2 : 1;
-    PF<NX> ka[KB], kb[4][KB];
-    const int ra = row(idx(w, r16));
+    // tile i here is tile w ^ i of the matrix: the first is this wave's own rows as well
+    PF<NX> kb[4][KB];
     auto fetch = [&](int k0) {
 #pragma unroll
         for (int ks = 0; ks < KB; ++ks) {
-            ka[ks] = frag_mem<NX>(kp, ra, stride, k0 + ks, lane);
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt)
-                if (nt < 2 || w >= 2) kb[nt][ks] = frag_mem<NX>(kp, row(idx(nt, r16)), stride, k0 + ks, lane);
+                if (nt < 2 || w >= 2) kb[nt][ks] = frag_mem<NX>(kp, row(idx(w ^ nt, r16)), stride, k0 + ks, lane);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -141,7 +141,7 @@ __global__ __launch_bounds__(256, NX == 1 ? 7 : 4) void prepare_kernel(Args p) {
         for (int nt = 0; nt < 4; ++nt)
             if (nt < 2 || w >= 2) {
 #pragma unroll
-                for (int ks = 0; ks < KB; ++ks) kk[nt] = pmma<NX>(kk[nt], ka[ks], kb[nt][ks]);
+                for (int ks = 0; ks < KB; ++ks) kk[nt] = pmma<NX>(kk[nt], kb[0][ks], kb[nt][ks]);
             }
     }
     __syncthreads();
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256, NX == 1 ? 7 : 4) void prepare_kernel(Args p) {
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
         if (nt >= 2 && w < 2) continue;
-        const int s = idx(nt, r16);
+        const int s = idx(w ^ nt, r16);
         f32x4 a;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -160,11 +160,12 @@ __global__ __launch_bounds__(256, NX == 1 ? 7 : 4) void prepare_kernel(Args p) {
     }
     __syncthreads();
 
-    if (lane < 16) {
-        const int o = 16 * w;
+    // all four diagonal blocks on one wave, 16 lanes each; which one varies, so that each SIMD gets its share
+    if (w == (int)(blockIdx.x * 0x9E3779B1u >> 30)) {
+        const int o = 16 * g4;
         float x[16];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) x[t] = t == lane ? 1.f : 0.f;
+        for (int t = 0; t < 16; ++t) x[t] = t == r16 ? 1.f : 0.f;
         // once x[s] is final every later row takes A[t][s] x[s]; column s of A is read in
         // 16-byte pieces, five columns ahead of their use
 #pragma unroll
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(256, NX == 1 ? 7 : 4) void prepare_kernel(Args p) {
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int t = 0; t < 16; ++t) X[(o + t) * LDA + o + lane] = x[t];
+        for (int t = 0; t < 16; ++t) X[(o + t) * LDA + o + r16] = x[t];
     }
     __syncthreads();
     // blocks of 16, Z X' in its result's place; A's block then becomes T's zero block
