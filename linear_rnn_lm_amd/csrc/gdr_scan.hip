@@ -88,6 +88,20 @@ __device__ __forceinline__ void stage_rows(const Planes& x, char* buf, int64_t r
         }
 }
 
+// The packed sequence that is the r-th longest of N <= 64 (r from 0): one sequence per lane, each counts those before it.
+__device__ __forceinline__ int longest(const Seqs& s, int r) {
+    const int lane = threadIdx.x & 63;
+    int64_t tok0;
+    int len = -1, slot0;
+    if (lane < s.N) seq_span(s, lane, tok0, len, slot0);
+    int before = 0;
+    for (int k = 0; k < s.N; ++k) {
+        const int l = __builtin_amdgcn_readlane(len, k);
+        before += l > len || (l == len && k < lane);
+    }
+    return __ffsll(__ballot(lane < s.N && before == r)) - 1;
+}
+
 // The sequence, head and 16-row slice of a workgroup.
 struct Where {
     int n, h, hk, sub, len, slot0, nc;
@@ -103,7 +117,12 @@ struct Where {
         h = nh % p.H;
         n = nh / p.H;
         hk = h / (p.H / p.Hk);
-        seq_span(Seqs{p.cu, p.N, p.T, p.NC}, n, tok0, len, slot0);
+        const Seqs seqs{p.cu, p.N, p.T, p.NC};
+        // long ones first, so that none starts when the others are done (training of 9 packed sequences, 8200 tokens,
+        // 16 heads of 128: 495 -> 459 us, 472 -> 460, 466 -> 464 by the lengths); of many workgroups per unit the last
+        // is a small part, and the search costs more (23 sequences, 32 heads, 11 per unit: 341 -> 350)
+        if (p.cu && p.N > 1 && p.N <= 64 && gridDim.x <= 1024) n = longest(seqs, n);
+        seq_span(seqs, n, tok0, len, slot0);
         nc = (len + C - 1) / C;
     }
     __device__ __forceinline__ int64_t block(const Args& p, int c) const { return (int64_t)(slot0 + c) * p.H + h; }

@@ -530,3 +530,26 @@ def test_no_gradient_of_the_gradient():
         dv, = torch.autograd.grad(y.square().sum(), v, create_graph=True)
         with pytest.raises(RuntimeError):
             torch.autograd.grad(dv.sum(), v)
+
+
+@pytest.mark.parametrize("N,H", [(64, 2), (65, 2), (5, 300)])
+def test_packed_many_sequences(N, H):
+    """Around the number of sequences that the scans take by length, with equal and empty ones, and with more
+    workgroups than that is done for."""
+    note(f"gdr packed N{N} H{H}")
+    lens = [(7 * i * i) % 90 if i % 5 else 64 for i in range(N)]
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    x = make(1, cu[-1], 1, H, 64, 64, BF, seed=91, N=N)
+    q, k, v, g, beta, h0, do, dhT = x
+    got = run(x, cu)
+    for n in range(N):
+        a, b = cu[n], cu[n + 1]
+        if a == b:
+            assert torch.equal(got["hT"][n].cpu(), h0[n])
+            continue
+        if n % 9 and n != N - 1:
+            continue
+        r = reference(*[t[:, a:b] for t in (q, k, v, g, beta)], h0[n:n + 1])
+        assert rel(got["o"][:, a:b], r["o"]) <= tol_fwd(64, BF) and rel(got["hT"][n:n + 1], r["hT"]) <= tol_fwd(64, F32)
