@@ -39,7 +39,8 @@
  *   gdr_slots(...) chunk slots: N * ceil(T / 64) dense, T / 64 + N packed.  Chunk
  *   slots times H must stay below 2^22 - 15, and N * H at most 2^20 (gdr_step: B * H
  *   below 2^22).
- * - Every pointer is a device pointer aligned to 16 bytes (cu_seqlens and slots: 4).
+ * - Every pointer is a device pointer aligned to 16 bytes (g, beta, dg, dbeta,
+ *   cu_seqlens, slots and what gdr_zero_outside clears: 4).
  * - Results do not vary from run to run.
  */
 #ifndef GDR_H

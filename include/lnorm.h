@@ -20,7 +20,7 @@
  *   values); y and dx are rounded once.  NaN and Inf inputs propagate within their part.
  * - groups divides C, and D is at most 16384; C is at most 2^26, groups 2^20.
  * - Every pointer is a device pointer aligned to 16 bytes (mean, rstd, dweight and
- *   dbias: 4).
+ *   dbias: 4; where D is no multiple of 8, x, y, dy, dx, weight and bias: their values').
  * - Results do not vary from run to run: the sums over the rows go through
  *   per-workgroup parts in a fixed order, without atomics.
  */

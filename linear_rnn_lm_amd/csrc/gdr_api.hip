@@ -129,8 +129,8 @@ wkv7_status gdr_fwd(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dty
     wkv7_status st = shape(B, T, Hk, H, K, V, in_dtype, N, cu_seqlens != nullptr, &s);
     if (st != WKV7_OK) return st;
     const Buf bufs[] = {{q, s.q_elems * s.e(), true, false, 16}, {k, s.q_elems * s.e(), true, false, 16},
-                        {v, s.v_elems * s.e(), true, false, 16}, {g, s.gate_elems * 4, true, false, 16},
-                        {beta, s.gate_elems * 4, true, false, 16}, {cu_seqlens, (s.N + 1) * 4LL, false, false, 4},
+                        {v, s.v_elems * s.e(), true, false, 16}, {g, s.gate_elems * 4, true, false, 4},
+                        {beta, s.gate_elems * 4, true, false, 4}, {cu_seqlens, (s.N + 1) * 4LL, false, false, 4},
                         {h0, s.state_elems * 4, false, false, 16}, {o, s.v_elems * s.e(), false, true, 16},
                         {ckpt, s.ckpt_elems * 4, false, true, 16}, {hT, s.state_elems * 4, false, true, 16},
                         {workspace, fwd_ws(s), false, true, 16}};
@@ -163,10 +163,10 @@ wkv7_status gdr_bwd(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dty
     if (st != WKV7_OK) return st;
     const int64_t qb = s.q_elems * s.e(), vb = s.v_elems * s.e(), gb = s.gate_elems * 4, sb = s.state_elems * 4;
     const Buf bufs[] = {{dout, vb, true, false, 16}, {dhT, sb, false, false, 16}, {q, qb, true, false, 16},
-                        {k, qb, true, false, 16}, {v, vb, true, false, 16}, {g, gb, true, false, 16},
-                        {beta, gb, true, false, 16}, {cu_seqlens, (s.N + 1) * 4LL, false, false, 4},
+                        {k, qb, true, false, 16}, {v, vb, true, false, 16}, {g, gb, true, false, 4},
+                        {beta, gb, true, false, 4}, {cu_seqlens, (s.N + 1) * 4LL, false, false, 4},
                         {ckpt, s.ckpt_elems * 4, true, false, 16}, {dq, qb, true, true, 16}, {dk, qb, true, true, 16},
-                        {dv, vb, true, true, 16}, {dg, gb, true, true, 16}, {dbeta, gb, true, true, 16},
+                        {dv, vb, true, true, 16}, {dg, gb, true, true, 4}, {dbeta, gb, true, true, 4},
                         {dh0, sb, false, true, 16}, {workspace, bwd_ws(s), false, true, 16}};
     st = abi::check(bufs);
     if (st != WKV7_OK) return st;
@@ -194,7 +194,7 @@ wkv7_status gdr_zero_outside(int T, int N, const int32_t* cu_seqlens, int n, voi
     for (int i = 0; i < n; ++i) {
         if (!ptrs[i]) return WKV7_ERR_ARG;
         if (row_bytes[i] < 4 || row_bytes[i] % 4) return WKV7_ERR_SHAPE;
-        if (reinterpret_cast<uintptr_t>(ptrs[i]) & 15u) return WKV7_ERR_ALIGN;
+        if (reinterpret_cast<uintptr_t>(ptrs[i]) & 3u) return WKV7_ERR_ALIGN;
         a.p[i] = static_cast<uint32_t*>(ptrs[i]);
         a.words[i] = row_bytes[i] / 4;
     }
@@ -214,7 +214,7 @@ wkv7_status gdr_step(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dt
     const int64_t e = in_dtype == WKV7_BF16 ? 2 : 4, qb = tokens * Hk * K * e, vb = tokens * H * V * e;
     const int64_t gb = tokens * H * 4, sb = (int64_t)P * H * V * K * 4;
     const Buf bufs[] = {{q, qb, true, false, 16}, {k, qb, true, false, 16}, {v, vb, true, false, 16},
-                        {g, gb, true, false, 16}, {beta, gb, true, false, 16}, {slots, B * 4LL, false, false, 4},
+                        {g, gb, true, false, 4}, {beta, gb, true, false, 4}, {slots, B * 4LL, false, false, 4},
                         {state, sb, true, false, 16}, {state_out, sb, true, true, 16}, {o, vb, true, true, 16}};
     st = abi::check(bufs, state == state_out ? state : nullptr);
     if (st != WKV7_OK) return st;

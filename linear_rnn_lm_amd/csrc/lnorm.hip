@@ -449,6 +449,7 @@ wkv7_status check_shape(int64_t rows, int C, int groups, int xd, int yd, int wd)
 }
 
 int64_t esz(wkv7_dtype d) { return d == WKV7_BF16 ? 2 : 4; }
+int align_of(int D, wkv7_dtype d) { return D % 8 == 0 ? 16 : (int)esz(d); }   // rows by vectors, or value by value
 
 }  // namespace
 }  // namespace lnorm
@@ -462,8 +463,9 @@ wkv7_status ln_fwd(int64_t rows, int C, int groups, wkv7_dtype x_dtype, wkv7_dty
     if (st != WKV7_OK) return st;
     if ((mean == nullptr) != (rstd == nullptr)) return WKV7_ERR_ARG;
     const int64_t n = rows * C, wb = C * lnorm::esz(w_dtype), sb = rows * groups * 4;
-    const abi::Buf bufs[] = {{x, n * lnorm::esz(x_dtype), true, false, 16}, {weight, wb, false, false, 16},
-                             {bias, wb, false, false, 16}, {y, n * lnorm::esz(y_dtype), true, true, 16},
+    const int D = C / groups, xa = lnorm::align_of(D, x_dtype), ya = lnorm::align_of(D, y_dtype), wa = lnorm::align_of(D, w_dtype);
+    const abi::Buf bufs[] = {{x, n * lnorm::esz(x_dtype), true, false, xa}, {weight, wb, false, false, wa},
+                             {bias, wb, false, false, wa}, {y, n * lnorm::esz(y_dtype), true, true, ya},
                              {mean, sb, false, true, 4}, {rstd, sb, false, true, 4}};
     st = abi::check(bufs);
     if (st != WKV7_OK) return st;
@@ -487,9 +489,10 @@ wkv7_status ln_bwd(int64_t rows, int C, int groups, wkv7_dtype x_dtype, wkv7_dty
     if ((dweight == nullptr) != (dbias == nullptr) || (!dx && !dweight)) return WKV7_ERR_ARG;
     const int64_t n = rows * C, sb = rows * groups * 4;
     const int64_t need = dweight ? (int64_t)ln_bwd_workspace_bytes(rows, C, groups) : 0;
-    const abi::Buf bufs[] = {{dy, n * lnorm::esz(y_dtype), true, false, 16}, {x, n * lnorm::esz(x_dtype), true, false, 16},
-                             {weight, C * lnorm::esz(w_dtype), false, false, 16}, {mean, sb, true, false, 4},
-                             {rstd, sb, true, false, 4}, {dx, n * lnorm::esz(x_dtype), false, true, 16},
+    const int D = C / groups, xa = lnorm::align_of(D, x_dtype), ya = lnorm::align_of(D, y_dtype), wa = lnorm::align_of(D, w_dtype);
+    const abi::Buf bufs[] = {{dy, n * lnorm::esz(y_dtype), true, false, ya}, {x, n * lnorm::esz(x_dtype), true, false, xa},
+                             {weight, C * lnorm::esz(w_dtype), false, false, wa}, {mean, sb, true, false, 4},
+                             {rstd, sb, true, false, 4}, {dx, n * lnorm::esz(x_dtype), false, true, xa},
                              {dweight, C * 4LL, false, true, 4}, {dbias, C * 4LL, false, true, 4},
                              {workspace, need, false, true, 16}};
     st = abi::check(bufs);

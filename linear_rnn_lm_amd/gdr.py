@@ -15,7 +15,11 @@ are fp32.  ``scale`` defaults to K ** -0.5.
 ``cu_seqlens`` (int32, N + 1 offsets on the GPU, B = 1) packs N sequences of any
 lengths, empty ones included, along T; states are then (N, H, V, K).  The
 offsets stay on the GPU: nothing waits for them, and a call can be captured into
-a graph and replayed with other offsets.
+a graph and replayed with other offsets.  (As with every autograd op, capture a
+backward only on leaves that no live eager graph uses.)
+
+Tensors are dense; GDR makes copies of those that are not.  Calls of several
+streams or threads may overlap as long as they share no output and no workspace.
 """
 from __future__ import annotations
 

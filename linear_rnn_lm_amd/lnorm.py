@@ -10,6 +10,7 @@ y = (x - mean) / sqrt(var + eps) * weight + bias.  x: (..., C) fp32 or bf16; y h
 x's type, or bf16 for an fp32 x with ``out_dtype=torch.bfloat16`` (the
 recurrence's fp32 output into a bf16 layer).  weight, bias: (C,) fp32 or bf16, or
 None.  mean, rstd: (rows, groups) fp32.  dx has x's type, dweight and dbias are fp32.
+Tensors are dense; LN makes copies of those that are not.
 """
 from __future__ import annotations
 

@@ -88,7 +88,7 @@ def test_gdr_bwd_rejects_bad_arguments():
         assert c(**{n: None}) == ERR_ARG
     assert c(dq=fake(8)) == ERR_ALIAS and c(dv=fake(0)) == ERR_ALIAS and c(dh0=fake(6)) == ERR_ALIAS
     assert c(dhT=fake(14), dh0=fake(14)) == ERR_ALIAS
-    assert c(dg=fake(10) + 4) == ERR_ALIGN
+    assert c(dg=fake(10) + 2) == ERR_ALIGN and c(dq=fake(7) + 8) == ERR_ALIGN
     assert c(wsb=1000) == ERR_WS
 
 
@@ -115,7 +115,7 @@ def test_gdr_zero_outside_rejects_bad_arguments():
 
     assert c(T=0) == ERR_SHAPE and c(N=0) == ERR_SHAPE and c(rb=2) == ERR_SHAPE
     assert c(cu=None) == ERR_ARG and c(p=None) == ERR_ARG and c(n=9) == ERR_ARG and c(n=0) == ERR_ARG
-    assert c(p=fake(1) + 4) == ERR_ALIGN
+    assert c(p=fake(1) + 2) == ERR_ALIGN
 
 
 @needs_no_gpu
@@ -303,3 +303,12 @@ def test_sizes_that_no_launch_takes_are_refused():
     for C, G in ((2 ** 27, 2 ** 17), (2 ** 21, 2 ** 21)):
         assert ln(1, C, G, 0, 0, 0, fake(0), None, None, 1e-5, fake(1), None, None, None) == ERR_SHAPE
     assert gdr._lib().gdr_ckpt_bytes(1, 2 ** 23, 1, 64, 64, 64, 0, 0) == 0
+
+
+@needs_no_gpu
+def test_ln_alignment_goes_by_the_parts():
+    """Rows of parts of a multiple of 8 values go by vectors; others value by value."""
+    f = lnorm._lib().ln_fwd
+    assert f(4, 64, 1, 1, 1, 0, fake(0) + 2, None, None, 1e-5, fake(1), None, None, None) == ERR_ALIGN
+    assert f(4, 63, 1, 1, 1, 0, fake(0) + 1, None, None, 1e-5, fake(1), None, None, None) == ERR_ALIGN
+    assert f(4, 63, 1, 1, 1, 0, fake(0), fake(2) + 2, None, 1e-5, fake(1), None, None, None) == ERR_ALIGN

@@ -553,3 +553,24 @@ def test_packed_many_sequences(N, H):
             continue
         r = reference(*[t[:, a:b] for t in (q, k, v, g, beta)], h0[n:n + 1])
         assert rel(got["o"][:, a:b], r["o"]) <= tol_fwd(64, BF) and rel(got["hT"][n:n + 1], r["hT"]) <= tol_fwd(64, F32)
+
+
+def test_one_token_views_and_checkpoints_alone():
+    """Slices of longer tensors, whose gates lie at odd addresses, and a forward that only leaves checkpoints."""
+    note("gdr views")
+    q, k, v, g, beta, h0, do, dhT = dev(*make(1, 70, 1, 3, 64, 64, BF, seed=95))
+    s, s2 = h0.clone(), h0.clone()
+    for t in range(3):
+        cut = [x[:, t:t + 1] for x in (q, k, v, g, beta)]
+        o = L.gdr_step(*cut, s)
+        o2 = L.gdr_step(*[x.clone() for x in cut], s2)
+        assert torch.equal(o, o2) and torch.equal(s, s2)
+    cut = [x[:, 1:68] for x in (q, k, v, g, beta)]
+    assert cut[3].data_ptr() % 16
+    o, ck, hT = L.gdr_fwd(*cut, h0)
+    o2, ck2, hT2 = L.gdr_fwd(*[x.clone() for x in cut], h0)
+    none, ck3, none2 = L.gdr_fwd(*cut, h0, want_o=False, want_hT=False)
+    a, b = (L.gdr_bwd(do[:, 1:68].contiguous(), *c, x, dhT) for c, x in ((cut, ck3), ([x.clone() for x in cut], ck2)))
+    torch.cuda.synchronize()
+    assert none is None and none2 is None
+    assert torch.equal(o, o2) and torch.equal(hT, hT2) and all(torch.equal(x, y) for x, y in zip(a, b))

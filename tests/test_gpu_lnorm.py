@@ -202,3 +202,18 @@ def test_offsets_past_31_bits():
     # total at most, on either side
     for a, b in ((dw, dws), (db, dbs)):
         assert (a - b).abs().max() <= 2 * n * 2.0 ** -24 * n * ds.abs().max().float() * 5
+
+
+@pytest.mark.parametrize("C,groups", [(333, 1), (36, 3)])
+def test_views_at_odd_addresses(C, groups):
+    note(f"ln views C{C}")
+    x, w, b, dy = make(9, C, BF, BF, BF, seed=4)
+    x, w, b, dy = (t.to(DEV) for t in (x, w, b, dy))
+    xs, ds = x[1:], dy[1:]
+    assert xs.data_ptr() % 16
+    got = L.ln_fwd(xs, w, b, groups=groups)
+    want = L.ln_fwd(xs.clone(), w, b, groups=groups)
+    gg = L.ln_bwd(ds, xs, w, got[1], got[2], groups=groups)
+    gw = L.ln_bwd(ds.clone(), xs.clone(), w, want[1], want[2], groups=groups)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip((*got, *gg), (*want, *gw)))
