@@ -43,7 +43,8 @@ struct Plan {
     static constexpr int Kr = 0, T = Kr + NX * XB, G = T + NP * kTriBytes, V = G + kGateFloats * 4;
     static constexpr int bytes = V + (BWD ? 0 : VB);
     static constexpr int QB = BWD ? NX * XB + VB : 0;
-    static constexpr int ST = K / 16 * 1024, UT = 4 * 1024;   // state tiles, token tiles of one wave
+    // what one wave passes on: state tiles (fp32, or all planes of the forward's S for bf16 inputs), token tiles
+    static constexpr int ST = BWD || NX > 1 ? K / 16 * 1024 : NP * K / 32 * 1024, UT = 4 * 1024;
     static constexpr int pass = 2 * NCW * (ST + UT), OB = BWD ? 0 : 4 * 16 * RB, rest = 2 * QB + pass + OB;
     static constexpr int NBUF = 3 * bytes + rest <= kLds ? 3 : 2 * bytes + rest <= kLds ? 2 : 1;
     static constexpr int NQ = NBUF > 1 ? 2 : 1;
@@ -356,15 +357,15 @@ __device__ __forceinline__ void rows_step(f32x4 (&a)[4], const PF<NX> (&f)[4], c
                 for (int t = T0; t < T0 + N; ++t) a[t] = wkv7::mfma_bf16(f[t].p[i], sf.p[o - i], a[t]);
 }
 // a = X S^T over all columns but the last 32 (whose planes it returns), S split on the way; the
-// leading two planes go to `pass` if given
+// planes go to `pass` if given
 template <int NX, int KS, int KT>
 __device__ __forceinline__ PF<NP> rows_times_state(f32x4 (&a)[4], const PF<NX> (&f)[KS][4], const f32x4 (&s)[KT],
                                                    char* pass) {
     PF<NP> sf = pf_acc<NP>(s[0], s[1]);
     auto hand = [&](int ks) {
         if (pass) {
-            *reinterpret_cast<bf16x8*>(pass + 2048 * ks) = sf.p[0];
-            *reinterpret_cast<bf16x8*>(pass + 2048 * ks + 1024) = sf.p[1];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x8*>(pass + (NP * ks + i) * 1024) = sf.p[i];
         }
     };
     hand(0);
@@ -424,16 +425,13 @@ __device__ __forceinline__ void load_row(PF<NX> (&f)[KS], const Planes& x, const
 template <typename InT, int NX, int K, int NCW, int TT>
 __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char* smem, int lane) {
     using L = Plan<InT, NX, K, NCW, false>;
-    // o leaves in in_dtype: for bf16 two planes (2^-17) in its own products lose nothing
-    // beside its rounding; the products of the state keep all three
-    constexpr int NO = NX == 1 ? 2 : NP;
     constexpr int U = K / 8, KS = K / 32, KT = K / 16, MS = TT / 2 + 1;   // 32-token steps of M's rows
     const int g4 = lane >> 4, r16 = lane & 15, t = idx(TT, r16);
     InT* o = static_cast<InT*>(p.o);
     const bool want = o || p.ckpt;
     char* stage = smem + L::O0 + TT * 16 * L::RB;
     PF<NX> qn[KS], qf[KS];
-    PF<NO> mf[MS];
+    PF<NP> mf[MS];
     f32x4 eg = zero4();
     auto load = [&](int c) {
         if (c < w.nc && want) load_row<NX, KS>(qn, p.qp, p, w, c, t, g4);
@@ -451,9 +449,9 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
             constexpr int TWO = NCW < 2 ? 1 : 2;          // slices at a time
 #pragma unroll
             for (int c0 = 0; c0 < NCW; c0 += TWO) {
-                // S arrives as its leading two planes for bf16 inputs, as fp32 tiles otherwise
+                // S arrives in planes for bf16 inputs, as fp32 tiles otherwise
                 f32x4 s[TWO][NX == 1 ? 1 : KT], u[TWO][4];
-                PF<NO> sf[TWO][KS];
+                PF<NP> sf[TWO][KS];
 #pragma unroll
                 for (int cs = 0; cs < TWO; ++cs) {
                     const char* ps = pass + (c0 + cs) * (L::ST + L::UT);
@@ -461,8 +459,8 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                            for (int j = 0; j < NO; ++j)
-                                sf[cs][ks].p[j] = *reinterpret_cast<const bf16x8*>(ps + 2048 * ks + 1024 * j + 16 * lane);
+                            for (int j = 0; j < NP; ++j)
+                                sf[cs][ks].p[j] = *reinterpret_cast<const bf16x8*>(ps + (NP * ks + j) * 1024 + 16 * lane);
                     } else {
                         pass_get(ps, lane, s[cs]);
                     }
@@ -474,12 +472,12 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
                     f32x4 b = zero4();
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
-                        if constexpr (NX > 1) sf[cs][ks] = pf_acc<NO>(s[cs][2 * ks], s[cs][2 * ks + 1]);
-                        b = pmma<NO>(b, qf[ks], sf[cs][ks]);
+                        if constexpr (NX > 1) sf[cs][ks] = pf_acc<NP>(s[cs][2 * ks], s[cs][2 * ks + 1]);
+                        b = pmma<NP>(b, qf[ks], sf[cs][ks]);
                     }
                     b = eg * b;
 #pragma unroll
-                    for (int ks = 0; ks < MS; ++ks) b = pmma<NO>(b, mf[ks], pf_acc<NO>(u[cs][2 * ks], u[cs][2 * ks + 1]));
+                    for (int ks = 0; ks < MS; ++ks) b = pmma<NP>(b, mf[ks], pf_acc<NP>(u[cs][2 * ks], u[cs][2 * ks + 1]));
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         st(reinterpret_cast<InT*>(stage + (4 * g4 + q) * L::RB) + 16 * (c0 + cs) + r16, p.scale * b[q]);
@@ -558,7 +556,7 @@ __device__ __forceinline__ void output_wave(const Args& p, const Where& w, char*
                     }
                 }
 #pragma unroll
-                for (int m = 0; m < MS; ++m) mf[m] = pf_acc<NO>(x[2 * m], x[2 * m + 1]);
+                for (int m = 0; m < MS; ++m) mf[m] = pf_acc<NP>(x[2 * m], x[2 * m + 1]);
                 if (p.ckpt && w.sub == 0) {
                     // piece (tile ts of s, 32 tokens): this wave's half of each lane's eight tokens
                     float* mt = p.ckpt + w.block(p, it) * p.ckpt_stride + (int64_t)p.V * (K + C) + 4 * (TT & 1);
