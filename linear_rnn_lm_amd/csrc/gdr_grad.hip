@@ -7,13 +7,16 @@
 //     dQ = scale e^G DO S + P K
 //     dK = [N K - b e^G Z S]  +  [P^T Q + N^T K + e^(G_C - G) U G1]
 //     db_t = (Z_t . U_t) / b_t
-//     dG_t = q_t . dQ_t + k_t . (first part of dK)_t - k_t . (second part)_t
-//     dG_C += sum_t k_t . e^(G_C - G_t) (U G1)_t + e^(G_C) <S, G1>
-//     dg_t = sum_{t' >= t} dG_t'
+//     dg_j = sum_{s < j <= t} W[t][s] + sum_{t >= j} a_t + sum_{s < j} e_s + e^(G_C) <S, G1>
+//       W[t][s] = P[t][s] q_t . k_s + N[t][s] k_t . k_s,   e_s = k_s . e^(G_C - G_s) (U G1)_s
+//       a_t = q_t . scale e^G (dO S)_t - k_t . b e^G (Z S)_t
 //
-// (the decays enter every product as a row or column factor, so their gradients
-// are row sums of terms that are there anyway).  q and k of one key head serve
-// H / Hk value heads: one workgroup does all of them in turn, so the sums over
+// Each term of dg_j is one that the decay of token j enters, once, as a factor.  (Suffix
+// sums of q.dQ and k.dK would need no W, but undecayed terms, the diagonal of P and the end
+// terms of later tokens, come and go in them: with log decays of -5 dg was off by 6e-5 to 1e-4
+// of itself, with -10 by 1e-2, with -20 it had no digit left.)  The sum over s < j is a prefix along a lane's eight s and the
+// lanes of a row, the sum over t >= j one over the lanes of a tile.  q and k of one key head
+// serve H / Hk value heads: one workgroup does all of them in turn, so the sums over
 // the heads stay in registers and in one order.
 //
 // It reads S, U, G1, Z, q, k and dout and writes dq and dk: 1.73 GB at B8 T4096 H32 64 x 64,
@@ -43,7 +46,7 @@ struct Lds {
     static constexpr int P = 0, N = P + NP * MB;
     static constexpr int DO = G + NP * HB, Kr = DO + NX * MB, Qr = Kr + NX * MB;
     static constexpr int small = Qr + NX * MB;
-    static constexpr int bytes = small + 7 * 64 * 4 + 2 * 128 * 4;
+    static constexpr int bytes = small + 8 * 64 * 4 + 2 * 128 * 4 + 256 * 4;
     static_assert(N + NP * MB <= DO, "P and N in place of U, Z, S, G1");
 };
 
@@ -81,6 +84,23 @@ __device__ __forceinline__ F8 get8(const char* X, int row, int unit) {
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
     return fmaf(a[0], b[0], fmaf(a[1], b[1], fmaf(a[2], b[2], a[3] * b[3])));
 }
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, false));
+}
+// Eight sums over the 16 lanes of a row: lane r gets that of x[r / 2].  Each step halves the
+// values and the lanes that a value is spread over.
+__device__ __forceinline__ float row_sums8(const float (&x)[8], int r) {
+    float y[4], z[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)                           // row_mirror
+        y[i] = (r & 8 ? x[4 + i] : x[i]) + dpp<0x140>(r & 8 ? x[i] : x[4 + i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)                           // row_half_mirror
+        z[i] = (r & 4 ? y[2 + i] : y[i]) + dpp<0x141>(r & 4 ? y[i] : y[2 + i]);
+    const float w = (r & 2 ? z[1] : z[0]) + dpp<0x4E>(r & 2 ? z[0] : z[1]);   // quad_perm 2,3,0,1
+    return w + dpp<0xB1>(w);                              // quad_perm 1,0,3,2
+}
 
 // ONE: one value head to a key head, so nothing is summed over heads.
 template <typename InT, int NX, int K, bool ONE>
@@ -95,8 +115,10 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
     float* beta = toEnd + 64;
     float* dbeta = beta + 64;
     float* red = dbeta + 64;             // 8 floats used
-    float* dGp = red + 64;               // [2][64]
-    float* ep = dGp + 128;               // [2][64]
+    float* rest = red + 64;              // row sums of W over s < 32
+    float* ap = rest + 64;               // [2][64]
+    float* ep = ap + 128;                // [2][64]
+    float* wp = ep + 128;                // [tile of t][s]
     const int tid0 = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid0 >> 6);
     // K = 128: two workgroups, one for either half js of the columns, eight apart in the launch's order, so
     // that they are on one XCD and share U and Z in its L2
@@ -226,15 +248,51 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
                     na[j][q] = s < t ? -bt * lam * na[j][q] : 0.f;
                 }
             }
+            if (c <= (tt >> 1)) {                     // W, and for every s its sums over t > s of sum_{s' <= s} W[t][s']
+                f32x4 qk[2], kk[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) qk[j] = kk[j] = zero4();
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const PF<NX> qt = frag_row<8, NX>(smem + L::Qr, L::MB, t, ks, lane);
+                    const PF<NX> kt = frag_row<8, NX>(smem + L::Kr, L::MB, t, ks, lane);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const PF<NX> kf = frag_row<8, NX>(smem + L::Kr, L::MB, idx(2 * c + j, r16), ks, lane);
+                        qk[j] = pmma<NX>(qk[j], kf, qt);
+                        kk[j] = pmma<NX>(kk[j], kf, kt);
+                    }
+                }
+                const int s0 = 32 * c + 8 * g4;
+                float x[8], sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = e / 4, q = e % 4;
+                    if (s0 + e < t) sum += pa[j][q] * qk[j][q] + na[j][q] * kk[j][q];
+                    x[e] = sum;
+                }
+                const float by16 = __shfl_xor(sum, 16), pair = sum + by16, by32 = __shfl_xor(pair, 32);
+                const float before = (g4 & 1 ? by16 : 0.f) + (g4 & 2 ? by32 : 0.f);
+                if (c == 0 && g4 == 0) rest[t] = pair + by32;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = s0 + e < t ? x[e] + before : 0.f;
+                const float w = row_sums8(x, r16);
+                if (!(r16 & 1)) wp[64 * tt + s0 + (r16 >> 1)] = w;
+            }
             __syncthreads();
             put8<8, NP>(smem + L::P, L::MB, t, 4 * c + g4, pf_acc<NP>(pa[0], pa[1]));
             put8<8, NP>(smem + L::N, L::MB, t, 4 * c + g4, pf_acc<NP>(na[0], na[1]));
             __syncthreads();
-            f32x4 nk[2], pq[2];
+            const F8 kv = get8<NX>(smem + L::Kr, t, 4 * c + g4), qv = get8<NX>(smem + L::Qr, t, 4 * c + g4);
+            float a = 0.f, e = 0.f;
+            f32x4 dk[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+                const f32x4 k4 = j ? kv.b : kv.a, q4 = j ? qv.b : qv.a, zt = egt * bt * zs[j], end = tet * ug[j];
                 dos[j] = p.scale * egt * dos[j];      // then + P K
-                nk[j] = pq[j] = zero4();
+                a += dot4(q4, dos[j]) - dot4(k4, zt);
+                e += dot4(k4, end);
+                dk[j] = end - zt;                     // then + P^T Q + N^T K + N K
             }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -245,7 +303,7 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
                     for (int j = 0; j < 2; ++j) {
                         const PF<NX> kf = frag_col<8, NX>(smem + L::Kr, L::MB, 2 * c + j, ks, lane);
                         dos[j] = pmma<NP>(dos[j], kf, pr);
-                        nk[j] = pmma<NP>(nk[j], kf, nr);
+                        dk[j] = pmma<NP>(dk[j], kf, nr);
                     }
                 }
                 if (ks >= (tt >> 1)) {
@@ -253,38 +311,26 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
                     const PF<NP> nc = frag_col<8, NP>(smem + L::N, L::MB, tt, ks, lane);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        pq[j] = pmma<NP>(pq[j], frag_col<8, NX>(smem + L::Qr, L::MB, 2 * c + j, ks, lane), pc);
-                        pq[j] = pmma<NP>(pq[j], frag_col<8, NX>(smem + L::Kr, L::MB, 2 * c + j, ks, lane), nc);
+                        dk[j] = pmma<NP>(dk[j], frag_col<8, NX>(smem + L::Qr, L::MB, 2 * c + j, ks, lane), pc);
+                        dk[j] = pmma<NP>(dk[j], frag_col<8, NX>(smem + L::Kr, L::MB, 2 * c + j, ks, lane), nc);
                     }
                 }
             }
-            const F8 kv = get8<NX>(smem + L::Kr, t, 4 * c + g4), qv = get8<NX>(smem + L::Qr, t, 4 * c + g4);
-            float dG = 0.f, e = 0.f;
-            F8 oq, ok;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const f32x4 k4 = j ? kv.b : kv.a, q4 = j ? qv.b : qv.a;
-                const f32x4 plus = nk[j] - egt * bt * zs[j], end = tet * ug[j], minus = pq[j] + end;
-                dG += dot4(q4, dos[j]) + dot4(k4, plus - minus);
-                e += dot4(k4, end);
-                (j ? oq.b : oq.a) = dos[j];
-                (j ? ok.b : ok.a) = plus + minus;
-            }
             if constexpr (ONE) {
-                store(oq, ok);
+                store(F8{dos[0], dos[1]}, F8{dk[0], dk[1]});
             } else {
-                gq.a += oq.a;
-                gq.b += oq.b;
-                gk.a += ok.a;
-                gk.b += ok.b;
+                gq.a += dos[0];
+                gq.b += dos[1];
+                gk.a += dk[0];
+                gk.b += dk[1];
                 if (hr == rep - 1) store(gq, gk);
             }
-            dG += __shfl_xor(dG, 16);
+            a += __shfl_xor(a, 16);
             e += __shfl_xor(e, 16);
-            dG += __shfl_xor(dG, 32);
+            a += __shfl_xor(a, 32);
             e += __shfl_xor(e, 32);
             if (g4 == 0) {                            // one lane per (c, t)
-                dGp[c * 64 + t] = dG;
+                ap[c * 64 + t] = a;
                 ep[c * 64 + t] = e;
             }
         }
@@ -293,26 +339,30 @@ __global__ __launch_bounds__(NT, NX == 1 ? 4 : 2) void grad_kernel(Args p) {
         if (lane == 0) red[wave] = sg;
         __syncthreads();
         if (wave == 0) {
-            double x = (double)dGp[lane] + dGp[64 + lane];
-            float e = ep[lane] + ep[64 + lane];
+            // token `lane`: a_t and, where s < 32 lies left of what wp holds for it, whole rows of those s, from
+            // itself on; e_s before itself; <S, G1>; W's sums
+            float a = ap[lane] + ap[64 + lane], r = lane > 32 ? rest[lane] : 0.f;
+            float e = lane > 0 ? ep[lane - 1] + ep[63 + lane] : 0.f, x = 0.f;
 #pragma unroll
-            for (int d = 32; d; d >>= 1) e += __shfl_xor(e, d);
-            if (lane == 63) {
-                float sgs = 0.f;
-#pragma unroll
-                for (int i = 0; i < NT / 64; ++i) sgs += red[i];
-                x += (double)e + (double)eG[63] * sgs;
+            for (int i = 0; i < NT / 64; ++i) x += red[i];
+            x *= eG[63];
+            if (lane > 0) {
+                if (lane <= 32) x += wp[lane - 1] + wp[64 + lane - 1];   // tiles of t below 32 have no s from 32 on
+                x += wp[128 + lane - 1] + wp[192 + lane - 1];
             }
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
-                const double o = __shfl_down(x, d);
-                if (lane + d < 64) x += o;
+                const float ad = __shfl_down(a, d), rd = __shfl_down(r, d), eu = __shfl_up(e, d);
+                a += lane + d < 64 ? ad : 0.f;
+                r += lane + d < 64 ? rd : 0.f;
+                e += lane >= d ? eu : 0.f;
             }
+            x += a + e + (lane > 32 ? r : 0.f);
             if (lane < len) {
                 float* dg = p.dg + (tok + lane) * p.H + h;
                 // two halves, added to the zero that the scan left: the order makes no difference to a sum of two
-                if (KJ > 1) unsafeAtomicAdd(dg, (float)x);
-                else *dg = (float)x;
+                if (KJ > 1) unsafeAtomicAdd(dg, x);
+                else *dg = x;
                 if (js == 0) p.dbeta[(tok + lane) * p.H + h] = dbeta[lane];
             }
         }

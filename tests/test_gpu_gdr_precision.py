@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import linear_rnn_lm_amd as L
-from tests.gdr_util import make, reference
+from tests.gdr_util import make, reference, rel, tol_bwd
 from tests.gpu_util import note
 
 pytestmark = pytest.mark.gpu
@@ -37,3 +37,36 @@ def test_a_large_state_is_overwritten(K, V, B, Hk, H, dtype):
     first = (o.double().cpu() - want["o"]).abs() - half * want["o"].abs()
     assert first.max() <= 16 * 2.0 ** -24 * R * scale, first.max()
     assert (hT.double().cpu() - want["hT"]).abs().max() <= 16 * 2.0 ** -24 * R
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K,V,Hk,H", [(64, 64, 2, 2), (64, 128, 1, 3), (128, 64, 2, 2), (128, 128, 2, 4)])
+@pytest.mark.parametrize("kind", [-2.0, -5.0, -10.0, -20.0, "some"])
+def test_gradient_of_strong_decays(kind, K, V, Hk, H, dtype):
+    """dg in relation to its own size, however much the heads forget.
+
+    Every part of dg carries the decay of its token, so the sums' bound holds relative to dg.  A
+    decay e^x is rounded by 2^-24 |x| log2(e) relative (the exponent's last place), twice where it
+    is a factor of a derived operand too: 3 |g| 2^-24 more.  "some": g = -20 at every seventh token, -0.01 at the
+    others, and the two kinds of tokens are looked at apart."""
+    note(f"gdr dg under decays {kind} K{K} V{V} Hk{Hk} H{H} {dtype}")
+    T = 150
+    q, k, v, g, beta, h0, do, dhT = make(2, T, Hk, H, K, V, dtype, seed=17)
+    strong = torch.zeros(T, dtype=torch.bool)
+    if kind == "some":
+        strong[::7] = True
+        g = torch.where(strong[:, None], torch.tensor(-20.0), torch.tensor(-0.01)).expand_as(g).contiguous()
+    else:
+        g = torch.full_like(g, kind)
+    want = reference(q, k, v, g, beta, h0, do, dhT)
+    ins = [t.to(DEV) for t in (q, k, v, g, beta)]
+    _, ckpt, _ = L.gdr_fwd(*ins, h0.to(DEV))
+    got = L.gdr_bwd(do.to(DEV), *ins, ckpt, dhT.to(DEV))
+    torch.cuda.synchronize()
+    for n, t in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), got):
+        tol = tol_bwd(K, V, t.dtype) + 3 * g.abs().max().item() * 2.0 ** -24
+        if n == "dg" and kind == "some":
+            for at in (strong, ~strong):
+                assert rel(t[:, at], want[n][:, at]) <= tol, (n, rel(t[:, at], want[n][:, at]), tol)
+        else:
+            assert rel(t, want[n]) <= tol, (n, rel(t, want[n]), tol)
