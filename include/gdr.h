@@ -62,8 +62,10 @@ int64_t gdr_slots(int B, int T, int N, int packed);
  * triangular matrices and its gates.  0 for invalid shapes. */
 size_t gdr_ckpt_bytes(int B, int T, int Hk, int H, int K, int V, int N, int packed);
 
-/* Device workspace of gdr_fwd and gdr_bwd.  0 for invalid shapes. */
+/* Device workspace of gdr_fwd (without and with ckpt: that holds the larger part by
+ * itself) and of gdr_bwd.  0 for invalid shapes. */
 size_t gdr_fwd_workspace_bytes(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dtype, int N, int packed);
+size_t gdr_fwd_train_workspace_bytes(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dtype, int N, int packed);
 size_t gdr_bwd_workspace_bytes(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dtype, int N, int packed);
 
 /*
@@ -72,7 +74,8 @@ size_t gdr_bwd_workspace_bytes(int B, int T, int Hk, int H, int K, int V, wkv7_d
  *   o    : output, or NULL.   hT : final states, or NULL; may be h0 itself.
  *   ckpt : what gdr_bwd needs (gdr_ckpt_bytes), or NULL.
  *   At least one of o, hT, ckpt must be given.
- *   workspace: gdr_fwd_workspace_bytes bytes, clobbered; nothing in it is kept.
+ *   workspace: gdr_fwd_workspace_bytes bytes, with ckpt gdr_fwd_train_workspace_bytes
+ *   (never more), clobbered; nothing in it is kept.
  */
 wkv7_status gdr_fwd(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dtype,
                     const void *q, const void *k, const void *v, const float *g, const float *beta,

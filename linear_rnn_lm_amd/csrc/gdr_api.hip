@@ -58,9 +58,14 @@ wkv7_status shape(int B, int T, int Hk, int H, int K, int V, int dt, int N, bool
     return WKV7_OK;
 }
 
-// T and gates of a forward without checkpoints (or 0 bytes), planes of fp32 inputs;
-// the backward's state gradients and Z, and those planes.
-int64_t fwd_ws(const Shape& s) { return s.tri_bytes + s.split_bytes; }
+// T and gates of a forward without checkpoints (with them they lie there), planes of fp32 inputs;
+// the backward's state gradients and Z, and those planes.  Never 0, so that a size of 0 is always
+// one of invalid shapes, and a NULL workspace always an error.
+constexpr int64_t kMinWorkspace = 256;
+int64_t fwd_ws(const Shape& s, bool ckpt) {
+    const int64_t n = (ckpt ? 0 : s.tri_bytes) + s.split_bytes;
+    return n < kMinWorkspace ? kMinWorkspace : n;
+}
 int64_t bwd_ws(const Shape& s) { return s.dend_bytes + s.z_bytes + s.split_bytes; }
 
 wkv7_status status_of(hipError_t e) { return e == hipSuccess ? WKV7_OK : WKV7_ERR_HIP; }
@@ -113,7 +118,12 @@ size_t gdr_ckpt_bytes(int B, int T, int Hk, int H, int K, int V, int N, int pack
 
 size_t gdr_fwd_workspace_bytes(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dtype, int N, int packed) {
     Shape s;
-    return shape(B, T, Hk, H, K, V, in_dtype, N, packed != 0, &s) == WKV7_OK ? (size_t)fwd_ws(s) : 0;
+    return shape(B, T, Hk, H, K, V, in_dtype, N, packed != 0, &s) == WKV7_OK ? (size_t)fwd_ws(s, false) : 0;
+}
+
+size_t gdr_fwd_train_workspace_bytes(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dtype, int N, int packed) {
+    Shape s;
+    return shape(B, T, Hk, H, K, V, in_dtype, N, packed != 0, &s) == WKV7_OK ? (size_t)fwd_ws(s, true) : 0;
 }
 
 size_t gdr_bwd_workspace_bytes(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dtype, int N, int packed) {
@@ -133,13 +143,13 @@ wkv7_status gdr_fwd(int B, int T, int Hk, int H, int K, int V, wkv7_dtype in_dty
                         {beta, s.gate_elems * 4, true, false, 4}, {cu_seqlens, (s.N + 1) * 4LL, false, false, 4},
                         {h0, s.state_elems * 4, false, false, 16}, {o, s.v_elems * s.e(), false, true, 16},
                         {ckpt, s.ckpt_elems * 4, false, true, 16}, {hT, s.state_elems * 4, false, true, 16},
-                        {workspace, fwd_ws(s), false, true, 16}};
+                        {workspace, fwd_ws(s, ckpt != nullptr), false, true, 16}};
     if (!o && !ckpt && !hT) return WKV7_ERR_ARG;
     st = abi::check(bufs, h0 == hT ? h0 : nullptr);
     if (st != WKV7_OK) return st;
-    if (!workspace || workspace_bytes < (size_t)fwd_ws(s)) return WKV7_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < (size_t)fwd_ws(s, ckpt != nullptr)) return WKV7_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
-    gdr::Args a = args_of(B, T, Hk, H, K, V, s, q, k, v, g, beta, cu_seqlens, scale, ws + s.tri_bytes);
+    gdr::Args a = args_of(B, T, Hk, H, K, V, s, q, k, v, g, beta, cu_seqlens, scale, ws + (ckpt ? 0 : s.tri_bytes));
     a.h0 = h0; a.o = o; a.ckpt = ckpt; a.hT = hT;
     if (ckpt) {
         tri_in_ckpt(&a);

@@ -38,7 +38,7 @@ def _lib():
     dims = [i] * 6
     L.gdr_slots.argtypes, L.gdr_slots.restype = [i] * 4, i64
     L.gdr_ckpt_bytes.argtypes, L.gdr_ckpt_bytes.restype = dims + [i] * 2, sz
-    for n in ("gdr_fwd_workspace_bytes", "gdr_bwd_workspace_bytes"):
+    for n in ("gdr_fwd_workspace_bytes", "gdr_fwd_train_workspace_bytes", "gdr_bwd_workspace_bytes"):
         getattr(L, n).argtypes, getattr(L, n).restype = dims + [i] * 3, sz
     L.gdr_fwd.argtypes = dims + [i] + [vp] * 6 + [i, f] + [vp] * 4 + [vp, sz, vp]
     L.gdr_bwd.argtypes = dims + [i] + [vp] * 8 + [i, f] + [vp] * 7 + [vp, sz, vp]
@@ -58,10 +58,10 @@ def _types():
 
 @functools.lru_cache(maxsize=1024)
 def _sizes(dims, code, N):
-    """Bytes of the checkpoints and of both workspaces."""
+    """Bytes of the checkpoints, of the forward's workspace without and with them, and of the backward's."""
     L, packed = _lib(), int(N > 0)
     return (L.gdr_ckpt_bytes(*dims, N, packed), L.gdr_fwd_workspace_bytes(*dims, code, N, packed),
-            L.gdr_bwd_workspace_bytes(*dims, code, N, packed))
+            L.gdr_fwd_train_workspace_bytes(*dims, code, N, packed), L.gdr_bwd_workspace_bytes(*dims, code, N, packed))
 
 
 def _check_inputs(fn, q, k, v, g, beta):
@@ -154,7 +154,7 @@ def gdr_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, scale=None, want_o=Tr
         o = torch.empty_like(v)
         fresh.append(o)
     code = _code(q.dtype)
-    nck, nws, _ = _sizes(dims, code, N)
+    nck, nws, nws_train, _ = _sizes(dims, code, N)
     if ckpt is not None:
         _check_state(fn, "ckpt", ckpt, (nck // 4,), dev)
     elif want_ckpt:
@@ -163,7 +163,7 @@ def gdr_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, scale=None, want_o=Tr
         _check_state(fn, "hT", hT, states, dev)
     elif want_hT:
         hT = torch.empty(states, dtype=torch.float32, device=dev)
-    workspace, wsb = _workspace(fn, workspace, nws, dev)
+    workspace, wsb = _workspace(fn, workspace, nws if ckpt is None else nws_train, dev)
     _launch(fn, L.gdr_fwd, dev, *dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
             _ptr(cu_seqlens), N, K ** -0.5 if scale is None else scale, _ptr(h0), _ptr(o), _ptr(ckpt), _ptr(hT),
             workspace.data_ptr(), wsb)
@@ -184,7 +184,7 @@ def gdr_bwd(do, q, k, v, g, beta, ckpt, dhT=None, *, cu_seqlens=None, scale=None
     dims = (B, T, Hk, H, K, V)
     _check_tensor(fn, "do", do, v.shape, v.dtype, dev)
     code = _code(q.dtype)
-    nck, _, nws = _sizes(dims, code, N)
+    nck, *_, nws = _sizes(dims, code, N)
     _check_state(fn, "ckpt", ckpt, (nck // 4,), dev)
     _check_state(fn, "dhT", dhT, states, dev)
     fresh = []

@@ -312,3 +312,20 @@ def test_ln_alignment_goes_by_the_parts():
     assert f(4, 64, 1, 1, 1, 0, fake(0) + 2, None, None, 1e-5, fake(1), None, None, None) == ERR_ALIGN
     assert f(4, 63, 1, 1, 1, 0, fake(0) + 1, None, None, 1e-5, fake(1), None, None, None) == ERR_ALIGN
     assert f(4, 63, 1, 1, 1, 0, fake(0), fake(2) + 2, None, 1e-5, fake(1), None, None, None) == ERR_ALIGN
+
+
+def test_workspace_of_a_training_forward():
+    """The checkpoints hold T and the gates, so that a forward that leaves them needs the planes of fp32 inputs only."""
+    lib = gdr._lib()
+    train = [lib.gdr_fwd_train_workspace_bytes(2, 65, 2, 4, 64, 128, dt, 0, 0) for dt in (0, 1)]
+    assert train == [2 * 3 * 2 * (2 * 65 * 2 * 64), 256]
+    assert train[0] == lib.gdr_fwd_workspace_bytes(2, 65, 2, 4, 64, 128, 0, 0, 0) - 16 * 3392 * 4
+    assert lib.gdr_fwd_train_workspace_bytes(2, 65, 3, 4, 64, 128, 0, 0, 0) == 0
+
+
+@needs_no_gpu
+def test_workspace_of_a_training_forward_is_checked():
+    assert _fwd(wsb=255) == ERR_WS and _fwd(ck=None, wsb=256) == ERR_WS
+    n = gdr._lib().gdr_fwd_train_workspace_bytes(1, 64, 1, 2, 64, 64, 0, 0, 0)
+    assert n > 256 and _fwd(dt=0, wsb=n - 1) == ERR_WS
+    assert _fwd(ws=fake(6) + 64) == ERR_ALIAS                           # inside ckpt
