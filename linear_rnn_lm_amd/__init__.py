@@ -536,6 +536,13 @@ def _fits(t, shape, dtype, dev):
     return t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous()
 
 
+def _dense(t, align=16):
+    """`t` itself, or a copy that is dense and at an address the library takes.  (A gradient may
+    arrive as a piece of a longer one, at any address; so may a tensor cut from a larger one.)"""
+    t = t.contiguous()
+    return t if t.data_ptr() % align == 0 else t.clone()
+
+
 def _launch(fn, entry, dev, *args):
     """Call a library entry point on the current stream of `dev` with that device
     current, and raise its error."""

@@ -18,7 +18,8 @@ offsets stay on the GPU: nothing waits for them, and a call can be captured into
 a graph and replayed with other offsets.  (As with every autograd op, capture a
 backward only on leaves that no live eager graph uses.)
 
-Tensors are dense; GDR makes copies of those that are not.  Calls of several
+Tensors are dense and lie at multiples of 16 bytes (g and beta: 4); GDR makes copies of
+those that do not.  Calls of several
 streams or threads may overlap as long as they share no output and no workspace.
 """
 from __future__ import annotations
@@ -26,7 +27,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import BF16, F32, _check_bytes, _dense_on, _fits, _launch, _LazyOpOf, _ptr, _where, lib
+from . import BF16, F32, _check_bytes, _dense, _dense_on, _fits, _launch, _LazyOpOf, _ptr, _where, lib
 
 GDR_CHUNK = 64
 
@@ -249,8 +250,8 @@ def _make_autograd():
         @staticmethod
         def forward(ctx, q, k, v, g, beta, h0=None, cu_seqlens=None, scale=None):
             ctx.set_materialize_grads(False)               # a gradient that is not there costs nothing
-            ins = [q.contiguous(), k.contiguous(), v.contiguous(), g.contiguous().float(), beta.contiguous().float()]
-            h0c = None if h0 is None else h0.contiguous().float()
+            ins = [_dense(q), _dense(k), _dense(v), g.contiguous().float(), beta.contiguous().float()]
+            h0c = None if h0 is None else _dense(h0.float())
             need = any(ctx.needs_input_grad)
             o, ckpt, hT = gdr_fwd(*ins, h0c, cu_seqlens=cu_seqlens, scale=scale, want_ckpt=need)
             ctx.save_for_backward(*ins, ckpt, cu_seqlens)
@@ -261,8 +262,8 @@ def _make_autograd():
         @once_differentiable                               # a gradient of the gradient is an error, not a zero
         def backward(ctx, do, dhT):
             *ins, ckpt, cu = ctx.saved_tensors
-            do = torch.zeros_like(ins[2]) if do is None else do.to(ins[2].dtype).contiguous()
-            dhT = None if dhT is None else dhT.contiguous().float()
+            do = torch.zeros_like(ins[2]) if do is None else _dense(do.to(ins[2].dtype))
+            dhT = None if dhT is None else _dense(dhT.float())
             tg, tb, th = ctx.types
             dq, dk, dv, dg, dbeta, dh0 = gdr_bwd(do, *ins, ckpt, dhT, cu_seqlens=cu, scale=ctx.scale,
                                                  want_dh0=th is not None)

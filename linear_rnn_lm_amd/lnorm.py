@@ -10,14 +10,15 @@ y = (x - mean) / sqrt(var + eps) * weight + bias.  x: (..., C) fp32 or bf16; y h
 x's type, or bf16 for an fp32 x with ``out_dtype=torch.bfloat16`` (the
 recurrence's fp32 output into a bf16 layer).  weight, bias: (C,) fp32 or bf16, or
 None.  mean, rstd: (rows, groups) fp32.  dx has x's type, dweight and dbias are fp32.
-Tensors are dense; LN makes copies of those that are not.
+Tensors are dense and, where the parts are a multiple of 8 channels, lie at multiples of
+16 bytes; LN makes copies of those that do not.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
 
-from . import BF16, F32, _check_bytes, _dense_on, _fits, _launch, _LazyOpOf, _ptr, _where, lib
+from . import BF16, F32, _check_bytes, _dense, _dense_on, _fits, _launch, _LazyOpOf, _ptr, _where, lib
 
 
 @functools.lru_cache(maxsize=None)
@@ -153,12 +154,13 @@ def _make_autograd():
 
         @staticmethod
         def forward(ctx, x, weight=None, bias=None, groups=1, eps=1e-5, out_dtype=None):
-            x = x.contiguous()
-            weight = None if weight is None else weight.contiguous()
-            y, mean, rstd = ln_fwd(x, weight, None if bias is None else bias.contiguous(), groups=groups, eps=eps,
-                                   out_dtype=out_dtype)
+            # other widths go value by value, at any address of theirs
+            align = 1 if x.dim() and x.shape[-1] % 8 else 16
+            x = _dense(x, align)
+            weight, bias = (None if t is None else _dense(t, align) for t in (weight, bias))
+            y, mean, rstd = ln_fwd(x, weight, bias, groups=groups, eps=eps, out_dtype=out_dtype)
             ctx.save_for_backward(x, weight, mean, rstd)
-            ctx.groups, ctx.out, ctx.tb = groups, y.dtype, None if bias is None else bias.dtype
+            ctx.groups, ctx.out, ctx.align, ctx.tb = groups, y.dtype, align, None if bias is None else bias.dtype
             return y
 
         @staticmethod
@@ -168,7 +170,7 @@ def _make_autograd():
             nx, nw, nb = (*ctx.needs_input_grad, False, False)[:3]     # only what was passed is listed
             if not (nx or nw or nb):
                 return (None,) * 6
-            dx, dw, db = ln_bwd(dy.to(ctx.out).contiguous(), x, weight, mean, rstd, groups=ctx.groups, want_dx=nx,
+            dx, dw, db = ln_bwd(_dense(dy.to(ctx.out), ctx.align), x, weight, mean, rstd, groups=ctx.groups, want_dx=nx,
                                 want_dw=nw or nb)
             return dx, dw.to(weight.dtype) if nw else None, db.to(ctx.tb) if nb else None, None, None, None
 
