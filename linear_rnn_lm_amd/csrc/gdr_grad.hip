@@ -19,12 +19,12 @@
 // serve H / Hk value heads: one workgroup does all of them in turn, so the sums over
 // the heads stay in registers and in one order.
 //
-// It reads S, U, G1, Z, q, k and dout and writes dq and dk: 1.73 GB at B8 T4096 H32 64 x 64,
-// 340 us at the rate of a large copy; it takes 445 to 480 (the splitting into planes
+// It reads S, U, G1, Z, q, k and dout and writes dq and dk: 1.83 GB at B8 T4096 H32 64 x 64,
+// 360 us at the rate of a large copy; it takes 490 to 510 (the splitting into planes
 // and the products overlap the loads of the other workgroup on the unit, not wholly).
 // K = 128 takes a workgroup for either half of the columns: with one for both, 8200 packed
-// tokens of 8 key and 16 value heads made 2.1 rounds of the chip's 512 and 232 us, now
-// 4.3 rounds of half the work and 207 us.
+// tokens of 8 key and 16 value heads made 2.1 rounds of the chip's 512 and 232 us, with
+// 4.3 rounds of half the work 207 (213 since dg has W).
 #include "gdr_device.h"
 #include "gdr_internal.h"
 #include "wkv7_internal.h"

@@ -4,8 +4,9 @@
 //     T = (I + A)^-1,  A = strict_lower(b_t Lam K K^T)
 //
 // with the chunk's gates (see gdr_device.h).  All chunks of all heads run at
-// once, one workgroup of four waves each.  The data moved would take 57 us at B8
-// T4096 H32 K64 (16384 chunks of heads; 290 MB), the kernel takes 124: each workgroup is a row
+// once, one workgroup of four waves each.  The data moved would take 83 us at B8
+// T4096 H32 K64 (16384 chunks of heads; 420 MB by the counters, g and beta once per XCD), the
+// kernel takes 122 to 129: each workgroup is a row
 // of dependent steps (loads, products, substitution, two levels of block products), so
 // what counts is how many of them a unit holds.  Seven fit 18 KB of LDS and 72 registers
 // each; four, with A and T apart and five columns of A ahead, took 171 us, and eight, which
@@ -166,8 +167,8 @@ __global__ __launch_bounds__(256, NX == 1 ? 7 : 4) void prepare_kernel(Args p) {
         float x[16];
 #pragma unroll
         for (int t = 0; t < 16; ++t) x[t] = t == r16 ? 1.f : 0.f;
-        // once x[s] is final every later row takes A[t][s] x[s]; column s of A is read in
-        // 16-byte pieces, five columns ahead of their use
+        // once x[s] is final every later row takes A[t][s] x[s]; the columns of A are read three
+        // at a time, in 16-byte pieces, and then used (more of them ahead cost a workgroup per unit)
 #pragma unroll
         for (int s0 = 0; s0 < 15; s0 += 3) {
             f32x4 col[3][4];

@@ -13,12 +13,12 @@
 // order.  Of two memory waves one copies the next chunks' K, v and gates into
 // LDS, the other splits their T into planes there.  One barrier per chunk.
 //
-// What bounds it.  With few heads the chain: one chunk of 64 tokens takes 2.1 us at K = V =
-// 128 (B1 T32768 H32: 1.10 ms for 512 chunks, 1.8 us of each the state wave's MFMAs and
-// the VALU work between them) and about 2.6 us at K = V = 64 with two slices (B12 T1024 H6:
-// 42 and 40 us for 16 chunks).  With heads enough HBM: at B8 T4096 H32 64 x 64 the
-// training forward moves 1.47 GB (S, U, M and T to and fro) in 335 us, the backward
-// scan 1.44 GB in 376 us, 4.4 and 3.8 TB/s.
+// What bounds it.  With few heads the chain: one chunk of 64 tokens takes 4700 cycles at K = V =
+// 128 (B1 T32768 H32: 1.15 ms a call, 0.14 of them preparation, 512 chunks; the state wave's MFMAs
+// and the VALU work between them, measured alone, took seven eighths of that) and about 3.0 us forward, 2.5
+// backward at K = V = 64 with two slices (B12 T1024 H6: 48 and 40 us for 16 chunks).  With heads
+// enough HBM: at B8 T4096 H32 64 x 64 the training forward moves 1.51 GB (S, U, M and T to and fro)
+// in 383 to 411 us, the backward scan 1.51 GB in 376 to 383, 3.7 to 4.0 TB/s.
 //
 // Memory instructions are issued one wave at a time on a compute unit, 16 and more
 // cycles each, and a wave that issues one waits its turn; so token columns
@@ -120,8 +120,10 @@ struct Where {
         hk = h / (p.H / p.Hk);
         const Seqs seqs{p.cu, p.N, p.T, p.NC};
         // long ones first, so that none starts when the others are done (training of 9 packed sequences, 8200 tokens,
-        // 16 heads of 128: 495 -> 459 us, 472 -> 460, 466 -> 464 by the lengths); of many workgroups per unit the last
-        // is a small part, and the search costs more (23 sequences, 32 heads, 11 per unit: 341 -> 350)
+        // 16 heads of 128, 576 workgroups: 513 -> 488 us, 485 -> 468, 506 -> 472 by the lengths); of many workgroups per
+        // unit the last is a small part, and the search costs as much (1536 of 12 sequences, forward: 255 -> 247,
+        // 265 -> 249, 262 -> 245; 1152 of 9: 229 -> 220, 217 -> 221, 215 -> 216; 2048 of 16: 330 -> 328, 323 -> 325,
+        // 321 -> 329; 2944 of 23: 354 -> 363, 360 -> 361, 356 -> 361).  1024: four per unit.
         if (p.cu && p.N > 1 && p.N <= 64 && gridDim.x <= 1024) n = longest(seqs, n);
         seq_span(seqs, n, tok0, len, slot0);
         nc = (len + C - 1) / C;

@@ -375,7 +375,10 @@ int teams_of(int64_t rows, int G, int L, int n_cu, int waves_per_cu) {
 // are written and read again, and more rows in flight no longer help (gradients of 65536
 // x 768: 53 us, with 1024 of them 60, with 256 53; 32768 x 2048 in 32 parts: 84, 86, 119;
 // 4096 x 2048: 22 with 256, 24 with 512).  Without combining: 65536 x 768 92 us,
-// 12288 x 384 20 instead of 14.
+// 12288 x 384 20 instead of 14; part counts that do not divide 256 / L go that way (forward and
+// gradients of 32768 x 768 in 12 parts 54 us, in 8 parts 47; 12288 x 384 in 6 parts 30, in one 29).
+// 256 units of 16 waves bound the teams then: the chip's own, since the workspace is asked
+// for without a device.
 struct Share {
     bool combine;
     int parts;

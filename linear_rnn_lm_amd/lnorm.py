@@ -11,7 +11,10 @@ x's type, or bf16 for an fp32 x with ``out_dtype=torch.bfloat16`` (the
 recurrence's fp32 output into a bf16 layer).  weight, bias: (C,) fp32 or bf16, or
 None.  mean, rstd: (rows, groups) fp32.  dx has x's type, dweight and dbias are fp32.
 Tensors are dense and, where the parts are a multiple of 8 channels, lie at multiples of
-16 bytes; LN makes copies of those that do not.
+16 bytes; LN makes copies of those that do not.  Calls of several streams or threads
+may overlap as long as they share no output and no workspace, and calls can be captured
+into a graph (as with every autograd op, a backward only on leaves that no live eager
+graph uses).
 """
 from __future__ import annotations
 
