@@ -14,10 +14,10 @@
 // Each term of dg_j is one that the decay of token j enters, once, as a factor.  (Suffix
 // sums of q.dQ and k.dK would need no W, but undecayed terms, the diagonal of P and the end
 // terms of later tokens, come and go in them: with log decays of -5 dg was off by 6e-5 to 1e-4
-// of itself, with -10 by 1e-2, with -20 it had no digit left.)  The sum over s < j is a prefix along a lane's eight s and the
-// lanes of a row, the sum over t >= j one over the lanes of a tile.  q and k of one key head
-// serve H / Hk value heads: one workgroup does all of them in turn, so the sums over
-// the heads stay in registers and in one order.
+// of itself, with -10 by 1e-2, with -20 it had no digit left.)  The sum over s < j is a
+// prefix along a lane's eight s and the lanes that hold a row, the sum over t >= j one over
+// the lanes of a tile.  q and k of one key head serve H / Hk value heads: one workgroup does
+// all of them in turn, so the sums over the heads stay in registers and in one order.
 //
 // It reads S, U, G1, Z, q, k and dout and writes dq and dk: 1.83 GB at B8 T4096 H32 64 x 64,
 // 360 us at the rate of a large copy; it takes 490 to 510 (the splitting into planes
