@@ -14,6 +14,10 @@ CPU fallback; if the library is missing, calls raise.
     o = gdr_step(q, k, v, g, beta, state, slots=slots) # its recurrent step over a pool
     y, mean, rstd = ln_fwd(x, weight, bias, groups=H)  # layer norm, see lnorm.py
 
+    y, hT = conv_fwd(x, weight, bias)                  # short causal convolution, see conv.py
+    y, ckpt, hT = ssm_fwd(x, dt, A, b, c, D, z)        # selective state space scan, see ssm.py
+    r, h, stats = rn_fwd(o, gate, res, norm2="rms")    # norm, gate, residual, next norm, see rnorm.py
+
 The recurrence (rwkv-mlx page, section "Metal kernel architecture"): per
 head a 64x64 fp32 state S; per token sa = S a, S = S diag(w) + v k^T + sa b^T,
 y = S r.  Inputs r, w, k, v, a, b are fp32 or bf16; all outputs are fp32.
@@ -27,7 +31,9 @@ import os
 __all__ = ["lib", "fwd", "fwd_sequential", "fwd_scan", "chunk_prepare", "chunk_inverse", "bwd", "bwd_scan",
            "bwd_inputs", "step", "WKV7", "Wkv7Error",
            "num_chunks", "workspace_bytes", "chunk_ops_bytes", "CHUNK", "HEAD_SIZE",
-           "gdr_fwd", "gdr_bwd", "gdr_step", "GDR", "GDR_CHUNK", "ln_fwd", "ln_bwd", "LN"]
+           "gdr_fwd", "gdr_bwd", "gdr_step", "GDR", "GDR_CHUNK", "ln_fwd", "ln_bwd", "LN",
+           "ssm_fwd", "ssm_bwd", "ssm_step", "SSM", "SSM_BLOCK", "conv_fwd", "conv_bwd", "conv_step", "CONV",
+           "rn_fwd", "rn_bwd", "RN"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libwkv7.so")
@@ -578,6 +584,63 @@ class _LazyOpOf:
         return getattr(self._op, name)
 
 
+@functools.lru_cache(maxsize=None)
+def _types():
+    """The two input types and their codes, and fp32."""
+    import torch
+    return {torch.float32: F32, torch.bfloat16: BF16}, torch.float32
+
+
+def _ld_of(t):
+    """Values between two rows of a token tensor (B, T, ...) whose rows lie at one distance,
+    each row's values side by side; None for any other layout."""
+    shape, stride = t.shape, t.stride()
+    inner = 1
+    for d in range(len(shape) - 1, 1, -1):
+        if shape[d] > 1 and stride[d] != inner:
+            return None
+        inner *= shape[d]
+    B, T = shape[:2]
+    ld = stride[1] if T > 1 else stride[0] if B > 1 else inner
+    return ld if ld >= inner and (B < 2 or T < 2 or stride[0] == T * ld) else None
+
+
+def _row_ld(fn, name, t, shape, dtype, dev):
+    """The same, checked (0 for None)."""
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} is {_where(t)}, expected {tuple(shape)} {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, expected {dev} (the device of the inputs)")
+    ld = _ld_of(t)
+    if ld is None:
+        raise ValueError(f"{fn}: {name}'s rows must have one distance and their values lie side by side "
+                         f"(got strides {t.stride()})")
+    return ld
+
+
+def _rows(t):
+    """`t` itself where a call takes its layout, else a dense copy."""
+    return t if t.dim() < 3 or _ld_of(t) is not None else t.contiguous()
+
+
+def _fresh_rows(shape, dtype, dev, N, fresh):
+    """A new token tensor.  With packed sequences (N > 0) the rows that none covers have to be
+    zeroed: its entry in `fresh` asks for that, or it is made of zeros where a row is no
+    multiple of four bytes."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if N:
+        if t.element_size() * (t.numel() // shape[1]) % 4:
+            return t.zero_()
+        fresh.append(t)
+    return t
+
+
 # The operators beside the recurrence; their modules use the helpers above.
 from .gdr import GDR, GDR_CHUNK, gdr_bwd, gdr_fwd, gdr_step  # noqa: E402
 from .lnorm import LN, ln_bwd, ln_fwd  # noqa: E402
+from .ssm import SSM, SSM_BLOCK, ssm_bwd, ssm_fwd, ssm_step  # noqa: E402
+from .conv import CONV, conv_bwd, conv_fwd, conv_step  # noqa: E402
+from .rnorm import RN, rn_bwd, rn_fwd  # noqa: E402

@@ -21,7 +21,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwkv7.so")
 SOURCES = ["wkv7_api.hip", "wkv7_scan.hip", "wkv7_seq.hip", "wkv7_grad.hip", "wkv7_division.hip",
            "gdr_api.hip", "gdr_prepare.hip", "gdr_scan.hip", "gdr_grad.hip", "gdr_step.hip",
-           "lnorm.hip"]
+           "lnorm.hip",
+           "ssm_api.hip", "ssm_scan.hip", "ssm_grad.hip", "ssm_step.hip",
+           "conv.hip", "rnorm.hip", "column_sums.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -1,0 +1,46 @@
+// column_sums.hip -- column sums of partial sums (gfx950): 32 columns by 32 rows of
+// threads, four rows of each in flight; bound by the launch and one round trip.
+#include "column_sums.h"
+
+namespace sums {
+namespace {
+
+__global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, int rows, int64_t n, float* out0, int64_t n0,
+                                                           float* out1) {
+    __shared__ float red[32][33];
+    const int cl = threadIdx.x & 31, r0 = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + cl;
+    const float* src = part + (c < n ? c : n - 1);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r = r0; r < rows; r += 128) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int q = r + 32 * u;
+            const float x = src[(int64_t)(q < rows ? q : rows - 1) * n];
+            s[u] += q < rows ? x : 0.f;
+        }
+    }
+    red[r0][cl] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    if (r0 == 0 && c < n) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x += red[i][cl];
+        if (c < n0) {
+            if (out0) out0[c] = x;
+        } else if (out1) {
+            out1[c - n0] = x;
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_column_sums(const float* part, int rows, int64_t n, float* out0, int64_t n0, float* out1,
+                              hipStream_t s) {
+    hipLaunchKernelGGL(column_sums_kernel, dim3((uint32_t)((n + 31) / 32)), dim3(1024), 0, s, part, rows, n, out0, n0,
+                       out1);
+    return hipGetLastError();
+}
+
+}  // namespace sums

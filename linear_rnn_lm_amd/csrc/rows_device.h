@@ -1,0 +1,108 @@
+// rows_device.h -- device-side building blocks of the selective scan, the short
+// convolution and the block norm (gfx950): token values, activations, lane sums, and where
+// the sequences of a call lie.
+#pragma once
+
+#include "wkv7_device.h"
+
+namespace rows {
+
+using wkv7::f32x4;
+using wkv7::lds_barrier;
+
+// One value of a token tensor.  widen() is apart from the load, so that a load ahead of its
+// use does not wait where it is issued.
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+template <typename T>
+__device__ __forceinline__ float ld(const T* p) { return widen(*p); }
+__device__ __forceinline__ void st(float* p, float v) { *p = v; }
+__device__ __forceinline__ void st(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
+// 1 / (1 + e^-v): e^-v may overflow to infinity, its reciprocal is then 0, as it should be.
+__device__ __forceinline__ float sigmoid(float v) {
+    return __builtin_amdgcn_rcpf(1.f + exp2_f(-kLog2e * v));
+}
+// max(v, 0) + log(1 + e), e = e^-|v|.  With w = 1 + e rounded, log(1 + e) = e log(w) / (w - 1)
+// to a few roundings, since log(w) / (w - 1) hardly changes between w and 1 + e; for e below half a
+// step of 1 (w = 1) it is e.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = exp2_f(-kLog2e * __builtin_fabsf(v)), w = 1.f + e;
+    const float l = kLn2 * __builtin_amdgcn_logf(w) * (e * __builtin_amdgcn_rcpf(w - 1.f));
+    return __builtin_fmaxf(v, 0.f) + (w == 1.f ? e : l) + (v != v ? v : 0.f);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, false));
+}
+
+// Sums over the four lanes l, l + 16, l + 32, l + 48 of four values: lane (g, r), g = l / 16,
+// gets the sum of value row_of(g).  A swap and an add sum two values at once, each half of the
+// lanes keeping one.
+__device__ __forceinline__ int row_of(int g) { return ((g & 1) << 1) | (g >> 1); }
+__device__ __forceinline__ float rows_sum4(float y0, float y1, float y2, float y3) {
+    auto pair32 = [](float a, float b) {
+        const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+    };
+    const float p = pair32(y0, y1), q = pair32(y2, y3);
+    const auto h = __builtin_amdgcn_permlane16_swap(__float_as_uint(p), __float_as_uint(q), false, false);
+    return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+}
+
+// Where the sequences lie, and how they are cut into pieces of `len` tokens.  Dense: sequence
+// n is row n of (B, T), its pieces are slots n per + i.  Packed: sequence n is the tokens cu[n] ..
+// cu[n + 1] - 1, its piece i is slot cu[n] / len + n + i: strictly increasing over
+// sequences and pieces, at most T / len + N - 1, so no table is needed.  The offsets come from
+// device memory: they are clamped to 0 .. T and to non-decreasing pairs, so that no value of
+// theirs leads outside the tensors.
+struct Seqs {
+    const int* cu;   // NULL: dense
+    int N, T;
+};
+
+__device__ __forceinline__ void seq_span(const Seqs& s, int n, int64_t& tok0, int& len) {
+    if (s.cu) {
+        const int a = min(max(s.cu[n], 0), s.T), b = min(max(s.cu[n + 1], a), s.T);
+        tok0 = a;
+        len = b - a;
+    } else {
+        tok0 = (int64_t)n * s.T;
+        len = s.T;
+    }
+}
+__device__ __forceinline__ int pieces_dense(int T, int len) { return (T - 1) / len + 1; }
+__device__ __forceinline__ int first_slot(const Seqs& s, int n, int64_t tok0, int len) {
+    return s.cu ? (int)tok0 / len + n : n * pieces_dense(s.T, len);
+}
+
+// The piece of a slot: its sequence n and its index i there; false if the slot is no
+// sequence's.  The first piece of an empty sequence exists.
+__device__ __forceinline__ bool slot_piece(const Seqs& s, int slot, int len, int& n, int& i) {
+    if (!s.cu) {
+        const int per = pieces_dense(s.T, len);
+        n = slot / per;
+        i = slot % per;
+        return true;
+    }
+    // the last sequence whose first slot is at or before this one
+    int lo = 0, hi = s.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (min(max(s.cu[mid], 0), s.T) / len + mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    int64_t t0;
+    int L;
+    seq_span(s, lo, t0, L);
+    n = lo;
+    i = slot - first_slot(s, lo, t0, len);
+    return i == 0 || (i > 0 && (int64_t)i * len < L);
+}
+
+}  // namespace rows

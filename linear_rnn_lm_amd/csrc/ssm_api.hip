@@ -1,0 +1,186 @@
+// ssm_api.hip -- the C ABI of the selective scan (declared in include/ssm.h): argument
+// checks on the host, then kernel launches on the caller's stream.
+#include <stdint.h>
+
+#include "abi_checks.h"
+#include "ssm.h"
+#include "ssm_internal.h"
+
+namespace {
+
+using abi::Buf;
+
+struct Shape {
+    int64_t tokens, slots, state, ckpt;   // checkpoint slots; values of the states and of the checkpoints
+    int64_t part_A, part_D, part_bc;      // values of the backward's parts
+    int N, seg, segs;
+    int e;
+};
+
+constexpr int64_t kMax = int64_t(1) << 40;
+
+int64_t slots_of(int B, int T, int N, bool packed, int len) {
+    return packed ? T / len + (int64_t)N : (int64_t)B * ((T - 1) / len + 1);
+}
+
+wkv7_status dims_ok(int B, int T, int C, int S, int G) {
+    if (B < 1 || T < 1 || C < 1 || G < 1 || (S != 16 && S != 32 && S != 64)) return WKV7_ERR_SHAPE;
+    if (C % G || (G > 1 && C / G % 64) || C > (1 << 20)) return WKV7_ERR_SHAPE;
+    if ((int64_t)B * T > kMax / C || (int64_t)B * T > INT32_MAX) return WKV7_ERR_SHAPE;
+    return WKV7_OK;
+}
+
+wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* s) {
+    if (dims_ok(B, T, C, S, G) != WKV7_OK || (packed && (B != 1 || N < 1))) return WKV7_ERR_SHAPE;
+    s->N = packed ? N : B;
+    s->tokens = (int64_t)B * T;
+    s->slots = slots_of(B, T, N, packed, ssm::kBlock);
+    s->seg = (T + ssm::kBlock - 1) / ssm::kBlock * ssm::kBlock;
+    const int64_t segs = slots_of(B, T, N, packed, s->seg), blocks = (C + ssm::chans(S) - 1) / ssm::chans(S);
+    // a launch takes fewer than 2^32 threads: at most 512 for each segment and channel block
+    if (segs > (1 << 22) / (2 * blocks) || s->slots > INT32_MAX) return WKV7_ERR_SHAPE;
+    s->segs = (int)segs;
+    s->state = (int64_t)s->N * C * S;
+    s->ckpt = s->slots * C * S;
+    if (s->slots > kMax / (C * S) || s->N > kMax / (C * S)) return WKV7_ERR_SHAPE;
+    s->part_A = segs * C * S;
+    s->part_D = segs * C;
+    s->part_bc = blocks * s->tokens * 2 * S;
+    return WKV7_OK;
+}
+
+int64_t bwd_ws(const Shape& s) { return (s.part_bc + s.part_A + 2 * s.part_D) * 4; }
+int64_t span(int64_t rows, int64_t ld, int64_t n, int e) { return ((rows - 1) * ld + n) * e; }
+bool lds_ok(int64_t tokens, int C, int GS, int64_t x, int64_t dt, int64_t b, int64_t c, const void* z, int64_t z_ld) {
+    const int64_t most = kMax / tokens;
+    return x >= C && dt >= C && b >= GS && c >= GS && (!z || z_ld >= C) && x <= most && dt <= most && b <= most && c <= most &&
+           (!z || z_ld <= most);
+}
+wkv7_status status_of(hipError_t e) { return e == hipSuccess ? WKV7_OK : WKV7_ERR_HIP; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t ssm_slots(int B, int T, int N, int packed) {
+    if (B < 1 || T < 1 || (packed && (N < 1 || B != 1))) return 0;
+    return slots_of(B, T, N, packed != 0, ssm::kBlock);
+}
+
+size_t ssm_ckpt_bytes(int B, int T, int C, int S, int G, int N, int packed) {
+    Shape s;
+    return shape(B, T, C, S, G, N, packed != 0, &s) == WKV7_OK ? (size_t)s.ckpt * 4 : 0;
+}
+size_t ssm_fwd_workspace_bytes(int B, int T, int C, int S, int G, int N, int packed) {
+    Shape s;
+    return shape(B, T, C, S, G, N, packed != 0, &s) == WKV7_OK ? 16 : 0;
+}
+size_t ssm_bwd_workspace_bytes(int B, int T, int C, int S, int G, int N, int packed) {
+    Shape s;
+    return shape(B, T, C, S, G, N, packed != 0, &s) == WKV7_OK ? (size_t)bwd_ws(s) : 0;
+}
+
+wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, const void* x, int64_t x_ld, const void* dt,
+                    int64_t dt_ld, const float* A, const void* b, int64_t b_ld, const void* c, int64_t c_ld,
+                    const float* D, const void* z, int64_t z_ld, const float* dt_bias, int softplus,
+                    const int32_t* cu_seqlens, int N, const float* h0, void* y, float* ckpt, float* hT, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    if (in_dtype != WKV7_F32 && in_dtype != WKV7_BF16) return WKV7_ERR_DTYPE;
+    Shape s;
+    wkv7_status st = shape(B, T, C, S, G, N, cu_seqlens != nullptr, &s);
+    if (st != WKV7_OK) return st;
+    if (!lds_ok(s.tokens, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld)) return WKV7_ERR_SHAPE;
+    const int e = in_dtype == WKV7_BF16 ? 2 : 4;
+    const int64_t need = (int64_t)ssm_fwd_workspace_bytes(B, T, C, S, G, N, cu_seqlens != nullptr), n = s.tokens;
+    const Buf bufs[] = {{x, span(n, x_ld, C, e), true, false, e}, {dt, span(n, dt_ld, C, e), true, false, e},
+                        {A, (int64_t)C * S * 4, true, false, 16}, {b, span(n, b_ld, G * S, e), true, false, e},
+                        {c, span(n, c_ld, G * S, e), true, false, e}, {D, C * 4LL, false, false, 4},
+                        {z, span(n, z_ld, C, e), false, false, e}, {dt_bias, C * 4LL, false, false, 4},
+                        {cu_seqlens, (s.N + 1) * 4LL, false, false, 4}, {h0, s.state * 4, false, false, 16},
+                        {y, n * C * e, false, true, e}, {ckpt, s.ckpt * 4, false, true, 16},
+                        {hT, s.state * 4, false, true, 16}, {workspace, need, false, true, 16}};
+    if (!y && !ckpt && !hT) return WKV7_ERR_ARG;
+    st = abi::check(bufs, h0 == hT ? h0 : nullptr);
+    if (st != WKV7_OK) return st;
+    if (!workspace || workspace_bytes < (size_t)need) return WKV7_ERR_WORKSPACE;
+    ssm::Args a = {};
+    a.x = x; a.dt = dt; a.b = b; a.c = c; a.z = z; a.x_ld = x_ld; a.dt_ld = dt_ld; a.b_ld = b_ld; a.c_ld = c_ld;
+    a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.h0 = h0; a.y = y; a.ckpt = ckpt; a.hT = hT; a.cu = cu_seqlens;
+    a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.N = s.N; a.seg = s.seg; a.segs = s.segs;
+    return status_of(ssm::launch_fwd(a, in_dtype == WKV7_BF16, static_cast<hipStream_t>(stream)));
+}
+
+wkv7_status ssm_bwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, const void* dy, const float* dhT,
+                    const void* x, int64_t x_ld, const void* dt, int64_t dt_ld, const float* A, const void* b,
+                    int64_t b_ld, const void* c, int64_t c_ld, const float* D, const void* z, int64_t z_ld,
+                    const float* dt_bias, int softplus, const int32_t* cu_seqlens, int N, const float* ckpt, void* dx,
+                    void* ddt, float* dA, void* db, void* dc, float* dD, void* dz, float* ddt_bias, float* dh0,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    if (in_dtype != WKV7_F32 && in_dtype != WKV7_BF16) return WKV7_ERR_DTYPE;
+    Shape s;
+    wkv7_status st = shape(B, T, C, S, G, N, cu_seqlens != nullptr, &s);
+    if (st != WKV7_OK) return st;
+    if (!lds_ok(s.tokens, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld)) return WKV7_ERR_SHAPE;
+    if ((D != nullptr) != (dD != nullptr) || (z != nullptr) != (dz != nullptr)) return WKV7_ERR_ARG;
+    const int e = in_dtype == WKV7_BF16 ? 2 : 4;
+    const int64_t n = s.tokens, rows = n * C * e, brows = n * G * S * e, sb = s.state * 4;
+    const Buf bufs[] = {{dy, rows, true, false, e}, {dhT, sb, false, false, 16}, {x, span(n, x_ld, C, e), true, false, e},
+                        {dt, span(n, dt_ld, C, e), true, false, e}, {A, (int64_t)C * S * 4, true, false, 16},
+                        {b, span(n, b_ld, G * S, e), true, false, e}, {c, span(n, c_ld, G * S, e), true, false, e},
+                        {D, C * 4LL, false, false, 4}, {z, span(n, z_ld, C, e), false, false, e},
+                        {dt_bias, C * 4LL, false, false, 4}, {cu_seqlens, (s.N + 1) * 4LL, false, false, 4},
+                        {ckpt, s.ckpt * 4, true, false, 16}, {dx, rows, true, true, e}, {ddt, rows, true, true, e},
+                        {dA, (int64_t)C * S * 4, true, true, 4}, {db, brows, true, true, e}, {dc, brows, true, true, e},
+                        {dD, C * 4LL, false, true, 4}, {dz, rows, false, true, e}, {ddt_bias, C * 4LL, false, true, 4},
+                        {dh0, sb, false, true, 16}, {workspace, bwd_ws(s), false, true, 16}};
+    st = abi::check(bufs);
+    if (st != WKV7_OK) return st;
+    if (!workspace || workspace_bytes < (size_t)bwd_ws(s)) return WKV7_ERR_WORKSPACE;
+    ssm::Args a = {};
+    a.x = x; a.dt = dt; a.b = b; a.c = c; a.z = z; a.x_ld = x_ld; a.dt_ld = dt_ld; a.b_ld = b_ld; a.c_ld = c_ld;
+    a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.dy = dy; a.dhT = dhT; a.ckpt = const_cast<float*>(ckpt);
+    a.dx = dx; a.ddt = ddt; a.dz = dz; a.dh0 = dh0; a.cu = cu_seqlens;
+    a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.N = s.N; a.seg = s.seg; a.segs = s.segs;
+    float* ws = static_cast<float*>(workspace);
+    a.part_bc = ws;
+    a.part_A = ws + s.part_bc;
+    a.part_D = a.part_A + s.part_A;
+    a.part_bias = a.part_D + s.part_D;
+    ssm::ReduceArgs r = {};
+    r.part_A = a.part_A; r.part_D = a.part_D; r.part_bias = a.part_bias; r.part_bc = a.part_bc;
+    r.dA = dA; r.dD = dD; r.ddt_bias = ddt_bias; r.db = db; r.dc = dc; r.cu = cu_seqlens;
+    r.B = B; r.T = T; r.C = C; r.S = S; r.G = G; r.N = s.N; r.segs = s.segs;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    hipError_t err = ssm::launch_bwd(a, in_dtype == WKV7_BF16, hs);
+    if (err == hipSuccess) err = ssm::launch_reduce(r, in_dtype == WKV7_BF16, hs);
+    return status_of(err);
+}
+
+wkv7_status ssm_step(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, const void* x, int64_t x_ld, const void* dt,
+                     int64_t dt_ld, const float* A, const void* b, int64_t b_ld, const void* c, int64_t c_ld,
+                     const float* D, const void* z, int64_t z_ld, const float* dt_bias, int softplus,
+                     const int32_t* slots, int P, const float* state, float* state_out, void* y, void* stream) {
+    if (in_dtype != WKV7_F32 && in_dtype != WKV7_BF16) return WKV7_ERR_DTYPE;
+    wkv7_status st = dims_ok(B, T, C, S, G);
+    if (st != WKV7_OK) return st;
+    if (P < 1 || (!slots && P < B) || P > kMax / ((int64_t)C * S)) return WKV7_ERR_SHAPE;
+    if (B > (1 << 24) / ((C + 15) / 16 + 1)) return WKV7_ERR_SHAPE;   // a launch takes fewer than 2^32 threads
+    const int64_t n = (int64_t)B * T, sb = (int64_t)P * C * S * 4;
+    if (!lds_ok(n, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld)) return WKV7_ERR_SHAPE;
+    const int e = in_dtype == WKV7_BF16 ? 2 : 4;
+    const Buf bufs[] = {{x, span(n, x_ld, C, e), true, false, e}, {dt, span(n, dt_ld, C, e), true, false, e},
+                        {A, (int64_t)C * S * 4, true, false, 16}, {b, span(n, b_ld, G * S, e), true, false, e},
+                        {c, span(n, c_ld, G * S, e), true, false, e}, {D, C * 4LL, false, false, 4},
+                        {z, span(n, z_ld, C, e), false, false, e}, {dt_bias, C * 4LL, false, false, 4},
+                        {slots, B * 4LL, false, false, 4}, {state, sb, true, false, 16}, {state_out, sb, true, true, 16},
+                        {y, n * C * e, true, true, e}};
+    st = abi::check(bufs, state == state_out ? state : nullptr);
+    if (st != WKV7_OK) return st;
+    ssm::StepArgs a = {};
+    a.x = x; a.dt = dt; a.b = b; a.c = c; a.z = z; a.x_ld = x_ld; a.dt_ld = dt_ld; a.b_ld = b_ld; a.c_ld = c_ld;
+    a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.state = state; a.state_out = state_out; a.y = y;
+    a.slots = slots; a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.P = P;
+    return status_of(ssm::launch_step(a, in_dtype == WKV7_BF16, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,48 @@
+// ssm_internal.h -- launchers of the selective scan, shared between its translation units.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ssm {
+
+constexpr int kBlock = 16;      // tokens that are worked on together; a checkpoint lies before each
+constexpr int chans(int S) { return S == 64 ? 32 : 64; }   // channels of a workgroup, with S states each
+
+struct Args {
+    const void *x, *dt, *b, *c, *z, *dy;
+    int64_t x_ld, dt_ld, b_ld, c_ld, z_ld;
+    const float *A, *D, *dt_bias, *h0, *dhT;
+    void *y, *dx, *ddt, *dz;
+    float *ckpt, *hT, *dh0;
+    float *part_A, *part_D, *part_bias, *part_bc;   // backward: sums per segment; per channel block and token
+    const int* cu;
+    int softplus, B, T, C, S, G, N;
+    int seg, segs;   // tokens of a segment (a multiple of kBlock) and segment slots
+};
+
+struct StepArgs {
+    const void *x, *dt, *b, *c, *z;
+    int64_t x_ld, dt_ld, b_ld, c_ld, z_ld;
+    const float *A, *D, *dt_bias, *state;
+    float* state_out;
+    void* y;
+    const int* slots;
+    int softplus, B, T, C, S, G, P;
+};
+
+// Sums of the backward's parts.
+struct ReduceArgs {
+    const float *part_A, *part_D, *part_bias, *part_bc;
+    float *dA, *dD, *ddt_bias;
+    void *db, *dc;
+    const int* cu;
+    int B, T, C, S, G, N, segs;
+};
+
+hipError_t launch_fwd(const Args& a, bool bf16, hipStream_t s);
+hipError_t launch_bwd(const Args& a, bool bf16, hipStream_t s);
+hipError_t launch_reduce(const ReduceArgs& a, bool bf16, hipStream_t s);
+hipError_t launch_step(const StepArgs& a, bool bf16, hipStream_t s);
+
+}  // namespace ssm
