@@ -27,14 +27,29 @@ __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f
 __device__ __forceinline__ float sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.f + exp2_f(-kLog2e * v));
 }
-// max(v, 0) + log(1 + e), e = e^-|v|.  With w = 1 + e rounded, log(1 + e) = e log(w) / (w - 1)
-// to a few roundings, since log(w) / (w - 1) hardly changes between w and 1 + e; for e below half a
-// step of 1 (w = 1) it is e.
+// max(v, 0) + log(1 + e), e = e^-|v|.  With w = 1 + e rounded and r = e - (w - 1) what the rounding
+// took, log(1 + e) = log(w) + r / w up to r^2; r is at most half a last place, so 1 - e / 2 is
+// near enough to 1 / w.  For e below half a last place of 1 that leaves e itself.
 __device__ __forceinline__ float softplus(float v) {
-    const float e = exp2_f(-kLog2e * __builtin_fabsf(v)), w = 1.f + e;
-    const float l = kLn2 * __builtin_amdgcn_logf(w) * (e * __builtin_amdgcn_rcpf(w - 1.f));
-    return __builtin_fmaxf(v, 0.f) + (w == 1.f ? e : l) + (v != v ? v : 0.f);
+    const float e = exp2_f(-kLog2e * __builtin_fabsf(v)), w = 1.f + e, r = e - (w - 1.f);
+    return __builtin_fmaxf(v, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), r * fmaf(-0.5f, e, 1.f));
 }
+
+// A value at a byte offset of the lane's from a pointer that is the same for the whole wave: one
+// 32-bit register per lane instead of a 64-bit address.
+template <typename T>
+__device__ __forceinline__ T ldo(const void* base, uint32_t off) {
+    return *reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
+}
+template <typename T>
+__device__ __forceinline__ T* pto(void* base, uint32_t off) {
+    return reinterpret_cast<T*>(static_cast<char*>(base) + off);
+}
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x) {

@@ -12,8 +12,9 @@ using abi::Buf;
 
 struct Shape {
     int64_t tokens, slots, state, ckpt;   // checkpoint slots; values of the states and of the checkpoints
-    int64_t part_A, part_D, part_bc;      // values of the backward's parts
+    int64_t part_A, part_D, part_bc;      // values of the backward's parts (per segment: (C, S) and (C))
     int N, seg, segs;
+    bool split;
     int e;
 };
 
@@ -30,12 +31,26 @@ wkv7_status dims_ok(int B, int T, int C, int S, int G) {
     return WKV7_OK;
 }
 
+// Tokens of a segment.  One segment per sequence where the sequences alone give the chip
+// kWaves waves; otherwise as many more as are missing, of 64 tokens at least, at most kMostSegs.
+constexpr int64_t kWaves = 4096, kMostSegs = 16;
+int segment_of(int B, int T, int C, int S) {
+    const int64_t waves = (int64_t)B * ((C + 15) / 16) * (S / 16);
+    int64_t n = (kWaves + waves - 1) / waves;
+    if (n > kMostSegs) n = kMostSegs;
+    int64_t seg = (T + n - 1) / n;
+    if (seg < 64) seg = 64;
+    if (seg > T) seg = T;
+    return (int)((seg + ssm::kBlock - 1) / ssm::kBlock * ssm::kBlock);
+}
+
 wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* s) {
     if (dims_ok(B, T, C, S, G) != WKV7_OK || (packed && (B != 1 || N < 1))) return WKV7_ERR_SHAPE;
     s->N = packed ? N : B;
     s->tokens = (int64_t)B * T;
     s->slots = slots_of(B, T, N, packed, ssm::kBlock);
-    s->seg = (T + ssm::kBlock - 1) / ssm::kBlock * ssm::kBlock;
+    s->seg = segment_of(B, T, C, S);
+    s->split = s->seg < T;
     const int64_t segs = slots_of(B, T, N, packed, s->seg), blocks = (C + ssm::chans(S) - 1) / ssm::chans(S);
     // a launch takes fewer than 2^32 threads: at most 512 for each segment and channel block
     if (segs > (1 << 22) / (2 * blocks) || s->slots > INT32_MAX) return WKV7_ERR_SHAPE;
@@ -49,10 +64,14 @@ wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* 
     return WKV7_OK;
 }
 
-int64_t bwd_ws(const Shape& s) { return (s.part_bc + s.part_A + 2 * s.part_D) * 4; }
+// What the segments leave; behind the parts of the backward.  Never 0, so that a size of 0 is
+// always one of invalid shapes, and a NULL workspace always an error.
+int64_t fwd_ws(const Shape& s) { return s.split ? (s.part_A + s.part_D) * 4 : 256; }
+int64_t bwd_ws(const Shape& s) { return (s.part_bc + s.part_A + 2 * s.part_D + (s.split ? s.part_A + s.part_D : 0)) * 4; }
 int64_t span(int64_t rows, int64_t ld, int64_t n, int e) { return ((rows - 1) * ld + n) * e; }
+constexpr int64_t kMaxLd = 1 << 24;   // 16 rows are addressed with 32-bit byte offsets
 bool lds_ok(int64_t tokens, int C, int GS, int64_t x, int64_t dt, int64_t b, int64_t c, const void* z, int64_t z_ld) {
-    const int64_t most = kMax / tokens;
+    const int64_t most = kMax / tokens < kMaxLd ? kMax / tokens : kMaxLd;
     return x >= C && dt >= C && b >= GS && c >= GS && (!z || z_ld >= C) && x <= most && dt <= most && b <= most && c <= most &&
            (!z || z_ld <= most);
 }
@@ -73,7 +92,7 @@ size_t ssm_ckpt_bytes(int B, int T, int C, int S, int G, int N, int packed) {
 }
 size_t ssm_fwd_workspace_bytes(int B, int T, int C, int S, int G, int N, int packed) {
     Shape s;
-    return shape(B, T, C, S, G, N, packed != 0, &s) == WKV7_OK ? 16 : 0;
+    return shape(B, T, C, S, G, N, packed != 0, &s) == WKV7_OK ? (size_t)fwd_ws(s) : 0;
 }
 size_t ssm_bwd_workspace_bytes(int B, int T, int C, int S, int G, int N, int packed) {
     Shape s;
@@ -91,7 +110,7 @@ wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     if (st != WKV7_OK) return st;
     if (!lds_ok(s.tokens, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld)) return WKV7_ERR_SHAPE;
     const int e = in_dtype == WKV7_BF16 ? 2 : 4;
-    const int64_t need = (int64_t)ssm_fwd_workspace_bytes(B, T, C, S, G, N, cu_seqlens != nullptr), n = s.tokens;
+    const int64_t need = fwd_ws(s), n = s.tokens;
     const Buf bufs[] = {{x, span(n, x_ld, C, e), true, false, e}, {dt, span(n, dt_ld, C, e), true, false, e},
                         {A, (int64_t)C * S * 4, true, false, 16}, {b, span(n, b_ld, G * S, e), true, false, e},
                         {c, span(n, c_ld, G * S, e), true, false, e}, {D, C * 4LL, false, false, 4},
@@ -107,7 +126,13 @@ wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     a.x = x; a.dt = dt; a.b = b; a.c = c; a.z = z; a.x_ld = x_ld; a.dt_ld = dt_ld; a.b_ld = b_ld; a.c_ld = c_ld;
     a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.h0 = h0; a.y = y; a.ckpt = ckpt; a.hT = hT; a.cu = cu_seqlens;
     a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.N = s.N; a.seg = s.seg; a.segs = s.segs;
-    return status_of(ssm::launch_fwd(a, in_dtype == WKV7_BF16, static_cast<hipStream_t>(stream)));
+    a.split = s.split;
+    a.sum_h = static_cast<float*>(workspace);
+    a.sum_d = a.sum_h + s.part_A;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    hipError_t err = s.split ? ssm::launch_segments(a, in_dtype == WKV7_BF16, false, hs) : hipSuccess;
+    if (err == hipSuccess) err = ssm::launch_fwd(a, in_dtype == WKV7_BF16, hs);
+    return status_of(err);
 }
 
 wkv7_status ssm_bwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, const void* dy, const float* dhT,
@@ -146,12 +171,16 @@ wkv7_status ssm_bwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     a.part_A = ws + s.part_bc;
     a.part_D = a.part_A + s.part_A;
     a.part_bias = a.part_D + s.part_D;
+    a.split = s.split;
+    a.sum_h = a.part_bias + s.part_D;
+    a.sum_d = a.sum_h + s.part_A;
     ssm::ReduceArgs r = {};
     r.part_A = a.part_A; r.part_D = a.part_D; r.part_bias = a.part_bias; r.part_bc = a.part_bc;
     r.dA = dA; r.dD = dD; r.ddt_bias = ddt_bias; r.db = db; r.dc = dc; r.cu = cu_seqlens;
     r.B = B; r.T = T; r.C = C; r.S = S; r.G = G; r.N = s.N; r.segs = s.segs;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t err = ssm::launch_bwd(a, in_dtype == WKV7_BF16, hs);
+    hipError_t err = s.split ? ssm::launch_segments(a, in_dtype == WKV7_BF16, true, hs) : hipSuccess;
+    if (err == hipSuccess) err = ssm::launch_bwd(a, in_dtype == WKV7_BF16, hs);
     if (err == hipSuccess) err = ssm::launch_reduce(r, in_dtype == WKV7_BF16, hs);
     return status_of(err);
 }

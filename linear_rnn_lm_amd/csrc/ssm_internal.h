@@ -16,9 +16,12 @@ struct Args {
     void *y, *dx, *ddt, *dz;
     float *ckpt, *hT, *dh0;
     float *part_A, *part_D, *part_bias, *part_bc;   // backward: sums per segment; per channel block and token
+    float *sum_h, *sum_d;    // per segment slot: what it leaves of a zero state (backward: of a zero gradient), (C, S);
+                             // the sum of its steps, (C)
     const int* cu;
     int softplus, B, T, C, S, G, N;
     int seg, segs;   // tokens of a segment (a multiple of kBlock) and segment slots
+    bool split;      // whether a sequence may have more than one segment
 };
 
 struct StepArgs {
@@ -40,6 +43,8 @@ struct ReduceArgs {
     int B, T, C, S, G, N, segs;
 };
 
+// With several segments to a sequence (split): their sums first, then all segments at once.
+hipError_t launch_segments(const Args& a, bool bf16, bool backward, hipStream_t s);
 hipError_t launch_fwd(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_bwd(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_reduce(const ReduceArgs& a, bool bf16, hipStream_t s);
