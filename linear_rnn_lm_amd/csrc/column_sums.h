@@ -6,9 +6,9 @@
 
 namespace sums {
 
-// out0[c] for c < n0, out1[c - n0] from there on: the sums of the n columns of `part`
-// (rows x n).  Either output may be NULL.
-hipError_t launch_column_sums(const float* part, int rows, int64_t n, float* out0, int64_t n0, float* out1,
-                              hipStream_t s);
+// The sums of the n columns of `part` (rows x n): the first n0 of them to out0, the next n1 to out1,
+// the rest to out2.  Any output may be NULL.
+hipError_t launch_column_sums(const float* part, int rows, int64_t n, float* out0, int64_t n0, float* out1, int64_t n1,
+                              float* out2, hipStream_t s);
 
 }  // namespace sums

@@ -6,7 +6,7 @@ namespace sums {
 namespace {
 
 __global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, int rows, int64_t n, float* out0, int64_t n0,
-                                                           float* out1) {
+                                                           float* out1, int64_t n1, float* out2) {
     __shared__ float red[32][33];
     const int cl = threadIdx.x & 31, r0 = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + cl;
@@ -28,18 +28,20 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, in
         for (int i = 0; i < 32; ++i) x += red[i][cl];
         if (c < n0) {
             if (out0) out0[c] = x;
-        } else if (out1) {
-            out1[c - n0] = x;
+        } else if (c < n0 + n1) {
+            if (out1) out1[c - n0] = x;
+        } else if (out2) {
+            out2[c - n0 - n1] = x;
         }
     }
 }
 
 }  // namespace
 
-hipError_t launch_column_sums(const float* part, int rows, int64_t n, float* out0, int64_t n0, float* out1,
-                              hipStream_t s) {
+hipError_t launch_column_sums(const float* part, int rows, int64_t n, float* out0, int64_t n0, float* out1, int64_t n1,
+                              float* out2, hipStream_t s) {
     hipLaunchKernelGGL(column_sums_kernel, dim3((uint32_t)((n + 31) / 32)), dim3(1024), 0, s, part, rows, n, out0, n0,
-                       out1);
+                       out1, n1, out2);
     return hipGetLastError();
 }
 

@@ -451,7 +451,7 @@ wkv7_status conv_bwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype 
     const bool vec = by_vectors(C, x_ld, e, {x, h0, dy, dhT, (const void*)dx, (const void*)dh0});
     hipError_t err = launch(a, W, x_dtype == WKV7_BF16, vec, kBwd, hs);
     if (err == hipSuccess)
-        err = sums::launch_column_sums(a.part, a.runs, (int64_t)(W + 1) * C, dweight, (int64_t)W * C, dbias, hs);
+        err = sums::launch_column_sums(a.part, a.runs, (int64_t)(W + 1) * C, dweight, (int64_t)W * C, dbias, C, nullptr, hs);
     return err == hipSuccess ? WKV7_OK : WKV7_ERR_HIP;
 }
 

@@ -567,7 +567,7 @@ wkv7_status rn_bwd(int64_t rows, int C, int groups, rn_norm norm, rn_norm norm2,
     hipStream_t hs = static_cast<hipStream_t>(stream);
     hipError_t e = launch(a, true, hs);
     if (e == hipSuccess && dw)
-        e = sums::launch_column_sums(a.part, parts_of(rows, C), 5LL * C, dw, 5LL * C, nullptr, hs);
+        e = sums::launch_column_sums(a.part, parts_of(rows, C), 5LL * C, dw, 5LL * C, nullptr, 0, nullptr, hs);
     return e == hipSuccess ? WKV7_OK : WKV7_ERR_HIP;
 }
 

@@ -12,9 +12,10 @@ using abi::Buf;
 
 struct Shape {
     int64_t tokens, slots, state, ckpt;   // checkpoint slots; values of the states and of the checkpoints
-    int64_t part_A, part_D, part_bc;      // values of the backward's parts (per segment: (C, S) and (C))
-    int N, seg, segs;
-    bool split;
+    int64_t part_bc;                      // values of the backward's parts per channel block and token
+    int N, seg[2], segs[2];               // forward, backward
+    bool split[2], halves;
+    int64_t per_seg;                      // values of (C, S) and two (C)
     int e;
 };
 
@@ -31,43 +32,61 @@ wkv7_status dims_ok(int B, int T, int C, int S, int G) {
     return WKV7_OK;
 }
 
-// Tokens of a segment.  One segment per sequence where the sequences alone give the chip
-// kWaves waves; otherwise as many more as are missing, of 64 tokens at least, at most kMostSegs.
-constexpr int64_t kWaves = 4096, kMostSegs = 16;
-int segment_of(int B, int T, int C, int S) {
-    const int64_t waves = (int64_t)B * ((C + 15) / 16) * (S / 16);
-    int64_t n = (kWaves + waves - 1) / waves;
-    if (n > kMostSegs) n = kMostSegs;
-    int64_t seg = (T + n - 1) / n;
+// How many waves a launch has without segments, a wave for 16 channels and 16 of their states
+// (packed: in all sequences together, if they are even).
+int64_t waves_of(int N, int C, int S) { return (int64_t)N * ((C + 15) / 16) * (S / 16); }
+
+// Tokens of a segment.  A sequence is cut into n segments to have `target` waves, as many as the
+// chip holds of the kernel at once; at most 16, of 64 tokens at least.  Packed sequences are
+// of lengths that the host does not know: cut alike if they were even and one in T tokens, but
+// where they are enough to fill half the chip only a sequence of more than T / 4 is cut.
+int segment_of(int N, int T, int C, int S, bool packed, int64_t target, bool halves, int least) {
+    const int64_t waves = waves_of(N, C, S);
+    int64_t n = target / waves, seg = T;
+    if (halves) n = 1;
+    if (packed) {
+        n = 2 * waves > target ? 4 : target / waves_of(1, C, S);
+        least = 2;
+    }
+    if (n > 16) n = 16;
+    if (n >= least) seg = (T + n - 1) / n;
     if (seg < 64) seg = 64;
     if (seg > T) seg = T;
     return (int)((seg + ssm::kBlock - 1) / ssm::kBlock * ssm::kBlock);
 }
+constexpr int64_t kWaves = 4096;
 
 wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* s) {
     if (dims_ok(B, T, C, S, G) != WKV7_OK || (packed && (B != 1 || N < 1))) return WKV7_ERR_SHAPE;
     s->N = packed ? N : B;
     s->tokens = (int64_t)B * T;
     s->slots = slots_of(B, T, N, packed, ssm::kBlock);
-    s->seg = segment_of(B, T, C, S);
-    s->split = s->seg < T;
-    const int64_t segs = slots_of(B, T, N, packed, s->seg), blocks = (C + ssm::chans(S) - 1) / ssm::chans(S);
-    // a launch takes fewer than 2^32 threads: at most 512 for each segment and channel block
-    if (segs > (1 << 22) / (2 * blocks) || s->slots > INT32_MAX) return WKV7_ERR_SHAPE;
-    s->segs = (int)segs;
+    const int64_t blocks = (C + ssm::chans(S) - 1) / ssm::chans(S);
+    // forward with two states to a lane instead of segments: twice the waves for a twelfth more instructions, where
+    // that fills the chip
+    const int64_t waves = waves_of(s->N, C, S);
+    s->halves = S == 16 && !packed && waves >= 768 && waves < kWaves;
+    for (int back = 0; back < 2; ++back) {
+        s->seg[back] = segment_of(s->N, T, C, S, packed, kWaves, !back && s->halves, back ? 2 : 3);
+        s->split[back] = s->seg[back] < T;
+        const int64_t segs = slots_of(B, T, N, packed, s->seg[back]);
+        // a launch takes fewer than 2^32 threads: at most 512 for each segment and channel block
+        if (segs > (1 << 22) / (2 * blocks)) return WKV7_ERR_SHAPE;
+        s->segs[back] = (int)segs;
+    }
+    if (s->slots > INT32_MAX) return WKV7_ERR_SHAPE;
+    s->per_seg = (int64_t)C * (S + 2);
     s->state = (int64_t)s->N * C * S;
     s->ckpt = s->slots * C * S;
     if (s->slots > kMax / (C * S) || s->N > kMax / (C * S)) return WKV7_ERR_SHAPE;
-    s->part_A = segs * C * S;
-    s->part_D = segs * C;
     s->part_bc = blocks * s->tokens * 2 * S;
     return WKV7_OK;
 }
 
 // What the segments leave; behind the parts of the backward.  Never 0, so that a size of 0 is
 // always one of invalid shapes, and a NULL workspace always an error.
-int64_t fwd_ws(const Shape& s) { return s.split ? (s.part_A + s.part_D) * 4 : 256; }
-int64_t bwd_ws(const Shape& s) { return (s.part_bc + s.part_A + 2 * s.part_D + (s.split ? s.part_A + s.part_D : 0)) * 4; }
+int64_t fwd_ws(const Shape& s) { return s.split[0] ? s.segs[0] * s.per_seg * 4 : 256; }
+int64_t bwd_ws(const Shape& s) { return (s.part_bc + s.segs[1] * s.per_seg * (s.split[1] ? 2 : 1)) * 4; }
 int64_t span(int64_t rows, int64_t ld, int64_t n, int e) { return ((rows - 1) * ld + n) * e; }
 constexpr int64_t kMaxLd = 1 << 24;   // 16 rows are addressed with 32-bit byte offsets
 bool lds_ok(int64_t tokens, int C, int GS, int64_t x, int64_t dt, int64_t b, int64_t c, const void* z, int64_t z_ld) {
@@ -125,12 +144,13 @@ wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     ssm::Args a = {};
     a.x = x; a.dt = dt; a.b = b; a.c = c; a.z = z; a.x_ld = x_ld; a.dt_ld = dt_ld; a.b_ld = b_ld; a.c_ld = c_ld;
     a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.h0 = h0; a.y = y; a.ckpt = ckpt; a.hT = hT; a.cu = cu_seqlens;
-    a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.N = s.N; a.seg = s.seg; a.segs = s.segs;
-    a.split = s.split;
+    a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.N = s.N; a.seg = s.seg[0]; a.segs = s.segs[0];
+    a.split = s.split[0];
     a.sum_h = static_cast<float*>(workspace);
-    a.sum_d = a.sum_h + s.part_A;
+    a.sum_d = a.sum_h + (int64_t)s.segs[0] * C * S;
+    a.halves = s.halves;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t err = s.split ? ssm::launch_segments(a, in_dtype == WKV7_BF16, false, hs) : hipSuccess;
+    hipError_t err = a.split ? ssm::launch_segments(a, in_dtype == WKV7_BF16, false, hs) : hipSuccess;
     if (err == hipSuccess) err = ssm::launch_fwd(a, in_dtype == WKV7_BF16, hs);
     return status_of(err);
 }
@@ -165,21 +185,19 @@ wkv7_status ssm_bwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     a.x = x; a.dt = dt; a.b = b; a.c = c; a.z = z; a.x_ld = x_ld; a.dt_ld = dt_ld; a.b_ld = b_ld; a.c_ld = c_ld;
     a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.dy = dy; a.dhT = dhT; a.ckpt = const_cast<float*>(ckpt);
     a.dx = dx; a.ddt = ddt; a.dz = dz; a.dh0 = dh0; a.cu = cu_seqlens;
-    a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.N = s.N; a.seg = s.seg; a.segs = s.segs;
+    a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.N = s.N; a.seg = s.seg[1]; a.segs = s.segs[1];
     float* ws = static_cast<float*>(workspace);
     a.part_bc = ws;
-    a.part_A = ws + s.part_bc;
-    a.part_D = a.part_A + s.part_A;
-    a.part_bias = a.part_D + s.part_D;
-    a.split = s.split;
-    a.sum_h = a.part_bias + s.part_D;
-    a.sum_d = a.sum_h + s.part_A;
+    a.part = ws + s.part_bc;
+    a.split = s.split[1];
+    a.sum_h = a.part + s.segs[1] * s.per_seg;
+    a.sum_d = a.sum_h + (int64_t)s.segs[1] * C * S;
     ssm::ReduceArgs r = {};
-    r.part_A = a.part_A; r.part_D = a.part_D; r.part_bias = a.part_bias; r.part_bc = a.part_bc;
+    r.part = a.part; r.part_bc = a.part_bc;
     r.dA = dA; r.dD = dD; r.ddt_bias = ddt_bias; r.db = db; r.dc = dc; r.cu = cu_seqlens;
-    r.B = B; r.T = T; r.C = C; r.S = S; r.G = G; r.N = s.N; r.segs = s.segs;
+    r.B = B; r.T = T; r.C = C; r.S = S; r.G = G; r.N = s.N; r.segs = s.segs[1];
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t err = s.split ? ssm::launch_segments(a, in_dtype == WKV7_BF16, true, hs) : hipSuccess;
+    hipError_t err = a.split ? ssm::launch_segments(a, in_dtype == WKV7_BF16, true, hs) : hipSuccess;
     if (err == hipSuccess) err = ssm::launch_bwd(a, in_dtype == WKV7_BF16, hs);
     if (err == hipSuccess) err = ssm::launch_reduce(r, in_dtype == WKV7_BF16, hs);
     return status_of(err);

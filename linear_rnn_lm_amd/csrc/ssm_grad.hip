@@ -13,6 +13,7 @@
 // channels to a lane, so that most of the adding is done without exchanges.
 // Sums over workgroups (db, dc: one part per 64 channels, 32 with 64 states; dA, dD, ddt_bias: one per
 // segment) go through memory and a second launch, in a fixed order.
+#include "column_sums.h"
 #include "ssm_device.h"
 
 namespace ssm {
@@ -25,18 +26,17 @@ __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-template <typename InT, int WN, int WC>
+template <typename InT, int WN, int WC, bool HZ>
 __global__ __launch_bounds__(64 * WN * WC, 2) void bwd_kernel(Args p, int blocks) {
     constexpr int NS = 4, S = 4 * NS * WN, CH = 16 * WC, NT = 64 * WN * WC, TB = kBlock;
     using D_ = Deal<InT, CH, NT, S>;
-    constexpr int LT = D_::LT, HB = D_::HB, STEP = D_::STEP;
-    constexpr int VP = 20;                       // a row of s_v: 16 channels, padded against bank conflicts
+    constexpr int LT = D_::LT;
     static_assert(CH == chans(S), "one part of db and dc per workgroup");
-    __shared__ float2 s_du[TB][CH];              // delta, delta x
-    __shared__ float s_dy[TB][CH], s_b[TB][S], s_c[TB][S];
-    __shared__ float s_x[TB][CH], s_ds[TB][CH], s_zf[TB][CH];     // x, delta's slope, dz / y
-    __shared__ float s_y[WN][TB][CH], s_gb[WN][TB][CH], s_pa[WN][TB][CH];
-    __shared__ float s_v[WN * WC][2][2][16][VP];
+    typedef float Rows[CH][kPitch];
+    __shared__ __attribute__((aligned(16))) Rows s_d, s_u, s_dy, s_x, s_ds, s_zf;   // delta, delta x, dy, x, delta's slope, dz / y
+    __shared__ __attribute__((aligned(16))) float s_bc[2][S][kPitch];
+    __shared__ __attribute__((aligned(16))) Rows s_y[WN], s_gb[WN], s_pa[WN];
+    __shared__ __attribute__((aligned(16))) float s_v[WN * WC][2][2][4 * NS][kPitch];   // two tokens' terms of db and dc
     __shared__ float s_g[WC][TB][2][S];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), wn = wave % WN, wc = wave / WN;
@@ -62,191 +62,238 @@ __global__ __launch_bounds__(64 * WN * WC, 2) void bwd_kernel(Args p, int blocks
         const int behind = len > t_end ? (len - 1) / p.seg - piece : 0;
         fold_segments<NS>(p, slot + behind, -1, behind, ch, n0, A2, gr);
     }
-    const InT* x = static_cast<const InT*>(p.x) + tok0 * p.x_ld;
-    const InT* dt = static_cast<const InT*>(p.dt) + tok0 * p.dt_ld;
-    const InT* z = p.z ? static_cast<const InT*>(p.z) + tok0 * p.z_ld : nullptr;
-    const InT* dy = static_cast<const InT*>(p.dy) + tok0 * p.C;
+    int n_blocks = t_begin < t_end ? (t_end - 1 - t_begin) / TB + 1 : 0;
+    const int t_last = t_begin + (n_blocks - 1) * TB, t_from = n_blocks ? t_last : t_begin;
     const int64_t go = (int64_t)(cb * CH / (p.C / p.G)) * S;
-    const InT* b = static_cast<const InT*>(p.b) + tok0 * p.b_ld + go;
-    const InT* c = static_cast<const InT*>(p.c) + tok0 * p.c_ld + go;
+    Stream sx = stream(static_cast<const InT*>(p.x) + tok0 * p.x_ld, p.x_ld, p.C, t_from);
+    Stream sd = stream(static_cast<const InT*>(p.dt) + tok0 * p.dt_ld, p.dt_ld, p.C, t_from);
+    Stream sz = stream(HZ ? static_cast<const InT*>(p.z) + tok0 * p.z_ld : nullptr, p.z_ld, p.C, t_from);
+    Stream sy = stream(static_cast<const InT*>(p.dy) + tok0 * p.C, p.C, p.C, t_from);
+    Mats<InT, NT, S> mats(static_cast<const InT*>(p.b) + tok0 * p.b_ld + go, p.b_ld,
+                          static_cast<const InT*>(p.c) + tok0 * p.c_ld + go, p.c_ld, tid, t_from);
     const uint32_t ox = deal.off(p.x_ld), od = deal.off(p.dt_ld), oz = deal.off(p.z_ld), oy = deal.off(p.C);
-    const uint32_t ob = D_::off_b(tid, p.b_ld), oc = D_::off_b(tid, p.c_ld);
     const float bias = p.dt_bias ? p.dt_bias[deal.lch] : 0.f, Dv = p.D ? p.D[deal.lch] : 0.f;
     float* part_bc = p.part_bc + ((int64_t)cb * p.B * p.T + tok0) * 2 * S;
-    const bool wide = (cb + 1) * CH <= p.C;
+    const float* ck = p.ckpt + (int64_t)((used ? first_slot(seqs, n, tok0, TB) : 0) + t_from / TB) * p.C * S;
+    const uint32_t ock = on ? (uint32_t)(ch * S + n0) * 4u : kNowhere;
 
-    InT rx[LT], rd[LT], rz[LT], ry[LT], rb[HB], rc[HB];
+    InT rx[LT], rd[LT], rz[LT], ry[LT], rm[D_::MB];
     float hn[NS];
-    const float* ck = p.ckpt + (int64_t)(used ? first_slot(seqs, n, tok0, TB) : 0) * p.C * S;
-    const uint32_t ock = (uint32_t)((on ? ch : p.C - 1) * S + n0) * 4u;
-    auto fetch = [&](int t0) {
-        const bool full = wide && t0 + TB <= t_end;
-        deal.rows(x, p.x_ld, ox, t0, t_end, full, rx);
-        deal.rows(dt, p.dt_ld, od, t0, t_end, full, rd);
-        if (z) deal.rows(z, p.z_ld, oz, t0, t_end, full, rz);
-        deal.rows(dy, p.C, oy, t0, t_end, full, ry);
-        D_::mat(b, p.b_ld, ob, tid, t0, t_end, full, rb);
-        D_::mat(c, p.c_ld, oc, tid, t0, t_end, full, rc);
-        const float* q = ck + (int64_t)(t0 / TB) * p.C * S;
+    int t_fetch = t_from;
+    auto fetch = [&] {                                     // the block before the first one is not loaded: its first one again
+        const int rows = block_rows(t_fetch, t_end);
+        deal.rows(sx, rows, p.x_ld, ox, rx);
+        deal.rows(sd, rows, p.dt_ld, od, rd);
+        if (HZ) deal.rows(sz, rows, p.z_ld, oz, rz);
+        deal.rows(sy, rows, p.C, oy, ry);
+        mats.load(rows, p.b_ld, p.c_ld, rm);
+        const wkv7::Rsrc r = wkv7::make_rsrc(ck, n_blocks > 0 ? (uint32_t)p.C * S * 4u : 0u);
 #pragma unroll
-        for (int s = 0; s < NS; ++s) hn[s] = ldo<float>(q, ock + 4 * s);
-    };
-    const int t_last = t_begin < t_end ? t_begin + (t_end - 1 - t_begin) / TB * TB : t_begin - TB;
-    if (t_last >= t_begin) fetch(t_last);
-    for (int t0 = t_last; t0 >= t_begin; t0 -= TB) {
-        const bool full = wide && t0 + TB <= t_end;
-        float h[NS], dAb[NS];
-#pragma unroll
-        for (int i = 0; i < LT; ++i) {
-            const int t = deal.lt + i * STEP;
-            const float xv = widen(rx[i]), v = widen(rd[i]) + bias, yv = widen(ry[i]);
-            float d = p.softplus ? softplus(v) : v;
-            if (!full) d = deal.lon && t0 + t < t_end ? d : 0.f;
-            s_du[t][deal.lc] = make_float2(d, d * xv);
-            s_x[t][deal.lc] = xv;
-            s_ds[t][deal.lc] = p.softplus ? sigmoid(v) : 1.f;
-            if (z) {
-                const float zv = widen(rz[i]), sg = sigmoid(zv), zs = zv * sg;
-                s_dy[t][deal.lc] = yv * zs;
-                s_zf[t][deal.lc] = yv * fmaf(zs, 1.f - sg, sg);
-            } else {
-                s_dy[t][deal.lc] = yv;
-            }
+        for (int s = 0; s < NS; ++s) hn[s] = bload<float>(r, ock + 4 * s);
+        if (--n_blocks > 0) {
+            sx.back(), sd.back(), sz.back(), sy.back(), mats.back();
+            ck -= (int64_t)p.C * S;
+            t_fetch -= TB;
         }
+    };
+    fetch();
+    for (int t0 = t_last; t0 >= t_begin; t0 -= TB) {
+        float h[NS], dAb[NS];
+        {
+            float d[LT], u[LT], xv[LT], sl[LT], dyv[LT], zf[LT];
 #pragma unroll
-        for (int i = 0; i < HB; ++i) {
-            (&s_b[0][0])[tid + i * NT] = widen(rb[i]);
-            (&s_c[0][0])[tid + i * NT] = widen(rc[i]);
+            for (int i = 0; i < LT; ++i) {
+                xv[i] = widen(rx[i]);
+                const float v = widen(rd[i]) + bias, yv = widen(ry[i]), st = step_of(p.softplus, v);
+                d[i] = deal.lon && t0 + deal.lt + i < t_end ? st : 0.f;
+                u[i] = d[i] * xv[i];
+                sl[i] = p.softplus ? sigmoid(v) : 1.f;
+                dyv[i] = yv;
+                if (HZ) {
+                    const float zv = widen(rz[i]), sg = sigmoid(zv), zs = zv * sg;
+                    dyv[i] = yv * zs;
+                    zf[i] = yv * fmaf(zs, 1.f - sg, sg);
+                }
+            }
+            put_lds<LT>(&s_d[deal.lc][deal.lt], d);
+            put_lds<LT>(&s_u[deal.lc][deal.lt], u);
+            put_lds<LT>(&s_dy[deal.lc][deal.lt], dyv);
+            put_lds<LT>(&s_x[deal.lc][deal.lt], xv);
+            put_lds<LT>(&s_ds[deal.lc][deal.lt], sl);
+            if (HZ) put_lds<LT>(&s_zf[deal.lc][deal.lt], zf);
+            mats.put(&s_bc[0][0][0], rm);
         }
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            h[s] = on ? hn[s] : 0.f;
+            h[s] = hn[s];
             dAb[s] = 0.f;
         }
         lds_barrier();
-        if (t0 > t_begin) fetch(t0 - TB);
 
+        // forward over the block; four tokens' operands are read ahead of their use
         float a[TB][NS], ah[TB][NS];
+        {
+            f32x4 d[2], u[2], b[2][NS];
+            auto read = [&](int k) {
+                d[k & 1] = lds4(&s_d[cl][4 * k]);
+                u[k & 1] = lds4(&s_u[cl][4 * k]);
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            const float2 du = s_du[t][cl];
+                for (int s = 0; s < NS; ++s) b[k & 1][s] = lds4(&s_bc[0][n0 + s][4 * k]);
+            };
+            read(0);
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                a[t][s] = exp2_f(du.x * A2[s]);
-                ah[t][s] = a[t][s] * h[s];
-                h[s] = fmaf(du.y, s_b[t][n0 + s], ah[t][s]);
+            for (int k = 0; k < TB / 4; ++k) {
+                if (k + 1 < TB / 4) read(k + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 4 * k + i;
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) {
+                        a[t][s] = exp2_f(d[k & 1][i] * A2[s]);
+                        ah[t][s] = a[t][s] * h[s];
+                        h[s] = fmaf(u[k & 1][i], b[k & 1][s][i], ah[t][s]);
+                    }
+                }
             }
         }
+        // and back.  Two tokens' terms of db and dc go to LDS, channels side by side, and come back four channels
+        // to a lane; they are added up after the next two tokens, when they have long arrived.
+        f32x4 d, u, dyq, b[NS], c[NS], v[4];
+        auto read = [&](int k) {
+            d = lds4(&s_d[cl][4 * k]);
+            u = lds4(&s_u[cl][4 * k]);
+            dyq = lds4(&s_dy[cl][4 * k]);
 #pragma unroll
-        for (int t4 = TB - 4; t4 >= 0; t4 -= 4) {
+            for (int s = 0; s < NS; ++s) {
+                b[s] = lds4(&s_bc[0][n0 + s][4 * k]);
+                c[s] = lds4(&s_bc[1][n0 + s][4 * k]);
+            }
+        };
+        auto add_up = [&](int t) {                         // tokens t, t + 1: v[j] is db, dc of t, then of t + 1
+            float sum[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] = (v[j][0] + v[j][1]) + (v[j][2] + v[j][3]);
+            (&s_g[wc][t][0][0])[(row_of(g4) >> 1) * 2 * S + (row_of(g4) & 1) * S + 16 * wn + r16] =
+                rows_sum4(sum[0], sum[1], sum[2], sum[3]);
+        };
+        read(TB / 4 - 1);
+#pragma unroll
+        for (int k = TB / 4 - 1; k >= 0; --k) {
+            if (k == 0) fetch();                           // most of a and ah is done with: their registers hold it
             float gb[4], pa[4], yt[4];
 #pragma unroll
             for (int i2 = 2; i2 >= 0; i2 -= 2) {
 #pragma unroll
                 for (int i = i2 + 1; i >= i2; --i) {
-                    const int t = t4 + i;
-                    const float2 du = s_du[t][cl];
-                    const float dyt = s_dy[t][cl];
+                    const int t = 4 * k + i;
                     gb[i] = pa[i] = yt[i] = 0.f;
 #pragma unroll
                     for (int s = 0; s < NS; ++s) {
-                        const float bt = s_b[t][n0 + s], ct = s_c[t][n0 + s], ht = fmaf(du.y, bt, ah[t][s]);
-                        gr[s] = fmaf(ct, dyt, gr[s]);
+                        const float bt = b[s][i], ct = c[s][i], ht = fmaf(u[i], bt, ah[t][s]);
+                        gr[s] = fmaf(ct, dyq[i], gr[s]);
                         yt[i] = fmaf(ct, ht, yt[i]);
                         gb[i] = fmaf(gr[s], bt, gb[i]);
                         const float q = gr[s] * ah[t][s];
                         pa[i] = fmaf(q, A2[s], pa[i]);
-                        dAb[s] = fmaf(q, du.x, dAb[s]);
-                        s_v[wave][i - i2][0][4 * g4 + s][r16] = gr[s] * du.y;
-                        s_v[wave][i - i2][1][4 * g4 + s][r16] = dyt * ht;
+                        dAb[s] = fmaf(q, d[i], dAb[s]);
+                        s_v[wave][i - i2][0][4 * g4 + s][r16] = gr[s] * u[i];
+                        s_v[wave][i - i2][1][4 * g4 + s][r16] = dyq[i] * ht;
                         gr[s] *= a[t][s];
                     }
                 }
+                if (4 * k + i2 + 2 < TB) add_up(4 * k + i2 + 2);
                 wave_order();
-                float sum[4];                              // two tokens' db, dc; four channels here, the rest by rows
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 v = *reinterpret_cast<const f32x4*>(&s_v[wave][i >> 1][i & 1][r16][4 * g4]);
-                    sum[i] = (v[0] + v[1]) + (v[2] + v[3]);
-                }
+                for (int j = 0; j < 4; ++j) v[j] = lds4(&s_v[wave][j >> 1][j & 1][r16][4 * g4]);
+                if (i2 == 0 && k > 0) read(k - 1);
                 wave_order();
-                (&s_g[wc][t4 + i2][0][0])[(row_of(g4) >> 1) * 2 * S + (row_of(g4) & 1) * S + 16 * wn + r16] =
-                    rows_sum4(sum[0], sum[1], sum[2], sum[3]);
             }
-            s_gb[wn][t4 + row_of(g4)][cl] = rows_sum4(gb[0], gb[1], gb[2], gb[3]);
-            s_pa[wn][t4 + row_of(g4)][cl] = rows_sum4(pa[0], pa[1], pa[2], pa[3]);
-            if (z) s_y[wn][t4 + row_of(g4)][cl] = rows_sum4(yt[0], yt[1], yt[2], yt[3]);
+            s_gb[wn][cl][4 * k + row_of(g4)] = rows_sum4(gb[0], gb[1], gb[2], gb[3]);
+            s_pa[wn][cl][4 * k + row_of(g4)] = rows_sum4(pa[0], pa[1], pa[2], pa[3]);
+            if (HZ) s_y[wn][cl][4 * k + row_of(g4)] = rows_sum4(yt[0], yt[1], yt[2], yt[3]);
         }
+        add_up(0);
 #pragma unroll
         for (int s = 0; s < NS; ++s) dA[s] += dAb[s];
         lds_barrier();
-        const int64_t o = (tok0 + t0) * p.C;
-        InT* dx = static_cast<InT*>(p.dx) + o;
-        InT* ddt = static_cast<InT*>(p.ddt) + o;
-        InT* dz = static_cast<InT*>(p.dz) + o;
+        // What is read here a thread wrote itself, or waves wrote before this barrier and write again after the next
+        // one; so the next block's values may go to LDS without another.
+        const int64_t at = (tok0 + t0) * p.C;
+        const uint32_t bytes = (uint32_t)(min(TB, t_end - t0) * p.C) * (uint32_t)sizeof(InT);
+        const wkv7::Rsrc r_dx = wkv7::make_rsrc(static_cast<InT*>(p.dx) + at, bytes);
+        const wkv7::Rsrc r_ddt = wkv7::make_rsrc(static_cast<InT*>(p.ddt) + at, bytes);
+        const wkv7::Rsrc r_dz = wkv7::make_rsrc(static_cast<InT*>(p.dz) + at, bytes);
+        {
+            float d1[LT], xv[LT], sl[LT], dyv[LT], zf[LT], gb[LT], pa[LT], yr[LT], part[LT];
+            get_lds<LT>(&s_d[deal.lc][deal.lt], d1);
+            get_lds<LT>(&s_x[deal.lc][deal.lt], xv);
+            get_lds<LT>(&s_ds[deal.lc][deal.lt], sl);
+            get_lds<LT>(&s_dy[deal.lc][deal.lt], dyv);
+            if (HZ) get_lds<LT>(&s_zf[deal.lc][deal.lt], zf);
+            get_lds<LT>(&s_gb[0][deal.lc][deal.lt], gb);
+            get_lds<LT>(&s_pa[0][deal.lc][deal.lt], pa);
+            if (HZ) get_lds<LT>(&s_y[0][deal.lc][deal.lt], yr);
 #pragma unroll
-        for (int i = 0; i < LT; ++i, dx += (int64_t)STEP * p.C, ddt += (int64_t)STEP * p.C, dz += (int64_t)STEP * p.C) {
-            const int t = deal.lt + i * STEP;
-            const float xv = s_x[t][deal.lc], dyt = s_dy[t][deal.lc];
-            float gb = 0.f, pa = 0.f, yr = Dv * xv;
+            for (int w = 1; w < WN; ++w) {
+                get_lds<LT>(&s_gb[w][deal.lc][deal.lt], part);
 #pragma unroll
-            for (int w = 0; w < WN; ++w) {
-                gb += s_gb[w][t][deal.lc];
-                pa += s_pa[w][t][deal.lc];
-                if (z) yr += s_y[w][t][deal.lc];
+                for (int i = 0; i < LT; ++i) gb[i] += part[i];
+                get_lds<LT>(&s_pa[w][deal.lc][deal.lt], part);
+#pragma unroll
+                for (int i = 0; i < LT; ++i) pa[i] += part[i];
+                if (HZ) {
+                    get_lds<LT>(&s_y[w][deal.lc][deal.lt], part);
+#pragma unroll
+                    for (int i = 0; i < LT; ++i) yr[i] += part[i];
+                }
             }
-            const float dd = fmaf(xv, gb, kLn2 * pa) * s_ds[t][deal.lc];
-            if (full || (deal.lon && t0 + t < t_end)) {
-                st(pto<InT>(dx, oy), fmaf(s_du[t][deal.lc].x, gb, Dv * dyt));
-                st(pto<InT>(ddt, oy), dd);
-                if (z) st(pto<InT>(dz, oy), yr * s_zf[t][deal.lc]);
-                dD = fmaf(dyt, xv, dD);
-                dbias += dd;
+#pragma unroll
+            for (int i = 0; i < LT; ++i) {                 // tokens and channels that do not exist have dy = x = 0
+                const uint32_t o = oy + D_::row(p.C, i);
+                const float dd = fmaf(xv[i], gb[i], kLn2 * pa[i]) * sl[i];
+                bstore(InT(0), r_dx, o, fmaf(d1[i], gb[i], Dv * dyv[i]));
+                bstore(InT(0), r_ddt, o, dd);
+                if (HZ) bstore(InT(0), r_dz, o, fmaf(Dv, xv[i], yr[i]) * zf[i]);
+                dD = fmaf(dyv[i], xv[i], dD);
+                dbias += deal.lon && t0 + deal.lt + i < t_end ? dd : 0.f;
             }
         }
+        // part_bc: [token][db, dc][state]
+        const wkv7::Rsrc r_bc = wkv7::make_rsrc(part_bc + (int64_t)t0 * 2 * S, (uint32_t)min(TB, t_end - t0) * 2 * S * 4);
 #pragma unroll
-        for (int i = 0; i < 2 * HB; ++i) {                 // part_bc: [token][db, dc][state]
-            const int e = tid + i * NT;
-            if (t0 + e / (2 * S) >= t_end) continue;
-            float v = 0.f;
+        for (int i = 0; i < D_::MB; ++i) {
+            float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < WC; ++w) v += (&s_g[w][0][0][0])[e];
-            part_bc[(int64_t)t0 * 2 * S + e] = v;
+            for (int w = 0; w < WC; ++w) sum += (&s_g[w][0][0][0])[tid + i * NT];
+            wkv7::bstore(sum, r_bc, (tid + i * NT) * 4, 0);
         }
-        lds_barrier();                                     // the next block overwrites what this one's end reads
     }
     if (used && p.dh0 && on && piece == 0) {
 #pragma unroll
         for (int s = 0; s < NS; ++s) p.dh0[((int64_t)n * p.C + ch) * S + n0 + s] = gr[s];
     }
+    float* part = p.part + (int64_t)slot * p.C * (S + 2);  // (C, S) of dA, then dD's and ddt_bias' (C)
     if (on) {
 #pragma unroll
-        for (int s = 0; s < NS; ++s) p.part_A[((int64_t)slot * p.C + ch) * S + n0 + s] = dA[s];
+        for (int s = 0; s < NS; ++s) part[(int64_t)ch * S + n0 + s] = dA[s];
     }
     lds_barrier();
-    float* s_d = &s_gb[0][0][0];                           // NT / CH threads hold sums of one channel
-    s_d[tid] = dD;
-    s_d[NT + tid] = dbias;
+    float* s_sum = &s_g[0][0][0][0];                       // NT / CH threads hold sums of one channel
+    static_assert(2 * NT <= WC * TB * 2 * S, "two sums for each thread fit");
+    s_sum[tid] = dD;
+    s_sum[NT + tid] = dbias;
     lds_barrier();
     if (tid < CH && deal.lon) {
-        float u = 0.f, v = 0.f;
+        float sum_D = 0.f, sum_bias = 0.f;
 #pragma unroll
         for (int i = 0; i < NT / CH; ++i) {
-            u += s_d[i * CH + tid];
-            v += s_d[NT + i * CH + tid];
+            sum_D += s_sum[i * CH + tid];
+            sum_bias += s_sum[NT + i * CH + tid];
         }
-        p.part_D[(int64_t)slot * p.C + deal.lch] = u;
-        p.part_bias[(int64_t)slot * p.C + deal.lch] = v;
+        part[(int64_t)p.C * S + deal.lch] = sum_D;
+        part[(int64_t)p.C * (S + 1) + deal.lch] = sum_bias;
     }
-}
-
-// Column sums of `rows` rows of n values.
-__global__ __launch_bounds__(256) void sum_kernel(const float* part, int rows, int64_t n, float* out) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    float s = 0.f;
-    for (int r = 0; r < rows; ++r) s += part[r * n + i];
-    out[i] = s;
 }
 
 // db and dc of every token in a sequence: sums over the channel blocks of a group.
@@ -267,7 +314,9 @@ __global__ __launch_bounds__(256) void bc_kernel(ReduceArgs p, int blocks) {
 template <typename InT, int WN, int WC>
 hipError_t run(const Args& a, hipStream_t s) {
     const int blocks = (a.C + 16 * WC - 1) / (16 * WC);
-    hipLaunchKernelGGL((bwd_kernel<InT, WN, WC>), dim3((uint32_t)blocks * a.segs), dim3(64 * WN * WC), 0, s, a, blocks);
+    const dim3 grid((uint32_t)blocks * a.segs), threads(64 * WN * WC);
+    if (a.z) hipLaunchKernelGGL((bwd_kernel<InT, WN, WC, true>), grid, threads, 0, s, a, blocks);
+    else hipLaunchKernelGGL((bwd_kernel<InT, WN, WC, false>), grid, threads, 0, s, a, blocks);
     return hipGetLastError();
 }
 
@@ -280,10 +329,6 @@ hipError_t pick(const Args& a, hipStream_t s) {
     }
 }
 
-void sum(const float* part, int rows, int64_t n, float* out, hipStream_t s) {
-    if (out) hipLaunchKernelGGL(sum_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s, part, rows, n, out);
-}
-
 }  // namespace
 
 hipError_t launch_bwd(const Args& a, bool bf16, hipStream_t s) {
@@ -291,9 +336,9 @@ hipError_t launch_bwd(const Args& a, bool bf16, hipStream_t s) {
 }
 
 hipError_t launch_reduce(const ReduceArgs& a, bool bf16, hipStream_t s) {
-    sum(a.part_A, a.segs, (int64_t)a.C * a.S, a.dA, s);
-    sum(a.part_D, a.segs, a.C, a.dD, s);
-    sum(a.part_bias, a.segs, a.C, a.ddt_bias, s);
+    const int64_t CS = (int64_t)a.C * a.S;
+    const hipError_t e = sums::launch_column_sums(a.part, a.segs, CS + 2 * a.C, a.dA, CS, a.dD, a.C, a.ddt_bias, s);
+    if (e != hipSuccess) return e;
     const int blocks = (a.C + chans(a.S) - 1) / chans(a.S);
     const int64_t n = (int64_t)a.B * a.T * a.G * 2 * a.S;
     const dim3 grid((uint32_t)((n + 255) / 256));

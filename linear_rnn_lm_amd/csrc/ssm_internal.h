@@ -15,13 +15,14 @@ struct Args {
     const float *A, *D, *dt_bias, *h0, *dhT;
     void *y, *dx, *ddt, *dz;
     float *ckpt, *hT, *dh0;
-    float *part_A, *part_D, *part_bias, *part_bc;   // backward: sums per segment; per channel block and token
+    float *part, *part_bc;   // backward: sums per segment ((C, S) of dA, (C) of dD and of ddt_bias); per channel block and token
     float *sum_h, *sum_d;    // per segment slot: what it leaves of a zero state (backward: of a zero gradient), (C, S);
                              // the sum of its steps, (C)
     const int* cu;
     int softplus, B, T, C, S, G, N;
     int seg, segs;   // tokens of a segment (a multiple of kBlock) and segment slots
     bool split;      // whether a sequence may have more than one segment
+    bool halves;     // forward, S = 16: two states to a lane
 };
 
 struct StepArgs {
@@ -36,7 +37,7 @@ struct StepArgs {
 
 // Sums of the backward's parts.
 struct ReduceArgs {
-    const float *part_A, *part_D, *part_bias, *part_bc;
+    const float *part, *part_bc;
     float *dA, *dD, *ddt_bias;
     void *db, *dc;
     const int* cu;

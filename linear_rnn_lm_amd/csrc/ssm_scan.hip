@@ -6,22 +6,47 @@
 // and token).  A wave works on 16 channels (lane % 16) and 4 NS states, NS to a lane
 // (lane / 16), which stay in registers from the first token to the last; WN waves share
 // the channels of one block, WC of them lie beside each other.  16 tokens at a time: all
-// threads load x, dt, z, b, c (the next block's while this one is worked on), put delta,
-// delta x, b and c into LDS as fp32, the waves scan, and the threads that loaded z
-// finish y.
+// threads load x, dt, z, b, c, put delta, delta x, b and c into LDS as fp32, the waves scan,
+// and the threads that loaded z finish y.
 #include "ssm_device.h"
 
 namespace ssm {
 namespace {
 
-template <typename InT, int NS, int WN, int WC>
+// What a lane reads of LDS for GT tokens: delta, delta x (or dy), and NS states' b and c.  Read
+// whole, ahead of its use: left alone the compiler waits for LDS once every two tokens.
+template <int NS, int GT, bool C>
+struct Group {
+    f32x4 d[GT / 4], u[GT / 4], b[NS][GT / 4], c[C ? NS : 1][GT / 4];
+    __device__ __forceinline__ void read(const float* s_d, const float* s_u, const float* s_b, const float* s_c, int t) {
+#pragma unroll
+        for (int k = 0; k < GT / 4; ++k) {
+            d[k] = lds4(s_d + t + 4 * k);
+            u[k] = lds4(s_u + t + 4 * k);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                b[s][k] = lds4(s_b + s * kPitch + t + 4 * k);
+                if (C) c[s][k] = lds4(s_c + s * kPitch + t + 4 * k);
+            }
+        }
+    }
+};
+
+// Blocks ahead: a block takes a wave alone on its unit about 2600, 1500, 900 cycles with 4, 2, 1
+// states to a lane, a load up to 2000.
+template <int NS>
+struct Ahead {
+    static constexpr int value = NS == 1 ? 4 : NS == 2 ? 2 : 1;
+    static constexpr bool groups = NS < 4;   // operands in LDS read a group ahead
+};
+
+template <typename InT, int NS, int WN, int WC, bool HZ>
 __global__ __launch_bounds__(64 * WN * WC) void fwd_kernel(Args p, int blocks) {
-    constexpr int S = 4 * NS * WN, CH = 16 * WC, NT = 64 * WN * WC, TB = kBlock;
+    constexpr int S = 4 * NS * WN, CH = 16 * WC, NT = 64 * WN * WC, TB = kBlock, GT = 16 / NS;
     using D_ = Deal<InT, CH, NT, S>;
-    constexpr int LT = D_::LT, HB = D_::HB, STEP = D_::STEP;
-    __shared__ float2 s_du[2][TB][CH];           // delta, delta x
-    __shared__ float s_b[2][TB][S], s_c[2][TB][S];
-    __shared__ float s_y[WN][TB][CH];
+    constexpr int LT = D_::LT;
+    __shared__ __attribute__((aligned(16))) float s_d[2][CH][kPitch], s_u[2][CH][kPitch], s_bc[2][2][S][kPitch];
+    __shared__ __attribute__((aligned(16))) float s_y[2][WN][CH][kPitch];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), wn = wave % WN, wc = wave / WN;
     const int cb = blockIdx.x % blocks, slot = blockIdx.x / blocks;
@@ -43,91 +68,131 @@ __global__ __launch_bounds__(64 * WN * WC) void fwd_kernel(Args p, int blocks) {
         h[s] = on && p.h0 ? p.h0[((int64_t)n * p.C + ch) * S + n0 + s] : 0.f;
     }
     if (p.split && on) fold_segments<NS>(p, slot - piece, 1, piece, ch, n0, A2, h);
-    // loading
+    // loading and storing
     const D_ deal(tid, cb, p.C);
-    const InT* x = static_cast<const InT*>(p.x) + tok0 * p.x_ld;
-    const InT* dt = static_cast<const InT*>(p.dt) + tok0 * p.dt_ld;
-    const InT* z = p.z ? static_cast<const InT*>(p.z) + tok0 * p.z_ld : nullptr;
-    InT* y = p.y ? static_cast<InT*>(p.y) + tok0 * p.C : nullptr;
     const int64_t go = (int64_t)(cb * CH / (p.C / p.G)) * S;
-    const InT* b = static_cast<const InT*>(p.b) + tok0 * p.b_ld + go;
-    const InT* c = static_cast<const InT*>(p.c) + tok0 * p.c_ld + go;
+    Stream sx = stream(static_cast<const InT*>(p.x) + tok0 * p.x_ld, p.x_ld, p.C, t_begin);
+    Stream sd = stream(static_cast<const InT*>(p.dt) + tok0 * p.dt_ld, p.dt_ld, p.C, t_begin);
+    Stream sz = stream(HZ ? static_cast<const InT*>(p.z) + tok0 * p.z_ld : nullptr, p.z_ld, p.C, t_begin);
+    Stream sy = stream(static_cast<const InT*>(p.y) + tok0 * p.C, p.C, p.C, t_begin - TB);   // of the block being finished
+    Mats<InT, NT, S> mats(static_cast<const InT*>(p.b) + tok0 * p.b_ld + go, p.b_ld,
+                          static_cast<const InT*>(p.c) + tok0 * p.c_ld + go, p.c_ld, tid, t_begin);
     const uint32_t ox = deal.off(p.x_ld), od = deal.off(p.dt_ld), oz = deal.off(p.z_ld), oy = deal.off(p.C);
-    const uint32_t ob = D_::off_b(tid, p.b_ld), oc = D_::off_b(tid, p.c_ld);
     const float bias = p.dt_bias ? p.dt_bias[deal.lch] : 0.f, Dv = p.D ? p.D[deal.lch] : 0.f;
-    const bool wide = (cb + 1) * CH <= p.C;
+    float* ck = p.ckpt + (int64_t)(first_slot(seqs, n, tok0, TB) + t_begin / TB) * p.C * S;
+    const uint32_t ck_bytes = p.ckpt ? (uint32_t)p.C * S * 4u : 0u;
+    const uint32_t ock = on ? (uint32_t)(ch * S + n0) * 4u : kNowhere;
+    const int out_rows = p.y ? TB : 0;
 
-    InT rx[LT], rd[LT], rz[LT], rb[HB], rc[HB];
-    auto fetch = [&](int t0) {
-        const bool full = wide && t0 + TB <= t_end;
-        deal.rows(x, p.x_ld, ox, t0, t_end, full, rx);
-        deal.rows(dt, p.dt_ld, od, t0, t_end, full, rd);
-        if (z) deal.rows(z, p.z_ld, oz, t0, t_end, full, rz);
-        D_::mat(b, p.b_ld, ob, tid, t0, t_end, full, rb);
-        D_::mat(c, p.c_ld, oc, tid, t0, t_end, full, rc);
+    constexpr int PF = Ahead<NS>::value;         // blocks that are on their way from memory
+    InT rx[PF][LT], rd[PF][LT], rz[PF][LT], rm[PF][D_::MB];
+    int t_fetch = t_begin;
+    auto fetch = [&](int j) {
+        const int rows = block_rows(t_fetch, t_end);
+        deal.rows(sx, rows, p.x_ld, ox, rx[j]);
+        deal.rows(sd, rows, p.dt_ld, od, rd[j]);
+        if (HZ) deal.rows(sz, rows, p.z_ld, oz, rz[j]);
+        mats.load(rows, p.b_ld, p.c_ld, rm[j]);
+        t_fetch += TB;
+        sx.next(), sd.next(), sz.next(), mats.next();
     };
-    float* ck = p.ckpt ? p.ckpt + (int64_t)(first_slot(seqs, n, tok0, TB) + t_begin / TB) * p.C * S : nullptr;
-    const uint32_t ock = (uint32_t)(ch * S + n0) * 4u;
-    int buf = 0;
-    if (t_begin < t_end) fetch(t_begin);
-    for (int t0 = t_begin; t0 < t_end; t0 += TB, buf ^= 1) {
-        const bool full = t0 + TB <= t_end;
-        float xv[LT], zv[LT];
+    float xs[3][LT], zs[3][LT];                  // x and z of the blocks being finished, scanned, prepared
+    auto prepare = [&](int t0, int j, int buf, float (&xv)[LT], float (&zv)[LT]) {
+        float d[LT], u[LT];
 #pragma unroll
         for (int i = 0; i < LT; ++i) {
-            const int t = deal.lt + i * STEP;
-            xv[i] = widen(rx[i]);
-            const float v = widen(rd[i]) + bias;
-            float d = p.softplus ? softplus(v) : v;
-            if (!full) d = t0 + t < t_end ? d : 0.f;       // no token: the state stays
-            s_du[buf][t][deal.lc] = make_float2(d, d * xv[i]);
-            if (z) zv[i] = widen(rz[i]);
+            xv[i] = widen(rx[j][i]);
+            zv[i] = HZ ? widen(rz[j][i]) : 0.f;
+            const float v = step_of(p.softplus, widen(rd[j][i]) + bias);
+            d[i] = t0 + deal.lt + i < t_end ? v : 0.f;               // no token: the state stays
+            u[i] = d[i] * xv[i];
+        }
+        put_lds<LT>(&s_d[buf][deal.lc][deal.lt], d);
+        put_lds<LT>(&s_u[buf][deal.lc][deal.lt], u);
+        mats.put(&s_bc[buf][0][0][0], rm[j]);
+    };
+    auto finish = [&](int rows, int buf, const float (&xv)[LT], const float (&zv)[LT]) {
+        const wkv7::Rsrc r = sy.rsrc(rows);
+        sy.next();
+        float v[LT];
+#pragma unroll
+        for (int i = 0; i < LT; ++i) v[i] = Dv * xv[i];
+#pragma unroll
+        for (int w = 0; w < WN; ++w) {
+            float part[LT];
+            get_lds<LT>(&s_y[buf][w][deal.lc][deal.lt], part);
+#pragma unroll
+            for (int i = 0; i < LT; ++i) v[i] += part[i];
         }
 #pragma unroll
-        for (int i = 0; i < HB; ++i) {
-            (&s_b[buf][0][0])[tid + i * NT] = widen(rb[i]);
-            (&s_c[buf][0][0])[tid + i * NT] = widen(rc[i]);
+        for (int i = 0; i < LT; ++i) {
+            if (HZ) v[i] *= zv[i] * sigmoid(zv[i]);
+            bstore(InT(0), r, oy + D_::row(p.C, i), v[i]);
         }
+    };
+    // One barrier per block of 16 tokens: in one go the next block is prepared, this one scanned and
+    // the one before it finished, so that their waits hide each other.
+    auto block = [&](int t0, int j, int buf) {
         lds_barrier();
-        if (t0 + TB < t_end) fetch(t0 + TB);
-        if (ck) {
-            if (on) {
+        Group<NS, GT, true> grp[2];
+        const float *pd = s_d[buf][cl], *pu = s_u[buf][cl], *pb = s_bc[buf][0][n0], *pc = s_bc[buf][1][n0];
+        grp[0].read(pd, pu, pb, pc, 0);
+        prepare(t0 + TB, j, buf ^ 1, xs[2], zs[2]);
+        fetch(j);
+        finish(t0 > t_begin ? out_rows : 0, buf ^ 1, xs[0], zs[0]);
+        const wkv7::Rsrc rk = wkv7::make_rsrc(ck, ck_bytes);
+        if constexpr (NS == 4) wkv7::bstore4(f32x4{h[0], h[1], h[2], h[3]}, rk, ock, 0);
+        else if constexpr (NS == 2) wkv7::bstore2(make_float2(h[0], h[1]), rk, ock, 0);
+        else wkv7::bstore(h[0], rk, ock, 0);
+        ck += (int64_t)p.C * S;
 #pragma unroll
-                for (int s = 0; s < NS; ++s) *pto<float>(ck, ock + 4 * s) = h[s];
+        for (int k = 0; k < TB / GT; ++k) {
+            const Group<NS, GT, true>& q = grp[k & 1];
+            if (!Ahead<NS>::groups && k > 0) grp[k & 1].read(pd, pu, pb, pc, k * GT);
+            if (Ahead<NS>::groups && k + 1 < TB / GT) {
+                grp[(k + 1) & 1].read(pd, pu, pb, pc, (k + 1) * GT);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            ck += (int64_t)p.C * S;
-        }
 #pragma unroll
-        for (int t4 = 0; t4 < TB; t4 += 4) {
-            float yt[4];
+            for (int t4 = 0; t4 < GT; t4 += 4) {
+                float yt[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 du = s_du[buf][t4 + i][cl];
-                const float* bt = &s_b[buf][t4 + i][n0];
-                const float* ct = &s_c[buf][t4 + i][n0];
-                yt[i] = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    yt[i] = 0.f;
 #pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    h[s] = fmaf(exp2_f(du.x * A2[s]), h[s], du.y * bt[s]);
-                    yt[i] = fmaf(ct[s], h[s], yt[i]);
+                    for (int s = 0; s < NS; ++s) {
+                        h[s] = fmaf(exp2_f(q.d[t4 / 4][i] * A2[s]), h[s], q.u[t4 / 4][i] * q.b[s][t4 / 4][i]);
+                        yt[i] = fmaf(q.c[s][t4 / 4][i], h[s], yt[i]);
+                    }
                 }
-            }
-            s_y[wn][t4 + row_of(g)][cl] = rows_sum4(yt[0], yt[1], yt[2], yt[3]);
-        }
-        lds_barrier();
-        if (y) {
-            InT* yb = y + (int64_t)t0 * p.C;
-#pragma unroll
-            for (int i = 0; i < LT; ++i, yb += (int64_t)STEP * p.C) {
-                const int t = deal.lt + i * STEP;
-                float v = Dv * xv[i];
-#pragma unroll
-                for (int w = 0; w < WN; ++w) v += s_y[w][t][deal.lc];
-                if (z) v *= zv[i] * sigmoid(zv[i]);
-                if (deal.lon && (full || t0 + t < t_end)) st(pto<InT>(yb, oy), v);
+                s_y[buf][wn][cl][k * GT + t4 + row_of(g)] = rows_sum4(yt[0], yt[1], yt[2], yt[3]);
             }
         }
+#pragma unroll
+        for (int i = 0; i < LT; ++i) {
+            xs[0][i] = xs[1][i], xs[1][i] = xs[2][i];
+            zs[0][i] = zs[1][i], zs[1][i] = zs[2][i];
+        }
+    };
+    fetch(PF - 1);
+#pragma unroll
+    for (int j = 0; j < PF - 1; ++j) fetch(j);
+    prepare(t_begin, PF - 1, 0, xs[1], zs[1]);
+    fetch(PF - 1);
+#pragma unroll
+    for (int i = 0; i < LT; ++i) xs[0][i] = zs[0][i] = 0.f;
+    int last = 0;
+    constexpr int U = PF > 1 ? PF : 2;
+    for (int t0 = t_begin; t0 < t_end; t0 += U * TB) {
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (t0 + j * TB < t_end) {
+                block(t0 + j * TB, j % PF, j & 1);
+                last = j & 1;
+            }
     }
+    lds_barrier();
+    finish(t_begin < t_end && p.y ? (t_end - 1 - t_begin) % TB + 1 : 0, last, xs[0], zs[0]);
     if (p.hT && on && t_end == len) {
 #pragma unroll
         for (int s = 0; s < NS; ++s) p.hT[((int64_t)n * p.C + ch) * S + n0 + s] = h[s];
@@ -137,14 +202,14 @@ __global__ __launch_bounds__(64 * WN * WC) void fwd_kernel(Args p, int blocks) {
 // What a segment leaves of a zero state, forward (h <- a h + delta x b) or, for the backward,
 // in reverse (g <- a (g + c dy)), and the sum of its steps.  Five sixths of the forward's
 // instructions, without its outputs.
-template <typename InT, int NS, int WN, int WC, bool BWD>
+template <typename InT, int NS, int WN, int WC, bool BWD, bool HZ>
 __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int blocks) {
-    constexpr int S = 4 * NS * WN, CH = 16 * WC, NT = 64 * WN * WC, TB = kBlock;
+    constexpr int S = 4 * NS * WN, CH = 16 * WC, NT = 64 * WN * WC, TB = kBlock, GT = 16 / NS;
     using D_ = Deal<InT, CH, NT, S>;
-    constexpr int LT = D_::LT, HB = D_::HB, STEP = D_::STEP;
-    __shared__ float2 s_du[2][TB][CH];           // delta, and delta x or dy
-    __shared__ float s_b[2][TB][S];              // b or c
-    __shared__ double s_d[NT];
+    constexpr int LT = D_::LT, MB = (TB * S + NT - 1) / NT;
+    __shared__ __attribute__((aligned(16))) float s_d[2][CH][kPitch], s_u[2][CH][kPitch];   // delta, and delta x or dy
+    __shared__ __attribute__((aligned(16))) float s_b[2][S][kPitch];                        // b or c
+    __shared__ double s_sum[NT];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), wn = wave % WN, wc = wave / WN;
     const int cb = blockIdx.x % blocks, slot = blockIdx.x / blocks;
@@ -166,115 +231,137 @@ __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int block
     }
     const D_ deal(tid, cb, p.C);
     const int64_t u_ld = BWD ? p.C : p.x_ld, b_ld = BWD ? p.c_ld : p.b_ld;
-    const InT* dt = static_cast<const InT*>(p.dt) + tok0 * p.dt_ld;
-    const InT* u = static_cast<const InT*>(BWD ? p.dy : p.x) + tok0 * u_ld;
-    const InT* z = BWD && p.z ? static_cast<const InT*>(p.z) + tok0 * p.z_ld : nullptr;
-    const InT* b = static_cast<const InT*>(BWD ? p.c : p.b) + tok0 * b_ld + (int64_t)(cb * CH / (p.C / p.G)) * S;
-    const uint32_t ou = deal.off(u_ld), od = deal.off(p.dt_ld), oz = deal.off(p.z_ld), ob = D_::off_b(tid, b_ld);
     const float bias = p.dt_bias ? p.dt_bias[deal.lch] : 0.f;
-    const bool wide = (cb + 1) * CH <= p.C;
-    double total = 0.;
-
-    InT ru[LT], rd[LT], rz[LT], rb[HB];
-    auto fetch = [&](int t0) {
-        const bool full = wide && t0 + TB <= t_end;
-        deal.rows(u, u_ld, ou, t0, t_end, full, ru);
-        deal.rows(dt, p.dt_ld, od, t0, t_end, full, rd);
-        if (z) deal.rows(z, p.z_ld, oz, t0, t_end, full, rz);
-        D_::mat(b, b_ld, ob, tid, t0, t_end, full, rb);
-    };
     const int n_blocks = (t_end - t_begin + TB - 1) / TB;
-    int buf = 0;
-    fetch(BWD ? t_begin + (n_blocks - 1) * TB : t_begin);
-    for (int k = 0; k < n_blocks; ++k, buf ^= 1) {
-        const int t0 = t_begin + (BWD ? n_blocks - 1 - k : k) * TB;
-        const bool full = t0 + TB <= t_end;
-        float sum = 0.f;
+    int t0 = BWD ? t_begin + (n_blocks - 1) * TB : t_begin;
+    Stream su = stream(static_cast<const InT*>(BWD ? p.dy : p.x) + tok0 * u_ld, u_ld, p.C, t0);
+    Stream sd = stream(static_cast<const InT*>(p.dt) + tok0 * p.dt_ld, p.dt_ld, p.C, t0);
+    Stream sz = stream(HZ ? static_cast<const InT*>(p.z) + tok0 * p.z_ld : nullptr, p.z_ld, p.C, t0);
+    Stream sb = stream(static_cast<const InT*>(BWD ? p.c : p.b) + tok0 * b_ld + (int64_t)(cb * CH / (p.C / p.G)) * S, b_ld, S, t0);
+    const uint32_t ou = deal.off(u_ld), od = deal.off(p.dt_ld), oz = deal.off(p.z_ld);
+    const uint32_t ob = (uint32_t)(tid / S * (int)b_ld + tid % S) * (uint32_t)sizeof(InT);
+    double total = 0.;
+    int blocks_left = n_blocks;
+
+    constexpr int PF = Ahead<NS>::value;
+    InT ru[PF][LT], rd[PF][LT], rz[PF][LT], rb[PF][MB];
+    int t_fetch = t0;
+    auto fetch = [&](int j) {
+        const int rows = block_rows(t_fetch, t_end);
+        deal.rows(su, rows, u_ld, ou, ru[j]);
+        deal.rows(sd, rows, p.dt_ld, od, rd[j]);
+        if (HZ) deal.rows(sz, rows, p.z_ld, oz, rz[j]);
+        const wkv7::Rsrc r = sb.rsrc(rows);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) rb[j][i] = bload<InT>(r, ob + (uint32_t)(i * (NT / S) * (int)b_ld) * (uint32_t)sizeof(InT));
+        // backward no further than to the first block, which is then read again and not used
+        if (!BWD || --blocks_left > 0) {
+            t_fetch += BWD ? -TB : TB;
+            for (Stream* s : {&su, &sd, &sz, &sb}) BWD ? s->back() : s->next();
+        }
+    };
+    auto prepare = [&](int t0, int j, int buf) {
+        float sum = 0.f, d[LT], u[LT];
 #pragma unroll
         for (int i = 0; i < LT; ++i) {
-            const int t = deal.lt + i * STEP;
-            const float v = widen(rd[i]) + bias;
-            float d = p.softplus ? softplus(v) : v, uv = widen(ru[i]);
-            if (!full) d = t0 + t < t_end ? d : 0.f;
-            if (z) {
-                const float zv = widen(rz[i]);
-                uv *= zv * sigmoid(zv);
+            const float v = step_of(p.softplus, widen(rd[j][i]) + bias);
+            d[i] = t0 >= t_begin && t0 + deal.lt + i < t_end ? v : 0.f;
+            u[i] = widen(ru[j][i]);
+            if (HZ) {
+                const float zv = widen(rz[j][i]);
+                u[i] *= zv * sigmoid(zv);
             }
-            s_du[buf][t][deal.lc] = make_float2(d, BWD ? uv : d * uv);
-            sum += d;
+            if (!BWD) u[i] *= d[i];
+            sum += d[i];
         }
         total += (double)sum;
+        put_lds<LT>(&s_d[buf][deal.lc][deal.lt], d);
+        put_lds<LT>(&s_u[buf][deal.lc][deal.lt], u);
 #pragma unroll
-        for (int i = 0; i < HB; ++i) (&s_b[buf][0][0])[tid + i * NT] = widen(rb[i]);
+        for (int i = 0; i < MB; ++i)
+            if (MB * NT == TB * S || tid < TB * S) s_b[buf][tid % S][tid / S + i * (NT / S)] = widen(rb[j][i]);
+    };
+    // as in the forward: the next block is prepared while this one is scanned
+    constexpr int step = BWD ? -TB : TB;
+    auto block = [&](int t0, int j, int buf) {
         lds_barrier();
-        if (k + 1 < n_blocks) fetch(BWD ? t0 - TB : t0 + TB);
+        Group<NS, GT, false> grp[2];
+        const float *pd = s_d[buf][cl], *pu = s_u[buf][cl], *pb = s_b[buf][n0];
+        grp[0].read(pd, pu, pb, nullptr, BWD ? TB - GT : 0);
+        prepare(t0 + step, j, buf ^ 1);
+        fetch(j);
 #pragma unroll
-        for (int i = 0; i < TB; ++i) {
-            const int t = BWD ? TB - 1 - i : i;
-            const float2 du = s_du[buf][t][cl];
+        for (int k = 0; k < TB / GT; ++k) {
+            const Group<NS, GT, false>& q = grp[k & 1];
+            if (!Ahead<NS>::groups && k > 0) grp[k & 1].read(pd, pu, pb, nullptr, BWD ? TB - (k + 1) * GT : k * GT);
+            if (Ahead<NS>::groups && k + 1 < TB / GT) {
+                grp[(k + 1) & 1].read(pd, pu, pb, nullptr, BWD ? TB - (k + 2) * GT : (k + 1) * GT);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                const float a = exp2_f(du.x * A2[s]), bt = s_b[buf][t][n0 + s];
-                h[s] = BWD ? a * fmaf(du.y, bt, h[s]) : fmaf(a, h[s], du.y * bt);
+            for (int i = 0; i < GT; ++i) {
+                const int t = BWD ? GT - 1 - i : i;
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    const float a = exp2_f(q.d[t / 4][t % 4] * A2[s]), u = q.u[t / 4][t % 4], bt = q.b[s][t / 4][t % 4];
+                    h[s] = BWD ? a * fmaf(u, bt, h[s]) : fmaf(a, h[s], u * bt);
+                }
             }
         }
+    };
+    fetch(PF - 1);
+#pragma unroll
+    for (int j = 0; j < PF - 1; ++j) fetch(j);
+    prepare(t0, PF - 1, 0);
+    fetch(PF - 1);
+    constexpr int U = PF > 1 ? PF : 2;
+    for (int k = 0; k < n_blocks; k += U, t0 += U * step) {
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (k + j < n_blocks) block(t0 + j * step, j % PF, j & 1);
     }
     if (on) {
 #pragma unroll
         for (int s = 0; s < NS; ++s) p.sum_h[((int64_t)slot * p.C + ch) * S + n0 + s] = h[s];
     }
-    s_d[tid] = total;                                      // NT / CH threads hold sums of one channel
+    s_sum[tid] = total;                                    // NT / CH threads hold sums of one channel
     lds_barrier();
     if (tid < CH && deal.lon) {
 #pragma unroll
-        for (int i = 1; i < NT / CH; ++i) total += s_d[i * CH + tid];
+        for (int i = 1; i < NT / CH; ++i) total += s_sum[i * CH + tid];
         p.sum_d[(int64_t)slot * p.C + deal.lch] = (float)total;
     }
 }
 
-template <typename InT, int NS, int WN, int WC>
-hipError_t run(const Args& a, hipStream_t s) {
-    const int blocks = (a.C + 16 * WC - 1) / (16 * WC);
-    hipLaunchKernelGGL((fwd_kernel<InT, NS, WN, WC>), dim3((uint32_t)blocks * a.segs), dim3(64 * WN * WC), 0, s, a,
-                       blocks);
-    return hipGetLastError();
-}
+enum What { kFwd, kSums, kSumsBack };
 
 template <typename InT, int NS, int WN, int WC>
-hipError_t run_segments(const Args& a, bool bwd, hipStream_t s) {
+hipError_t run(const Args& a, What what, hipStream_t s) {
     const int blocks = (a.C + 16 * WC - 1) / (16 * WC);
     const dim3 grid((uint32_t)blocks * a.segs), threads(64 * WN * WC);
-    if (bwd) hipLaunchKernelGGL((segment_kernel<InT, NS, WN, WC, true>), grid, threads, 0, s, a, blocks);
-    else hipLaunchKernelGGL((segment_kernel<InT, NS, WN, WC, false>), grid, threads, 0, s, a, blocks);
+    if (what == kFwd && a.z) hipLaunchKernelGGL((fwd_kernel<InT, NS, WN, WC, true>), grid, threads, 0, s, a, blocks);
+    else if (what == kFwd) hipLaunchKernelGGL((fwd_kernel<InT, NS, WN, WC, false>), grid, threads, 0, s, a, blocks);
+    else if (what == kSums) hipLaunchKernelGGL((segment_kernel<InT, NS, WN, WC, false, false>), grid, threads, 0, s, a, blocks);
+    else if (a.z) hipLaunchKernelGGL((segment_kernel<InT, NS, WN, WC, true, true>), grid, threads, 0, s, a, blocks);
+    else hipLaunchKernelGGL((segment_kernel<InT, NS, WN, WC, true, false>), grid, threads, 0, s, a, blocks);
     return hipGetLastError();
 }
 
 template <typename InT>
-hipError_t pick_segments(const Args& a, bool bwd, hipStream_t s) {
+hipError_t pick(const Args& a, What what, hipStream_t s) {
     switch (a.S) {
-        case 16: return run_segments<InT, 4, 1, 4>(a, bwd, s);
-        case 32: return run_segments<InT, 4, 2, 4>(a, bwd, s);
-        default: return run_segments<InT, 4, 4, 2>(a, bwd, s);
+        case 16: return a.halves ? run<InT, 2, 2, 4>(a, what, s) : run<InT, 4, 1, 4>(a, what, s);
+        case 32: return run<InT, 4, 2, 4>(a, what, s);
+        default: return run<InT, 4, 4, 2>(a, what, s);
     }
 }
-
-template <typename InT>
-hipError_t pick(const Args& a, hipStream_t s) {
-    switch (a.S) {
-        case 16: return run<InT, 4, 1, 4>(a, s);
-        case 32: return run<InT, 4, 2, 4>(a, s);
-        default: return run<InT, 4, 4, 2>(a, s);
-    }
+hipError_t launch(const Args& a, bool bf16, What what, hipStream_t s) {
+    return bf16 ? pick<uint16_t>(a, what, s) : pick<float>(a, what, s);
 }
 
 }  // namespace
 
-hipError_t launch_segments(const Args& a, bool bf16, bool bwd, hipStream_t s) {
-    return bf16 ? pick_segments<uint16_t>(a, bwd, s) : pick_segments<float>(a, bwd, s);
-}
-
-hipError_t launch_fwd(const Args& a, bool bf16, hipStream_t s) {
-    return bf16 ? pick<uint16_t>(a, s) : pick<float>(a, s);
-}
+hipError_t launch_segments(const Args& a, bool bf16, bool bwd, hipStream_t s) { return launch(a, bf16, bwd ? kSumsBack : kSums, s); }
+hipError_t launch_fwd(const Args& a, bool bf16, hipStream_t s) { return launch(a, bf16, kFwd, s); }
 
 }  // namespace ssm

@@ -339,7 +339,8 @@ def test_autograd_op():
 
 
 def test_offsets_past_31_bits():
-    """The last rows of an x of more than 2^31 values, against the same rows alone."""
+    """The last rows of an x of more than 2^31 values, against the same rows alone: another batch may deal the
+    states to other lanes and sum y in another order, so each is within its tolerance of the same value."""
     note("ssm, long offsets")
     B, T, C, S, n = 70, 8192, 4096, 16, 40
     assert B * T * C > 2 ** 31
@@ -350,4 +351,4 @@ def test_offsets_past_31_bits():
     y, _, hT = L.ssm_fwd(big["x"], big["dt"], p["A"], big["b"], big["c"], p["D"], dt_bias=p["dt_bias"], want_ckpt=False)
     ys, _, _ = L.ssm_fwd(p["x"], p["dt"], p["A"], p["b"], p["c"], p["D"], dt_bias=p["dt_bias"], want_ckpt=False)
     torch.cuda.synchronize()
-    assert torch.equal(y[-1, :n], ys[0]) and (y[0] == 0).all()
+    assert rel(y[-1, :n], ys[0]) <= 2 * scan_tol(n, S, BF) and (y[0] == 0).all()
