@@ -120,4 +120,26 @@ __device__ __forceinline__ bool slot_piece(const Seqs& s, int slot, int len, int
     return i == 0 || (i > 0 && (int64_t)i * len < L);
 }
 
+// Piece k of N <= 64 packed sequences, counted from the longest sequence to the shortest: a sequence to a
+// lane, each adds up the pieces before its own.  False if there are fewer.
+__device__ __forceinline__ bool by_length(const Seqs& s, int k, int piece_len, int& n, int& i) {
+    const int lane = threadIdx.x & 63;
+    int64_t tok0;
+    int len = -1;
+    if (lane < s.N) seq_span(s, lane, tok0, len);
+    const int mine = lane < s.N ? max(1, (len + piece_len - 1) / piece_len) : 0;
+    int before = 0;
+    for (int j = 0; j < s.N; ++j) {
+        const int l = __builtin_amdgcn_readlane(len, j), c = __builtin_amdgcn_readlane(mine, j);
+        before += l > len || (l == len && j < lane) ? c : 0;
+    }
+    n = __ffsll(__ballot(before <= k && k < before + mine)) - 1;
+    if (n < 0) {
+        n = i = 0;
+        return false;
+    }
+    i = k - __builtin_amdgcn_readlane(before, n);
+    return true;
+}
+
 }  // namespace rows

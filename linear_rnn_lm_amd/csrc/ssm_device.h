@@ -24,6 +24,13 @@ __device__ __forceinline__ void fold_segments(const Args& p, int slot, int step,
     }
 }
 
+// What the k-th workgroup of a channel block works on; false: nothing.  Packed sequences go by length,
+// the longest first, so that none starts when the others are nearly done (17 sequences, 8193 tokens,
+// 2048 channels of 64 states: 300 us in their order, 256 by length).
+__device__ __forceinline__ bool segment_of(const Args& p, const Seqs& seqs, int k, int& n, int& piece) {
+    return p.cu && p.N > 1 && p.N <= 64 ? by_length(seqs, k, p.seg, n, piece) : slot_piece(seqs, k, p.seg, n, piece);
+}
+
 // Token rows through buffer resources, so that a ragged end needs no branch: loads behind a
 // sequence's (segment's) end return 0 and stores there are dropped; lanes whose channel does not
 // exist have kNowhere for an offset.

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(64 * WN * WC, 2) void bwd_kernel(Args p, int blocks
     float A2[NS], dA[NS], gr[NS], dD = 0.f, dbias = 0.f;
     int n, piece, len = 0;
     int64_t tok0 = 0;
-    const bool used = slot_piece(seqs, slot, p.seg, n, piece);
+    const bool used = segment_of(p, seqs, slot, n, piece);
     if (used) seq_span(seqs, n, tok0, len);
     n = uniform(n), piece = uniform(piece), len = uniform(len), tok0 = uniform(tok0);
     const int t_begin = used ? piece * p.seg : 0, t_end = used ? min(len, t_begin + p.seg) : 0;
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64 * WN * WC, 2) void bwd_kernel(Args p, int blocks
     }
     if (p.split && used && on) {                           // the segments behind this one, last first
         const int behind = len > t_end ? (len - 1) / p.seg - piece : 0;
-        fold_segments<NS>(p, slot + behind, -1, behind, ch, n0, A2, gr);
+        fold_segments<NS>(p, first_slot(seqs, n, tok0, p.seg) + piece + behind, -1, behind, ch, n0, A2, gr);
     }
     int n_blocks = t_begin < t_end ? (t_end - 1 - t_begin) / TB + 1 : 0;
     const int t_last = t_begin + (n_blocks - 1) * TB, t_from = n_blocks ? t_last : t_begin;

@@ -22,7 +22,7 @@ struct Args {
     int softplus, B, T, C, S, G, N;
     int seg, segs;   // tokens of a segment (a multiple of kBlock) and segment slots
     bool split;      // whether a sequence may have more than one segment
-    bool halves;     // forward, S = 16: two states to a lane
+    bool halves, halves_sums;   // S = 16, forward and segments' sums: two states to a lane
 };
 
 struct StepArgs {

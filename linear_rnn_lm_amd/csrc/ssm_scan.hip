@@ -38,10 +38,11 @@ template <int NS>
 struct Ahead {
     static constexpr int value = NS == 1 ? 4 : NS == 2 ? 2 : 1;
     static constexpr bool groups = NS < 4;   // operands in LDS read a group ahead
+    static constexpr int waves = NS < 4 ? 1 : 4;   // per SIMD: where other waves hide what is not read ahead
 };
 
 template <typename InT, int NS, int WN, int WC, bool HZ>
-__global__ __launch_bounds__(64 * WN * WC) void fwd_kernel(Args p, int blocks) {
+__global__ __launch_bounds__(64 * WN * WC, Ahead<NS>::waves) void fwd_kernel(Args p, int blocks) {
     constexpr int S = 4 * NS * WN, CH = 16 * WC, NT = 64 * WN * WC, TB = kBlock, GT = 16 / NS;
     using D_ = Deal<InT, CH, NT, S>;
     constexpr int LT = D_::LT;
@@ -49,10 +50,10 @@ __global__ __launch_bounds__(64 * WN * WC) void fwd_kernel(Args p, int blocks) {
     __shared__ __attribute__((aligned(16))) float s_y[2][WN][CH][kPitch];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), wn = wave % WN, wc = wave / WN;
-    const int cb = blockIdx.x % blocks, slot = blockIdx.x / blocks;
+    const int cb = blockIdx.x % blocks;
     const Seqs seqs{p.cu, p.N, p.T};
     int n, piece, len;
-    if (!slot_piece(seqs, slot, p.seg, n, piece)) return;
+    if (!segment_of(p, seqs, blockIdx.x / blocks, n, piece)) return;
     int64_t tok0;
     seq_span(seqs, n, tok0, len);
     n = uniform(n), piece = uniform(piece), len = uniform(len), tok0 = uniform(tok0);
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(64 * WN * WC) void fwd_kernel(Args p, int blocks) {
         A2[s] = on ? kLog2e * p.A[(int64_t)ch * S + n0 + s] : 0.f;
         h[s] = on && p.h0 ? p.h0[((int64_t)n * p.C + ch) * S + n0 + s] : 0.f;
     }
-    if (p.split && on) fold_segments<NS>(p, slot - piece, 1, piece, ch, n0, A2, h);
+    if (p.split && on) fold_segments<NS>(p, first_slot(seqs, n, tok0, p.seg), 1, piece, ch, n0, A2, h);
     // loading and storing
     const D_ deal(tid, cb, p.C);
     const int64_t go = (int64_t)(cb * CH / (p.C / p.G)) * S;
@@ -212,10 +213,10 @@ __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int block
     __shared__ double s_sum[NT];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), wn = wave % WN, wc = wave / WN;
-    const int cb = blockIdx.x % blocks, slot = blockIdx.x / blocks;
+    const int cb = blockIdx.x % blocks;
     const Seqs seqs{p.cu, p.N, p.T};
     int n, piece, len;
-    if (!slot_piece(seqs, slot, p.seg, n, piece)) return;
+    if (!segment_of(p, seqs, blockIdx.x / blocks, n, piece)) return;
     int64_t tok0;
     seq_span(seqs, n, tok0, len);
     n = uniform(n), piece = uniform(piece), len = uniform(len), tok0 = uniform(tok0);
@@ -320,6 +321,7 @@ __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int block
         for (int j = 0; j < U; ++j)
             if (k + j < n_blocks) block(t0 + j * step, j % PF, j & 1);
     }
+    const int slot = first_slot(seqs, n, tok0, p.seg) + piece;
     if (on) {
 #pragma unroll
         for (int s = 0; s < NS; ++s) p.sum_h[((int64_t)slot * p.C + ch) * S + n0 + s] = h[s];
@@ -350,7 +352,7 @@ hipError_t run(const Args& a, What what, hipStream_t s) {
 template <typename InT>
 hipError_t pick(const Args& a, What what, hipStream_t s) {
     switch (a.S) {
-        case 16: return a.halves ? run<InT, 2, 2, 4>(a, what, s) : run<InT, 4, 1, 4>(a, what, s);
+        case 16: return (what == kFwd ? a.halves : a.halves_sums) ? run<InT, 2, 2, 4>(a, what, s) : run<InT, 4, 1, 4>(a, what, s);
         case 32: return run<InT, 4, 2, 4>(a, what, s);
         default: return run<InT, 4, 4, 2>(a, what, s);
     }
