@@ -20,7 +20,8 @@ namespace {
 using namespace rows;
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kAhead = 8;   // tokens loaded at once; runs are multiples of it
+constexpr int kAhead = 8;       // tokens loaded at once; runs are multiples of it
+constexpr int kAheadFwd = 4;    // (B8 T4096 C4096: 97 us, with 8 104)
 constexpr int NT = 256;
 
 struct Args {
@@ -30,7 +31,7 @@ struct Args {
     int64_t x_ld;
     const int* cu;
     int silu, B, T, C, N, run, runs;   // tokens of a run, run slots
-    bool wbf16;
+    bool wbf16, wfour;   // filters in bf16; at a multiple of four values
 };
 
 struct StepArgs {
@@ -39,19 +40,21 @@ struct StepArgs {
     int64_t x_ld;
     const int* slots;
     int silu, B, T, C, P;
-    bool wbf16;
+    bool wbf16, wfour;   // filters in bf16; at a multiple of four values
 };
 
 // VEC values as stored.
 template <typename T, int VEC>
-struct Raw {
+struct __attribute__((aligned(sizeof(T) * VEC))) Raw {
     T v[VEC];
     __device__ __forceinline__ void load(const T* p) {
         if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<u32x4*>(v) = *reinterpret_cast<const u32x4*>(p);
+        else if constexpr (VEC * sizeof(T) == 8) *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
         else v[0] = *p;
     }
     __device__ __forceinline__ void store(T* p) const {
         if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<u32x4*>(p) = *reinterpret_cast<const u32x4*>(v);
+        else if constexpr (VEC * sizeof(T) == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
         else *p = v[0];
     }
     __device__ __forceinline__ void clear() {
@@ -67,17 +70,39 @@ __device__ __forceinline__ void store_as(T* p, const float (&f)[VEC]) {
     r.store(p);
 }
 
+// The filters (C, W) and biases of channels c .. c + VEC - 1; `four`: in pieces of four values.
 template <int W, int VEC>
-__device__ __forceinline__ void load_filters(const void* w, const void* bias, bool bf16, int c, float (&f)[W][VEC],
+__device__ __forceinline__ void load_filters(const void* w, const void* bias, bool bf16, bool four, int c, float (&f)[W][VEC],
                                              float (&b)[VEC]) {
+    const int64_t at = (int64_t)c * W;
+    if (VEC % 4 == 0 && four) {
+        float all[VEC * W];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        const int64_t at = (int64_t)(c + e) * W;
+        for (int i = 0; i < VEC * W; i += 4) {
+            if (bf16) {
+                const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at + i);
+                all[i] = __uint_as_float(u.x << 16), all[i + 1] = __uint_as_float(u.x & 0xffff0000u);
+                all[i + 2] = __uint_as_float(u.y << 16), all[i + 3] = __uint_as_float(u.y & 0xffff0000u);
+            } else {
+                const f32x4 u = *reinterpret_cast<const f32x4*>(static_cast<const float*>(w) + at + i);
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            f[j][e] = bf16 ? widen(static_cast<const uint16_t*>(w)[at + j]) : static_cast<const float*>(w)[at + j];
-        b[e] = !bias ? 0.f : bf16 ? widen(static_cast<const uint16_t*>(bias)[c + e]) : static_cast<const float*>(bias)[c + e];
+                for (int k = 0; k < 4; ++k) all[i + k] = u[k];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+#pragma unroll
+            for (int j = 0; j < W; ++j) f[j][e] = all[e * W + j];
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                f[j][e] = bf16 ? widen(static_cast<const uint16_t*>(w)[at + e * W + j]) : static_cast<const float*>(w)[at + e * W + j];
     }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+        b[e] = !bias ? 0.f : bf16 ? widen(static_cast<const uint16_t*>(bias)[c + e]) : static_cast<const float*>(bias)[c + e];
 }
 
 // The W - 1 inputs before token t of a sequence (its state before its first token).
@@ -107,22 +132,22 @@ __global__ __launch_bounds__(NT) void fwd_kernel(Args p) {
     const T* h0 = p.h0 ? static_cast<const T*>(p.h0) + (int64_t)n * (W - 1) * p.C + c : nullptr;
     T* y = static_cast<T*>(p.y) + tok0 * p.C + c;
     float f[W][VEC], b[VEC];
-    load_filters<W, VEC>(p.w, p.bias, p.wbf16, c, f, b);
-    Raw<T, VEC> win[W - 1], next[kAhead];
+    load_filters<W, VEC>(p.w, p.bias, p.wbf16, p.wfour, c, f, b);
+    Raw<T, VEC> win[W - 1], next[kAheadFwd];
     load_window<T, W, VEC>(x, p.x_ld, h0, p.C, t_begin, win);
     auto fetch = [&](int t0) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
+        for (int i = 0; i < kAheadFwd; ++i)
             if (t0 + i < t_end) next[i].load(x + (t0 + i) * p.x_ld);
     };
     fetch(t_begin);
-    for (int t0 = t_begin; t0 < t_end; t0 += kAhead) {
-        Raw<T, VEC> cur[kAhead];
+    for (int t0 = t_begin; t0 < t_end; t0 += kAheadFwd) {
+        Raw<T, VEC> cur[kAheadFwd];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) cur[i] = next[i];
-        fetch(t0 + kAhead);
+        for (int i = 0; i < kAheadFwd; ++i) cur[i] = next[i];
+        fetch(t0 + kAheadFwd);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < kAheadFwd; ++i) {
             if (t0 + i >= t_end) break;
             float s[VEC];
 #pragma unroll
@@ -174,22 +199,59 @@ __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
         const T* h0 = p.h0 ? static_cast<const T*>(p.h0) + state : nullptr;
         const T* dhT = p.dhT ? static_cast<const T*>(p.dhT) + state : nullptr;
         T* dh0 = p.dh0 ? static_cast<T*>(p.dh0) + state : nullptr;
-        float f[W][VEC], b[VEC], ds[W][VEC];     // ds[j]: of token t - j
-        load_filters<W, VEC>(p.w, p.bias, p.wbf16, c, f, b);
+        float f[W][VEC], b[VEC], win[W - 1][VEC], ds[W - 1][VEC];     // x of the W - 1 tokens before, ds[j] of token t - 1 - j
+        load_filters<W, VEC>(p.w, p.bias, p.wbf16, p.wfour, c, f, b);
+        {
+            Raw<T, VEC> raw[W - 1];
+            load_window<T, W, VEC>(x, p.x_ld, h0, p.C, t_begin, raw);
 #pragma unroll
-        for (int j = 0; j < W; ++j)
+            for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) ds[j][e] = 0.f;
-        Raw<T, VEC> win[W - 1], nx[kAhead], ny[kAhead];
-        load_window<T, W, VEC>(x, p.x_ld, h0, p.C, t_begin, win);
-        const int t_stop = t_end + W - 1;
+                for (int e = 0; e < VEC; ++e) {
+                    win[j][e] = widen(raw[j].v[e]);
+                    ds[j][e] = 0.f;
+                }
+        }
+        Raw<T, VEC> nx[kAhead], ny[kAhead];
+        const int t_stop = t_end + W - 1;                  // the last tokens' dx need what lies behind
         auto fetch = [&](int t0) {
+            const int end = min(t_stop, len);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                if (t0 + i < t_stop && t0 + i < len) {
+                if (t0 + i < end) {
                     nx[i].load(x + (t0 + i) * p.x_ld);
                     ny[i].load(dy + (int64_t)(t0 + i) * p.C);
                 }
+        };
+        // One token of x and dy; its sums count if it lies in this run.
+        auto token = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& ry, bool mine, float (&g)[VEC]) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float xe = widen(rx.v[e]);
+                float s = b[e], d = widen(ry.v[e]);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) s = fmaf(f[j][e], win[j][e], s);
+                s = fmaf(f[W - 1][e], xe, s);
+                if (p.silu) {
+                    const float sg = sigmoid(s);
+                    d *= fmaf(s * sg, 1.f - sg, sg);
+                }
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(d, win[j][e], dw[j][e]);
+                    dw[W - 1][e] = fmaf(d, xe, dw[W - 1][e]);
+                    db[e] += d;
+                }
+                g[e] = f[0][e] * d;
+#pragma unroll
+                for (int j = 1; j < W; ++j) g[e] = fmaf(f[j][e], ds[j - 1][e], g[e]);
+#pragma unroll
+                for (int j = W - 2; j > 0; --j) ds[j][e] = ds[j - 1][e];
+                ds[0][e] = d;
+#pragma unroll
+                for (int j = 0; j < W - 2; ++j) win[j][e] = win[j + 1][e];
+                win[W - 2][e] = xe;
+            }
         };
         fetch(t_begin);
         for (int t0 = t_begin; t0 < t_stop; t0 += kAhead) {
@@ -200,53 +262,30 @@ __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
                 cy[i] = ny[i];
             }
             fetch(t0 + kAhead);
+            float g[VEC];
+            if (t0 > t_begin && t0 + kAhead <= t_end) {    // whole blocks, all but the first
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    token(cx[i], cy[i], true, g);
+                    store_as(dx + (int64_t)(t0 + i - (W - 1)) * p.C, g);
+                }
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int t = t0 + i, q = t - (W - 1);
                 if (t >= t_stop) break;
-#pragma unroll
-                for (int j = W - 1; j > 0; --j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) ds[j][e] = ds[j - 1][e];
-                if (t < len) {
-                    const bool mine = t < t_end;
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        float s = b[e];
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) s = fmaf(f[j][e], widen(win[j].v[e]), s);
-                        const float xe = widen(cx[i].v[e]);
-                        s = fmaf(f[W - 1][e], xe, s);
-                        float d = widen(cy[i].v[e]);
-                        if (p.silu) {
-                            const float sg = sigmoid(s);
-                            d *= sg * fmaf(s, 1.f - sg, 1.f);
-                        }
-                        ds[0][e] = d;
-                        if (mine) {
-#pragma unroll
-                            for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(d, widen(win[j].v[e]), dw[j][e]);
-                            dw[W - 1][e] = fmaf(d, xe, dw[W - 1][e]);
-                            db[e] += d;
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < W - 2; ++j) win[j] = win[j + 1];
-                    win[W - 2] = cx[i];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) ds[0][e] = 0.f;
+                if (t >= len) {                            // behind the sequence: its ds is 0
+                    cx[i].clear();
+                    cy[i].clear();
                 }
+                token(cx[i], cy[i], t < t_end, g);
                 if (q < t_begin && !(piece == 0 && dh0)) continue;
-                float g[VEC];
-                Raw<T, VEC> last;
-                const bool tail = dhT && q >= len - (W - 1);
-                if (tail) last.load(dhT + (int64_t)(q - len + W - 1) * p.C);
+                if (dhT && q >= len - (W - 1)) {
+                    Raw<T, VEC> last;
+                    last.load(dhT + (int64_t)(q - len + W - 1) * p.C);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    g[e] = tail ? widen(last.v[e]) : 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) g[e] = fmaf(f[j][e], ds[j][e], g[e]);
+                    for (int e = 0; e < VEC; ++e) g[e] += widen(last.v[e]);
                 }
                 if (q >= 0) store_as(dx + (int64_t)q * p.C, g);
                 else store_as(dh0 + (int64_t)(q + W - 1) * p.C, g);
@@ -294,7 +333,7 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) win[j].load(static_cast<const T*>(p.state) + at + (int64_t)j * p.C);
     float f[W][VEC], b[VEC];
-    load_filters<W, VEC>(p.w, p.bias, p.wbf16, c, f, b);
+    load_filters<W, VEC>(p.w, p.bias, p.wbf16, p.wfour, c, f, b);
     for (int row = r; row < end; ++row) {
         if (row != r && p.slots[row] != slot) continue;
         for (int t = 0; t < p.T; ++t) {
@@ -324,10 +363,11 @@ enum { kFwd, kBwd };
 
 template <typename T, int W, int VEC>
 hipError_t run(const Args& a, int what, hipStream_t s) {
-    const int64_t threads = (int64_t)a.runs * (a.C / VEC);
+    constexpr int BV = VEC > 4 ? 4 : VEC;      // the backward by four channels: its sums and windows are many registers
+    const int64_t threads = (int64_t)a.runs * (a.C / (what == kFwd ? VEC : BV));
     const dim3 grid((uint32_t)((threads + NT - 1) / NT));
     if (what == kFwd) hipLaunchKernelGGL((fwd_kernel<T, W, VEC>), grid, dim3(NT), 0, s, a);
-    else hipLaunchKernelGGL((bwd_kernel<T, W, VEC>), grid, dim3(NT), 0, s, a);
+    else hipLaunchKernelGGL((bwd_kernel<T, W, BV>), grid, dim3(NT), 0, s, a);
     return hipGetLastError();
 }
 template <typename T, int W, int VEC>
@@ -350,11 +390,12 @@ hipError_t launch(const A& a, int W, bool bf16, bool vec, int what, hipStream_t 
     return vec ? pick_w<float, 4>(a, W, what, s) : pick_w<float, 1>(a, W, what, s);
 }
 
-// Tokens of a run: as many as still leave 2^17 threads of 16 bytes each, 16 to 128.
+// Tokens of a run: as many as still leave 2^16 threads of 16 bytes each, 16 to 128 (12289 tokens of 2048
+// channels, packed: runs of 32 28 us, of 16 31).
 int run_of(int64_t tokens, int C) {
     const int64_t threads = tokens * ((C + 7) / 8);
     int run = 16;
-    while (run < 128 && threads / (2 * run) >= 131072) run *= 2;
+    while (run < 128 && threads / (2 * run) >= 65536) run *= 2;
     return run;
 }
 int64_t runs_of(int B, int T, int N, bool packed, int run) {
@@ -406,7 +447,7 @@ wkv7_status conv_fwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype 
     if (st != WKV7_OK) return st;
     Args a = {};
     a.x = x; a.w = weight; a.bias = bias; a.h0 = h0; a.y = y; a.hT = hT; a.x_ld = x_ld; a.cu = cu_seqlens;
-    a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16;
+    a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16; a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
     a.run = run_of(tokens, C);
     a.runs = (int)runs_of(B, T, N, packed, a.run);
     const bool vec = by_vectors(C, x_ld, e, {x, h0, (const void*)y, (const void*)hT});
@@ -443,7 +484,7 @@ wkv7_status conv_bwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype 
     if (!workspace || workspace_bytes < (size_t)need) return WKV7_ERR_WORKSPACE;
     Args a = {};
     a.x = x; a.w = weight; a.bias = bias; a.h0 = h0; a.dy = dy; a.dhT = dhT; a.dx = dx; a.dh0 = dh0; a.x_ld = x_ld;
-    a.cu = cu_seqlens; a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16;
+    a.cu = cu_seqlens; a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16; a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
     a.run = run_of(tokens, C);
     a.runs = (int)runs_of(B, T, N, packed, a.run);
     a.part = static_cast<float*>(workspace);
@@ -474,7 +515,7 @@ wkv7_status conv_step(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype
     if (st != WKV7_OK) return st;
     StepArgs a = {};
     a.x = x; a.w = weight; a.bias = bias; a.state = state; a.state_out = state_out; a.y = y; a.x_ld = x_ld;
-    a.slots = slots; a.silu = silu; a.B = B; a.T = T; a.C = C; a.P = P; a.wbf16 = w_dtype == WKV7_BF16;
+    a.slots = slots; a.silu = silu; a.B = B; a.T = T; a.C = C; a.P = P; a.wbf16 = w_dtype == WKV7_BF16; a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
     const bool vec = by_vectors(C, x_ld, e, {x, state, (const void*)state_out, (const void*)y});
     return launch(a, W, x_dtype == WKV7_BF16, vec, 0, static_cast<hipStream_t>(stream)) == hipSuccess ? WKV7_OK
                                                                                                       : WKV7_ERR_HIP;
