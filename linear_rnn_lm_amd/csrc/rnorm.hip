@@ -272,69 +272,134 @@ __global__ __launch_bounds__(threads<L>()) void fwd_kernel(Args p, int64_t step)
 //     do = rstd1 (e1 - mean(e1) - oh mean(e1 oh))                              (means over a part)
 // and over the rows dweight = sum du oh, dbias = sum du, dscale = sum dr' a u, dweight2 = sum dh
 // rh, dbias2 = sum dh; a root-mean-square norm has no mean(e).
+// VEC values as stored, of either type, widened at their use, so that the next row's loads do not
+// wait where they are issued.
+template <int VEC>
+struct Raw {
+    u32x4 v[VEC == 8 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* base, int64_t at, bool bf) {
+        if constexpr (VEC == 8) {
+            const char* p = static_cast<const char*>(base) + at * (bf ? 2 : 4);
+            v[0] = reinterpret_cast<const u32x4*>(p)[0];
+            if (!bf) v[1] = reinterpret_cast<const u32x4*>(p)[1];
+        } else {
+            v[0][0] = bf ? (uint32_t)static_cast<const uint16_t*>(base)[at] << 16 : static_cast<const uint32_t*>(base)[at];
+        }
+    }
+    __device__ __forceinline__ void widen(bool bf, float (&o)[VEC]) const {
+        if constexpr (VEC == 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] = __uint_as_float(bf ? e % 2 ? v[0][e / 2] & 0xffff0000u : v[0][e / 2] << 16 : v[e / 4][e % 4]);
+        } else {
+            o[0] = __uint_as_float(v[0][0]);
+        }
+    }
+};
+
+// A row's weights lie in LDS as fp32 (weight, bias, scale, weight2), vectors of 8 in two planes of four so
+// that neighbouring lanes' accesses are neighbours: they would be 32 registers for each vector.
+template <int VEC>
+__device__ __forceinline__ void lds_w(const float* s_w, int C, int k, int c, float (&v)[VEC]) {
+    if constexpr (VEC == 8) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(s_w + k * C + c / 2);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(s_w + k * C + C / 2 + c / 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+    } else {
+        v[0] = s_w[k * C + c];
+    }
+}
+
 template <int VEC, int L, int NV>
-__global__ __launch_bounds__(threads<L>()) void bwd_kernel(Args p, int64_t step) {
+__global__ __launch_bounds__(threads<L>(), NV * VEC > 8 ? 1 : 2) void bwd_kernel(Args p, int64_t step) {
     __shared__ float red[4][8];
-    __shared__ float s_sum[threads<L>() * NV * VEC];
+    extern __shared__ __attribute__((aligned(16))) float s_mem[];     // the weights; in the end the teams' sums
     const int lane = threadIdx.x % L;
     TeamSum<L> team(red);
+    for (int q = threadIdx.x; q < p.C; q += threads<L>()) {
+        const int to = VEC == 8 ? (q % 8 / 4) * (p.C / 2) + q / 8 * 4 + q % 4 : q;
+        const void* w[4] = {p.weight, p.bias, p.scale, p.weight2};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float v[1];
+            load_w<1>(p, w[k], q, k == 1 ? 0.f : 1.f, v);
+            s_mem[k * p.C + to] = v[0];
+        }
+    }
+    __syncthreads();
     int c[NV];
     bool on[NV];
-    float w1[NV][VEC], b1[NV][VEC], sc[NV][VEC], w2[NV][VEC], acc[5][NV][VEC];
+    float acc[5][NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         c[i] = (i * L + lane) * VEC;
         on[i] = c[i] < p.C;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w1[i][e] = b1[i][e] = sc[i][e] = w2[i][e] = 0.f;
+        for (int e = 0; e < VEC; ++e)
 #pragma unroll
             for (int k = 0; k < 5; ++k) acc[k][i][e] = 0.f;
-        }
-        if (!on[i]) continue;
-        load_w<VEC>(p, p.weight, c[i], 1.f, w1[i]);
-        load_w<VEC>(p, p.bias, c[i], 0.f, b1[i]);
-        load_w<VEC>(p, p.scale, c[i], 1.f, sc[i]);
-        load_w<VEC>(p, p.weight2, c[i], 1.f, w2[i]);
     }
     const float inv1 = 1.f / (float)(p.C / p.G), inv2 = 1.f / (float)p.C;
-    for (int64_t row = ((int64_t)blockIdx.x * threads<L>() + threadIdx.x) / L; row < p.rows; row += step) {
+    constexpr bool AHEAD = NV == 1;            // the next row on its way while this one is worked on
+    Raw<VEC> ro[NV], rg[NV], rr[NV], rd[NV], ry[NV];
+    float nm[NV], nrs[NV], nm2 = 0.f, nrs2 = 0.f;
+    auto fetch = [&](int64_t row) {
         const int64_t at = row * p.C;
         const float* stat = p.stats + row * (2 * p.G + 2);
-        float oh[NV][VEC], g[NV][VEC], d[NV][VEC], y[NV][VEC], r[NV][VEC], rs[NV];
+        nm2 = stat[2 * p.G], nrs2 = stat[2 * p.G + 1];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!on[i]) continue;
+            const int part = p.lanes ? c[i] / (8 * p.lanes) : 0;
+            nm[i] = stat[part], nrs[i] = stat[p.G + part];
+            ro[i].load(p.o, at + c[i], p.obf);
+            if (p.gate) rg[i].load(p.gate, row * p.gate_ld + c[i], p.iobf);
+            if (p.dr) rd[i].load(p.dr, at + c[i], p.rbf);
+            if (p.dh) ry[i].load(p.dh, at + c[i], p.iobf);
+            if (p.dh && p.res) rr[i].load(p.res, at + c[i], p.rbf);
+        }
+    };
+    int64_t row = ((int64_t)blockIdx.x * threads<L>() + threadIdx.x) / L;
+    if (AHEAD && row < p.rows) fetch(row);
+    for (; row < p.rows; row += step) {
+        const int64_t at = row * p.C;
+        if (!AHEAD) fetch(row);
+        float oh[NV][VEC], g[NV][VEC], d[NV][VEC], y[NV][VEC], r[NV][VEC], rs[NV], w1[VEC], b1[VEC], sc[VEC], w2[VEC];
+        const float m2 = nm2, rs2 = nrs2;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             rs[i] = 0.f;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) oh[i][e] = g[i][e] = d[i][e] = y[i][e] = r[i][e] = 0.f;
             if (!on[i]) continue;
-            const int part = p.lanes ? c[i] / (8 * p.lanes) : 0;
-            const float m = stat[part];
-            rs[i] = stat[p.G + part];
-            load<VEC>(p.o, at + c[i], p.obf, oh[i]);
-            if (p.gate) load<VEC>(p.gate, row * p.gate_ld + c[i], p.iobf, g[i]);
-            if (p.dr) load<VEC>(p.dr, at + c[i], p.rbf, d[i]);
-            if (p.dh) {
-                load<VEC>(p.dh, at + c[i], p.iobf, y[i]);
-                if (p.res) load<VEC>(p.res, at + c[i], p.rbf, r[i]);
-            }
+            rs[i] = nrs[i];
+            ro[i].widen(p.obf, oh[i]);
+            if (p.gate) rg[i].widen(p.iobf, g[i]);
+            if (p.dr) rd[i].widen(p.rbf, d[i]);
+            if (p.dh) ry[i].widen(p.iobf, y[i]);
+            if (p.dh && p.res) rr[i].widen(p.rbf, r[i]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) oh[i][e] = (oh[i][e] - m) * rs[i];
+            for (int e = 0; e < VEC; ++e) oh[i][e] = (oh[i][e] - nm[i]) * rs[i];
         }
+        if (AHEAD && row + step < p.rows) fetch(row + step);
         if (p.dh) {
-            const float m2 = stat[2 * p.G], rs2 = stat[2 * p.G + 1];
             float s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (!on[i]) continue;
+                lds_w<VEC>(s_mem, p.C, 0, c[i], w1);
+                lds_w<VEC>(s_mem, p.C, 1, c[i], b1);
+                lds_w<VEC>(s_mem, p.C, 2, c[i], sc);
+                lds_w<VEC>(s_mem, p.C, 3, c[i], w2);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    float u = fmaf(oh[i][e], w1[i][e], b1[i][e]);
+                    float u = fmaf(oh[i][e], w1[e], b1[e]);
                     if (p.gate) u *= act_of(p.act, g[i][e]);
-                    const float rh = (fmaf(sc[i][e], u, r[i][e]) - m2) * rs2;
+                    const float rh = (fmaf(sc[e], u, r[i][e]) - m2) * rs2;
                     acc[3][i][e] = fmaf(y[i][e], rh, acc[3][i][e]);
                     acc[4][i][e] += y[i][e];
-                    y[i][e] *= w2[i][e];
+                    y[i][e] *= w2[e];
                     s1 += y[i][e];
                     s2 = fmaf(y[i][e], rh, s2);
                     r[i][e] = rh;
@@ -353,9 +418,12 @@ __global__ __launch_bounds__(threads<L>()) void bwd_kernel(Args p, int64_t step)
             t1[i] = t2[i] = 0.f;
             if (!on[i]) continue;
             if (p.dres) store<VEC>(p.dres, at + c[i], p.rbf, d[i]);
+            lds_w<VEC>(s_mem, p.C, 0, c[i], w1);
+            lds_w<VEC>(s_mem, p.C, 1, c[i], b1);
+            lds_w<VEC>(s_mem, p.C, 2, c[i], sc);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float u = fmaf(oh[i][e], w1[i][e], b1[i][e]), ds = d[i][e] * sc[i][e];
+                const float u = fmaf(oh[i][e], w1[e], b1[e]), ds = d[i][e] * sc[e];
                 float du = ds, s = u;
                 if (p.gate) {
                     const float a = act_of(p.act, g[i][e]);
@@ -366,7 +434,7 @@ __global__ __launch_bounds__(threads<L>()) void bwd_kernel(Args p, int64_t step)
                 acc[2][i][e] = fmaf(d[i][e], s, acc[2][i][e]);
                 acc[0][i][e] = fmaf(du, oh[i][e], acc[0][i][e]);
                 acc[1][i][e] += du;
-                d[i][e] = du * w1[i][e];
+                d[i][e] = du * w1[e];
                 t1[i] += d[i][e];
                 t2[i] = fmaf(d[i][e], oh[i][e], t2[i]);
             }
@@ -394,11 +462,11 @@ __global__ __launch_bounds__(threads<L>()) void bwd_kernel(Args p, int64_t step)
         for (int i = 0; i < NV; ++i)
             if (on[i])
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s_sum[mine * p.C + c[i] + e] = acc[k][i][e];
+                for (int e = 0; e < VEC; ++e) s_mem[mine * p.C + c[i] + e] = acc[k][i][e];
         __syncthreads();
         for (int q = threadIdx.x; q < p.C; q += threads<L>()) {
             float s = 0.f;
-            for (int j = 0; j < TEAMS; ++j) s += s_sum[j * p.C + q];
+            for (int j = 0; j < TEAMS; ++j) s += s_mem[j * p.C + q];
             p.part[((int64_t)blockIdx.x * 5 + k) * p.C + q] = s;
         }
     }
@@ -447,7 +515,15 @@ hipError_t run(const Args& a, bool bwd, hipStream_t s) {
         const int64_t most = (int64_t)n_cu * 8, need = (a.rows + teams - 1) / teams;
         grid = need < most ? need : most;
     }
-    if (bwd) hipLaunchKernelGGL((bwd_kernel<VEC, L, NV>), dim3((uint32_t)grid), dim3(nt), 0, s, a, grid * teams);
+    if (bwd) {
+        const int rows_of = teams > 4 ? teams : 4;             // the weights' four rows, or the teams' sums
+        static wkv7::PerDeviceOnce once;
+        if (4 * VEC * L * NV * 4 > 65536 - 1024) {             // beyond what a launch may have unasked
+            const hipError_t e = wkv7::set_smem_once(once, bwd_kernel<VEC, L, NV>, 4 * VEC * L * NV * 4);
+            if (e != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL((bwd_kernel<VEC, L, NV>), dim3((uint32_t)grid), dim3(nt), rows_of * a.C * 4, s, a, grid * teams);
+    }
     else hipLaunchKernelGGL((fwd_kernel<VEC, L, NV>), dim3((uint32_t)grid), dim3(nt), 0, s, a, grid * teams);
     return hipGetLastError();
 }
