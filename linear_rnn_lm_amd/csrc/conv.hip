@@ -21,7 +21,7 @@ using namespace rows;
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAhead = 8;       // tokens loaded at once; runs are multiples of it
-constexpr int kAheadFwd = 4;    // (B8 T4096 C4096: 97 us, with 8 104)
+constexpr int kAheadFwd = 4;    // forward (B8 T4096 C4096: 95 us, with 8 101)
 constexpr int NT = 256;
 
 struct Args {
@@ -223,8 +223,9 @@ __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
                     ny[i].load(dy + (int64_t)(t0 + i) * p.C);
                 }
         };
-        // One token of x and dy; its sums count if it lies in this run.
-        auto token = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& ry, bool mine, float (&g)[VEC]) {
+        // One token of x and dy; behind the sequence (not real) its ds is 0 whatever the window holds, and its sums
+        // count if it lies in this run.
+        auto token = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& ry, bool real, bool mine, float (&g)[VEC]) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float xe = widen(rx.v[e]);
@@ -236,6 +237,7 @@ __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
                     const float sg = sigmoid(s);
                     d *= fmaf(s * sg, 1.f - sg, sg);
                 }
+                if (!real) d = 0.f;
                 if (mine) {
 #pragma unroll
                     for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(d, win[j][e], dw[j][e]);
@@ -266,7 +268,7 @@ __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
             if (t0 > t_begin && t0 + kAhead <= t_end) {    // whole blocks, all but the first
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
-                    token(cx[i], cy[i], true, g);
+                    token(cx[i], cy[i], true, true, g);
                     store_as(dx + (int64_t)(t0 + i - (W - 1)) * p.C, g);
                 }
                 continue;
@@ -275,11 +277,11 @@ __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
             for (int i = 0; i < kAhead; ++i) {
                 const int t = t0 + i, q = t - (W - 1);
                 if (t >= t_stop) break;
-                if (t >= len) {                            // behind the sequence: its ds is 0
+                if (t >= len) {
                     cx[i].clear();
                     cy[i].clear();
                 }
-                token(cx[i], cy[i], t < t_end, g);
+                token(cx[i], cy[i], t < len, t < t_end, g);
                 if (q < t_begin && !(piece == 0 && dh0)) continue;
                 if (dhT && q >= len - (W - 1)) {
                     Raw<T, VEC> last;
@@ -407,9 +409,10 @@ int esz(int d) { return d == WKV7_BF16 ? 2 : 4; }
 
 wkv7_status check_shape(int B, int T, int C, int W, int N, bool packed) {
     if (B < 1 || T < 1 || C < 1 || W < 2 || W > 4 || (packed && (B != 1 || N < 1))) return WKV7_ERR_SHAPE;
-    if (C > (1 << 20) || (int64_t)B * T > (int64_t(1) << 40) / C || (int64_t)B * T > INT32_MAX) return WKV7_ERR_SHAPE;
-    // a launch takes fewer than 2^32 threads: one for each run and channel
-    if (runs_of(B, T, N, packed, run_of((int64_t)B * T, C)) > (int64_t(1) << 31) / C) return WKV7_ERR_SHAPE;
+    if (C > (1 << 20) || (int64_t)B * T > (int64_t(1) << 40) / C || (int64_t)B * T > INT32_MAX - 1024)   // 32-bit positions, past the end too
+        return WKV7_ERR_SHAPE;
+    // a launch takes fewer than 2^32 threads: one for each run and channel at most
+    if (runs_of(B, T, N, packed, run_of((int64_t)B * T, C)) > (int64_t(1) << 30) / C) return WKV7_ERR_SHAPE;
     return WKV7_OK;
 }
 int64_t span(int64_t rows, int64_t ld, int64_t C, int e) { return ((rows - 1) * ld + C) * e; }
@@ -447,7 +450,8 @@ wkv7_status conv_fwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype 
     if (st != WKV7_OK) return st;
     Args a = {};
     a.x = x; a.w = weight; a.bias = bias; a.h0 = h0; a.y = y; a.hT = hT; a.x_ld = x_ld; a.cu = cu_seqlens;
-    a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16; a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
+    a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16;
+    a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
     a.run = run_of(tokens, C);
     a.runs = (int)runs_of(B, T, N, packed, a.run);
     const bool vec = by_vectors(C, x_ld, e, {x, h0, (const void*)y, (const void*)hT});
@@ -484,7 +488,8 @@ wkv7_status conv_bwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype 
     if (!workspace || workspace_bytes < (size_t)need) return WKV7_ERR_WORKSPACE;
     Args a = {};
     a.x = x; a.w = weight; a.bias = bias; a.h0 = h0; a.dy = dy; a.dhT = dhT; a.dx = dx; a.dh0 = dh0; a.x_ld = x_ld;
-    a.cu = cu_seqlens; a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16; a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
+    a.cu = cu_seqlens; a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16;
+    a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
     a.run = run_of(tokens, C);
     a.runs = (int)runs_of(B, T, N, packed, a.run);
     a.part = static_cast<float*>(workspace);
@@ -515,7 +520,8 @@ wkv7_status conv_step(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype
     if (st != WKV7_OK) return st;
     StepArgs a = {};
     a.x = x; a.w = weight; a.bias = bias; a.state = state; a.state_out = state_out; a.y = y; a.x_ld = x_ld;
-    a.slots = slots; a.silu = silu; a.B = B; a.T = T; a.C = C; a.P = P; a.wbf16 = w_dtype == WKV7_BF16; a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
+    a.slots = slots; a.silu = silu; a.B = B; a.T = T; a.C = C; a.P = P; a.wbf16 = w_dtype == WKV7_BF16;
+    a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
     const bool vec = by_vectors(C, x_ld, e, {x, state, (const void*)state_out, (const void*)y});
     return launch(a, W, x_dtype == WKV7_BF16, vec, 0, static_cast<hipStream_t>(stream)) == hipSuccess ? WKV7_OK
                                                                                                       : WKV7_ERR_HIP;

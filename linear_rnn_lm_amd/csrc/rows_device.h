@@ -35,16 +35,7 @@ __device__ __forceinline__ float softplus(float v) {
     return __builtin_fmaxf(v, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), r * fmaf(-0.5f, e, 1.f));
 }
 
-// A value at a byte offset of the lane's from a pointer that is the same for the whole wave: one
-// 32-bit register per lane instead of a 64-bit address.
-template <typename T>
-__device__ __forceinline__ T ldo(const void* base, uint32_t off) {
-    return *reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
-}
-template <typename T>
-__device__ __forceinline__ T* pto(void* base, uint32_t off) {
-    return reinterpret_cast<T*>(static_cast<char*>(base) + off);
-}
+// A value that is the same for the whole wave, in scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t x) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
     return (int64_t)((uint64_t)hi << 32 | lo);

@@ -20,6 +20,7 @@ struct Shape {
 };
 
 constexpr int64_t kMax = int64_t(1) << 40;
+constexpr int64_t kMaxTokens = INT32_MAX - 1024;   // the kernels' 32-bit positions go a few blocks past the end
 
 int64_t slots_of(int B, int T, int N, bool packed, int len) {
     return packed ? T / len + (int64_t)N : (int64_t)B * ((T - 1) / len + 1);
@@ -28,7 +29,7 @@ int64_t slots_of(int B, int T, int N, bool packed, int len) {
 wkv7_status dims_ok(int B, int T, int C, int S, int G) {
     if (B < 1 || T < 1 || C < 1 || G < 1 || (S != 16 && S != 32 && S != 64)) return WKV7_ERR_SHAPE;
     if (C % G || (G > 1 && C / G % 64) || C > (1 << 20)) return WKV7_ERR_SHAPE;
-    if ((int64_t)B * T > kMax / C || (int64_t)B * T > INT32_MAX) return WKV7_ERR_SHAPE;
+    if ((int64_t)B * T > kMax / C || (int64_t)B * T > kMaxTokens) return WKV7_ERR_SHAPE;
     return WKV7_OK;
 }
 
@@ -86,9 +87,9 @@ wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* 
     return WKV7_OK;
 }
 
-// What the segments leave; behind the parts of the backward.  Never 0, so that a size of 0 is
+// What the segments leave, and h0's copy; behind the parts of the backward.  Never 0, so that a size of 0 is
 // always one of invalid shapes, and a NULL workspace always an error.
-int64_t fwd_ws(const Shape& s) { return s.split[0] ? s.segs[0] * s.per_seg * 4 : 256; }
+int64_t fwd_ws(const Shape& s) { return s.split[0] ? (s.segs[0] * s.per_seg + s.state) * 4 : 256; }
 int64_t bwd_ws(const Shape& s) { return (s.part_bc + s.segs[1] * s.per_seg * (s.split[1] ? 2 : 1)) * 4; }
 int64_t span(int64_t rows, int64_t ld, int64_t n, int e) { return ((rows - 1) * ld + n) * e; }
 constexpr int64_t kMaxLd = 1 << 24;   // 16 rows are addressed with 32-bit byte offsets
@@ -149,11 +150,14 @@ wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.h0 = h0; a.y = y; a.ckpt = ckpt; a.hT = hT; a.cu = cu_seqlens;
     a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.N = s.N; a.seg = s.seg[0]; a.segs = s.segs[0];
     a.split = s.split[0];
-    a.sum_h = static_cast<float*>(workspace);
+    // h0 in place: every segment starts from h0, the last one writes hT, so they read a copy
+    if (a.split && h0 && h0 == hT) a.h0_copy = static_cast<float*>(workspace);
+    a.sum_h = static_cast<float*>(workspace) + s.state;
     a.sum_d = a.sum_h + (int64_t)s.segs[0] * C * S;
     a.halves = s.halves; a.halves_sums = s.halves_sums[0];
     hipStream_t hs = static_cast<hipStream_t>(stream);
     hipError_t err = a.split ? ssm::launch_segments(a, in_dtype == WKV7_BF16, false, hs) : hipSuccess;
+    if (a.h0_copy) a.h0 = a.h0_copy;
     if (err == hipSuccess) err = ssm::launch_fwd(a, in_dtype == WKV7_BF16, hs);
     return status_of(err);
 }

@@ -18,6 +18,7 @@ struct Args {
     float *part, *part_bc;   // backward: sums per segment ((C, S) of dA, (C) of dD and of ddt_bias); per channel block and token
     float *sum_h, *sum_d;    // per segment slot: what it leaves of a zero state (backward: of a zero gradient), (C, S);
                              // the sum of its steps, (C)
+    float* h0_copy;          // where the segments' sums put a copy of h0, or NULL
     const int* cu;
     int softplus, B, T, C, S, G, N;
     int seg, segs;   // tokens of a segment (a multiple of kBlock) and segment slots

@@ -2,7 +2,7 @@
 //
 // Per channel and state h <- e^(delta A) h + delta x b, y = sum c h: the decay differs
 // per channel, state and token, so the scan has no matrix form; it is bound by vector
-// instructions (an exponential, which takes four issue slots, and four more per state
+// instructions (an exponential, which takes two issue slots, and four more per state
 // and token).  A wave works on 16 channels (lane % 16) and 4 NS states, NS to a lane
 // (lane / 16), which stay in registers from the first token to the last; WN waves share
 // the channels of one block, WC of them lie beside each other.  16 tokens at a time: all
@@ -32,13 +32,13 @@ struct Group {
     }
 };
 
-// Blocks ahead: a block takes a wave alone on its unit about 2600, 1500, 900 cycles with 4, 2, 1
-// states to a lane, a load up to 2000.
+// Blocks ahead: a block takes a wave alone on its unit about 2600 cycles with 4 states to a lane, 1500
+// with 2, a load up to 2000.
 template <int NS>
 struct Ahead {
-    static constexpr int value = NS == 1 ? 4 : NS == 2 ? 2 : 1;
-    static constexpr bool groups = NS < 4;   // operands in LDS read a group ahead
-    static constexpr int waves = NS < 4 ? 1 : 4;   // per SIMD: where other waves hide what is not read ahead
+    static constexpr int value = NS == 2 ? 2 : 1;
+    static constexpr bool groups = NS == 2;        // operands in LDS read a group ahead
+    static constexpr int waves = NS == 2 ? 1 : 4;  // per SIMD: where other waves hide what is not read ahead
 };
 
 template <typename InT, int NS, int WN, int WC, bool HZ>
@@ -143,8 +143,7 @@ __global__ __launch_bounds__(64 * WN * WC, Ahead<NS>::waves) void fwd_kernel(Arg
         finish(t0 > t_begin ? out_rows : 0, buf ^ 1, xs[0], zs[0]);
         const wkv7::Rsrc rk = wkv7::make_rsrc(ck, ck_bytes);
         if constexpr (NS == 4) wkv7::bstore4(f32x4{h[0], h[1], h[2], h[3]}, rk, ock, 0);
-        else if constexpr (NS == 2) wkv7::bstore2(make_float2(h[0], h[1]), rk, ock, 0);
-        else wkv7::bstore(h[0], rk, ock, 0);
+        else wkv7::bstore2(make_float2(h[0], h[1]), rk, ock, 0);
         ck += (int64_t)p.C * S;
 #pragma unroll
         for (int k = 0; k < TB / GT; ++k) {
@@ -221,9 +220,14 @@ __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int block
     seq_span(seqs, n, tok0, len);
     n = uniform(n), piece = uniform(piece), len = uniform(len), tok0 = uniform(tok0);
     const int t_begin = piece * p.seg, t_end = min(len, t_begin + p.seg);
-    if (BWD ? t_begin == 0 : t_end == len) return;         // nothing lies behind it
     const int cl = wc * 16 + (lane & 15), g = lane >> 4, ch = cb * CH + cl, n0 = (wn * 4 + g) * NS;
     const bool on = ch < p.C;
+    if (!BWD && p.h0_copy && piece == 0 && on) {
+        const int64_t at = ((int64_t)n * p.C + ch) * S + n0;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) p.h0_copy[at + s] = p.h0[at + s];
+    }
+    if (BWD ? t_begin == 0 : t_end == len) return;         // nothing lies behind it
     float A2[NS], h[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {

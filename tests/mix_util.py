@@ -79,8 +79,8 @@ def ref_scan(v, softplus=True, cu=None, N=None):
     spans = [(slice(None), 0, T, slice(None))] if cu is None else \
         [(slice(0, 1), a, e, slice(n, n + 1)) for n, (a, e) in enumerate(zip(cu, cu[1:]))]
     N = B if cu is None else len(cu) - 1
-    h0 = torch.zeros(N, C, S, dtype=x.dtype) if v["h0"] is None else v["h0"]
-    zero = torch.zeros(x.shape[0], C, dtype=x.dtype)
+    h0 = x.new_zeros(N, C, S) if v["h0"] is None else v["h0"]
+    zero = x.new_zeros(x.shape[0], C)
     ys, hs = [zero] * T, []
     for rows, t0, t1, ns in spans:
         h = h0[ns]
@@ -95,8 +95,9 @@ def ref_scan(v, softplus=True, cu=None, N=None):
     return torch.stack(ys, 1), torch.cat(hs)
 
 
-def ref_scan_grads(p, softplus=True, cu=None):
-    """(y, hT) and a dict of gradients."""
+def ref_scan_grads(p, softplus=True, cu=None, dev="cpu"):
+    """(y, hT) and a dict of gradients (formed on `dev`, where elementary operations are quicker for many channels)."""
+    p = {n: None if t is None else t.to(dev) for n, t in p.items()}
     v = {n: None if p[n] is None else p[n].double().requires_grad_() for n in INS}
     y, hT = ref_scan(v, softplus, cu)
     outs, cots = [y], [p["dy"].double()]

@@ -95,6 +95,47 @@ def test_slices_of_wider_rows(C, off, dtype):
     assert all(torch.equal(got[2][n], want[2][n]) for n in want[2])
 
 
+def test_weights_at_any_address_and_workspace_of_its_size():
+    note("conv odd weights, exact workspace")
+    B, T, C, W = 2, 300, 64, 4
+    for wdtype in (F32, BF):
+        p = to_dev(make_conv(B, T, C, W, BF, seed=7, wdtype=wdtype))
+        want = run(p)
+        buf = torch.empty(C * W + 1, dtype=wdtype, device=DEV)
+        buf[1:] = p["weight"].flatten()
+        got = run({**p, "weight": buf[1:].view(C, W)})
+        need = L.conv._lib().conv_bwd_workspace_bytes(B, T, C, W, 0, 0)
+        guard = torch.full((need + 512,), 0xa5, dtype=torch.uint8, device=DEV)
+        tight = L.conv_bwd(p["dy"], p["x"], p["weight"], p["bias"], p["h0"], p["dhT"], workspace=guard[256:256 + need])
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and all(torch.equal(got[2][n], want[2][n]) for n in want[2])
+        assert all(torch.equal(a, b) for a, b in zip(tight, want[2].values()))
+        assert (guard[:256] == 0xa5).all() and (guard[-256:] == 0xa5).all()
+
+
+def test_nan_and_inf_reach_their_window_only():
+    """A value that is no number in one input or gradient: only the tokens whose windows hold it see it,
+    and never another channel, row or sequence."""
+    note("conv NaN")
+    p = make_conv(2, 40, 24, 4, F32, seed=8)
+    clean = run(to_dev(p))
+    for n, t, bad in (("x", 20, float("nan")), ("x", 39, float("inf")), ("dy", 20, float("nan")), ("dhT", 2, float("nan"))):
+        q = {k: None if v is None else v.clone() for k, v in p.items()}
+        q[n][1, t, 5] = bad
+        y, hT, got = run(to_dev(q))
+        torch.cuda.synchronize()
+        first = 0 if n == "dhT" else t
+        seen = torch.zeros(2, 40, 24, dtype=torch.bool, device=DEV)
+        seen[1, first:first + 4, 5] = n == "x"
+        assert not (~(y == clean[0]) & ~seen).any(), n
+        seen[1, 37 + t if n == "dhT" else max(t - 3, 0):, 5] = True
+        seen[1, (t if n == "dy" else 39 if n == "dhT" else t + 3) + 1:, 5] = False
+        assert not (~(got["dx"] == clean[2]["dx"]) & ~seen).any(), n
+        other = torch.arange(24, device=DEV) != 5
+        assert torch.equal(got["dweight"][other], clean[2]["dweight"][other])
+        assert torch.equal(got["dh0"][0], clean[2]["dh0"][0]) and torch.equal(hT[0], clean[1][0])
+
+
 def test_long_runs_and_same_bits():
     """Enough tokens for longer runs, against the first row alone in shorter ones."""
     note("conv long")

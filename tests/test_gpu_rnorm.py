@@ -219,6 +219,22 @@ def test_nan_stays_in_its_row():
         assert torch.equal(r[2, :64], clean[0][2, :64]) and not torch.isfinite(h[2]).any()
 
 
+@pytest.mark.parametrize("rows,C", [(1, 8), (700, 256), (3000, 2048), (40, 8192), (9, 1030)])
+def test_workspace_of_exactly_its_size(rows, C):
+    note(f"rn workspace {rows} {C}")
+    p = {n: None if t is None else t.to(DEV) for n, t in make(rows, C, seed=3).items()}
+    kw = {n: p[n] for n in WS}
+    r, h, stats = L.rn_fwd(p["o"], p["gate"], p["res"], norm2="rms", **kw)
+    dr, dh = torch.randn_like(r), torch.randn_like(h)
+    want = L.rn_bwd(dr, dh, p["o"], p["gate"], p["res"], stats, norm2="rms", **kw)
+    need = L.rnorm._lib().rn_bwd_workspace_bytes(rows, C, 1)
+    guard = torch.full((need + 512,), 0xa5, dtype=torch.uint8, device=DEV)
+    got = L.rn_bwd(dr, dh, p["o"], p["gate"], p["res"], stats, norm2="rms", workspace=guard[256:256 + need], **kw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (guard[:256] == 0xa5).all() and (guard[-256:] == 0xa5).all()
+
+
 def test_graph_and_same_bits():
     note("rn graph")
     p = make(700, 384, BF, BF, F32, F32, seed=12)

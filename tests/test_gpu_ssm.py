@@ -26,10 +26,10 @@ def run(p, softplus=True, cu=None, train=True):
     return y, hT, dict(zip(GRADS, L.ssm_bwd(p["dy"], *ins, ckpt, p["D"], p["z"], p["dhT"], want_dh0=p["h0"] is not None, **kw)))
 
 
-def check(p, softplus=True, cu=None):
+def check(p, softplus=True, cu=None, ref_on="cpu"):
     y, hT, got = run(to_dev(p), softplus, cu)
     torch.cuda.synchronize()
-    wy, wh, want = ref_scan_grads(p, softplus, cu)
+    wy, wh, want = ref_scan_grads(p, softplus, cu, ref_on)
     dt, S, T = p["x"].dtype, p["A"].shape[1], p["x"].shape[1]
     tokens = p["x"].shape[0] * T
     steps = T if cu is None else max(b - a for a, b in zip(cu, cu[1:]))
@@ -102,6 +102,32 @@ def test_longer_sequences():
     note("ssm T600")
     check(make_scan(1, 600, 20, 16, 1, F32, seed=2))
     check(make_scan(2, 300, 36, 64, 1, BF, seed=3))
+
+
+@pytest.mark.parametrize("B,T,C,S,dtype,what", [
+    (1, 70, 12289, 16, BF, "forward with two states to a lane, backward in two segments"),
+    (3, 40, 4111, 16, F32, "the same, one segment"),
+    (1, 900, 4096, 16, BF, "15 segments, their sums with four states to a lane"),
+    (2, 330, 48, 32, F32, "6 segments of 32 states"), (1, 257, 70, 64, BF, "5 segments of 64 states")])
+def test_variants_of_a_launch(B, T, C, S, dtype, what):
+    """Sizes at which a launch deals its work out in each of its ways."""
+    note(f"ssm B{B} T{T} C{C} S{S} {dtype}: {what}")
+    check(make_scan(B, T, C, S, 1, dtype, seed=T), ref_on=DEV)
+
+
+@pytest.mark.parametrize("S,G,C,dtype", [(16, 1, 40, F32), (32, 2, 128, BF), (64, 1, 33, F32)])
+def test_packed_long_and_many(S, G, C, dtype):
+    """Sequences of several segments beside empty and short ones; more sequences than a wave has lanes."""
+    note(f"ssm packed long S{S}")
+    cu = [2, 132, 133, 133, 480, 500]
+    check(make_scan(1, 510, C, S, G, dtype, seed=20, N=5), cu=cu, ref_on=DEV)
+    gen = torch.Generator().manual_seed(21)
+    lens = torch.randint(0, 9, (90,), generator=gen).tolist()
+    lens[50] = 200
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    check(make_scan(1, cu[-1] + 3, C, S, G, dtype, seed=22, N=90), cu=cu, ref_on=DEV)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
@@ -255,6 +281,75 @@ def test_state_in_place_and_carried():
     assert torch.equal(torch.cat(ys, 1), y) and torch.equal(h, hT)
 
 
+@pytest.mark.parametrize("cu,B,T", [(None, 2, 300), ([0, 3, 290, 300], 1, 300)])
+def test_long_state_in_place(cu, B, T):
+    """hT over h0 where a sequence has several segments: each of them starts from h0."""
+    note(f"ssm in place T{T} {cu}")
+    p = to_dev(make_scan(B, T, 40, 16, 1, F32, seed=23, N=B if cu is None else 3))
+    y, hT, _ = run(p, cu=cu, train=False)
+    kw = dict(dt_bias=p["dt_bias"], want_ckpt=False, cu_seqlens=None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV))
+    ins = [p[n] for n in ("x", "dt", "A", "b", "c")]
+    for _ in range(3):
+        h = p["h0"].clone()
+        y2, _, _ = L.ssm_fwd(*ins, p["D"], p["z"], h, hT=h, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(y2, y) and torch.equal(h, hT)
+    zero = torch.zeros_like(p["h0"])
+    y3, _, _ = L.ssm_fwd(*ins, p["D"], p["z"], zero, **kw)
+    y4, _, none = L.ssm_fwd(*ins, p["D"], p["z"], want_hT=False, **kw)     # neither of them
+    torch.cuda.synchronize()
+    assert torch.equal(y3, y4) and none is None
+
+
+@pytest.mark.parametrize("B,T,C,S,cu", [(2, 300, 40, 16, None), (1, 50, 70, 64, None), (1, 300, 64, 32, [0, 100, 300])])
+def test_workspace_of_exactly_its_size(B, T, C, S, cu):
+    note(f"ssm workspace B{B} T{T} C{C} S{S} {cu}")
+    N = 0 if cu is None else len(cu) - 1
+    p = to_dev(make_scan(B, T, C, S, 1, BF, seed=24, N=N or B))
+    want = run(p, cu=cu)
+    lib = L.ssm._lib()
+    dims = (B, T, C, S, 1, N, int(N > 0))
+    ins = [p[n] for n in ("x", "dt", "A", "b", "c")]
+    kw = dict(dt_bias=p["dt_bias"], cu_seqlens=None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV))
+
+    def guarded(n):
+        buf = torch.full((n + 512,), 0xa5, dtype=torch.uint8, device=DEV)
+        return buf, buf[256:256 + n]
+
+    guards = [guarded(lib.ssm_fwd_workspace_bytes(*dims)), guarded(lib.ssm_bwd_workspace_bytes(*dims)),
+              guarded(lib.ssm_ckpt_bytes(*dims))]
+    ckpt = guards[2][1].view(F32).view(-1, C, S)
+    y, _, hT = L.ssm_fwd(*ins, p["D"], p["z"], p["h0"], workspace=guards[0][1], ckpt=ckpt, **kw)
+    got = L.ssm_bwd(p["dy"], *ins, ckpt, p["D"], p["z"], p["dhT"], workspace=guards[1][1], **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(hT, want[1])
+    assert all(torch.equal(a, want[2][n]) for n, a in zip(GRADS, got))
+    assert all((b[:256] == 0xa5).all() and (b[-256:] == 0xa5).all() for b, _ in guards)
+
+
+def test_two_graphs_at_once():
+    """Two captured training passes, replayed beside each other and with eager work between the replays."""
+    note("ssm two graphs")
+    ps = [to_dev(make_scan(2, 200, 70, 16, 1, BF, seed=s)) for s in (25, 26)]
+    want = [run(p) for p in ps]
+    graphs, outs = [], []
+    for p in ps:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(run(p))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        run(ps[0])
+        for o, w in zip(outs, want):
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+            assert all(torch.equal(o[2][n], w[2][n]) for n in GRADS)
+
+
 # ------------------------------------------------------------------ step
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("B,T,C,S,G", [(1, 1, 1, 16, 1), (3, 1, 65, 16, 1), (2, 4, 100, 32, 1), (5, 1, 128, 64, 2),
@@ -300,6 +395,30 @@ def test_step_slots_padding_and_repeats():
     y2 = L.ssm_step(*args(slice(None)), pool, p["D"], p["z"], dt_bias=p["dt_bias"], slots=slots)
     torch.cuda.synchronize()
     assert torch.equal(y2, y) and torch.equal(pool, want)
+
+
+def test_step_graph_with_other_slots():
+    """A captured step, replayed with other slots, padding and repeated slots."""
+    note("ssm step graph")
+    B, C, S, P = 5, 70, 16, 6
+    p = to_dev(make_scan(B, 1, C, S, 1, BF, seed=27))
+    pool = torch.randn(P, C, S, generator=torch.Generator().manual_seed(2)).to(DEV)
+    slots = torch.arange(B, dtype=torch.int32, device=DEV)
+    step = lambda state: L.ssm_step(*[p[n] for n in ("x", "dt", "A", "b", "c")], state, p["D"], p["z"], dt_bias=p["dt_bias"],  # noqa: E731
+                                    slots=slots)
+    step(pool.clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = step(pool)
+    for ids in ([0, 1, 2, 3, 4], [5, 5, 0, 5, -1], [3, 2, 1, 0, 9], [-1] * 5):
+        slots.copy_(torch.tensor(ids, dtype=torch.int32))
+        other = pool.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(other)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(pool, other), ids
 
 
 def test_steps_continue_a_prompt():

@@ -39,6 +39,10 @@ def test_size_queries():
     c = conv._lib()
     assert c.conv_bwd_workspace_bytes(1, 16, 8, 4, 0, 0) == 5 * 8 * 4
     assert c.conv_bwd_workspace_bytes(1, 16, 8, 5, 0, 0) == 0 and c.conv_bwd_workspace_bytes(2, 16, 8, 4, 3, 1) == 0
+    # positions of 32 bits, with room behind the last token; and one more offset than sequences
+    assert lib.ssm_fwd_workspace_bytes(1, 2 ** 31 - 1024, 16, 16, 1, 0, 0) == 0 < lib.ssm_fwd_workspace_bytes(1, 2 ** 31 - 1025, 16, 16, 1, 0, 0)
+    assert c.conv_bwd_workspace_bytes(1, 2 ** 31 - 1024, 1, 4, 0, 0) == 0 < c.conv_bwd_workspace_bytes(1, 2 ** 31 - 1025, 1, 4, 0, 0)
+    assert c.conv_bwd_workspace_bytes(1, 16, 1, 4, 2 ** 31 - 1, 1) == 0 == lib.ssm_bwd_workspace_bytes(1, 16, 1, 16, 1, 2 ** 31 - 1, 1)
     r = rnorm._lib()
     assert r.rn_bwd_workspace_bytes(1, 8, 1) == 8 * 5 * 4
     assert r.rn_bwd_workspace_bytes(0, 8, 1) == 0 and r.rn_bwd_workspace_bytes(4, 96, 2) == 0
