@@ -609,6 +609,8 @@ def _row_ld(fn, name, t, shape, dtype, dev):
     """The same, checked (0 for None)."""
     if t is None:
         return 0
+    if _fits(t, shape, dtype, dev):
+        return shape[-1] if len(shape) == 3 else shape[-1] * shape[-2]
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{fn}: {name} is {_where(t)}, expected {tuple(shape)} {dtype}")
     if t.device != dev:
@@ -623,6 +625,12 @@ def _row_ld(fn, name, t, shape, dtype, dev):
 def _rows(t):
     """`t` itself where a call takes its layout, else a dense copy."""
     return t if t.dim() < 3 or _ld_of(t) is not None else t.contiguous()
+
+
+def _new_like(t, dtype):
+    """A new dense tensor of t's shape (a call's shortest way to one: these lie on the path of single tokens)."""
+    import torch
+    return torch.empty_like(t) if t.dtype == dtype and t.is_contiguous() else t.new_empty(t.shape, dtype=dtype)
 
 
 def _fresh_rows(shape, dtype, dev, N, fresh):

@@ -21,7 +21,8 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import _check_bytes, _dense, _fresh_rows, _launch, _LazyOpOf, _ptr, _row_ld, _rows, _types, _where, lib
+from . import (_check_bytes, _dense, _fresh_rows, _launch, _LazyOpOf, _new_like, _ptr, _row_ld, _rows, _types, _where,
+               lib)
 from .gdr import _check_cu, _zero_outside
 from .ssm import _check_tensor
 
@@ -151,7 +152,7 @@ def conv_step(x, weight, bias, state, *, silu=True, slots=None, state_out=None, 
     else:
         _check_tensor(fn, "state_out", state_out, (P, W - 1, C), x.dtype, dev)
     if y is None:
-        y = x.new_empty((B, T, C))
+        y = _new_like(x, x.dtype)
     else:
         _check_tensor(fn, "y", y, (B, T, C), x.dtype, dev)
     _launch(fn, _lib().conv_step, dev, *dims, x.data_ptr(), ld, weight.data_ptr(), _ptr(bias), int(bool(silu)),

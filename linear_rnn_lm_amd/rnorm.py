@@ -26,7 +26,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import F32, _check_bytes, _dense, _launch, _LazyOpOf, _ptr, _types, _where, lib
+from . import F32, _check_bytes, _dense, _launch, _LazyOpOf, _new_like, _ptr, _types, _where, lib
 from .ssm import _check_tensor
 
 _NORMS = {None: 0, "layer": 1, "rms": 2}
@@ -128,13 +128,13 @@ def rn_fwd(o, gate=None, res=None, *, weight=None, bias=None, scale=None, weight
     if norm2 is None and (weight2 is not None or bias2 is not None or h is not None):
         raise ValueError(f"{fn}: weight2, bias2 and h need norm2")
     if r is None:
-        r = torch.empty(shape, dtype=r_dtype, device=dev)
+        r = _new_like(o if res is None else res, r_dtype)
     else:
         _check_tensor(fn, "r", r, shape, r_dtype, dev)
     if h is not None:
         _check_tensor(fn, "h", h, shape, layer, dev)
     elif norm2 is not None:
-        h = torch.empty(shape, dtype=layer, device=dev)
+        h = _new_like(o if gate is None else gate, layer)
     if stats is not None:
         _check_tensor(fn, "stats", stats, (rows, 2 * groups + 2), torch.float32, dev)
     elif want_stats:

@@ -28,7 +28,8 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import _check_bytes, _dense, _dense_on, _fits, _fresh_rows, _launch, _LazyOpOf, _ptr, _row_ld, _rows, _types, _where, lib
+from . import (_check_bytes, _dense, _dense_on, _fresh_rows, _launch, _LazyOpOf, _new_like, _ptr, _row_ld, _rows, _types,
+               _where, lib)
 from .gdr import _check_cu, _zero_outside
 
 SSM_BLOCK = 16
@@ -60,7 +61,7 @@ def _sizes(dims, N):
 
 
 def _check_tensor(fn, name, t, shape, dtype, dev):
-    if t is None or _fits(t, shape, dtype, dev):
+    if t is None or (t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous()):
         return
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
         raise ValueError(f"{fn}: {name} is {_where(t)}, expected {tuple(shape)} {dtype}")
@@ -198,7 +199,7 @@ def ssm_step(x, dt, A, b, c, state, D=None, z=None, *, dt_bias=None, softplus=Tr
     else:
         _check_tensor(fn, "state_out", state_out, (P, C, S), torch.float32, dev)
     if y is None:
-        y = x.new_empty((B, T, C))
+        y = _new_like(x, x.dtype)
     else:
         _check_tensor(fn, "y", y, (B, T, C), x.dtype, dev)
     _launch(fn, _lib().ssm_step, dev, *dims, code, *args, _ptr(slots), P, state.data_ptr(), state_out.data_ptr(),
