@@ -606,15 +606,15 @@ def _ld_of(t):
 
 
 def _row_ld(fn, name, t, shape, dtype, dev):
-    """The same, checked (0 for None)."""
+    """The same, checked (0 for None); shape (B, T, C) or (B, T, G, S)."""
     if t is None:
         return 0
-    if _fits(t, shape, dtype, dev):
-        return shape[-1] if len(shape) == 3 else shape[-1] * shape[-2]
-    if t.shape != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{fn}: {name} is {_where(t)}, expected {tuple(shape)} {dtype}")
     if t.device != dev:
         raise ValueError(f"{fn}: {name} is on {t.device}, expected {dev} (the device of the inputs)")
+    if t.is_contiguous():
+        return shape[2] if len(shape) == 3 else shape[2] * shape[3]
     ld = _ld_of(t)
     if ld is None:
         raise ValueError(f"{fn}: {name}'s rows must have one distance and their values lie side by side "

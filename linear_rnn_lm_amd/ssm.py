@@ -61,7 +61,7 @@ def _sizes(dims, N):
 
 
 def _check_tensor(fn, name, t, shape, dtype, dev):
-    if t is None or (t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous()):
+    if t is None or (t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous()):
         return
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
         raise ValueError(f"{fn}: {name} is {_where(t)}, expected {tuple(shape)} {dtype}")
@@ -72,7 +72,7 @@ def _inputs(fn, x, dt, A, b, c, D, z, dt_bias, softplus):
     """(B, T, C, S, G) of the inputs, their type's code, and their part of a call's arguments."""
     if x.dim() != 3 or b.dim() != 4:
         raise ValueError(f"{fn}: x must be (B, T, C) and b (B, T, G, S), got {tuple(x.shape)} and {tuple(b.shape)}")
-    (B, T, C), (G, S) = x.shape, b.shape[2:]
+    (B, T, C), (_, _, G, S) = x.shape, b.shape
     if B < 1 or T < 1 or C < 1 or G < 1 or S not in (16, 32, 64):
         raise ValueError(f"{fn}: B, T, C and G must be at least 1 and S 16, 32 or 64, got x {tuple(x.shape)}, "
                          f"b {tuple(b.shape)}")
@@ -81,14 +81,16 @@ def _inputs(fn, x, dt, A, b, c, D, z, dt_bias, softplus):
     codes, f32 = _types()
     if x.dtype not in codes:
         raise TypeError(f"{fn}: x must be float32 or bfloat16, got {x.dtype}")
-    row, mat, dtype, dev = (B, T, C), (B, T, G, S), x.dtype, x.device
-    lds = [_row_ld(fn, n, t, shape, dtype, dev) for n, t, shape in
-           (("x", x, row), ("dt", dt, row), ("b", b, mat), ("c", c, mat), ("z", z, row))]
+    row, mat, dtype, dev = x.shape, b.shape, x.dtype, x.device
+    if mat[0] != B or mat[1] != T:
+        raise ValueError(f"{fn}: b is {_where(b)}, expected {(B, T, G, S)} {dtype}")
+    args = (x.data_ptr(), _row_ld(fn, "x", x, row, dtype, dev), dt.data_ptr(), _row_ld(fn, "dt", dt, row, dtype, dev),
+            A.data_ptr(), b.data_ptr(), _row_ld(fn, "b", b, mat, dtype, dev), c.data_ptr(),
+            _row_ld(fn, "c", c, mat, dtype, dev), None if D is None else D.data_ptr(), None if z is None else z.data_ptr(),
+            _row_ld(fn, "z", z, row, dtype, dev), None if dt_bias is None else dt_bias.data_ptr(), 1 if softplus else 0)
     _check_tensor(fn, "A", A, (C, S), f32, dev)
     _check_tensor(fn, "D", D, (C,), f32, dev)
     _check_tensor(fn, "dt_bias", dt_bias, (C,), f32, dev)
-    args = (x.data_ptr(), lds[0], dt.data_ptr(), lds[1], A.data_ptr(), b.data_ptr(), lds[2], c.data_ptr(), lds[3], _ptr(D),
-            _ptr(z), lds[4], _ptr(dt_bias), int(bool(softplus)))
     return (B, T, C, S, G), codes[dtype], args
 
 
