@@ -3,10 +3,15 @@
 //
 // Bound by HBM: a row's o, gate and res are read once and stay in registers for both norms.
 // A row belongs to a team of L lanes (part of a wave, a wave or a workgroup), NV vectors of
-// VEC values per lane; a team walks rows with its weights in registers, in the backward
-// with its sums for the five weights' gradients too.  A part of norm1 is 8 to 64
+// VEC values per lane; a team walks rows with the sums for the five weights' gradients in
+// registers, in the forward with its weights too; the backward has those in LDS, and the next
+// row's values on their way while it works on one.  A part of norm1 is 8 to 64
 // neighbouring lanes of one vector, so its sums are exchanges within a wave.  The backward
 // forms r again from what the forward read (res costs what r would), unrounded.
+//
+// 32768 rows of 2048 channels, 32 parts, fp32 o, the rest bf16: forward 150 us (5.4 TB/s), backward
+// 280 us (4.8 TB/s).  Rows of more than 4096 channels are the exception: a lane of 1024 has half the
+// registers, the backward spills some and takes three times what its bytes take.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -105,15 +110,15 @@ __device__ __forceinline__ float lane_sum(float x, int lanes) {
 }
 
 template <int L>
-constexpr int threads() { return L > 256 ? L : 256; }
+constexpr int threads() { return L >= 128 ? L : 256; }
 
 // Sum over a team.  Workgroup-wide teams go through LDS, four buffers in turn: a buffer is
 // written again only after three other sums, so after barriers that every wave's reads precede.
 template <int L>
 struct TeamSum {
-    float (*red)[8];
+    float (*red)[16];
     int turn = 0;
-    __device__ __forceinline__ explicit TeamSum(float (*r)[8]) : red(r) {}
+    __device__ __forceinline__ explicit TeamSum(float (*r)[16]) : red(r) {}
     __device__ __forceinline__ float operator()(float x) {
         x = lane_sum(x, L < 64 ? L : 64);
         if constexpr (L > 64) {
@@ -165,7 +170,7 @@ __device__ __forceinline__ void load_w(const Args& p, const void* w, int c, floa
 
 template <int VEC, int L, int NV>
 __global__ __launch_bounds__(threads<L>()) void fwd_kernel(Args p, int64_t step) {
-    __shared__ float red[4][8];
+    __shared__ float red[4][16];
     const int lane = threadIdx.x % L;
     int64_t row = ((int64_t)blockIdx.x * threads<L>() + threadIdx.x) / L;
     TeamSum<L> team(red);
@@ -312,8 +317,8 @@ __device__ __forceinline__ void lds_w(const float* s_w, int C, int k, int c, flo
 }
 
 template <int VEC, int L, int NV>
-__global__ __launch_bounds__(threads<L>(), NV * VEC > 8 ? 1 : 2) void bwd_kernel(Args p, int64_t step) {
-    __shared__ float red[4][8];
+__global__ __launch_bounds__(threads<L>(), NV * VEC > 8 ? 1 : L > 512 ? 4 : 2) void bwd_kernel(Args p, int64_t step) {
+    __shared__ float red[4][16];
     extern __shared__ __attribute__((aligned(16))) float s_mem[];     // the weights; in the end the teams' sums
     const int lane = threadIdx.x % L;
     TeamSum<L> team(red);
@@ -341,7 +346,7 @@ __global__ __launch_bounds__(threads<L>(), NV * VEC > 8 ? 1 : 2) void bwd_kernel
             for (int k = 0; k < 5; ++k) acc[k][i][e] = 0.f;
     }
     const float inv1 = 1.f / (float)(p.C / p.G), inv2 = 1.f / (float)p.C;
-    constexpr bool AHEAD = NV == 1;            // the next row on its way while this one is worked on
+    constexpr bool AHEAD = NV == 1 && L <= 512; // the next row on its way while this one is worked on
     Raw<VEC> ro[NV], rg[NV], rr[NV], rd[NV], ry[NV];
     float nm[NV], nrs[NV], nm2 = 0.f, nrs2 = 0.f;
     auto fetch = [&](int64_t row) {
@@ -472,8 +477,10 @@ __global__ __launch_bounds__(threads<L>(), NV * VEC > 8 ? 1 : 2) void bwd_kernel
     }
 }
 
-// Lanes per team and vectors per lane for C channels: a row in one or two 16-byte vectors per
-// lane (the backward keeps ten values for each of a vector's), C that is no multiple of 8 by single values.
+// Lanes per team and vectors per lane for C channels: a 16-byte vector per lane and as many lanes as that
+// takes (4096 channels by 256 lanes of two vectors instead: forward of 4 rows 5.1 us against 4.0, of 16384 229
+// against 157, gradient 397 against 216; 1024 channels by a wave: 41 against 31, 102 against 68).  C that is no
+// multiple of 8 goes by single values.
 struct Plan {
     int vec, L, NV;
 };
@@ -483,23 +490,25 @@ Plan plan_of(int C) {
         if (u <= 16) return {8, 16, 1};
         if (u <= 32) return {8, 32, 1};
         if (u <= 64) return {8, 64, 1};
-        if (u <= 128) return {8, 64, 2};
+        if (u <= 128) return {8, 128, 1};
         if (u <= 256) return {8, 256, 1};
-        if (u <= 512) return {8, 256, 2};
-        return {8, 512, 2};
+        if (u <= 512) return {8, 512, 1};
+        return {8, 1024, 1};
     }
     if (C <= 256) return {1, 64, 4};
     if (C <= 1024) return {1, 64, 16};
     if (C <= 4096) return {1, 256, 16};
     return {1, 512, 16};
 }
-int team_threads(int L) { return L > 256 ? L : 256; }
+int team_threads(int L) { return L >= 128 ? L : 256; }
 
-// Workgroups of the backward, each of which leaves one row of sums: two rows to a team at least.
+// Workgroups of the backward, each of which leaves one row of sums: as many as are resident at once (two waves per
+// SIMD, of 1024 threads four), two rows to a team at least.
 int parts_of(int64_t rows, int C) {
     const Plan pl = plan_of(C);
     const int64_t per = 2 * (team_threads(pl.L) / pl.L), n = (rows + per - 1) / per;
-    return (int)(n < 512 ? n : 512);
+    const int most = pl.L >= 512 ? 256 : 131072 / team_threads(pl.L);   // of 256 CUs
+    return (int)(n < most ? n : most);
 }
 
 template <int VEC, int L, int NV>
@@ -523,8 +532,9 @@ hipError_t run(const Args& a, bool bwd, hipStream_t s) {
             if (e != hipSuccess) return e;
         }
         hipLaunchKernelGGL((bwd_kernel<VEC, L, NV>), dim3((uint32_t)grid), dim3(nt), rows_of * a.C * 4, s, a, grid * teams);
+    } else {
+        hipLaunchKernelGGL((fwd_kernel<VEC, L, NV>), dim3((uint32_t)grid), dim3(nt), 0, s, a, grid * teams);
     }
-    else hipLaunchKernelGGL((fwd_kernel<VEC, L, NV>), dim3((uint32_t)grid), dim3(nt), 0, s, a, grid * teams);
     return hipGetLastError();
 }
 
@@ -535,10 +545,10 @@ hipError_t launch(const Args& a, bool bwd, hipStream_t s) {
             case 16: return run<8, 16, 1>(a, bwd, s);
             case 32: return run<8, 32, 1>(a, bwd, s);
             case 64: return run<8, 64, 1>(a, bwd, s);
-            case 128: return run<8, 64, 2>(a, bwd, s);
+            case 128: return run<8, 128, 1>(a, bwd, s);
             case 256: return run<8, 256, 1>(a, bwd, s);
-            case 512: return run<8, 256, 2>(a, bwd, s);
-            default: return run<8, 512, 2>(a, bwd, s);
+            case 512: return run<8, 512, 1>(a, bwd, s);
+            default: return run<8, 1024, 1>(a, bwd, s);
         }
     }
     if (pl.L == 64) return pl.NV == 4 ? run<1, 64, 4>(a, bwd, s) : run<1, 64, 16>(a, bwd, s);

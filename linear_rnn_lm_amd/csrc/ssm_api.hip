@@ -234,6 +234,7 @@ wkv7_status ssm_step(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, con
     a.x = x; a.dt = dt; a.b = b; a.c = c; a.z = z; a.x_ld = x_ld; a.dt_ld = dt_ld; a.b_ld = b_ld; a.c_ld = c_ld;
     a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.state = state; a.state_out = state_out; a.y = y;
     a.slots = slots; a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.P = P;
+    a.bc_four = (reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c)) % (4 * e) == 0 && b_ld % 4 == 0 && c_ld % 4 == 0;
     return status_of(ssm::launch_step(a, in_dtype == WKV7_BF16, static_cast<hipStream_t>(stream)));
 }
 

@@ -34,6 +34,7 @@ struct StepArgs {
     void* y;
     const int* slots;
     int softplus, B, T, C, S, G, P;
+    bool bc_four;    // b and c lie at multiples of four values
 };
 
 // Sums of the backward's parts.
