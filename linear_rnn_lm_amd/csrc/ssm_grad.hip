@@ -296,19 +296,23 @@ __global__ __launch_bounds__(64 * WN * WC, 2) void bwd_kernel(Args p, int blocks
     }
 }
 
-// db and dc of every token in a sequence: sums over the channel blocks of a group.
+// db and dc of every token in a sequence: sums over the channel blocks of a group, four neighbours to a
+// thread.  Bound by HBM: the parts are the most that the gradient kernel writes.
 template <typename InT>
 __global__ __launch_bounds__(256) void bc_kernel(ReduceArgs p, int blocks) {
-    const int64_t tokens = (int64_t)p.B * p.T, all = tokens * p.G * 2 * p.S;
+    const int64_t tokens = (int64_t)p.B * p.T, all = tokens * p.G * (p.S / 2);
     const int per = p.G > 1 ? blocks / p.G : blocks;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-        const int e = (int)(i % (2 * p.S)), g = (int)(i / (2 * p.S) % p.G);
-        const int64_t t = i / (2 * p.S) / p.G;
+        const int e = (int)(i % (p.S / 2)) * 4, g = (int)(i / (p.S / 2) % p.G);
+        const int64_t t = i / (p.S / 2) / p.G;
         if (p.cu && (t < p.cu[0] || t >= p.cu[p.N])) continue;
-        float s = 0.f;
-        for (int k = 0; k < per; ++k) s += p.part_bc[((int64_t)(g * per + k) * tokens + t) * 2 * p.S + e];
-        InT* out = static_cast<InT*>(e < p.S ? p.db : p.dc);
-        st(out + (t * p.G + g) * p.S + e % p.S, s);
+        const float* src = p.part_bc + ((int64_t)g * per * tokens + t) * 2 * p.S + e;
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int k = 0; k < per; ++k) s += *reinterpret_cast<const f32x4*>(src + (int64_t)k * tokens * 2 * p.S);
+        InT* out = static_cast<InT*>(e < p.S ? p.db : p.dc) + (t * p.G + g) * p.S + e % p.S;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) st(out + q, s[q]);
     }
 }
 
@@ -341,7 +345,7 @@ hipError_t launch_reduce(const ReduceArgs& a, bool bf16, hipStream_t s) {
     const hipError_t e = sums::launch_column_sums(a.part, a.segs, CS + 2 * a.C, a.dA, CS, a.dD, a.C, a.ddt_bias, s);
     if (e != hipSuccess) return e;
     const int blocks = (a.C + chans(a.S) - 1) / chans(a.S);
-    const int64_t n = (int64_t)a.B * a.T * a.G * 2 * a.S;
+    const int64_t n = (int64_t)a.B * a.T * a.G * (a.S / 2);
     const dim3 grid((uint32_t)((n + 255) / 256 < 1 << 20 ? (n + 255) / 256 : 1 << 20));   // fewer than 2^32 threads
     if (bf16) hipLaunchKernelGGL(bc_kernel<uint16_t>, grid, dim3(256), 0, s, a, blocks);
     else hipLaunchKernelGGL(bc_kernel<float>, grid, dim3(256), 0, s, a, blocks);
