@@ -2,15 +2,15 @@
 //     r = res + scale act(gate) (norm1(o) weight + bias),   h = norm2(r) weight2 + bias2
 //
 // Bound by HBM: a row's o, gate and res are read once and stay in registers for both norms.
-// A row belongs to a team of L lanes (part of a wave, a wave or a workgroup), NV vectors of
-// VEC values per lane; a team walks rows with the sums for the five weights' gradients in
+// A row belongs to a team of L lanes (part of a wave, a wave or a workgroup), eight neighbouring
+// values to a lane; a team walks rows with the sums for the five weights' gradients in
 // registers, in the forward with its weights too; the backward has those in LDS, and the next
 // row's values on their way while it works on one.  A part of norm1 is 8 to 64
-// neighbouring lanes of one vector, so its sums are exchanges within a wave.  The backward
+// neighbouring lanes, so its sums are exchanges within a wave.  The backward
 // forms r again from what the forward read (res costs what r would), unrounded.
 //
 // 32768 rows of 2048 channels, 32 parts, fp32 o, the rest bf16: forward 150 us (5.4 TB/s), backward
-// 280 us (4.8 TB/s).  Rows of more than 4096 channels are the exception: a lane of 1024 has half the
+// 285 us (4.7 TB/s).  Rows of more than 4096 channels are the exception: a lane of 1024 has half the
 // registers, the backward spills some and takes three times what its bytes take.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -39,55 +39,84 @@ struct Args {
     bool obf, iobf, rbf, wbf;  // which types are bf16
 };
 
-// VEC values of either type; the type is the same for a whole launch.
-template <int VEC>
-__device__ __forceinline__ void load(const void* base, int64_t at, bool bf, float (&v)[VEC]) {
-    if (bf) {
-        const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-        if constexpr (VEC == 8) {
-            const u32x4 u = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = __uint_as_float(u[e] << 16);
-                v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            }
+// A lane's eight neighbouring values c .. c + 7 of a row.  Where C is no multiple of 8 (RAGGED) the last
+// lane's are the row's last eight: its first `twice` belong to the lane before it too, which counts them in
+// sums over the row; everything else both lanes do alike.  Loads and stores need no more alignment than a
+// value's own.  Fewer than 8 channels go one by one.
+struct Cols {
+    int c, twice, n;             // n: values that exist
+    bool on;
+    __device__ __forceinline__ Cols(int lane, int C) : c(lane * 8), twice(0), n(8), on(lane * 8 < C) {}
+};
+template <bool RAGGED>
+__device__ __forceinline__ Cols cols_of(int lane, int C) {
+    Cols k(lane, C);
+    if (RAGGED && k.on) {
+        k.n = min(8, C);
+        k.c = min(k.c, C - k.n);
+        k.twice = lane * 8 - k.c;
+    }
+    return k;
+}
+// Whether value e counts in sums over the row.
+template <bool RAGGED>
+__device__ __forceinline__ bool counts(const Cols& k, int e) { return !RAGGED || (e >= k.twice && e < k.n); }
+
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight values as stored, of either type (the same for a whole launch), widened at their use, so that loads
+// ahead of it do not wait where they are issued.
+struct Raw {
+    u32x4 v[2];
+    template <bool RAGGED>
+    __device__ __forceinline__ void load(const void* base, int64_t at, bool bf, const Cols& k) {
+        const char* p = static_cast<const char*>(base) + at * (bf ? 2 : 4);
+        if (!RAGGED || k.n == 8) {
+            v[0] = reinterpret_cast<const u32x4_any*>(p)[0];
+            if (!bf) v[1] = reinterpret_cast<const u32x4_any*>(p)[1];
         } else {
-            v[0] = ld(p);
-        }
-    } else {
-        const float* p = static_cast<const float*>(base) + at;
-        if constexpr (VEC == 8) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+            uint32_t x[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = a[e];
-                v[4 + e] = b[e];
-            }
-        } else {
-            v[0] = *p;
+            for (int e = 0; e < 8; ++e)
+                x[e] = e >= k.n ? 0u : bf ? reinterpret_cast<const uint16_t*>(p)[e] : reinterpret_cast<const uint32_t*>(p)[e];
+            v[0] = bf ? u32x4{x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16}
+                      : u32x4{x[0], x[1], x[2], x[3]};
+            v[1] = u32x4{x[4], x[5], x[6], x[7]};
         }
     }
-}
-template <int VEC>
-__device__ __forceinline__ void store(void* base, int64_t at, bool bf, const float (&v)[VEC]) {
-    if (bf) {
-        uint16_t* p = static_cast<uint16_t*>(base) + at;
-        if constexpr (VEC == 8) {
-            bf16x8 o;
+    __device__ __forceinline__ void widen(bool bf, float (&o)[8]) const {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = (__bf16)v[e];
-            *reinterpret_cast<bf16x8*>(p) = o;
-        } else {
-            st(p, v[0]);
+        for (int e = 0; e < 8; ++e)
+            o[e] = __uint_as_float(bf ? e % 2 ? v[0][e / 2] & 0xffff0000u : v[0][e / 2] << 16 : v[e / 4][e % 4]);
+    }
+};
+template <bool RAGGED>
+__device__ __forceinline__ void load(const void* base, int64_t at, bool bf, const Cols& k, float (&v)[8]) {
+    Raw r;
+    r.load<RAGGED>(base, at, bf, k);
+    r.widen(bf, v);
+}
+template <bool RAGGED>
+__device__ __forceinline__ void store(void* base, int64_t at, bool bf, const Cols& k, const float (&v)[8]) {
+    char* p = static_cast<char*>(base) + at * (bf ? 2 : 4);
+    if (RAGGED && k.n < 8) {
+#pragma unroll
+        for (int e = 0; e < 7; ++e) {
+            if (e >= k.n) continue;
+            if (bf) st(reinterpret_cast<uint16_t*>(p) + e, v[e]);
+            else reinterpret_cast<float*>(p)[e] = v[e];
         }
+    } else if (bf) {
+        bf16x8 o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = (__bf16)v[e];
+        *reinterpret_cast<u32x4_any*>(p) = __builtin_bit_cast(u32x4, o);
     } else {
-        float* p = static_cast<float*>(base) + at;
-        if constexpr (VEC == 8) {
-            *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-        } else {
-            *p = v[0];
-        }
+        u32x4 a, b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = __float_as_uint(v[e]), b[e] = __float_as_uint(v[4 + e]);
+        reinterpret_cast<u32x4_any*>(p)[0] = a;
+        reinterpret_cast<u32x4_any*>(p)[1] = b;
     }
 }
 
@@ -133,21 +162,9 @@ struct TeamSum {
     }
 };
 
-// Sums of s[i] over norm1's parts, in every lane of a part; a whole row's is one number.
-template <int L, int NV>
-__device__ __forceinline__ void part_sums(float (&s)[NV], int lanes, TeamSum<L>& team) {
-    if (lanes) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] = lane_sum(s[i], lanes);
-    } else {
-        float x = s[0];
-#pragma unroll
-        for (int i = 1; i < NV; ++i) x += s[i];
-        x = team(x);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] = x;
-    }
-}
+// Sum over a part of norm1, in every lane of it: `lanes` neighbours, or the row.
+template <int L>
+__device__ __forceinline__ float part_sum(float x, int lanes, TeamSum<L>& team) { return lanes ? lane_sum(x, lanes) : team(x); }
 
 __device__ __forceinline__ float act_of(int act, float g) {
     const float s = sigmoid(g);
@@ -158,111 +175,89 @@ __device__ __forceinline__ float slope_of(int act, float g) {
     return act == RN_SILU ? s * fmaf(g, 1.f - s, 1.f) : s * (1.f - s);
 }
 
-template <int VEC>
-__device__ __forceinline__ void load_w(const Args& p, const void* w, int c, float dflt, float (&v)[VEC]) {
+template <bool RAGGED>
+__device__ __forceinline__ void load_w(const Args& p, const void* w, const Cols& k, float dflt, float (&v)[8]) {
     if (w) {
-        load<VEC>(w, c, p.wbf, v);
+        load<RAGGED>(w, k.c, p.wbf, k, v);
     } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = dflt;
+        for (int e = 0; e < 8; ++e) v[e] = dflt;
     }
 }
 
-template <int VEC, int L, int NV>
+template <int L, bool RAGGED>
 __global__ __launch_bounds__(threads<L>()) void fwd_kernel(Args p, int64_t step) {
     __shared__ float red[4][16];
     const int lane = threadIdx.x % L;
     int64_t row = ((int64_t)blockIdx.x * threads<L>() + threadIdx.x) / L;
     TeamSum<L> team(red);
-    int c[NV];
-    bool on[NV];
-    float w1[NV][VEC], b1[NV][VEC], sc[NV][VEC], w2[NV][VEC], b2[NV][VEC];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        c[i] = (i * L + lane) * VEC;
-        on[i] = c[i] < p.C;
-        if (!on[i]) continue;
-        load_w<VEC>(p, p.weight, c[i], 1.f, w1[i]);
-        load_w<VEC>(p, p.bias, c[i], 0.f, b1[i]);
-        load_w<VEC>(p, p.scale, c[i], 1.f, sc[i]);
-        load_w<VEC>(p, p.weight2, c[i], 1.f, w2[i]);
-        load_w<VEC>(p, p.bias2, c[i], 0.f, b2[i]);
+    const Cols k = cols_of<RAGGED>(lane, p.C);
+    const int part = p.lanes ? lane / p.lanes : 0;
+    float w1[8], b1[8], sc[8], w2[8], b2[8];
+    if (k.on) {
+        load_w<RAGGED>(p, p.weight, k, 1.f, w1);
+        load_w<RAGGED>(p, p.bias, k, 0.f, b1);
+        load_w<RAGGED>(p, p.scale, k, 1.f, sc);
+        load_w<RAGGED>(p, p.weight2, k, 1.f, w2);
+        load_w<RAGGED>(p, p.bias2, k, 0.f, b2);
     }
     const float inv1 = 1.f / (float)(p.C / p.G), inv2 = 1.f / (float)p.C;
     for (; row < p.rows; row += step) {
-        const int64_t at = row * p.C;
-        float v[NV][VEC], a[NV][VEC], r[NV][VEC], m[NV], q[NV];
+        const int64_t at = row * p.C + k.c;
+        float v[8], a[8], r[8], m = 0.f, q = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            m[i] = q[i] = 0.f;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                v[i][e] = r[i][e] = 0.f;
-                a[i][e] = 1.f;
-            }
-            if (!on[i]) continue;
-            load<VEC>(p.o, at + c[i], p.obf, v[i]);
-            if (p.gate) load<VEC>(p.gate, row * p.gate_ld + c[i], p.iobf, a[i]);
-            if (p.res) load<VEC>(p.res, at + c[i], p.rbf, r[i]);
+        for (int e = 0; e < 8; ++e) {
+            v[e] = r[e] = 0.f;
+            a[e] = 1.f;
+        }
+        if (k.on) {
+            load<RAGGED>(p.o, at, p.obf, k, v);
+            if (p.gate) load<RAGGED>(p.gate, row * p.gate_ld + k.c, p.iobf, k, a);
+            if (p.res) load<RAGGED>(p.res, at, p.rbf, k, r);
         }
         if (p.norm == RN_LAYER) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) m[i] += v[i][e];
-            part_sums<L, NV>(m, p.lanes, team);
+            for (int e = 0; e < 8; ++e) m += counts<RAGGED>(k, e) ? v[e] : 0.f;
+            m = part_sum<L>(m, p.lanes, team) * inv1;
         }
+        if (k.on)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            m[i] *= inv1;
-            if (on[i])
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    v[i][e] -= m[i];
-                    q[i] = fmaf(v[i][e], v[i][e], q[i]);
-                }
-        }
-        part_sums<L, NV>(q, p.lanes, team);
-        float m2 = 0.f, q2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            q[i] = 1.f / sqrtf(fmaf(q[i], inv1, p.eps));
-            if (!on[i]) continue;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float u = fmaf(v[i][e] * q[i], w1[i][e], b1[i][e]);
-                if (p.gate) u *= act_of(p.act, a[i][e]);
-                r[i][e] = fmaf(sc[i][e], u, r[i][e]);
-                m2 += r[i][e];
+            for (int e = 0; e < 8; ++e) {
+                v[e] -= m;
+                const float d = counts<RAGGED>(k, e) ? v[e] : 0.f;
+                q = fmaf(d, d, q);
             }
-            store<VEC>(p.r, at + c[i], p.rbf, r[i]);
-            if (p.stats) {
-                // one lane of each part writes its statistics
+        q = 1.f / sqrtf(fmaf(part_sum<L>(q, p.lanes, team), inv1, p.eps));
+        float m2 = 0.f, q2 = 0.f;
+        if (k.on) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float u = fmaf(v[e] * q, w1[e], b1[e]);
+                if (p.gate) u *= act_of(p.act, a[e]);
+                r[e] = fmaf(sc[e], u, r[e]);
+                m2 += counts<RAGGED>(k, e) ? r[e] : 0.f;
+            }
+            store<RAGGED>(p.r, at, p.rbf, k, r);
+            if (p.stats && (p.lanes ? lane % p.lanes : lane) == 0) {    // one lane of each part
                 float* s = p.stats + row * (2 * p.G + 2);
-                const int part = p.lanes ? c[i] / (8 * p.lanes) : 0;
-                if (p.lanes ? lane % p.lanes == 0 : i == 0 && lane == 0) {
-                    s[part] = m[i];
-                    s[p.G + part] = q[i];
-                }
+                s[part] = m;
+                s[p.G + part] = q;
             }
         }
         if (p.norm2 == RN_NONE) continue;
         m2 = p.norm2 == RN_LAYER ? team(m2) * inv2 : 0.f;
+        if (k.on)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (on[i])
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    r[i][e] -= m2;
-                    q2 = fmaf(r[i][e], r[i][e], q2);
-                }
+            for (int e = 0; e < 8; ++e) {
+                r[e] -= m2;
+                const float d = counts<RAGGED>(k, e) ? r[e] : 0.f;
+                q2 = fmaf(d, d, q2);
+            }
         q2 = 1.f / sqrtf(fmaf(team(q2), inv2, p.eps2));
+        if (k.on) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!on[i]) continue;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) r[i][e] = fmaf(r[i][e] * q2, w2[i][e], b2[i][e]);
-            store<VEC>(p.h, at + c[i], p.iobf, r[i]);
+            for (int e = 0; e < 8; ++e) r[e] = fmaf(r[e] * q2, w2[e], b2[e]);
+            store<RAGGED>(p.h, at, p.iobf, k, r);
         }
         if (p.stats && lane == 0) {
             p.stats[row * (2 * p.G + 2) + 2 * p.G] = m2;
@@ -271,288 +266,219 @@ __global__ __launch_bounds__(threads<L>()) void fwd_kernel(Args p, int64_t step)
     }
 }
 
+// The weights in LDS as fp32 (weight, bias, scale, weight2): a lane's eight in two planes of four, so that
+// neighbouring lanes' accesses are neighbours.  In registers they would be 32 of them.
+template <int L>
+__device__ __forceinline__ float* lds_at(float* s_w, int k, int lane) { return s_w + k * 8 * L + lane * 4; }
+template <int L>
+__device__ __forceinline__ void lds_w(float* s_w, int k, int lane, float (&v)[8]) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(lds_at<L>(s_w, k, lane));
+    const f32x4 b = *reinterpret_cast<const f32x4*>(lds_at<L>(s_w, k, lane) + 4 * L);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+}
+// Floats of LDS: the weights, or in the end the teams' sums.
+template <int L>
+constexpr int lds_floats(int C) { return 4 * 8 * L > threads<L>() / L * C ? 4 * 8 * L : threads<L>() / L * C; }
+
 // With oh, rh the normalised o and r, a = act(gate), u = oh weight + bias:
 //     dr' = dr + rstd2 (e2 - mean(e2) - rh mean(e2 rh)),  e2 = dh weight2       (= dres)
 //     du = dr' scale a,  dgate = dr' scale u act'(gate),  e1 = du weight
 //     do = rstd1 (e1 - mean(e1) - oh mean(e1 oh))                              (means over a part)
 // and over the rows dweight = sum du oh, dbias = sum du, dscale = sum dr' a u, dweight2 = sum dh
 // rh, dbias2 = sum dh; a root-mean-square norm has no mean(e).
-// VEC values as stored, of either type, widened at their use, so that the next row's loads do not
-// wait where they are issued.
-template <int VEC>
-struct Raw {
-    u32x4 v[VEC == 8 ? 2 : 1];
-    __device__ __forceinline__ void load(const void* base, int64_t at, bool bf) {
-        if constexpr (VEC == 8) {
-            const char* p = static_cast<const char*>(base) + at * (bf ? 2 : 4);
-            v[0] = reinterpret_cast<const u32x4*>(p)[0];
-            if (!bf) v[1] = reinterpret_cast<const u32x4*>(p)[1];
-        } else {
-            v[0][0] = bf ? (uint32_t)static_cast<const uint16_t*>(base)[at] << 16 : static_cast<const uint32_t*>(base)[at];
-        }
-    }
-    __device__ __forceinline__ void widen(bool bf, float (&o)[VEC]) const {
-        if constexpr (VEC == 8) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                o[e] = __uint_as_float(bf ? e % 2 ? v[0][e / 2] & 0xffff0000u : v[0][e / 2] << 16 : v[e / 4][e % 4]);
-        } else {
-            o[0] = __uint_as_float(v[0][0]);
-        }
-    }
-};
-
-// A row's weights lie in LDS as fp32 (weight, bias, scale, weight2), vectors of 8 in two planes of four so
-// that neighbouring lanes' accesses are neighbours: they would be 32 registers for each vector.
-template <int VEC>
-__device__ __forceinline__ void lds_w(const float* s_w, int C, int k, int c, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(s_w + k * C + c / 2);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(s_w + k * C + C / 2 + c / 2);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-    } else {
-        v[0] = s_w[k * C + c];
-    }
-}
-
-template <int VEC, int L, int NV>
-__global__ __launch_bounds__(threads<L>(), NV * VEC > 8 ? 1 : L > 512 ? 4 : 2) void bwd_kernel(Args p, int64_t step) {
+template <int L, bool RAGGED>
+__global__ __launch_bounds__(threads<L>(), L > 512 ? 4 : 2) void bwd_kernel(Args p, int64_t step) {
     __shared__ float red[4][16];
-    extern __shared__ __attribute__((aligned(16))) float s_mem[];     // the weights; in the end the teams' sums
+    extern __shared__ __attribute__((aligned(16))) float s_mem[];
     const int lane = threadIdx.x % L;
     TeamSum<L> team(red);
-    for (int q = threadIdx.x; q < p.C; q += threads<L>()) {
-        const int to = VEC == 8 ? (q % 8 / 4) * (p.C / 2) + q / 8 * 4 + q % 4 : q;
+    const Cols k = cols_of<RAGGED>(lane, p.C);
+    const int part = p.lanes ? lane / p.lanes : 0;
+    if (threadIdx.x < L && k.on) {
         const void* w[4] = {p.weight, p.bias, p.scale, p.weight2};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float v[1];
-            load_w<1>(p, w[k], q, k == 1 ? 0.f : 1.f, v);
-            s_mem[k * p.C + to] = v[0];
+        for (int j = 0; j < 4; ++j) {
+            float v[8];
+            load_w<RAGGED>(p, w[j], k, j == 1 ? 0.f : 1.f, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) lds_at<L>(s_mem, j, lane)[e / 4 * 4 * L + e % 4] = v[e];
         }
     }
     __syncthreads();
-    int c[NV];
-    bool on[NV];
-    float acc[5][NV][VEC];
+    float acc[5][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        c[i] = (i * L + lane) * VEC;
-        on[i] = c[i] < p.C;
+    for (int e = 0; e < 8; ++e)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-#pragma unroll
-            for (int k = 0; k < 5; ++k) acc[k][i][e] = 0.f;
-    }
+        for (int j = 0; j < 5; ++j) acc[j][e] = 0.f;
     const float inv1 = 1.f / (float)(p.C / p.G), inv2 = 1.f / (float)p.C;
-    constexpr bool AHEAD = NV == 1 && L <= 512; // the next row on its way while this one is worked on
-    Raw<VEC> ro[NV], rg[NV], rr[NV], rd[NV], ry[NV];
-    float nm[NV], nrs[NV], nm2 = 0.f, nrs2 = 0.f;
+    constexpr bool AHEAD = L <= 512;           // the next row on its way while this one is worked on
+    Raw ro, rg, rr, rd, ry;
+    float nm = 0.f, nrs = 0.f, nm2 = 0.f, nrs2 = 0.f;
     auto fetch = [&](int64_t row) {
-        const int64_t at = row * p.C;
+        const int64_t at = row * p.C + k.c;
         const float* stat = p.stats + row * (2 * p.G + 2);
         nm2 = stat[2 * p.G], nrs2 = stat[2 * p.G + 1];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!on[i]) continue;
-            const int part = p.lanes ? c[i] / (8 * p.lanes) : 0;
-            nm[i] = stat[part], nrs[i] = stat[p.G + part];
-            ro[i].load(p.o, at + c[i], p.obf);
-            if (p.gate) rg[i].load(p.gate, row * p.gate_ld + c[i], p.iobf);
-            if (p.dr) rd[i].load(p.dr, at + c[i], p.rbf);
-            if (p.dh) ry[i].load(p.dh, at + c[i], p.iobf);
-            if (p.dh && p.res) rr[i].load(p.res, at + c[i], p.rbf);
-        }
+        if (!k.on) return;
+        nm = stat[part], nrs = stat[p.G + part];
+        ro.load<RAGGED>(p.o, at, p.obf, k);
+        if (p.gate) rg.load<RAGGED>(p.gate, row * p.gate_ld + k.c, p.iobf, k);
+        if (p.dr) rd.load<RAGGED>(p.dr, at, p.rbf, k);
+        if (p.dh) ry.load<RAGGED>(p.dh, at, p.iobf, k);
+        if (p.dh && p.res) rr.load<RAGGED>(p.res, at, p.rbf, k);
     };
     int64_t row = ((int64_t)blockIdx.x * threads<L>() + threadIdx.x) / L;
     if (AHEAD && row < p.rows) fetch(row);
     for (; row < p.rows; row += step) {
-        const int64_t at = row * p.C;
+        const int64_t at = row * p.C + k.c;
         if (!AHEAD) fetch(row);
-        float oh[NV][VEC], g[NV][VEC], d[NV][VEC], y[NV][VEC], r[NV][VEC], rs[NV], w1[VEC], b1[VEC], sc[VEC], w2[VEC];
+        float oh[8], g[8], d[8], y[8], r[8], rs = 0.f, w1[8], b1[8], sc[8], w2[8];
         const float m2 = nm2, rs2 = nrs2;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            rs[i] = 0.f;
+        for (int e = 0; e < 8; ++e) oh[e] = g[e] = d[e] = y[e] = r[e] = 0.f;
+        if (k.on) {
+            rs = nrs;
+            ro.widen(p.obf, oh);
+            if (p.gate) rg.widen(p.iobf, g);
+            if (p.dr) rd.widen(p.rbf, d);
+            if (p.dh) ry.widen(p.iobf, y);
+            if (p.dh && p.res) rr.widen(p.rbf, r);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) oh[i][e] = g[i][e] = d[i][e] = y[i][e] = r[i][e] = 0.f;
-            if (!on[i]) continue;
-            rs[i] = nrs[i];
-            ro[i].widen(p.obf, oh[i]);
-            if (p.gate) rg[i].widen(p.iobf, g[i]);
-            if (p.dr) rd[i].widen(p.rbf, d[i]);
-            if (p.dh) ry[i].widen(p.iobf, y[i]);
-            if (p.dh && p.res) rr[i].widen(p.rbf, r[i]);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) oh[i][e] = (oh[i][e] - nm[i]) * rs[i];
+            for (int e = 0; e < 8; ++e) oh[e] = (oh[e] - nm) * rs;
         }
         if (AHEAD && row + step < p.rows) fetch(row + step);
         if (p.dh) {
             float s1 = 0.f, s2 = 0.f;
+            if (k.on) {
+                lds_w<L>(s_mem, 0, lane, w1);
+                lds_w<L>(s_mem, 1, lane, b1);
+                lds_w<L>(s_mem, 2, lane, sc);
+                lds_w<L>(s_mem, 3, lane, w2);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (!on[i]) continue;
-                lds_w<VEC>(s_mem, p.C, 0, c[i], w1);
-                lds_w<VEC>(s_mem, p.C, 1, c[i], b1);
-                lds_w<VEC>(s_mem, p.C, 2, c[i], sc);
-                lds_w<VEC>(s_mem, p.C, 3, c[i], w2);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    float u = fmaf(oh[i][e], w1[e], b1[e]);
-                    if (p.gate) u *= act_of(p.act, g[i][e]);
-                    const float rh = (fmaf(sc[e], u, r[i][e]) - m2) * rs2;
-                    acc[3][i][e] = fmaf(y[i][e], rh, acc[3][i][e]);
-                    acc[4][i][e] += y[i][e];
-                    y[i][e] *= w2[e];
-                    s1 += y[i][e];
-                    s2 = fmaf(y[i][e], rh, s2);
-                    r[i][e] = rh;
+                for (int e = 0; e < 8; ++e) {
+                    float u = fmaf(oh[e], w1[e], b1[e]);
+                    if (p.gate) u *= act_of(p.act, g[e]);
+                    const float rh = (fmaf(sc[e], u, r[e]) - m2) * rs2;
+                    acc[3][e] = fmaf(y[e], rh, acc[3][e]);
+                    acc[4][e] += y[e];
+                    y[e] *= w2[e];
+                    const float yc = counts<RAGGED>(k, e) ? y[e] : 0.f;
+                    s1 += yc;
+                    s2 = fmaf(yc, rh, s2);
+                    r[e] = rh;
                 }
             }
             s1 = p.norm2 == RN_LAYER ? team(s1) * inv2 : 0.f;
             s2 = team(s2) * inv2;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) d[i][e] = fmaf(rs2, y[i][e] - s1 - r[i][e] * s2, d[i][e]);
+            for (int e = 0; e < 8; ++e) d[e] = fmaf(rs2, y[e] - s1 - r[e] * s2, d[e]);
         }
-        float t1[NV], t2[NV];
+        float t1 = 0.f, t2 = 0.f;
+        if (k.on) {
+            if (p.dres) store<RAGGED>(p.dres, at, p.rbf, k, d);
+            lds_w<L>(s_mem, 0, lane, w1);
+            lds_w<L>(s_mem, 1, lane, b1);
+            lds_w<L>(s_mem, 2, lane, sc);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            t1[i] = t2[i] = 0.f;
-            if (!on[i]) continue;
-            if (p.dres) store<VEC>(p.dres, at + c[i], p.rbf, d[i]);
-            lds_w<VEC>(s_mem, p.C, 0, c[i], w1);
-            lds_w<VEC>(s_mem, p.C, 1, c[i], b1);
-            lds_w<VEC>(s_mem, p.C, 2, c[i], sc);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float u = fmaf(oh[i][e], w1[e], b1[e]), ds = d[i][e] * sc[e];
+            for (int e = 0; e < 8; ++e) {
+                const float u = fmaf(oh[e], w1[e], b1[e]), ds = d[e] * sc[e];
                 float du = ds, s = u;
                 if (p.gate) {
-                    const float a = act_of(p.act, g[i][e]);
+                    const float a = act_of(p.act, g[e]);
                     du *= a;
                     s *= a;
-                    g[i][e] = ds * u * slope_of(p.act, g[i][e]);
+                    g[e] = ds * u * slope_of(p.act, g[e]);
                 }
-                acc[2][i][e] = fmaf(d[i][e], s, acc[2][i][e]);
-                acc[0][i][e] = fmaf(du, oh[i][e], acc[0][i][e]);
-                acc[1][i][e] += du;
-                d[i][e] = du * w1[e];
-                t1[i] += d[i][e];
-                t2[i] = fmaf(d[i][e], oh[i][e], t2[i]);
+                acc[2][e] = fmaf(d[e], s, acc[2][e]);
+                acc[0][e] = fmaf(du, oh[e], acc[0][e]);
+                acc[1][e] += du;
+                d[e] = du * w1[e];
+                const float dc = counts<RAGGED>(k, e) ? d[e] : 0.f;
+                t1 += dc;
+                t2 = fmaf(dc, oh[e], t2);
             }
-            if (p.gate) store<VEC>(p.dgate, at + c[i], p.iobf, g[i]);
+            if (p.gate) store<RAGGED>(p.dgate, at, p.iobf, k, g);
         }
         if (!p.do_) continue;
-        if (p.norm == RN_LAYER) part_sums<L, NV>(t1, p.lanes, team);
-        part_sums<L, NV>(t2, p.lanes, team);
+        t1 = p.norm == RN_LAYER ? part_sum<L>(t1, p.lanes, team) * inv1 : 0.f;
+        t2 = part_sum<L>(t2, p.lanes, team) * inv1;
+        if (k.on) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!on[i]) continue;
-            const float u1 = p.norm == RN_LAYER ? t1[i] * inv1 : 0.f, u2 = t2[i] * inv1;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) d[i][e] = rs[i] * (d[i][e] - u1 - oh[i][e] * u2);
-            store<VEC>(p.do_, at + c[i], p.obf, d[i]);
+            for (int e = 0; e < 8; ++e) d[e] = rs * (d[e] - t1 - oh[e] * t2);
+            store<RAGGED>(p.do_, at, p.obf, k, d);
         }
     }
     if (!p.part) return;
     constexpr int TEAMS = threads<L>() / L;
     const int mine = threadIdx.x / L;
 #pragma unroll
-    for (int k = 0; k < 5; ++k) {
+    for (int j = 0; j < 5; ++j) {
         __syncthreads();
+        if (k.on)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (on[i])
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) s_mem[mine * p.C + c[i] + e] = acc[k][i][e];
+            for (int e = 0; e < 8; ++e)
+                if (!RAGGED || e < k.n) s_mem[mine * p.C + k.c + e] = acc[j][e];
         __syncthreads();
         for (int q = threadIdx.x; q < p.C; q += threads<L>()) {
             float s = 0.f;
-            for (int j = 0; j < TEAMS; ++j) s += s_mem[j * p.C + q];
-            p.part[((int64_t)blockIdx.x * 5 + k) * p.C + q] = s;
+            for (int t = 0; t < TEAMS; ++t) s += s_mem[t * p.C + q];
+            p.part[((int64_t)blockIdx.x * 5 + j) * p.C + q] = s;
         }
     }
 }
 
-// Lanes per team and vectors per lane for C channels: a 16-byte vector per lane and as many lanes as that
-// takes (4096 channels by 256 lanes of two vectors instead: forward of 4 rows 5.1 us against 4.0, of 16384 229
-// against 157, gradient 397 against 216; 1024 channels by a wave: 41 against 31, 102 against 68).  C that is no
-// multiple of 8 goes by single values.
-struct Plan {
-    int vec, L, NV;
-};
-Plan plan_of(int C) {
-    if (C % 8 == 0) {
-        const int u = C / 8;
-        if (u <= 16) return {8, 16, 1};
-        if (u <= 32) return {8, 32, 1};
-        if (u <= 64) return {8, 64, 1};
-        if (u <= 128) return {8, 128, 1};
-        if (u <= 256) return {8, 256, 1};
-        if (u <= 512) return {8, 512, 1};
-        return {8, 1024, 1};
-    }
-    if (C <= 256) return {1, 64, 4};
-    if (C <= 1024) return {1, 64, 16};
-    if (C <= 4096) return {1, 256, 16};
-    return {1, 512, 16};
+// Lanes of a team for C channels, eight to a lane (4096 channels by 256 lanes of sixteen instead: forward of 4
+// rows 5.1 us against 4.0, of 16384 229 against 157, gradient 397 against 216; 1024 channels by a wave: 41
+// against 31, 102 against 68).
+int lanes_of(int C) {
+    int L = 16;
+    while (8 * L < C) L *= 2;
+    return L;
 }
 int team_threads(int L) { return L >= 128 ? L : 256; }
 
 // Workgroups of the backward, each of which leaves one row of sums: as many as are resident at once (two waves per
 // SIMD, of 1024 threads four), two rows to a team at least.
 int parts_of(int64_t rows, int C) {
-    const Plan pl = plan_of(C);
-    const int64_t per = 2 * (team_threads(pl.L) / pl.L), n = (rows + per - 1) / per;
-    const int most = pl.L >= 512 ? 256 : 131072 / team_threads(pl.L);   // of 256 CUs
+    const int L = lanes_of(C);
+    const int64_t per = 2 * (team_threads(L) / L), n = (rows + per - 1) / per;
+    const int most = L >= 512 ? 256 : 131072 / team_threads(L);        // of 256 CUs
     return (int)(n < most ? n : most);
 }
 
-template <int VEC, int L, int NV>
+template <int L, bool RAGGED>
 hipError_t run(const Args& a, bool bwd, hipStream_t s) {
-    constexpr int nt = threads<L>(), teams = nt / L;
-    int64_t grid;
+    constexpr int nt = threads<L>(), teams = nt / L, most_lds = lds_floats<L>(8 * L) * 4;
     if (bwd) {
-        grid = parts_of(a.rows, a.C);
+        const int64_t grid = parts_of(a.rows, a.C);
+        static wkv7::PerDeviceOnce once;
+        if (most_lds > 65536 - 1024) {                         // beyond what a launch may have unasked
+            const hipError_t e = wkv7::set_smem_once(once, bwd_kernel<L, RAGGED>, most_lds);
+            if (e != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL((bwd_kernel<L, RAGGED>), dim3((uint32_t)grid), dim3(nt), lds_floats<L>(a.C) * 4, s, a, grid * teams);
     } else {
         int n_cu = 0;
         const hipError_t e = wkv7::device_cus(&n_cu);
         if (e != hipSuccess) return e;
-        const int64_t most = (int64_t)n_cu * 8, need = (a.rows + teams - 1) / teams;
-        grid = need < most ? need : most;
-    }
-    if (bwd) {
-        const int rows_of = teams > 4 ? teams : 4;             // the weights' four rows, or the teams' sums
-        static wkv7::PerDeviceOnce once;
-        if (4 * VEC * L * NV * 4 > 65536 - 1024) {             // beyond what a launch may have unasked
-            const hipError_t e = wkv7::set_smem_once(once, bwd_kernel<VEC, L, NV>, 4 * VEC * L * NV * 4);
-            if (e != hipSuccess) return e;
-        }
-        hipLaunchKernelGGL((bwd_kernel<VEC, L, NV>), dim3((uint32_t)grid), dim3(nt), rows_of * a.C * 4, s, a, grid * teams);
-    } else {
-        hipLaunchKernelGGL((fwd_kernel<VEC, L, NV>), dim3((uint32_t)grid), dim3(nt), 0, s, a, grid * teams);
+        const int64_t most = (int64_t)n_cu * 8, need = (a.rows + teams - 1) / teams, grid = need < most ? need : most;
+        hipLaunchKernelGGL((fwd_kernel<L, RAGGED>), dim3((uint32_t)grid), dim3(nt), 0, s, a, grid * teams);
     }
     return hipGetLastError();
 }
+template <int L>
+hipError_t run(const Args& a, bool bwd, hipStream_t s) { return a.C % 8 ? run<L, true>(a, bwd, s) : run<L, false>(a, bwd, s); }
 
 hipError_t launch(const Args& a, bool bwd, hipStream_t s) {
-    const Plan pl = plan_of(a.C);
-    if (pl.vec == 8) {
-        switch (pl.L * pl.NV) {
-            case 16: return run<8, 16, 1>(a, bwd, s);
-            case 32: return run<8, 32, 1>(a, bwd, s);
-            case 64: return run<8, 64, 1>(a, bwd, s);
-            case 128: return run<8, 128, 1>(a, bwd, s);
-            case 256: return run<8, 256, 1>(a, bwd, s);
-            case 512: return run<8, 512, 1>(a, bwd, s);
-            default: return run<8, 1024, 1>(a, bwd, s);
-        }
+    switch (lanes_of(a.C)) {
+        case 16: return run<16>(a, bwd, s);
+        case 32: return run<32>(a, bwd, s);
+        case 64: return run<64>(a, bwd, s);
+        case 128: return run<128>(a, bwd, s);
+        case 256: return run<256>(a, bwd, s);
+        case 512: return run<512>(a, bwd, s);
+        default: return run<1024>(a, bwd, s);
     }
-    if (pl.L == 64) return pl.NV == 4 ? run<1, 64, 4>(a, bwd, s) : run<1, 64, 16>(a, bwd, s);
-    return pl.L == 256 ? run<1, 256, 16>(a, bwd, s) : run<1, 512, 16>(a, bwd, s);
 }
 
 bool is_dtype(int d) { return d == WKV7_F32 || d == WKV7_BF16; }
