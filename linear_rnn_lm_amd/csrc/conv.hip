@@ -2,10 +2,14 @@
 //
 // Bound by HBM: a thread holds VEC neighbouring channels (16 bytes) and their filters in
 // registers and walks a run of tokens with the last W - 1 inputs in a window, so x is read
-// once (and W - 1 tokens again per run), eight tokens being loaded ahead.  The backward forms
-// s again from x, walks W - 1 tokens past its run for the gradients that reach back into it,
+// once (and W - 1 tokens again per run), four tokens being loaded ahead.  The backward, with four channels to a
+// thread, forms s again from x, walks W - 1 tokens past its run for the gradients that reach back into it,
 // and sums the filters' gradients over its run; one row of sums per run, then one pass over
-// those.  Rows that are no multiples of 16 bytes go value by value.
+// those.  Where C is no multiple of VEC the last thread of a row has the row's last VEC channels, some of
+// them its neighbour's too, which both work out alike; loads and stores need a value's own alignment only.
+// Few channels or tokens go by single channels.
+//
+// B8 T4096 C4096 bf16: forward 95 us (5.7 TB/s), backward 191 us (4.2 TB/s), its sums 7 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -19,6 +23,9 @@ namespace {
 
 using namespace rows;
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));   // at any value's address
+typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 
 constexpr int kAhead = 8;       // tokens loaded at once; runs are multiples of it
 constexpr int kAheadFwd = 4;    // forward (B8 T4096 C4096: 95 us, with 8 101)
@@ -31,7 +38,7 @@ struct Args {
     int64_t x_ld;
     const int* cu;
     int silu, B, T, C, N, run, runs;   // tokens of a run, run slots
-    bool wbf16, wfour;   // filters in bf16; at a multiple of four values
+    bool wbf16;   // filters in bf16
 };
 
 struct StepArgs {
@@ -40,7 +47,7 @@ struct StepArgs {
     int64_t x_ld;
     const int* slots;
     int silu, B, T, C, P;
-    bool wbf16, wfour;   // filters in bf16; at a multiple of four values
+    bool wbf16;   // filters in bf16
 };
 
 // VEC values as stored.
@@ -48,14 +55,24 @@ template <typename T, int VEC>
 struct __attribute__((aligned(sizeof(T) * VEC))) Raw {
     T v[VEC];
     __device__ __forceinline__ void load(const T* p) {
-        if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<u32x4*>(v) = *reinterpret_cast<const u32x4*>(p);
-        else if constexpr (VEC * sizeof(T) == 8) *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+        if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<u32x4*>(v) = *reinterpret_cast<const u32x4_any*>(p);
+        else if constexpr (VEC * sizeof(T) == 8) *reinterpret_cast<u32x2*>(v) = *reinterpret_cast<const u32x2_any*>(p);
         else v[0] = *p;
     }
     __device__ __forceinline__ void store(T* p) const {
-        if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<u32x4*>(p) = *reinterpret_cast<const u32x4*>(v);
-        else if constexpr (VEC * sizeof(T) == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
+        if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<u32x4_any*>(p) = *reinterpret_cast<const u32x4*>(v);
+        else if constexpr (VEC * sizeof(T) == 8) *reinterpret_cast<u32x2_any*>(p) = *reinterpret_cast<const u32x2*>(v);
         else *p = v[0];
+    }
+    // without the first `skip`
+    __device__ __forceinline__ void store(T* p, int skip) const {
+        if (skip == 0) {
+            store(p);
+        } else {
+#pragma unroll
+            for (int e = 1; e < VEC; ++e)
+                if (e >= skip) p[e] = v[e];
+        }
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -63,46 +80,50 @@ struct __attribute__((aligned(sizeof(T) * VEC))) Raw {
     }
 };
 template <typename T, int VEC>
-__device__ __forceinline__ void store_as(T* p, const float (&f)[VEC]) {
+__device__ __forceinline__ void store_as(T* p, const float (&f)[VEC], int skip = 0) {
     Raw<T, VEC> r;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) st(&r.v[e], f[e]);
-    r.store(p);
+    r.store(p, skip);
 }
 
-// The filters (C, W) and biases of channels c .. c + VEC - 1; `four`: in pieces of four values.
-template <int W, int VEC>
-__device__ __forceinline__ void load_filters(const void* w, const void* bias, bool bf16, bool four, int c, float (&f)[W][VEC],
-                                             float (&b)[VEC]) {
-    const int64_t at = (int64_t)c * W;
-    if (VEC % 4 == 0 && four) {
-        float all[VEC * W];
+// N values of either type; four at a time where N is a multiple of four.
+template <int N>
+__device__ __forceinline__ void load_values(const void* base, bool bf16, int64_t at, float (&v)[N]) {
+    if constexpr (N % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < VEC * W; i += 4) {
+        for (int i = 0; i < N; i += 4) {
             if (bf16) {
-                const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at + i);
-                all[i] = __uint_as_float(u.x << 16), all[i + 1] = __uint_as_float(u.x & 0xffff0000u);
-                all[i + 2] = __uint_as_float(u.y << 16), all[i + 3] = __uint_as_float(u.y & 0xffff0000u);
+                const u32x2 u = *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(base) + at + i);
+                v[i] = __uint_as_float(u[0] << 16), v[i + 1] = __uint_as_float(u[0] & 0xffff0000u);
+                v[i + 2] = __uint_as_float(u[1] << 16), v[i + 3] = __uint_as_float(u[1] & 0xffff0000u);
             } else {
-                const f32x4 u = *reinterpret_cast<const f32x4*>(static_cast<const float*>(w) + at + i);
+                const u32x4 u = *reinterpret_cast<const u32x4_any*>(static_cast<const float*>(base) + at + i);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) all[i + k] = u[k];
+                for (int k = 0; k < 4; ++k) v[i + k] = __uint_as_float(u[k]);
             }
         }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-#pragma unroll
-            for (int j = 0; j < W; ++j) f[j][e] = all[e * W + j];
     } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                f[j][e] = bf16 ? widen(static_cast<const uint16_t*>(w)[at + e * W + j]) : static_cast<const float*>(w)[at + e * W + j];
+        for (int i = 0; i < N; ++i)
+            v[i] = bf16 ? widen(static_cast<const uint16_t*>(base)[at + i]) : static_cast<const float*>(base)[at + i];
     }
+}
+// The filters (C, W) and biases of channels c .. c + VEC - 1.
+template <int W, int VEC>
+__device__ __forceinline__ void load_filters(const void* w, const void* bias, bool bf16, int c, float (&f)[W][VEC], float (&b)[VEC]) {
+    float all[VEC * W];
+    load_values<VEC * W>(w, bf16, (int64_t)c * W, all);
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-        b[e] = !bias ? 0.f : bf16 ? widen(static_cast<const uint16_t*>(bias)[c + e]) : static_cast<const float*>(bias)[c + e];
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[j][e] = all[e * W + j];
+    if (bias) {
+        load_values<VEC>(bias, bf16, c, b);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) b[e] = 0.f;
+    }
 }
 
 // The W - 1 inputs before token t of a sequence (its state before its first token).
@@ -119,9 +140,9 @@ __device__ __forceinline__ void load_window(const T* x, int64_t x_ld, const T* h
 
 template <typename T, int W, int VEC>
 __global__ __launch_bounds__(NT) void fwd_kernel(Args p) {
-    const int CV = p.C / VEC;
+    const int CV = (p.C + VEC - 1) / VEC;
     const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
-    const int slot = (int)(id / CV), c = (int)(id % CV) * VEC;
+    const int slot = (int)(id / CV), c = min((int)(id % CV) * VEC, p.C - VEC);
     const Seqs seqs{p.cu, p.N, p.T};
     int n, piece, len;
     if (slot >= p.runs || !slot_piece(seqs, slot, p.run, n, piece)) return;
@@ -132,7 +153,7 @@ __global__ __launch_bounds__(NT) void fwd_kernel(Args p) {
     const T* h0 = p.h0 ? static_cast<const T*>(p.h0) + (int64_t)n * (W - 1) * p.C + c : nullptr;
     T* y = static_cast<T*>(p.y) + tok0 * p.C + c;
     float f[W][VEC], b[VEC];
-    load_filters<W, VEC>(p.w, p.bias, p.wbf16, p.wfour, c, f, b);
+    load_filters<W, VEC>(p.w, p.bias, p.wbf16, c, f, b);
     Raw<T, VEC> win[W - 1], next[kAheadFwd];
     load_window<T, W, VEC>(x, p.x_ld, h0, p.C, t_begin, win);
     auto fetch = [&](int t0) {
@@ -175,9 +196,9 @@ __global__ __launch_bounds__(NT) void fwd_kernel(Args p) {
 // dx_q = sum_j w_j ds_(q + W - 1 - j), and for q before the first token that is dh0.
 template <typename T, int W, int VEC>
 __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
-    const int CV = p.C / VEC;
+    const int CV = (p.C + VEC - 1) / VEC;
     const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
-    const int slot = (int)(id / CV), c = (int)(id % CV) * VEC;
+    const int slot = (int)(id / CV), c = min((int)(id % CV) * VEC, p.C - VEC);
     if (slot >= p.runs) return;
     const Seqs seqs{p.cu, p.N, p.T};
     float dw[W][VEC], db[VEC];
@@ -200,7 +221,7 @@ __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
         const T* dhT = p.dhT ? static_cast<const T*>(p.dhT) + state : nullptr;
         T* dh0 = p.dh0 ? static_cast<T*>(p.dh0) + state : nullptr;
         float f[W][VEC], b[VEC], win[W - 1][VEC], ds[W - 1][VEC];     // x of the W - 1 tokens before, ds[j] of token t - 1 - j
-        load_filters<W, VEC>(p.w, p.bias, p.wbf16, p.wfour, c, f, b);
+        load_filters<W, VEC>(p.w, p.bias, p.wbf16, c, f, b);
         {
             Raw<T, VEC> raw[W - 1];
             load_window<T, W, VEC>(x, p.x_ld, h0, p.C, t_begin, raw);
@@ -307,8 +328,9 @@ __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
 // in batch order, so no two workgroups share a state.
 template <typename T, int W, int VEC>
 __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
-    const int sub = blockIdx.x % nsub, r = blockIdx.x / nsub, c = (sub * NT + threadIdx.x) * VEC;
-    const bool on = c < p.C;
+    const int sub = blockIdx.x % nsub, r = blockIdx.x / nsub, c0 = (sub * NT + threadIdx.x) * VEC, c = min(c0, p.C - VEC);
+    const bool on = c0 < p.C;
+    const int twice = c0 - c;    // channels that a neighbour has too; it alone writes them, for their states may change in place
     T* y = static_cast<T*>(p.y) + c;
     int slot = r, end = r + 1;                             // rows r .. end - 1 are looked through
     if (p.slots) {
@@ -316,7 +338,7 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
         if (slot < 0 || slot >= p.P) {
             Raw<T, VEC> zero;
             zero.clear();
-            for (int t = 0; t < p.T && on; ++t) zero.store(y + ((int64_t)r * p.T + t) * p.C);
+            for (int t = 0; t < p.T && on; ++t) zero.store(y + ((int64_t)r * p.T + t) * p.C, twice);
             return;
         }
         bool before = false, after = false;                // whether other rows have this slot; every wave for itself
@@ -335,7 +357,7 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) win[j].load(static_cast<const T*>(p.state) + at + (int64_t)j * p.C);
     float f[W][VEC], b[VEC];
-    load_filters<W, VEC>(p.w, p.bias, p.wbf16, p.wfour, c, f, b);
+    load_filters<W, VEC>(p.w, p.bias, p.wbf16, c, f, b);
     for (int row = r; row < end; ++row) {
         if (row != r && p.slots[row] != slot) continue;
         for (int t = 0; t < p.T; ++t) {
@@ -351,14 +373,14 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
                 s[e] = fmaf(f[W - 1][e], widen(cur.v[e]), s[e]);
                 if (p.silu) s[e] *= sigmoid(s[e]);
             }
-            store_as(y + tok * p.C, s);
+            store_as(y + tok * p.C, s, twice);
 #pragma unroll
             for (int j = 0; j < W - 2; ++j) win[j] = win[j + 1];
             win[W - 2] = cur;
         }
     }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j].store(static_cast<T*>(p.state_out) + at + (int64_t)j * p.C);
+    for (int j = 0; j < W - 1; ++j) win[j].store(static_cast<T*>(p.state_out) + at + (int64_t)j * p.C, twice);
 }
 
 enum { kFwd, kBwd };
@@ -366,7 +388,8 @@ enum { kFwd, kBwd };
 template <typename T, int W, int VEC>
 hipError_t run(const Args& a, int what, hipStream_t s) {
     constexpr int BV = VEC > 4 ? 4 : VEC;      // the backward by four channels: its sums and windows are many registers
-    const int64_t threads = (int64_t)a.runs * (a.C / (what == kFwd ? VEC : BV));
+    const int BW = what == kFwd ? VEC : BV;
+    const int64_t threads = (int64_t)a.runs * ((a.C + BW - 1) / BW);
     const dim3 grid((uint32_t)((threads + NT - 1) / NT));
     if (what == kFwd) hipLaunchKernelGGL((fwd_kernel<T, W, VEC>), grid, dim3(NT), 0, s, a);
     else hipLaunchKernelGGL((bwd_kernel<T, W, BV>), grid, dim3(NT), 0, s, a);
@@ -377,7 +400,7 @@ hipError_t run(const StepArgs& a, int, hipStream_t s) {
     // by four channels too: half the loads to a thread before its first product (4096 channels of bf16: 4 rows 4.0 -> 2.5
     // us, 256 rows 8.7 -> 6.8)
     constexpr int BV = VEC > 4 ? 4 : VEC;
-    const int nsub = (a.C / BV + NT - 1) / NT;
+    const int nsub = (a.C + BV * NT - 1) / (BV * NT);
     hipLaunchKernelGGL((step_kernel<T, W, BV>), dim3((uint32_t)a.B * nsub), dim3(NT), 0, s, a, nsub);
     return hipGetLastError();
 }
@@ -389,8 +412,19 @@ hipError_t pick_w(const A& a, int W, int what, hipStream_t s) {
         default: return run<T, 4, VEC>(a, what, s);
     }
 }
+// Vectors, or one channel to a thread: many short loads beat few long ones until the vectors alone fill the
+// chip.  1001 channels of bf16, forward: of 2000 tokens (16 thousand threads in runs of 16) 7.9 us by
+// vectors, 4.9 by single channels, of 4000 8.5 and 7.2, of 8000 9.3 and 10.8; gradient: of 2000 15.8 and
+// 11.5, of 4000 19.1 and 16.2, of 8000 (125 thousand threads) 25.1 and 25.2.
+bool by_vectors(const Args& a, int what, bool bf16) {
+    const int vec = bf16 && what == kFwd ? 8 : 4;
+    return a.C >= (bf16 ? 8 : 4) && (int64_t)a.B * a.T / 16 * ((a.C + vec - 1) / vec) >= (what == kFwd ? 49152 : 131072);
+}
+bool by_vectors(const StepArgs& a, int, bool bf16) { return a.C >= (bf16 ? 8 : 4); }
+
 template <typename A>
-hipError_t launch(const A& a, int W, bool bf16, bool vec, int what, hipStream_t s) {
+hipError_t launch(const A& a, int W, bool bf16, int what, hipStream_t s) {
+    const bool vec = by_vectors(a, what, bf16);
     if (bf16) return vec ? pick_w<uint16_t, 8>(a, W, what, s) : pick_w<uint16_t, 1>(a, W, what, s);
     return vec ? pick_w<float, 4>(a, W, what, s) : pick_w<float, 1>(a, W, what, s);
 }
@@ -420,15 +454,6 @@ wkv7_status check_shape(int B, int T, int C, int W, int N, bool packed) {
 }
 int64_t span(int64_t rows, int64_t ld, int64_t C, int e) { return ((rows - 1) * ld + C) * e; }
 
-// Rows by 16-byte pieces: everything that is read or written by rows lies at multiples of 16 bytes.
-template <int N>
-bool by_vectors(int C, int64_t ld, int e, const void* const (&ptrs)[N]) {
-    if (C * e % 16 || ld * e % 16) return false;
-    for (const void* p : ptrs)
-        if (reinterpret_cast<uintptr_t>(p) & 15) return false;
-    return true;
-}
-
 }  // namespace
 }  // namespace conv
 
@@ -454,11 +479,9 @@ wkv7_status conv_fwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype 
     Args a = {};
     a.x = x; a.w = weight; a.bias = bias; a.h0 = h0; a.y = y; a.hT = hT; a.x_ld = x_ld; a.cu = cu_seqlens;
     a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16;
-    a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
     a.run = run_of(tokens, C);
     a.runs = (int)runs_of(B, T, N, packed, a.run);
-    const bool vec = by_vectors(C, x_ld, e, {x, h0, (const void*)y, (const void*)hT});
-    return launch(a, W, x_dtype == WKV7_BF16, vec, kFwd, static_cast<hipStream_t>(stream)) == hipSuccess ? WKV7_OK
+    return launch(a, W, x_dtype == WKV7_BF16, kFwd, static_cast<hipStream_t>(stream)) == hipSuccess ? WKV7_OK
                                                                                                          : WKV7_ERR_HIP;
 }
 
@@ -492,13 +515,11 @@ wkv7_status conv_bwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype 
     Args a = {};
     a.x = x; a.w = weight; a.bias = bias; a.h0 = h0; a.dy = dy; a.dhT = dhT; a.dx = dx; a.dh0 = dh0; a.x_ld = x_ld;
     a.cu = cu_seqlens; a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16;
-    a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
     a.run = run_of(tokens, C);
     a.runs = (int)runs_of(B, T, N, packed, a.run);
     a.part = static_cast<float*>(workspace);
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    const bool vec = by_vectors(C, x_ld, e, {x, h0, dy, dhT, (const void*)dx, (const void*)dh0});
-    hipError_t err = launch(a, W, x_dtype == WKV7_BF16, vec, kBwd, hs);
+    hipError_t err = launch(a, W, x_dtype == WKV7_BF16, kBwd, hs);
     if (err == hipSuccess)
         err = sums::launch_column_sums(a.part, a.runs, (int64_t)(W + 1) * C, dweight, (int64_t)W * C, dbias, C, nullptr, hs);
     return err == hipSuccess ? WKV7_OK : WKV7_ERR_HIP;
@@ -524,9 +545,7 @@ wkv7_status conv_step(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype
     StepArgs a = {};
     a.x = x; a.w = weight; a.bias = bias; a.state = state; a.state_out = state_out; a.y = y; a.x_ld = x_ld;
     a.slots = slots; a.silu = silu; a.B = B; a.T = T; a.C = C; a.P = P; a.wbf16 = w_dtype == WKV7_BF16;
-    a.wfour = reinterpret_cast<uintptr_t>(weight) % (4 * we) == 0;
-    const bool vec = by_vectors(C, x_ld, e, {x, state, (const void*)state_out, (const void*)y});
-    return launch(a, W, x_dtype == WKV7_BF16, vec, 0, static_cast<hipStream_t>(stream)) == hipSuccess ? WKV7_OK
+    return launch(a, W, x_dtype == WKV7_BF16, 0, static_cast<hipStream_t>(stream)) == hipSuccess ? WKV7_OK
                                                                                                       : WKV7_ERR_HIP;
 }
 

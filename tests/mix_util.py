@@ -134,17 +134,17 @@ def ref_conv(v, silu=True, cu=None):
     spans = [(slice(None), 0, T, slice(None))] if cu is None else \
         [(slice(0, 1), a, e, slice(n, n + 1)) for n, (a, e) in enumerate(zip(cu, cu[1:]))]
     N = B if cu is None else len(cu) - 1
-    h0 = torch.zeros(N, W - 1, C, dtype=x.dtype) if v["h0"] is None else v["h0"]
+    h0 = x.new_zeros(N, W - 1, C) if v["h0"] is None else v["h0"]
     ys, hs, at = [], [], 0
     for rows, t0, t1, ns in spans:
         ext = torch.cat([h0[ns], x[rows, t0:t1]], 1)
         s = sum(ext[:, j:j + t1 - t0] * w[:, j] for j in range(W))
         if v["bias"] is not None:
             s = s + v["bias"]
-        ys += [torch.zeros(ext.shape[0], t0 - at, C, dtype=x.dtype), s * torch.sigmoid(s) if silu else s]
+        ys += [x.new_zeros(ext.shape[0], t0 - at, C), s * torch.sigmoid(s) if silu else s]
         hs.append(ext[:, t1 - t0:])
         at = t1
-    ys.append(torch.zeros(x.shape[0] if cu is None else 1, T - at, C, dtype=x.dtype))
+    ys.append(x.new_zeros(x.shape[0] if cu is None else 1, T - at, C))
     return torch.cat(ys, 1), torch.cat(hs)
 
 

@@ -136,6 +136,56 @@ def test_nan_and_inf_reach_their_window_only():
         assert torch.equal(got["dh0"][0], clean[2]["dh0"][0]) and torch.equal(hT[0], clean[1][0])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("B,T,C,W", [(1, 9001, 1003, 4), (2, 4100, 1024, 3), (1, 33000, 261, 2)])
+def test_many_tokens_by_vectors(B, T, C, W, dtype):
+    """Enough work for vectors of channels: multiples of them, and rows whose last vector overlaps the one before.  The first
+    and last tokens, and every sum, against the definition on the GPU."""
+    note(f"conv vectors B{B} T{T} C{C} W{W} {dtype}")
+    p = make_conv(B, T, C, W, dtype, seed=9)
+    y, hT, got = run(to_dev(p))
+    torch.cuda.synchronize()
+    wy, wh, want = ref_conv_grads(to_dev(p))
+    assert rel(y, wy) <= conv_tol(W, dtype) and torch.equal(hT.double(), wh)
+    for n, w in want.items():
+        many = n in ("dweight", "dbias")
+        assert rel(got[n], w) <= conv_tol(W, F32 if many else dtype, B * T if many else 0, True), n
+        assert rel(got[n][..., -9:] if n in ("dx", "dh0") else got[n][-9:], w[..., -9:] if n in ("dx", "dh0") else w[-9:]) <= \
+            conv_tol(W, F32 if many else dtype, B * T if many else 0, True), n
+
+
+@pytest.mark.parametrize("C,W,dtype", [(1003, 4, BF), (1024, 3, F32), (1000, 2, BF)])
+def test_packed_by_vectors(C, W, dtype):
+    """Many sequences, empty, of one token and long, in a row long enough for vectors of channels."""
+    note(f"conv packed vectors C{C} W{W} {dtype}")
+    gen = torch.Generator().manual_seed(10)
+    cu = [3]
+    for n in [0, 1, 2, 3, 700, 0, 31, 32, 33, 9] + torch.randint(0, 900, (20,), generator=gen).tolist():
+        cu.append(cu[-1] + n)
+    T = max(cu[-1] + 5, 9000)
+    p = make_conv(1, T, C, W, dtype, seed=11, N=len(cu) - 1)
+    y, hT, got = run(to_dev(p), cu=cu)
+    torch.cuda.synchronize()
+    wy, wh, want = ref_conv_grads(to_dev(p), cu=cu)
+    assert rel(y, wy) <= conv_tol(W, dtype) and torch.equal(hT.double(), wh)
+    for n, w in want.items():
+        many = n in ("dweight", "dbias")
+        assert rel(got[n], w) <= conv_tol(W, F32 if many else dtype, T if many else 0, True), n
+
+
+@pytest.mark.parametrize("C", [9, 12, 37, 1029])
+def test_step_in_place_with_overlapping_vectors(C):
+    """Channels that two threads work on are written by one of them: many rows, several tokens, states in place."""
+    note(f"conv step in place C{C}")
+    for dtype in (F32, BF):
+        p = to_dev(make_conv(60, 3, C, 4, dtype, seed=C))
+        wy, wh = L.conv_fwd(p["x"], p["weight"], p["bias"], p["h0"])
+        state = p["h0"].clone()
+        y = L.conv_step(p["x"], p["weight"], p["bias"], state)
+        torch.cuda.synchronize()
+        assert torch.equal(y, wy) and torch.equal(state, wh)
+
+
 def test_long_runs_and_same_bits():
     """Enough tokens for longer runs, against the first row alone in shorter ones."""
     note("conv long")
