@@ -15,8 +15,7 @@
  *   States h0, hT and their gradients: (N, W - 1, C) x_dtype.
  * - Sums are fp32; y, dx and dh0 are rounded once.  A NaN or Inf input spoils its channel of
  *   the W tokens that read it.
- * - Every pointer is a device pointer aligned to its values (workspace: 16); rows that are
- *   multiples of 16 bytes at multiples of 16 bytes go faster.
+ * - Every pointer is a device pointer aligned to its values (workspace: 16).
  * - Results do not vary from run to run.
  */
 #ifndef CONV_H

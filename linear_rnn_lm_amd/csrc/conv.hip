@@ -111,7 +111,8 @@ __device__ __forceinline__ void load_values(const void* base, bool bf16, int64_t
 }
 // The filters (C, W) and biases of channels c .. c + VEC - 1.
 template <int W, int VEC>
-__device__ __forceinline__ void load_filters(const void* w, const void* bias, bool bf16, int c, float (&f)[W][VEC], float (&b)[VEC]) {
+__device__ __forceinline__ void load_filters(const void* w, const void* bias, bool bf16, int c, float (&f)[W][VEC],
+                                             float (&b)[VEC]) {
     float all[VEC * W];
     load_values<VEC * W>(w, bf16, (int64_t)c * W, all);
 #pragma unroll
@@ -446,8 +447,8 @@ int esz(int d) { return d == WKV7_BF16 ? 2 : 4; }
 
 wkv7_status check_shape(int B, int T, int C, int W, int N, bool packed) {
     if (B < 1 || T < 1 || C < 1 || W < 2 || W > 4 || (packed && (B != 1 || N < 1))) return WKV7_ERR_SHAPE;
-    if (C > (1 << 20) || (int64_t)B * T > (int64_t(1) << 40) / C || (int64_t)B * T > INT32_MAX - 1024)   // 32-bit positions, past the end too
-        return WKV7_ERR_SHAPE;
+    if (C > (1 << 20) || (int64_t)B * T > (int64_t(1) << 40) / C || (int64_t)B * T > INT32_MAX - 1024)
+        return WKV7_ERR_SHAPE;                             // 32-bit positions, past the end too
     // a launch takes fewer than 2^32 threads: one for each run and channel at most
     if (runs_of(B, T, N, packed, run_of((int64_t)B * T, C)) > (int64_t(1) << 30) / C) return WKV7_ERR_SHAPE;
     return WKV7_OK;

@@ -63,16 +63,17 @@ wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* 
     s->tokens = (int64_t)B * T;
     s->slots = slots_of(B, T, N, packed, ssm::kBlock);
     const int64_t blocks = (C + ssm::chans(S) - 1) / ssm::chans(S);
-    // forward with two states to a lane instead of segments: twice the waves for a twelfth more instructions, where
-    // that fills the chip
+    // Forward with two states to a lane instead of segments: twice the waves for a twelfth more instructions, in workgroups
+    // of eight of which a CU holds one, so where they are nearly as many as the CUs (4096 channels, T 4096, against segments:
+    // 4 sequences, 1024 waves without halves, 363 us to 433, but 3, 768 waves, 353 to 340; 1152 waves of T 1024 180 to 156).
     const int64_t waves = waves_of(s->N, C, S);
-    s->halves = S == 16 && !packed && waves >= 768 && waves < kWaves;
+    s->halves = S == 16 && !packed && waves > 832 && waves <= 1024;
     for (int back = 0; back < 2; ++back) {
         s->seg[back] = segment_of(s->N, T, C, S, packed, kWaves, !back && s->halves, back ? 2 : 3);
         s->split[back] = s->seg[back] < T;
-        // the segments' sums alike, up to three waves per SIMD (backward of 4 x 4096 tokens of 4096 channels, 3072 waves: 244
+        // the segments' sums alike, up to three waves per SIMD (backward of 4 x 4096 tokens of 4096 channels, as many: 244
         // -> 186 us; forward of 16384, 3840 waves: 229 -> 245)
-        s->halves_sums[back] = S == 16 && !packed && waves * ((T - 1) / s->seg[back]) <= 3072;
+        s->halves_sums[back] = S == 16 && !packed && waves * ((T - 1) / s->seg[back]) <= 3 * 1024;
         const int64_t segs = slots_of(B, T, N, packed, s->seg[back]);
         // a launch takes fewer than 2^32 threads: at most 512 for each segment and channel block
         if (segs > (1 << 22) / (2 * blocks)) return WKV7_ERR_SHAPE;
@@ -234,7 +235,7 @@ wkv7_status ssm_step(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, con
     a.x = x; a.dt = dt; a.b = b; a.c = c; a.z = z; a.x_ld = x_ld; a.dt_ld = dt_ld; a.b_ld = b_ld; a.c_ld = c_ld;
     a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.state = state; a.state_out = state_out; a.y = y;
     a.slots = slots; a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.P = P;
-    a.bc_four = (reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c)) % (4 * e) == 0 && b_ld % 4 == 0 && c_ld % 4 == 0;
+    a.bc_four = (reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c)) % (4 * e) == 0 && (b_ld | c_ld) % 4 == 0;
     return status_of(ssm::launch_step(a, in_dtype == WKV7_BF16, static_cast<hipStream_t>(stream)));
 }
 

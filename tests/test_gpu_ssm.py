@@ -105,8 +105,9 @@ def test_longer_sequences():
 
 
 @pytest.mark.parametrize("B,T,C,S,dtype,what", [
-    (1, 70, 12289, 16, BF, "forward with two states to a lane, backward in two segments"),
-    (3, 40, 4111, 16, F32, "the same, one segment"),
+    (1, 70, 12289, 16, BF, "two segments"), (3, 40, 4111, 16, F32, "one segment, not enough waves to fill the chip"),
+    (1, 70, 13401, 16, BF, "forward with two states to a lane, backward in two segments"),
+    (3, 40, 4501, 16, F32, "the same, one segment"),
     (1, 900, 4096, 16, BF, "15 segments, their sums with four states to a lane"),
     (2, 330, 48, 32, F32, "6 segments of 32 states"), (1, 257, 70, 64, BF, "5 segments of 64 states")])
 def test_variants_of_a_launch(B, T, C, S, dtype, what):
