@@ -37,25 +37,26 @@ wkv7_status dims_ok(int B, int T, int C, int S, int G) {
 // (packed: in all sequences together, if they are even).
 int64_t waves_of(int N, int C, int S) { return (int64_t)N * ((C + 15) / 16) * (S / 16); }
 
-// Tokens of a segment.  A sequence is cut into n segments to have `target` waves, as many as the
-// chip holds of the kernel at once; at most 16, of 64 tokens at least.  Packed sequences are
-// of lengths that the host does not know: cut alike if they were even and one in T tokens, but
+// Tokens of a segment: a sequence is cut into n, at most 16, of 64 tokens at least.  Up to one and a half waves per SIMD
+// many short segments, which fill the last round of workgroups evenly; beyond, the segments' sums cost more than the idle
+// waves, but for a backward (two waves per SIMD at once) with a little more than one round.  us with n = 1, 2, 4, 8, 16:
+//     forward  256 waves of T 4096 420 340 176 139 127, 1280 of 4096 622 625 562 518 536, 1792 of 2048 319 376 367 376 394
+//     backward 576 of 1024 305 287 228 189 180, 1024 of 4096 1245 1112 1047 1055 1067, 1280 of 4096 1698 1608 1337 1308 1330,
+//              1792 of 2048 866 976 934 933 969, 2560 of 2048 1368 1277 1288 1313 1370, 3584 of 1024 854 878 905 950 1038
+// Packed sequences are of lengths that the host does not know: cut as if they were one in T tokens, but
 // where they are enough to fill half the chip only a sequence of more than T / 4 is cut.
-int segment_of(int N, int T, int C, int S, bool packed, int64_t target, bool halves, int least) {
+int segment_of(int N, int T, int C, int S, bool packed, bool halves, bool back) {
     const int64_t waves = waves_of(N, C, S);
-    int64_t n = target / waves, seg = T;
-    if (halves) n = 1;
-    if (packed) {
-        n = 2 * waves > target ? 4 : target / waves_of(1, C, S);
-        least = 2;
-    }
+    int64_t n = 1;
+    if (packed) n = waves > 2048 ? 4 : 4096 / waves_of(1, C, S);
+    else if (!halves && waves <= 1536) n = 8192 / waves > 8 ? 8192 / waves : 8;
+    else if (back && waves > 2048 && waves <= 3 * 1024) n = 2;
     if (n > 16) n = 16;
-    if (n >= least) seg = (T + n - 1) / n;
+    int64_t seg = n > 1 ? (T + n - 1) / n : T;
     if (seg < 64) seg = 64;
     if (seg > T) seg = T;
     return (int)((seg + ssm::kBlock - 1) / ssm::kBlock * ssm::kBlock);
 }
-constexpr int64_t kWaves = 4096;
 
 wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* s) {
     if (dims_ok(B, T, C, S, G) != WKV7_OK || (packed && (B != 1 || N < 1))) return WKV7_ERR_SHAPE;
@@ -69,7 +70,7 @@ wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* 
     const int64_t waves = waves_of(s->N, C, S);
     s->halves = S == 16 && !packed && waves > 832 && waves <= 1024;
     for (int back = 0; back < 2; ++back) {
-        s->seg[back] = segment_of(s->N, T, C, S, packed, kWaves, !back && s->halves, back ? 2 : 3);
+        s->seg[back] = segment_of(s->N, T, C, S, packed, !back && s->halves, back);
         s->split[back] = s->seg[back] < T;
         // the segments' sums alike, up to three waves per SIMD (backward of 4 x 4096 tokens of 4096 channels, as many: 244
         // -> 186 us; forward of 16384, 3840 waves: 229 -> 245)
