@@ -37,21 +37,25 @@ wkv7_status dims_ok(int B, int T, int C, int S, int G) {
 // (packed: in all sequences together, if they are even).
 int64_t waves_of(int N, int C, int S) { return (int64_t)N * ((C + 15) / 16) * (S / 16); }
 
-// Tokens of a segment: a sequence is cut into n, at most 16, of 64 tokens at least.  Up to one and a half waves per SIMD
+// Tokens of a segment: a sequence is cut into n, at most 64, of 64 tokens at least.  Up to one and a half waves per SIMD
 // many short segments, which fill the last round of workgroups evenly; beyond, the segments' sums cost more than the idle
-// waves, but for a backward (two waves per SIMD at once) with a little more than one round.  us with n = 1, 2, 4, 8, 16:
-//     forward  256 waves of T 4096 420 340 176 139 127, 1280 of 4096 622 625 562 518 536, 1792 of 2048 319 376 367 376 394
-//     backward 576 of 1024 305 287 228 189 180, 1024 of 4096 1245 1112 1047 1055 1067, 1280 of 4096 1698 1608 1337 1308 1330,
-//              1792 of 2048 866 976 934 933 969, 2560 of 2048 1368 1277 1288 1313 1370, 3584 of 1024 854 878 905 950 1038
-// Packed sequences are of lengths that the host does not know: cut as if they were one in T tokens, but
-// where they are enough to fill half the chip only a sequence of more than T / 4 is cut.
+// waves, but for a backward (two waves per SIMD at once) with a little more than one round.  us with n = 1, 2, 4, 8, 16, 32, 64:
+//     forward  64 waves of T 8192 845 662 338 176 98 81 77, 256 of 4096 420 340 176 139 127 - -, of 8192 - - - 266 237 232 247,
+//              1280 of 4096 622 625 562 518 536, 1792 of 2048 319 376 367 376 394
+//     backward 128 of 4096 - - - 205 158 158 174, 576 of 1024 305 287 228 189 180, 1024 of 4096 1245 1112 1047 1055 1067,
+//              1280 of 4096 1698 1608 1337 1308 1330, 1792 of 2048 866 976 934 933 969, 2560 of 2048 1368 1277 1288 1313 1370,
+//              3584 of 1024 854 878 905 950 1038
+// Packed sequences are of lengths that the host does not know: pieces of T are what counts, and twice as many, but
+// where the sequences are enough to fill half the chip (backward: the chip) only one of more than T / 4 is cut.  n = 4, 16, 32, 64:
+//     backward of 5 sequences, T 8193, 64 waves each 650 293 177 178; of 17, 128 waves each 364 316 310 317, forward 127 197 140 137;
+//     of 17, 512 waves each (forward 1, 4, 8: 241 235 330) 904 988 1057 1140
 int segment_of(int N, int T, int C, int S, bool packed, bool halves, bool back) {
-    const int64_t waves = waves_of(N, C, S);
+    const int64_t waves = waves_of(N, C, S), each = waves_of(1, C, S);
     int64_t n = 1;
-    if (packed) n = waves > 2048 ? 4 : 4096 / waves_of(1, C, S);
-    else if (!halves && waves <= 1536) n = 8192 / waves > 8 ? 8192 / waves : 8;
+    if (packed) n = waves > (back ? 4096 : 2048) ? 4 : 8192 / each > 8 ? 8192 / each : 8;
+    else if (!halves && waves <= 1536) n = 4096 / waves > 8 ? 4096 / waves : 8;
     else if (back && waves > 2048 && waves <= 3 * 1024) n = 2;
-    if (n > 16) n = 16;
+    if (n > 64) n = 64;
     int64_t seg = n > 1 ? (T + n - 1) / n : T;
     if (seg < 64) seg = 64;
     if (seg > T) seg = T;
