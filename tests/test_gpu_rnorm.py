@@ -84,6 +84,35 @@ def test_shapes(rows, C, groups, od, iod, rd, wd):
     check(make(rows, C, od, iod, rd, wd, seed=C), groups)
 
 
+@pytest.mark.parametrize("od,iod,rd,wd", [TYPES[0], TYPES[2]])
+@pytest.mark.parametrize("rows,C", [(50, 9), (33, 15), (20, 71), (9, 129), (40, 255), (7, 513), (5, 1027), (6, 2051), (3, 4101), (2, 8189)])
+def test_last_vector_overlaps(rows, C, od, iod, rd, wd):
+    """Rows whose last eight channels begin inside another lane's: each channel counts once, in teams of every size."""
+    note(f"rn ragged rows{rows} C{C} {od} {iod}")
+    check(make(rows, C, od, iod, rd, wd, seed=C), norm="rms", norm2="rms")
+    check(make(rows, C, od, iod, rd, wd, seed=C + 1))
+
+
+@pytest.mark.parametrize("C", range(1, 9))
+def test_few_channels(C):
+    """Root-mean-square norms of 1 to 8 channels, and nothing is written beside the rows."""
+    note(f"rn C{C}")
+    for dtype in (F32, BF):
+        rows = 300
+        p = make(rows, C, dtype, dtype, dtype, seed=C)
+        d = {n: None if t is None else t.to(DEV) for n, t in p.items()}
+        bufs = [torch.full((rows * C + 64,), 7.0, dtype=dtype, device=DEV) for _ in range(2)]
+        r, h = (b[32:32 + rows * C].view(rows, C) for b in bufs)
+        if C == 8:
+            assert r.data_ptr() % 16 == 0
+        L.rn_fwd(d["o"], d["gate"], d["res"], **{n: d[n] for n in WS}, norm="rms", norm2="rms", r=r, h=h)
+        torch.cuda.synchronize()
+        wr, wh = ref_rn({n: None if p[n] is None else p[n].double() for n in ("o", "gate", "res", *WS)}, norm="rms", norm2="rms")
+        # a root mean square of a row loses nothing by cancellation; r's sum may, of terms of a few times its size
+        assert rel(r, wr) <= half_step(dtype) + 64 * E and rel(h, wh) <= half_step(dtype) + 256 * E
+        assert all((b[:32] == 7).all() and (b[-32:] == 7).all() for b in bufs)
+
+
 @pytest.mark.parametrize("norm", ["layer", "rms"])
 @pytest.mark.parametrize("norm2", ["layer", "rms", None])
 @pytest.mark.parametrize("act", ["silu", "sigmoid", None])
