@@ -37,7 +37,7 @@ wkv7_status dims_ok(int B, int T, int C, int S, int G) {
 // (packed: in all sequences together, if they are even).
 int64_t waves_of(int N, int C, int S) { return (int64_t)N * ((C + 15) / 16) * (S / 16); }
 
-// Tokens of a segment: a sequence is cut into n, at most 64, of 64 tokens at least.  Up to one and a half waves per SIMD
+// Tokens of a segment: a sequence is cut into n, at most 128, of 64 tokens at least.  Up to one and a half waves per SIMD
 // many short segments, which fill the last round of workgroups evenly; beyond, the segments' sums cost more than the idle
 // waves, but for a backward (two waves per SIMD at once) with a little more than one round.  us with n = 1, 2, 4, 8, 16, 32, 64:
 //     forward  64 waves of T 8192 845 662 338 176 98 81 77, 256 of 4096 420 340 176 139 127 - -, of 8192 - - - 266 237 232 247,
@@ -49,15 +49,18 @@ int64_t waves_of(int N, int C, int S) { return (int64_t)N * ((C + 15) / 16) * (S
 // where the sequences are enough to fill half the chip (backward: the chip) only one of more than T / 4 is cut.  n = 4, 16, 32, 64:
 //     backward of 5 sequences, T 8193, 64 waves each 650 293 177 178; of 17, 128 waves each 364 316 310 317, forward 127 197 140 137;
 //     of 17, 512 waves each (forward 1, 4, 8: 241 235 330) 904 988 1057 1140
+// Where even segments of 64 leave a wave for three quarters of the SIMDs at most they are of 32 (999 tokens of 320 channels, 32 states,
+// 6 sequences, forward and backward 27.7 + 50.6 -> 22.4 + 38.8; but 8 x 1024 of 256 channels 32.1 + 56.9 -> 37.5 + 65.5).
 int segment_of(int N, int T, int C, int S, bool packed, bool halves, bool back) {
     const int64_t waves = waves_of(N, C, S), each = waves_of(1, C, S);
     int64_t n = 1;
     if (packed) n = waves > (back ? 4096 : 2048) ? 4 : 8192 / each > 8 ? 8192 / each : 8;
     else if (!halves && waves <= 1536) n = 4096 / waves > 8 ? 4096 / waves : 8;
     else if (back && waves > 2048 && waves <= 3 * 1024) n = 2;
-    if (n > 64) n = 64;
+    if (n > 128) n = 128;
     int64_t seg = n > 1 ? (T + n - 1) / n : T;
-    if (seg < 64) seg = 64;
+    const int64_t least = T > 64 && (packed ? each : waves) * ((T + 63) / 64) <= 768 ? 32 : 64;
+    if (seg < least) seg = least;
     if (seg > T) seg = T;
     return (int)((seg + ssm::kBlock - 1) / ssm::kBlock * ssm::kBlock);
 }
