@@ -633,14 +633,13 @@ def _new_like(t, dtype):
     return torch.empty_like(t) if t.dtype == dtype and t.is_contiguous() else t.new_empty(t.shape, dtype=dtype)
 
 
-def _fresh_rows(shape, dtype, dev, N, fresh):
-    """A new token tensor.  With packed sequences (N > 0) the rows that none covers have to be
+def _fresh_rows(like, N, fresh):
+    """A new token tensor as `like`.  With packed sequences (N > 0) the rows that none covers have to be
     zeroed: its entry in `fresh` asks for that, or it is made of zeros where a row is no
     multiple of four bytes."""
-    import torch
-    t = torch.empty(shape, dtype=dtype, device=dev)
+    t = _new_like(like, like.dtype)
     if N:
-        if t.element_size() * (t.numel() // shape[1]) % 4:
+        if t.element_size() * (t.numel() // t.shape[1]) % 4:
             return t.zero_()
         fresh.append(t)
     return t

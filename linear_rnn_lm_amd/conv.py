@@ -75,7 +75,7 @@ def conv_fwd(x, weight, bias=None, h0=None, *, silu=True, cu_seqlens=None, want_
     _check_tensor(fn, "h0", h0, states, x.dtype, dev)
     fresh = []
     if y is None:
-        y = _fresh_rows((B, T, C), x.dtype, dev, N, fresh)
+        y = _fresh_rows(x, N, fresh)
     else:
         _check_tensor(fn, "y", y, (B, T, C), x.dtype, dev)
     if hT is not None:
@@ -105,7 +105,7 @@ def conv_bwd(dy, x, weight, bias=None, h0=None, dhT=None, *, silu=True, cu_seqle
     _check_tensor(fn, "dhT", dhT, states, x.dtype, dev)
     fresh = []
     if out is None:
-        dx = _fresh_rows((B, T, C), x.dtype, dev, N, fresh)
+        dx = _fresh_rows(x, N, fresh)
         dw = torch.empty((C, W), dtype=torch.float32, device=dev)
         db = None if bias is None else torch.empty((C,), dtype=torch.float32, device=dev)
     else:

@@ -164,10 +164,9 @@ def rn_bwd(dr, dh, o, gate, res, stats, *, weight=None, bias=None, scale=None, w
     _check_tensor(fn, "dr", dr, shape, r_dtype, dev)
     _check_tensor(fn, "dh", dh, shape, layer, dev)
     _check_tensor(fn, "stats", stats, (rows, 2 * groups + 2), torch.float32, dev)
-    new = lambda dt: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
-    do = new(o.dtype) if want_do else None
-    dgate = None if gate is None else new(layer)
-    dres = new(r_dtype) if res is not None and want_dres else None
+    do = torch.empty_like(o) if want_do else None
+    dgate = None if gate is None else _new_like(gate, layer)
+    dres = torch.empty_like(res) if res is not None and want_dres else None
     want_dw = want_dw and any(w is not None for _, w in ws)
     dw, need = None, 0
     if want_dw:

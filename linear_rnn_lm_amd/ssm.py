@@ -120,7 +120,7 @@ def ssm_fwd(x, dt, A, b, c, D=None, z=None, h0=None, *, dt_bias=None, softplus=T
     if y is not None:
         _check_tensor(fn, "y", y, (B, T, C), x.dtype, dev)
     elif want_y:
-        y = _fresh_rows((B, T, C), x.dtype, dev, N, fresh)
+        y = _fresh_rows(x, N, fresh)
     if ckpt is not None:
         _check_tensor(fn, "ckpt", ckpt, (nck // (4 * C * S), C, S), f32, dev)
     elif want_ckpt:
@@ -157,8 +157,7 @@ def ssm_bwd(dy, x, dt, A, b, c, ckpt, D=None, z=None, dhT=None, *, dt_bias=None,
             ("dz", (B, T, C), x.dtype, z), ("ddt_bias", (C,), f32, dt_bias))
     fresh = []
     if out is None:
-        out = [None if t is None else torch.empty(shape, dtype=dtype, device=dev) if dtype == f32 and len(shape) < 3
-               else _fresh_rows(shape, dtype, dev, N, fresh) for _, shape, dtype, t in want]
+        out = [None if t is None else torch.empty_like(t) if t.dim() < 3 else _fresh_rows(t, N, fresh) for *_, t in want]
     elif len(out) != 8:
         raise ValueError(f"{fn}: out must hold 8 entries, got {len(out)}")
     else:
