@@ -9,8 +9,8 @@
 // neighbouring lanes, so its sums are exchanges within a wave.  The backward
 // forms r again from what the forward read (res costs what r would), unrounded.
 //
-// 32768 rows of 2048 channels, 32 parts, fp32 o, the rest bf16: forward 150 us (5.4 TB/s), backward
-// 285 us (4.7 TB/s).  Rows of more than 4096 channels are the exception: a lane of 1024 has half the
+// 32768 rows of 2048 channels, 32 parts, fp32 o, the rest bf16: forward 165 us (4.9 TB/s), backward
+// 267 us (5.0 TB/s).  Rows of more than 4096 channels are the exception: a lane of 1024 has half the
 // registers, the backward spills some and takes three times what its bytes take.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
