@@ -81,7 +81,7 @@ def conv_fwd(x, weight, bias=None, h0=None, *, silu=True, cu_seqlens=None, want_
     if hT is not None:
         _check_tensor(fn, "hT", hT, states, x.dtype, dev)
     elif want_hT:
-        hT = torch.empty(states, dtype=x.dtype, device=dev)
+        hT = torch.empty(states, dtype=x.dtype, device=dev) if h0 is None else torch.empty_like(h0)
     _launch(fn, _lib().conv_fwd, dev, *dims, x.data_ptr(), ld, weight.data_ptr(), _ptr(bias), int(bool(silu)),
             _ptr(cu_seqlens), N, _ptr(h0), y.data_ptr(), _ptr(hT))
     if fresh:
@@ -106,8 +106,8 @@ def conv_bwd(dy, x, weight, bias=None, h0=None, dhT=None, *, silu=True, cu_seqle
     fresh = []
     if out is None:
         dx = _fresh_rows(x, N, fresh)
-        dw = torch.empty((C, W), dtype=torch.float32, device=dev)
-        db = None if bias is None else torch.empty((C,), dtype=torch.float32, device=dev)
+        dw = _new_like(weight, torch.float32)
+        db = None if bias is None else _new_like(bias, torch.float32)
     else:
         if len(out) != 3:
             raise ValueError(f"{fn}: out must hold 3 entries, got {len(out)}")

@@ -128,7 +128,7 @@ def ssm_fwd(x, dt, A, b, c, D=None, z=None, h0=None, *, dt_bias=None, softplus=T
     if hT is not None:
         _check_tensor(fn, "hT", hT, states, f32, dev)
     elif want_hT:
-        hT = torch.empty(states, dtype=f32, device=dev)
+        hT = torch.empty(states, dtype=f32, device=dev) if h0 is None else torch.empty_like(h0)
     workspace, wsb = _workspace(fn, workspace, nws, dev)
     _launch(fn, _lib().ssm_fwd, dev, *dims, code, *args, _ptr(cu_seqlens), N, _ptr(h0), _ptr(y), _ptr(ckpt), _ptr(hT),
             workspace.data_ptr(), wsb)
