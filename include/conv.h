@@ -33,7 +33,8 @@ extern "C" {
  */
 wkv7_status conv_fwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype w_dtype,
                      const void *x, int64_t x_ld, const void *weight, const void *bias, int silu,
-                     const int32_t *cu_seqlens, int N, const void *h0, void *y, void *hT, void *stream);
+                     const int32_t *cu_seqlens, int N, int zero_outside, const void *h0,
+                     void *y, void *hT, void *stream);
 
 /* Device workspace of conv_bwd.  0 for invalid shapes. */
 size_t conv_bwd_workspace_bytes(int B, int T, int C, int W, int N, int packed);
@@ -45,7 +46,7 @@ size_t conv_bwd_workspace_bytes(int B, int T, int C, int W, int N, int packed);
  */
 wkv7_status conv_bwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype w_dtype,
                      const void *dy, const void *dhT, const void *x, int64_t x_ld, const void *weight,
-                     const void *bias, int silu, const int32_t *cu_seqlens, int N, const void *h0,
+                     const void *bias, int silu, const int32_t *cu_seqlens, int N, int zero_outside, const void *h0,
                      void *dx, float *dweight, float *dbias, void *dh0,
                      void *workspace, size_t workspace_bytes, void *stream);
 

@@ -25,8 +25,8 @@
  *   the tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1, and may be empty (its final state is
  *   its initial one).  Offsets are not checked on the host; offsets out of range or
  *   decreasing give unspecified results, but no access outside the tensors.  Tokens outside
- *   every sequence are neither read nor written: their rows of y and of the token gradients
- *   stay as they were.
+ *   every sequence are not read; their rows of y and of the token gradients stay as they were, or
+ *   are set to zero with zero_outside.
  * - delta A should be at most 0; the states grow without bound otherwise.  A delta of 0
  *   passes the state on as it is.  A NaN or Inf in x, dt or z spoils its channel of its
  *   sequence only, from its token on, in b or c every channel of the group; in the
@@ -70,7 +70,7 @@ wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype,
                     const void *x, int64_t x_ld, const void *dt, int64_t dt_ld, const float *A,
                     const void *b, int64_t b_ld, const void *c, int64_t c_ld, const float *D,
                     const void *z, int64_t z_ld, const float *dt_bias, int softplus,
-                    const int32_t *cu_seqlens, int N, const float *h0, void *y, float *ckpt, float *hT,
+                    const int32_t *cu_seqlens, int N, int zero_outside, const float *h0, void *y, float *ckpt, float *hT,
                     void *workspace, size_t workspace_bytes, void *stream);
 
 /*
@@ -86,7 +86,7 @@ wkv7_status ssm_bwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype,
                     const void *x, int64_t x_ld, const void *dt, int64_t dt_ld, const float *A,
                     const void *b, int64_t b_ld, const void *c, int64_t c_ld, const float *D,
                     const void *z, int64_t z_ld, const float *dt_bias, int softplus,
-                    const int32_t *cu_seqlens, int N, const float *ckpt,
+                    const int32_t *cu_seqlens, int N, int zero_outside, const float *ckpt,
                     void *dx, void *ddt, float *dA, void *db, void *dc, float *dD, void *dz, float *ddt_bias,
                     float *dh0, void *workspace, size_t workspace_bytes, void *stream);
 

@@ -633,18 +633,6 @@ def _new_like(t, dtype):
     return torch.empty_like(t) if t.dtype == dtype and t.is_contiguous() else t.new_empty(t.shape, dtype=dtype)
 
 
-def _fresh_rows(like, N, fresh):
-    """A new token tensor as `like`.  With packed sequences (N > 0) the rows that none covers have to be
-    zeroed: its entry in `fresh` asks for that, or it is made of zeros where a row is no
-    multiple of four bytes."""
-    t = _new_like(like, like.dtype)
-    if N:
-        if t.element_size() * (t.numel() // t.shape[1]) % 4:
-            return t.zero_()
-        fresh.append(t)
-    return t
-
-
 # The operators beside the recurrence; their modules use the helpers above.
 from .gdr import GDR, GDR_CHUNK, gdr_bwd, gdr_fwd, gdr_step  # noqa: E402
 from .lnorm import LN, ln_bwd, ln_fwd  # noqa: E402

@@ -21,9 +21,9 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import (_check_bytes, _dense, _fresh_rows, _launch, _LazyOpOf, _new_like, _ptr, _row_ld, _rows, _types, _where,
+from . import (_check_bytes, _dense, _launch, _LazyOpOf, _new_like, _ptr, _row_ld, _rows, _types, _where,
                lib)
-from .gdr import _check_cu, _zero_outside
+from .gdr import _check_cu
 from .ssm import _check_tensor
 
 
@@ -32,9 +32,9 @@ def _lib():
     L = lib()
     vp, i, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
     dims = [i] * 6
-    L.conv_fwd.argtypes = dims + [vp, i64, vp, vp, i, vp, i] + [vp] * 4
+    L.conv_fwd.argtypes = dims + [vp, i64, vp, vp, i, vp, i, i] + [vp] * 4
     L.conv_bwd_workspace_bytes.argtypes, L.conv_bwd_workspace_bytes.restype = [i] * 6, sz
-    L.conv_bwd.argtypes = dims + [vp] * 3 + [i64, vp, vp, i, vp, i] + [vp] * 6 + [sz, vp]
+    L.conv_bwd.argtypes = dims + [vp] * 3 + [i64, vp, vp, i, vp, i, i] + [vp] * 6 + [sz, vp]
     L.conv_step.argtypes = dims + [vp, i64, vp, vp, i, vp, i] + [vp] * 4
     for n in ("conv_fwd", "conv_bwd", "conv_step"):
         getattr(L, n).restype = i
@@ -73,9 +73,9 @@ def conv_fwd(x, weight, bias=None, h0=None, *, silu=True, cu_seqlens=None, want_
     N = _check_cu(fn, cu_seqlens, B, dev)
     states = (N or B, W - 1, C)
     _check_tensor(fn, "h0", h0, states, x.dtype, dev)
-    fresh = []
-    if y is None:
-        y = _fresh_rows(x, N, fresh)
+    fresh = int(y is None)                                 # of a new y the rows outside packed sequences are zeroed
+    if fresh:
+        y = _new_like(x, x.dtype)
     else:
         _check_tensor(fn, "y", y, (B, T, C), x.dtype, dev)
     if hT is not None:
@@ -83,9 +83,7 @@ def conv_fwd(x, weight, bias=None, h0=None, *, silu=True, cu_seqlens=None, want_
     elif want_hT:
         hT = torch.empty(states, dtype=x.dtype, device=dev) if h0 is None else torch.empty_like(h0)
     _launch(fn, _lib().conv_fwd, dev, *dims, x.data_ptr(), ld, weight.data_ptr(), _ptr(bias), int(bool(silu)),
-            _ptr(cu_seqlens), N, _ptr(h0), y.data_ptr(), _ptr(hT))
-    if fresh:
-        _zero_outside(cu_seqlens, N, T, fresh)
+            _ptr(cu_seqlens), N, fresh, _ptr(h0), y.data_ptr(), _ptr(hT))
     return y, hT
 
 
@@ -103,9 +101,9 @@ def conv_bwd(dy, x, weight, bias=None, h0=None, dhT=None, *, silu=True, cu_seqle
     _check_tensor(fn, "dy", dy, (B, T, C), x.dtype, dev)
     _check_tensor(fn, "h0", h0, states, x.dtype, dev)
     _check_tensor(fn, "dhT", dhT, states, x.dtype, dev)
-    fresh = []
-    if out is None:
-        dx = _fresh_rows(x, N, fresh)
+    fresh = int(out is None)
+    if fresh:
+        dx = _new_like(x, x.dtype)
         dw = _new_like(weight, torch.float32)
         db = None if bias is None else _new_like(bias, torch.float32)
     else:
@@ -124,10 +122,8 @@ def conv_bwd(dy, x, weight, bias=None, h0=None, dhT=None, *, silu=True, cu_seqle
     else:
         _check_bytes(fn, "workspace", workspace, need, dev)
     _launch(fn, _lib().conv_bwd, dev, *dims, dy.data_ptr(), _ptr(dhT), x.data_ptr(), ld, weight.data_ptr(), _ptr(bias),
-            int(bool(silu)), _ptr(cu_seqlens), N, _ptr(h0), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(dh0),
+            int(bool(silu)), _ptr(cu_seqlens), N, fresh, _ptr(h0), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(dh0),
             workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    if fresh:
-        _zero_outside(cu_seqlens, N, T, fresh)
     return dx, dw, db, dh0
 
 

@@ -38,7 +38,9 @@ struct Args {
     int64_t x_ld;
     const int* cu;
     int silu, B, T, C, N, run, runs;   // tokens of a run, run slots
+    int zero;                          // rows outside the sequences are zeroed
     bool wbf16;   // filters in bf16
+    uint32_t zero_from;                // the workgroups from this one on zero rows outside the sequences
 };
 
 struct StepArgs {
@@ -141,6 +143,10 @@ __device__ __forceinline__ void load_window(const T* x, int64_t x_ld, const T* h
 
 template <typename T, int W, int VEC>
 __global__ __launch_bounds__(NT) void fwd_kernel(Args p) {
+    if (blockIdx.x >= p.zero_from) {
+        zero_outside(Seqs{p.cu, p.N, p.T}, p.y, (int64_t)p.C * sizeof(T), (int64_t)(blockIdx.x - p.zero_from) * NT + threadIdx.x);
+        return;
+    }
     const int CV = (p.C + VEC - 1) / VEC;
     const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
     const int slot = (int)(id / CV), c = min((int)(id % CV) * VEC, p.C - VEC);
@@ -197,6 +203,10 @@ __global__ __launch_bounds__(NT) void fwd_kernel(Args p) {
 // dx_q = sum_j w_j ds_(q + W - 1 - j), and for q before the first token that is dh0.
 template <typename T, int W, int VEC>
 __global__ __launch_bounds__(NT) void bwd_kernel(Args p) {
+    if (blockIdx.x >= p.zero_from) {
+        zero_outside(Seqs{p.cu, p.N, p.T}, p.dx, (int64_t)p.C * sizeof(T), (int64_t)(blockIdx.x - p.zero_from) * NT + threadIdx.x);
+        return;
+    }
     const int CV = (p.C + VEC - 1) / VEC;
     const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
     const int slot = (int)(id / CV), c = min((int)(id % CV) * VEC, p.C - VEC);
@@ -391,9 +401,11 @@ hipError_t run(const Args& a, int what, hipStream_t s) {
     constexpr int BV = VEC > 4 ? 4 : VEC;      // the backward by four channels: its sums and windows are many registers
     const int BW = what == kFwd ? VEC : BV;
     const int64_t threads = (int64_t)a.runs * ((a.C + BW - 1) / BW);
-    const dim3 grid((uint32_t)((threads + NT - 1) / NT));
-    if (what == kFwd) hipLaunchKernelGGL((fwd_kernel<T, W, VEC>), grid, dim3(NT), 0, s, a);
-    else hipLaunchKernelGGL((bwd_kernel<T, W, BV>), grid, dim3(NT), 0, s, a);
+    Args b = a;
+    b.zero_from = (uint32_t)((threads + NT - 1) / NT);
+    const dim3 grid(b.zero_from + (a.cu && a.zero ? kZeroBlocks : 0));
+    if (what == kFwd) hipLaunchKernelGGL((fwd_kernel<T, W, VEC>), grid, dim3(NT), 0, s, b);
+    else hipLaunchKernelGGL((bwd_kernel<T, W, BV>), grid, dim3(NT), 0, s, b);
     return hipGetLastError();
 }
 template <typename T, int W, int VEC>
@@ -461,8 +473,8 @@ int64_t span(int64_t rows, int64_t ld, int64_t C, int e) { return ((rows - 1) * 
 extern "C" {
 
 wkv7_status conv_fwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype w_dtype, const void* x, int64_t x_ld,
-                     const void* weight, const void* bias, int silu, const int32_t* cu_seqlens, int N, const void* h0,
-                     void* y, void* hT, void* stream) {
+                     const void* weight, const void* bias, int silu, const int32_t* cu_seqlens, int N, int zero_outside,
+                     const void* h0, void* y, void* hT, void* stream) {
     using namespace conv;
     if (!is_dtype(x_dtype) || !is_dtype(w_dtype)) return WKV7_ERR_DTYPE;
     const bool packed = cu_seqlens != nullptr;
@@ -480,6 +492,7 @@ wkv7_status conv_fwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype 
     Args a = {};
     a.x = x; a.w = weight; a.bias = bias; a.h0 = h0; a.y = y; a.hT = hT; a.x_ld = x_ld; a.cu = cu_seqlens;
     a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16;
+    a.zero = zero_outside;
     a.run = run_of(tokens, C);
     a.runs = (int)runs_of(B, T, N, packed, a.run);
     return launch(a, W, x_dtype == WKV7_BF16, kFwd, static_cast<hipStream_t>(stream)) == hipSuccess ? WKV7_OK
@@ -493,7 +506,7 @@ size_t conv_bwd_workspace_bytes(int B, int T, int C, int W, int N, int packed) {
 
 wkv7_status conv_bwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype w_dtype, const void* dy,
                      const void* dhT, const void* x, int64_t x_ld, const void* weight, const void* bias, int silu,
-                     const int32_t* cu_seqlens, int N, const void* h0, void* dx, float* dweight, float* dbias, void* dh0,
+                     const int32_t* cu_seqlens, int N, int zero_outside, const void* h0, void* dx, float* dweight, float* dbias, void* dh0,
                      void* workspace, size_t workspace_bytes, void* stream) {
     using namespace conv;
     if (!is_dtype(x_dtype) || !is_dtype(w_dtype)) return WKV7_ERR_DTYPE;
@@ -516,6 +529,7 @@ wkv7_status conv_bwd(int B, int T, int C, int W, wkv7_dtype x_dtype, wkv7_dtype 
     Args a = {};
     a.x = x; a.w = weight; a.bias = bias; a.h0 = h0; a.dy = dy; a.dhT = dhT; a.dx = dx; a.dh0 = dh0; a.x_ld = x_ld;
     a.cu = cu_seqlens; a.silu = silu; a.B = B; a.T = T; a.C = C; a.N = packed ? N : B; a.wbf16 = w_dtype == WKV7_BF16;
+    a.zero = zero_outside;
     a.run = run_of(tokens, C);
     a.runs = (int)runs_of(B, T, N, packed, a.run);
     a.part = static_cast<float*>(workspace);

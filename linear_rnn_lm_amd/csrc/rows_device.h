@@ -111,6 +111,26 @@ __device__ __forceinline__ bool slot_piece(const Seqs& s, int slot, int len, int
     return i == 0 || (i > 0 && (int64_t)i * len < L);
 }
 
+// Zeroes the rows of a token tensor that no packed sequence covers; by `count` threads, this one is number i.
+template <typename U>
+__device__ __forceinline__ void zero_span(void* base, int64_t from, int64_t to, int64_t i, int64_t count) {
+    U* p = static_cast<U*>(base);
+    for (int64_t u = from / sizeof(U) + i; u < to / (int64_t)sizeof(U); u += count) p[u] = U{};
+}
+constexpr int kZeroBlocks = 128;   // workgroups of 256 that do so, behind those of a launch
+__device__ __forceinline__ void zero_outside(const Seqs& s, void* base, int64_t row_bytes, int64_t i) {
+    const int a = min(max(s.cu[0], 0), s.T), b = min(max(s.cu[s.N], a), s.T);
+    constexpr int64_t count = kZeroBlocks * 256;
+    const int64_t any = reinterpret_cast<intptr_t>(base) | row_bytes;
+    const int64_t from[2] = {0, b * row_bytes}, to[2] = {a * row_bytes, s.T * row_bytes};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (any % 16 == 0) zero_span<uint4>(base, from[k], to[k], i, count);
+        else if (any % 4 == 0) zero_span<uint32_t>(base, from[k], to[k], i, count);
+        else zero_span<uint16_t>(base, from[k], to[k], i, count);
+    }
+}
+
 // Piece k of N <= 64 packed sequences, counted from the longest sequence to the shortest: a sequence to a
 // lane, each adds up the pieces before its own.  False if there are fewer.
 __device__ __forceinline__ bool by_length(const Seqs& s, int k, int piece_len, int& n, int& i) {

@@ -134,7 +134,7 @@ size_t ssm_bwd_workspace_bytes(int B, int T, int C, int S, int G, int N, int pac
 wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, const void* x, int64_t x_ld, const void* dt,
                     int64_t dt_ld, const float* A, const void* b, int64_t b_ld, const void* c, int64_t c_ld,
                     const float* D, const void* z, int64_t z_ld, const float* dt_bias, int softplus,
-                    const int32_t* cu_seqlens, int N, const float* h0, void* y, float* ckpt, float* hT, void* workspace,
+                    const int32_t* cu_seqlens, int N, int zero_outside, const float* h0, void* y, float* ckpt, float* hT, void* workspace,
                     size_t workspace_bytes, void* stream) {
     if (in_dtype != WKV7_F32 && in_dtype != WKV7_BF16) return WKV7_ERR_DTYPE;
     Shape s;
@@ -159,6 +159,7 @@ wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     a.z_ld = z_ld; a.A = A; a.D = D; a.dt_bias = dt_bias; a.h0 = h0; a.y = y; a.ckpt = ckpt; a.hT = hT; a.cu = cu_seqlens;
     a.softplus = softplus; a.B = B; a.T = T; a.C = C; a.S = S; a.G = G; a.N = s.N; a.seg = s.seg[0]; a.segs = s.segs[0];
     a.split = s.split[0];
+    a.zero = cu_seqlens && y && zero_outside;
     // h0 in place: every segment starts from h0, the last one writes hT, so they read a copy
     if (a.split && h0 && h0 == hT) a.h0_copy = static_cast<float*>(workspace);
     a.sum_h = static_cast<float*>(workspace) + s.state;
@@ -174,7 +175,7 @@ wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
 wkv7_status ssm_bwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, const void* dy, const float* dhT,
                     const void* x, int64_t x_ld, const void* dt, int64_t dt_ld, const float* A, const void* b,
                     int64_t b_ld, const void* c, int64_t c_ld, const float* D, const void* z, int64_t z_ld,
-                    const float* dt_bias, int softplus, const int32_t* cu_seqlens, int N, const float* ckpt, void* dx,
+                    const float* dt_bias, int softplus, const int32_t* cu_seqlens, int N, int zero_outside, const float* ckpt, void* dx,
                     void* ddt, float* dA, void* db, void* dc, float* dD, void* dz, float* ddt_bias, float* dh0,
                     void* workspace, size_t workspace_bytes, void* stream) {
     if (in_dtype != WKV7_F32 && in_dtype != WKV7_BF16) return WKV7_ERR_DTYPE;
@@ -211,6 +212,8 @@ wkv7_status ssm_bwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     ssm::ReduceArgs r = {};
     r.part = a.part; r.part_bc = a.part_bc;
     r.dA = dA; r.dD = dD; r.ddt_bias = ddt_bias; r.db = db; r.dc = dc; r.cu = cu_seqlens;
+    r.zero = cu_seqlens && zero_outside;
+    r.dx = dx; r.ddt = ddt; r.dz = dz;
     r.B = B; r.T = T; r.C = C; r.S = S; r.G = G; r.N = s.N; r.segs = s.segs[1];
     hipStream_t hs = static_cast<hipStream_t>(stream);
     hipError_t err = a.split ? ssm::launch_segments(a, in_dtype == WKV7_BF16, true, hs) : hipSuccess;

@@ -303,10 +303,20 @@ __global__ __launch_bounds__(64 * WN * WC, 2) void bwd_kernel(Args p, int blocks
 // db and dc of every token in a sequence: sums over the channel blocks of a group, four neighbours to a
 // thread.  Bound by HBM: the parts are the most that the gradient kernel writes.
 template <typename InT>
-__global__ __launch_bounds__(256) void bc_kernel(ReduceArgs p, int blocks) {
+__global__ __launch_bounds__(256) void bc_kernel(ReduceArgs p, int blocks, uint32_t zero_from) {
+    if (blockIdx.x >= zero_from) {                         // rows outside the sequences
+        const Seqs seqs{p.cu, p.N, p.T};
+        const int64_t at = (int64_t)(blockIdx.x - zero_from) * 256 + threadIdx.x, row = (int64_t)p.C * sizeof(InT);
+        zero_outside(seqs, p.dx, row, at);
+        zero_outside(seqs, p.ddt, row, at);
+        if (p.dz) zero_outside(seqs, p.dz, row, at);
+        zero_outside(seqs, p.db, (int64_t)p.G * p.S * sizeof(InT), at);
+        zero_outside(seqs, p.dc, (int64_t)p.G * p.S * sizeof(InT), at);
+        return;
+    }
     const int64_t tokens = (int64_t)p.B * p.T, all = tokens * p.G * (p.S / 2);
     const int per = p.G > 1 ? blocks / p.G : blocks;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)zero_from * 256) {
         const int e = (int)(i % (p.S / 2)) * 4, g = (int)(i / (p.S / 2) % p.G);
         const int64_t t = i / (p.S / 2) / p.G;
         if (p.cu && (t < p.cu[0] || t >= p.cu[p.N])) continue;
@@ -350,9 +360,10 @@ hipError_t launch_reduce(const ReduceArgs& a, bool bf16, hipStream_t s) {
     if (e != hipSuccess) return e;
     const int blocks = (a.C + chans(a.S) - 1) / chans(a.S);
     const int64_t n = (int64_t)a.B * a.T * a.G * (a.S / 2);
-    const dim3 grid((uint32_t)((n + 255) / 256 < 1 << 20 ? (n + 255) / 256 : 1 << 20));   // fewer than 2^32 threads
-    if (bf16) hipLaunchKernelGGL(bc_kernel<uint16_t>, grid, dim3(256), 0, s, a, blocks);
-    else hipLaunchKernelGGL(bc_kernel<float>, grid, dim3(256), 0, s, a, blocks);
+    const uint32_t main = (uint32_t)((n + 255) / 256 < 1 << 20 ? (n + 255) / 256 : 1 << 20);     // fewer than 2^32 threads
+    const dim3 grid(main + (a.zero ? kZeroBlocks : 0));
+    if (bf16) hipLaunchKernelGGL(bc_kernel<uint16_t>, grid, dim3(256), 0, s, a, blocks, main);
+    else hipLaunchKernelGGL(bc_kernel<float>, grid, dim3(256), 0, s, a, blocks, main);
     return hipGetLastError();
 }
 

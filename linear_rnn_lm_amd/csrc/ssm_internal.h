@@ -23,6 +23,7 @@ struct Args {
     int softplus, B, T, C, S, G, N;
     int seg, segs;   // tokens of a segment (a multiple of kBlock) and segment slots
     bool split;      // whether a sequence may have more than one segment
+    bool zero;       // rows of y outside the sequences are zeroed
     bool halves, halves_sums;   // S = 16, forward and segments' sums: two states to a lane
 };
 
@@ -44,11 +45,13 @@ struct ReduceArgs {
     void *db, *dc;
     const int* cu;
     int B, T, C, S, G, N, segs;
+    bool zero;       // rows of these and of db, dc outside the sequences are zeroed
+    void *dx, *ddt, *dz;
 };
 
 // With several segments to a sequence (split): their sums first, then all segments at once.
 hipError_t launch_segments(const Args& a, bool bf16, bool backward, hipStream_t s);
-hipError_t launch_fwd(const Args& a, bool bf16, hipStream_t s);
+hipError_t launch_fwd(const Args& a, bool bf16, hipStream_t s);      // y's rows outside the sequences too
 hipError_t launch_bwd(const Args& a, bool bf16, hipStream_t s);
 hipError_t launch_reduce(const ReduceArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_step(const StepArgs& a, bool bf16, hipStream_t s);

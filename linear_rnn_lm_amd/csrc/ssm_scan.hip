@@ -342,6 +342,10 @@ __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int block
     }
 }
 
+__global__ __launch_bounds__(256) void zero_kernel(Args p, int64_t row_bytes) {
+    zero_outside(Seqs{p.cu, p.N, p.T}, p.y, row_bytes, (int64_t)blockIdx.x * 256 + threadIdx.x);
+}
+
 enum What { kFwd, kSums, kSumsBack };
 
 template <typename InT, int NS, int WN, int WC>
@@ -371,6 +375,11 @@ hipError_t launch(const Args& a, bool bf16, What what, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_segments(const Args& a, bool bf16, bool bwd, hipStream_t s) { return launch(a, bf16, bwd ? kSumsBack : kSums, s); }
-hipError_t launch_fwd(const Args& a, bool bf16, hipStream_t s) { return launch(a, bf16, kFwd, s); }
+hipError_t launch_fwd(const Args& a, bool bf16, hipStream_t s) {
+    const hipError_t e = launch(a, bf16, kFwd, s);
+    if (e != hipSuccess || !a.zero) return e;
+    hipLaunchKernelGGL(zero_kernel, dim3(kZeroBlocks), dim3(256), 0, s, a, (int64_t)a.C * (bf16 ? 2 : 4));
+    return hipGetLastError();
+}
 
 }  // namespace ssm

@@ -28,9 +28,9 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import (_check_bytes, _dense, _dense_on, _fresh_rows, _launch, _LazyOpOf, _new_like, _ptr, _row_ld, _rows, _types,
-               _where, lib)
-from .gdr import _check_cu, _zero_outside
+from . import (_check_bytes, _dense, _dense_on, _launch, _LazyOpOf, _new_like, _ptr, _row_ld, _rows, _types, _where,
+               lib)
+from .gdr import _check_cu
 
 SSM_BLOCK = 16
 
@@ -44,8 +44,8 @@ def _lib():
     L.ssm_slots.argtypes, L.ssm_slots.restype = [i] * 4, i64
     for n in ("ssm_ckpt_bytes", "ssm_fwd_workspace_bytes", "ssm_bwd_workspace_bytes"):
         getattr(L, n).argtypes, getattr(L, n).restype = dims + [i] * 2, sz
-    L.ssm_fwd.argtypes = dims + [i] + ins + [vp, i] + [vp] * 4 + [vp, sz, vp]
-    L.ssm_bwd.argtypes = dims + [i] + [vp] * 2 + ins + [vp, i] + [vp] * 10 + [vp, sz, vp]
+    L.ssm_fwd.argtypes = dims + [i] + ins + [vp, i, i] + [vp] * 4 + [vp, sz, vp]
+    L.ssm_bwd.argtypes = dims + [i] + [vp] * 2 + ins + [vp, i, i] + [vp] * 10 + [vp, sz, vp]
     L.ssm_step.argtypes = dims + [i] + ins + [vp, i] + [vp] * 4
     for n in ("ssm_fwd", "ssm_bwd", "ssm_step"):
         getattr(L, n).restype = i
@@ -116,11 +116,11 @@ def ssm_fwd(x, dt, A, b, c, D=None, z=None, h0=None, *, dt_bias=None, softplus=T
     nck, nws, _ = _sizes(dims, N)
     states = (N or B, C, S)
     _check_tensor(fn, "h0", h0, states, f32, dev)
-    fresh = []
+    fresh = 0                                              # of a new y the rows outside packed sequences are zeroed
     if y is not None:
         _check_tensor(fn, "y", y, (B, T, C), x.dtype, dev)
     elif want_y:
-        y = _fresh_rows(x, N, fresh)
+        y, fresh = _new_like(x, x.dtype), 1
     if ckpt is not None:
         _check_tensor(fn, "ckpt", ckpt, (nck // (4 * C * S), C, S), f32, dev)
     elif want_ckpt:
@@ -130,10 +130,8 @@ def ssm_fwd(x, dt, A, b, c, D=None, z=None, h0=None, *, dt_bias=None, softplus=T
     elif want_hT:
         hT = torch.empty(states, dtype=f32, device=dev) if h0 is None else torch.empty_like(h0)
     workspace, wsb = _workspace(fn, workspace, nws, dev)
-    _launch(fn, _lib().ssm_fwd, dev, *dims, code, *args, _ptr(cu_seqlens), N, _ptr(h0), _ptr(y), _ptr(ckpt), _ptr(hT),
-            workspace.data_ptr(), wsb)
-    if fresh:
-        _zero_outside(cu_seqlens, N, T, fresh)
+    _launch(fn, _lib().ssm_fwd, dev, *dims, code, *args, _ptr(cu_seqlens), N, fresh, _ptr(h0), _ptr(y), _ptr(ckpt),
+            _ptr(hT), workspace.data_ptr(), wsb)
     return y, ckpt, hT
 
 
@@ -155,9 +153,9 @@ def ssm_bwd(dy, x, dt, A, b, c, ckpt, D=None, z=None, dhT=None, *, dt_bias=None,
     want = (("dx", (B, T, C), x.dtype, x), ("ddt", (B, T, C), x.dtype, dt), ("dA", (C, S), f32, A),
             ("db", (B, T, G, S), x.dtype, b), ("dc", (B, T, G, S), x.dtype, c), ("dD", (C,), f32, D),
             ("dz", (B, T, C), x.dtype, z), ("ddt_bias", (C,), f32, dt_bias))
-    fresh = []
+    fresh = int(out is None)                               # of new gradients the rows outside packed sequences are zeroed
     if out is None:
-        out = [None if t is None else torch.empty_like(t) if t.dim() < 3 else _fresh_rows(t, N, fresh) for *_, t in want]
+        out = [None if t is None else _new_like(t, t.dtype) for *_, t in want]
     elif len(out) != 8:
         raise ValueError(f"{fn}: out must hold 8 entries, got {len(out)}")
     else:
@@ -167,10 +165,8 @@ def ssm_bwd(dy, x, dt, A, b, c, ckpt, D=None, z=None, dhT=None, *, dt_bias=None,
             _check_tensor(fn, n, o, shape, dtype, dev)
     dh0 = torch.empty(states, dtype=f32, device=dev) if want_dh0 else None
     workspace, wsb = _workspace(fn, workspace, nws, dev)
-    _launch(fn, _lib().ssm_bwd, dev, *dims, code, dy.data_ptr(), _ptr(dhT), *args, _ptr(cu_seqlens), N, ckpt.data_ptr(),
-            *map(_ptr, out), _ptr(dh0), workspace.data_ptr(), wsb)
-    if fresh:
-        _zero_outside(cu_seqlens, N, T, fresh)
+    _launch(fn, _lib().ssm_bwd, dev, *dims, code, dy.data_ptr(), _ptr(dhT), *args, _ptr(cu_seqlens), N, fresh,
+            ckpt.data_ptr(), *map(_ptr, out), _ptr(dh0), workspace.data_ptr(), wsb)
     return (*out, dh0)
 
 

@@ -149,3 +149,24 @@ def test_captured_token(dtype):
             want = step(other)
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip((*outs, *pools), (*want, *other))), i
+
+
+@pytest.mark.parametrize("C,dtype", [(64, F32), (67, BF), (66, BF), (21, F32)])
+def test_new_rows_outside_sequences_are_zero(C, dtype):
+    """New outputs in memory that held other values: most of the row is padding, before and behind the sequences."""
+    note(f"mix: rows outside C{C} {dtype}")
+    T, S, cu = 400, 16, torch.tensor([37, 60, 60, 131], dtype=torch.int32, device=DEV)
+    gen = torch.Generator().manual_seed(6)
+    rn = lambda *s: torch.randn(*s, generator=gen).to(dtype).to(DEV)  # noqa: E731
+    x, dt, z, dy, b, c = rn(1, T, C), rn(1, T, C), rn(1, T, C), rn(1, T, C), rn(1, T, 1, S), rn(1, T, 1, S)
+    A, w = -torch.rand(C, S, generator=gen).to(DEV), rn(C, 4)
+    torch.cuda.synchronize()
+    stale = [torch.full((1, T, n), float("nan"), dtype=dtype, device=DEV) for n in (C, C, C, C, C, C, S, S)]
+    del stale
+    y, ckpt, _ = L.ssm_fwd(x, dt, A, b, c, None, z, cu_seqlens=cu)
+    dx, ddt, _, db, dc, _, dz, _, _ = L.ssm_bwd(dy, x, dt, A, b, c, ckpt, None, z, cu_seqlens=cu)
+    v, _ = L.conv_fwd(x, w, cu_seqlens=cu)
+    dv = L.conv_bwd(dy, x, w, cu_seqlens=cu)[0]
+    torch.cuda.synchronize()
+    for n, t in dict(y=y, dx=dx, ddt=ddt, dz=dz, db=db, dc=dc, v=v, dv=dv).items():
+        assert (t[:, :37] == 0).all() and (t[:, 131:] == 0).all() and t.isfinite().all() and t[:, 37:131].any(), n

@@ -78,9 +78,9 @@ def call(fn, base, over):
 def test_ssm_entry_points_reject_bad_arguments():
     lib = ssm._lib()
     dims = dict(B=1, T=40, C=64, S=16, G=1, t=1)
-    f = lambda **o: call(lib.ssm_fwd, dict(**dims, **ins(), cu=None, N=0, h0=None, y=fake(8), ck=fake(9), hT=fake(10),  # noqa: E731
+    f = lambda **o: call(lib.ssm_fwd, dict(**dims, **ins(), cu=None, N=0, zo=0, h0=None, y=fake(8), ck=fake(9), hT=fake(10),  # noqa: E731
                                            ws=fake(11), wsb=1 << 24), o)
-    g = lambda **o: call(lib.ssm_bwd, dict(**dims, dy=fake(8), dhT=None, **ins(), cu=None, N=0, ck=fake(9), dx=fake(10),  # noqa: E731
+    g = lambda **o: call(lib.ssm_bwd, dict(**dims, dy=fake(8), dhT=None, **ins(), cu=None, N=0, zo=0, ck=fake(9), dx=fake(10),  # noqa: E731
                                            ddt=fake(11), dA=fake(12), db=fake(13), dc=fake(14), dD=fake(15), dz=fake(16),
                                            dbias=fake(17), dh0=fake(18), ws=fake(19), wsb=1 << 24), o)
     s = lambda **o: call(lib.ssm_step, dict(**dims, **ins(), slots=None, P=1, st=fake(8), so=fake(9), y=fake(10)), o)  # noqa: E731
@@ -113,8 +113,8 @@ def test_conv_entry_points_reject_bad_arguments():
     lib = conv._lib()
     dims = dict(B=1, T=40, C=64, W=4, t=1, wt=0)
     x = dict(x=fake(0), xl=64, w=fake(1), bias=fake(2), silu=1)
-    f = lambda **o: call(lib.conv_fwd, dict(**dims, **x, cu=None, N=0, h0=fake(3), y=fake(4), hT=fake(5)), o)  # noqa: E731
-    g = lambda **o: call(lib.conv_bwd, dict(**dims, dy=fake(6), dhT=None, **x, cu=None, N=0, h0=fake(3), dx=fake(7),  # noqa: E731
+    f = lambda **o: call(lib.conv_fwd, dict(**dims, **x, cu=None, N=0, zo=0, h0=fake(3), y=fake(4), hT=fake(5)), o)  # noqa: E731
+    g = lambda **o: call(lib.conv_bwd, dict(**dims, dy=fake(6), dhT=None, **x, cu=None, N=0, zo=0, h0=fake(3), dx=fake(7),  # noqa: E731
                                             dw=fake(8), db=fake(9), dh0=fake(10), ws=fake(11), wsb=1 << 24), o)
     s = lambda **o: call(lib.conv_step, dict(**dims, **x, slots=None, P=1, st=fake(3), so=fake(4), y=fake(5)), o)  # noqa: E731
     for c in (f, g, s):
