@@ -184,7 +184,7 @@ __global__ __launch_bounds__(NT) void fwd_kernel(Args p) {
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) s[e] = fmaf(f[j][e], widen(win[j].v[e]), s[e]);
                 s[e] = fmaf(f[W - 1][e], widen(cur[i].v[e]), s[e]);
-                if (p.silu) s[e] *= sigmoid(s[e]);
+                if (p.silu) s[e] *= sigmoid_for<T>(s[e]);
             }
             store_as(y + (int64_t)(t0 + i) * p.C, s);
 #pragma unroll
@@ -382,7 +382,7 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) s[e] = fmaf(f[j][e], widen(win[j].v[e]), s[e]);
                 s[e] = fmaf(f[W - 1][e], widen(cur.v[e]), s[e]);
-                if (p.silu) s[e] *= sigmoid(s[e]);
+                if (p.silu) s[e] *= sigmoid_for<T>(s[e]);
             }
             store_as(y + tok * p.C, s, twice);
 #pragma unroll

@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * WN * WC, Ahead<NS>::waves) void fwd_kernel(Arg
         }
 #pragma unroll
         for (int i = 0; i < LT; ++i) {
-            if (HZ) v[i] *= zv[i] * sigmoid(zv[i]);
+            if (HZ) v[i] *= zv[i] * sigmoid_for<InT>(zv[i]);
             bstore(InT(0), r, oy + D_::row(p.C, i), v[i]);
         }
     };

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
                     s = fmaf(c[i], h[k][i], s);
                 }
                 s = fmaf(Dv[k], x[k], lanes_sum<LPC>(s));
-                if (on[k] && first) st(y + tok * p.C + ch[k], p.z ? s * z[k] * sigmoid(z[k]) : s);
+                if (on[k] && first) st(y + tok * p.C + ch[k], p.z ? s * z[k] * sigmoid_for<InT>(z[k]) : s);
             }
         }
     }

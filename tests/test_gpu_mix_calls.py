@@ -1,0 +1,80 @@
+"""More calls of the selective scan, the short convolution and the block norm on the GPU, against
+their definitions in 64 bits (tolerances: mix_util, or derived beside the test)."""
+import pytest
+import torch
+
+import linear_rnn_lm_amd as L
+from tests.gpu_util import note
+from tests.mix_util import E
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF, F32 = torch.bfloat16, torch.float32
+
+# Activations, value by value.  e^-v is good to 5 E: the exponential's last place (2 E), the corrected argument (2^t e^r
+# is one rounding, the constant ln 2 gives |v| E / 20, below 4.5 E at 88; the roundings of r itself are
+# smaller still): at most 5 E up to |v| of 30 and 7.5 E beyond, where 1 + e^-v and the logarithm add next to nothing of
+# their own.  Below 30 the sum 1 + e^-v adds E and the reciprocal's last place 2 E: 8 E; the logarithm's last place
+# 2 E and the product with ln 2 E: 8 E.
+SPANS = [(-86, -60), (-60, -30), (-30, -10), (-10, -7), (-7, -4), (-4, -1), (-1, 1), (1, 20), (20, 80)]
+
+
+def spread(lo, hi, n):
+    return torch.rand(n, generator=torch.Generator().manual_seed(1), dtype=torch.float64) * (hi - lo) + lo
+
+
+@pytest.mark.parametrize("lo,hi", SPANS)
+def test_steps_keep_their_bits(lo, hi):
+    """softplus alone: a state of zero, x = b = 1 and no decay leave delta as the state."""
+    note(f"mix: softplus {lo} {hi}")
+    v = spread(lo, hi, 1 << 16).float().view(1, 1, -1)
+    C = v.shape[2]
+    one, b = torch.ones(1, 1, C, device=DEV), torch.ones(1, 1, 1, 16, device=DEV)
+    state = torch.zeros(1, C, 16, device=DEV)
+    L.ssm_step(one, v.to(DEV), torch.zeros(C, 16, device=DEV), b, b, state)
+    _, _, hT = L.ssm_fwd(one, v.to(DEV), torch.zeros(C, 16, device=DEV), b, b, want_ckpt=False)
+    torch.cuda.synchronize()
+    want = torch.logaddexp(v.double(), torch.zeros(1, dtype=torch.float64)).view(1, C, 1)
+    for h in (state, hT):
+        err = ((h.double().cpu() - want).abs() / want).max().item()
+        assert err <= 8 * E, (lo, hi, err / E)
+
+
+@pytest.mark.parametrize("lo,hi", SPANS)
+def test_gates_keep_their_bits(lo, hi):
+    """silu and sigmoid alone: a filter of one tap gives s = x, a scan of y = D x = 1 its gate, a norm of
+    1 / sqrt(1 + 0) its activation; each adds at most two roundings to the sigmoid's 8 E."""
+    note(f"mix: sigmoid {lo} {hi}")
+    v = spread(lo, hi, 1 << 16).float()
+    v[v == 0] = 1.0
+    C, g = v.numel(), v.to(DEV)
+    w = torch.zeros(C, 2, device=DEV)
+    w[:, 1] = 1
+    y, _ = L.conv_fwd(g.view(1, 1, C), w, want_hT=False)
+    one, zero, S0 = torch.ones(1, 1, C, device=DEV), torch.zeros(1, 1, 1, 16, device=DEV), torch.zeros(C, 16, device=DEV)
+    gated, _, _ = L.ssm_fwd(one, one, S0, zero, zero, torch.ones(C, device=DEV), g.view(1, 1, C), want_ckpt=False, want_hT=False)
+    rows = lambda act: L.rn_fwd(torch.ones(C // 64, 64, device=DEV), g.view(-1, 64), norm="rms", act=act, eps=0.0)[0]  # noqa: E731
+    torch.cuda.synchronize()
+    s = torch.sigmoid(v.double())
+    for got, want in ((y, s * v), (gated, s * v), (rows("silu"), s * v), (rows("sigmoid"), s)):
+        err = ((got.double().cpu().flatten() - want).abs() / want.abs()).max().item()
+        assert err <= 10 * E, (lo, hi, err / E)
+
+
+def test_activations_of_no_numbers():
+    """Infinities keep the activations' limits where those are numbers, and NaN stays NaN."""
+    note("mix: activations of infinities")
+    inf, nan = float("inf"), float("nan")
+    v = torch.tensor([inf, -inf, nan, 3e38, -3e38, 1e30, -1e30, 200.0, -200.0], device=DEV)
+    n = v.numel()
+    one, b = torch.ones(1, 1, n, device=DEV), torch.ones(1, 1, 1, 16, device=DEV)
+    _, _, hT = L.ssm_fwd(one, v.view(1, 1, n), torch.zeros(n, 16, device=DEV), b, b, want_ckpt=False)
+    keep = [1, 3, 4, 5, 6, 7, 8]                           # no decay: e^0, but an infinite step of A = 0 is no number
+    want = torch.tensor([0, 3e38, 0, 1e30, 0, 200.0, 0], device=DEV)
+    torch.cuda.synchronize()
+    assert torch.equal(hT[0, keep, 0], want) and torch.isnan(hT[0, 2]).all() and not torch.isfinite(hT[0, 0]).any()
+    gate = v.view(n, 1).expand(n, 8).contiguous()
+    r = L.rn_fwd(torch.ones(n, 8, device=DEV), gate, norm="rms", act="sigmoid", eps=0.0)[0]
+    torch.cuda.synchronize()
+    want = torch.tensor([1, 0, nan, 1, 0, 1, 0, 1, 0.0], device=DEV).view(n, 1).expand(n, 8)
+    assert torch.equal(torch.isnan(r), torch.isnan(want)) and torch.equal(torch.nan_to_num(r), torch.nan_to_num(want))
