@@ -18,8 +18,8 @@
  * - Token tensors are rows of `in_dtype`: token t of batch row r is row r * T + t.  x, dt,
  *   z, y and their gradients have C values per row, b and c G * S ([g][s]).  y and the
  *   gradients are dense; each input has a distance between its rows, *_ld, in values, so
- *   that it may be a slice of a wider projection (at most 2^24).  y and the token gradients are
- *   rounded once, at the end.  A: (C, S) fp32, D, dt_bias: (C) fp32, states: (N, C, S) fp32.
+ *   that it may be a slice of a wider projection (at most 2^24; ssm_step takes any).  y and the token
+ *   gradients are rounded once, at the end.  A: (C, S) fp32, D, dt_bias: (C) fp32, states: (N, C, S) fp32.
  * - Sequences.  cu_seqlens NULL: N = B sequences of T tokens.  Otherwise B must be 1 and
  *   cu_seqlens is a device array of N + 1 non-decreasing offsets in 0 .. T: sequence n is
  *   the tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1, and may be empty (its final state is

@@ -622,9 +622,12 @@ def _row_ld(fn, name, t, shape, dtype, dev):
     return ld
 
 
-def _rows(t):
-    """`t` itself where a call takes its layout, else a dense copy."""
-    return t if t.dim() < 3 or _ld_of(t) is not None else t.contiguous()
+def _rows(t, most=None):
+    """`t` itself where a call takes its layout, with rows at most `most` values apart, else a dense copy."""
+    if t.dim() < 3 or t.is_contiguous():
+        return t
+    ld = _ld_of(t)
+    return t if ld is not None and (most is None or ld <= most) else t.contiguous()
 
 
 def _new_like(t, dtype):

@@ -101,9 +101,9 @@ wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* 
 int64_t fwd_ws(const Shape& s) { return s.split[0] ? (s.segs[0] * s.per_seg + s.state) * 4 : 256; }
 int64_t bwd_ws(const Shape& s) { return (s.part_bc + s.segs[1] * s.per_seg * (s.split[1] ? 2 : 1)) * 4; }
 int64_t span(int64_t rows, int64_t ld, int64_t n, int e) { return ((rows - 1) * ld + n) * e; }
-constexpr int64_t kMaxLd = 1 << 24;   // 16 rows are addressed with 32-bit byte offsets
-bool lds_ok(int64_t tokens, int C, int GS, int64_t x, int64_t dt, int64_t b, int64_t c, const void* z, int64_t z_ld) {
-    const int64_t most = kMax / tokens < kMaxLd ? kMax / tokens : kMaxLd;
+constexpr int64_t kMaxLd = 1 << 24;   // over sequences: 16 rows are addressed with 32-bit byte offsets; the step has 64 bits
+bool lds_ok(int64_t tokens, int C, int GS, int64_t x, int64_t dt, int64_t b, int64_t c, const void* z, int64_t z_ld, int64_t max_ld) {
+    const int64_t most = kMax / tokens < max_ld ? kMax / tokens : max_ld;
     return x >= C && dt >= C && b >= GS && c >= GS && (!z || z_ld >= C) && x <= most && dt <= most && b <= most && c <= most &&
            (!z || z_ld <= most);
 }
@@ -140,7 +140,7 @@ wkv7_status ssm_fwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     Shape s;
     wkv7_status st = shape(B, T, C, S, G, N, cu_seqlens != nullptr, &s);
     if (st != WKV7_OK) return st;
-    if (!lds_ok(s.tokens, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld)) return WKV7_ERR_SHAPE;
+    if (!lds_ok(s.tokens, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld, kMaxLd)) return WKV7_ERR_SHAPE;
     const int e = in_dtype == WKV7_BF16 ? 2 : 4;
     const int64_t need = fwd_ws(s), n = s.tokens;
     const Buf bufs[] = {{x, span(n, x_ld, C, e), true, false, e}, {dt, span(n, dt_ld, C, e), true, false, e},
@@ -182,7 +182,7 @@ wkv7_status ssm_bwd(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, cons
     Shape s;
     wkv7_status st = shape(B, T, C, S, G, N, cu_seqlens != nullptr, &s);
     if (st != WKV7_OK) return st;
-    if (!lds_ok(s.tokens, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld)) return WKV7_ERR_SHAPE;
+    if (!lds_ok(s.tokens, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld, kMaxLd)) return WKV7_ERR_SHAPE;
     if ((D != nullptr) != (dD != nullptr) || (z != nullptr) != (dz != nullptr)) return WKV7_ERR_ARG;
     const int e = in_dtype == WKV7_BF16 ? 2 : 4;
     const int64_t n = s.tokens, rows = n * C * e, brows = n * G * S * e, sb = s.state * 4;
@@ -232,7 +232,7 @@ wkv7_status ssm_step(int B, int T, int C, int S, int G, wkv7_dtype in_dtype, con
     if (P < 1 || (!slots && P < B) || P > kMax / ((int64_t)C * S)) return WKV7_ERR_SHAPE;
     if (B > (1 << 24) / ((C + 15) / 16 + 1)) return WKV7_ERR_SHAPE;   // a launch takes fewer than 2^32 threads
     const int64_t n = (int64_t)B * T, sb = (int64_t)P * C * S * 4;
-    if (!lds_ok(n, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld)) return WKV7_ERR_SHAPE;
+    if (!lds_ok(n, C, G * S, x_ld, dt_ld, b_ld, c_ld, z, z_ld, kMax)) return WKV7_ERR_SHAPE;
     const int e = in_dtype == WKV7_BF16 ? 2 : 4;
     const Buf bufs[] = {{x, span(n, x_ld, C, e), true, false, e}, {dt, span(n, dt_ld, C, e), true, false, e},
                         {A, (int64_t)C * S * 4, true, false, 16}, {b, span(n, b_ld, G * S, e), true, false, e},

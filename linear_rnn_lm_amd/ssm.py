@@ -18,8 +18,9 @@ lengths, empty ones included, along T.  The offsets stay on the GPU: nothing wai
 them, and a call can be captured into a graph and replayed with other offsets.  (As with
 every autograd op, capture a backward only on leaves that no live eager graph uses.)
 
-x, dt, b, c and z may be slices of wider rows (one distance between all rows, the values
-of a row side by side); everything else is dense.  SSM makes copies of what is neither.
+x, dt, b, c and z may be slices of wider rows (one distance between all rows, for ssm_fwd and
+ssm_bwd at most 2 ** 24 values, the values of a row side by side); everything else is dense.
+SSM makes copies of what is neither.
 Calls of several streams or threads may overlap as long as they share no output and no
 workspace.
 """
@@ -33,6 +34,7 @@ from . import (_check_bytes, _dense, _dense_on, _launch, _LazyOpOf, _new_like, _
 from .gdr import _check_cu
 
 SSM_BLOCK = 16
+_MAX_LD = 1 << 24
 
 
 @functools.lru_cache(maxsize=None)
@@ -216,7 +218,7 @@ def _make_autograd():
         @staticmethod
         def forward(ctx, x, dt, A, b, c, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, softplus=True):
             ctx.set_materialize_grads(False)               # a gradient that is not there costs nothing
-            toks = [None if t is None else _rows(t) for t in (x, dt, b, c, z)]
+            toks = [None if t is None else _rows(t, _MAX_LD) for t in (x, dt, b, c, z)]
             A_, D_, bias, h0_ = (None if t is None else _dense(t.float()) for t in (A, D, dt_bias, h0))
             need = any(ctx.needs_input_grad)
             X, DT, Bm, Cm, Z = toks

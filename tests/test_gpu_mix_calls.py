@@ -5,7 +5,7 @@ import torch
 
 import linear_rnn_lm_amd as L
 from tests.gpu_util import note
-from tests.mix_util import E
+from tests.mix_util import E, make_scan
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -78,3 +78,26 @@ def test_activations_of_no_numbers():
     torch.cuda.synchronize()
     want = torch.tensor([1, 0, nan, 1, 0, 1, 0, 1, 0.0], device=DEV).view(n, 1).expand(n, 8)
     assert torch.equal(torch.isnan(r), torch.isnan(want)) and torch.equal(torch.nan_to_num(r), torch.nan_to_num(want))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_last_tokens_of_long_rows(dtype):
+    """Views x[:, -1:] whose rows lie more than 2^24 values apart: a step takes them, SSM copies them, ssm_fwd refuses."""
+    note(f"ssm far rows {dtype}")
+    B, T, C, S = 2, 4099, 4096, 16
+    p = {n: None if t is None else t.to(DEV) for n, t in make_scan(B, 1, C, S, 1, dtype, seed=3).items()}
+    big = {n: torch.full((B, T if n != "b" else 2 ** 20 + 1, *p[n].shape[2:]), float("nan"), dtype=dtype, device=DEV) for n in "xzb"}
+    for n, t in big.items():
+        t[:, -1:] = p[n]
+        big[n] = t[:, -1:]
+        assert t.stride(0) > 2 ** 24
+    x, z, b = big["x"], big["z"], big["b"]
+    state, alone = p["h0"].clone(), p["h0"].clone()
+    y = L.ssm_step(x, p["dt"], p["A"], b, p["c"], state, p["D"], z, dt_bias=p["dt_bias"])
+    want = L.ssm_step(p["x"], p["dt"], p["A"], p["b"], p["c"], alone, p["D"], p["z"], dt_bias=p["dt_bias"])
+    ya, ha = L.SSM.apply(x, p["dt"], p["A"], b, p["c"], p["D"], z, p["dt_bias"], p["h0"])
+    yb, hb = L.SSM.apply(p["x"], p["dt"], p["A"], p["b"], p["c"], p["D"], p["z"], p["dt_bias"], p["h0"])
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(state, alone) and torch.equal(ya, yb) and torch.equal(ha, hb)
+    with pytest.raises(L.Wkv7Error, match="SHAPE"):
+        L.ssm_fwd(x, p["dt"], p["A"], b, p["c"])
