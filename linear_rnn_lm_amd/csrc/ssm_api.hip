@@ -84,7 +84,7 @@ wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* 
         s->halves_sums[back] = S == 16 && !packed && waves * ((T - 1) / s->seg[back]) <= 3 * 1024;
         const int64_t segs = slots_of(B, T, N, packed, s->seg[back]);
         // a launch takes fewer than 2^32 threads: at most 512 for each segment and channel block
-        if (segs > (1 << 22) / (2 * blocks)) return WKV7_ERR_SHAPE;
+        if (segs > ((1 << 23) - 1) / blocks) return WKV7_ERR_SHAPE;
         s->segs[back] = (int)segs;
     }
     if (s->slots > INT32_MAX) return WKV7_ERR_SHAPE;

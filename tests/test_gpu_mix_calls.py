@@ -5,7 +5,7 @@ import torch
 
 import linear_rnn_lm_amd as L
 from tests.gpu_util import note
-from tests.mix_util import E, make_scan
+from tests.mix_util import E, half_step, make_scan
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -101,3 +101,28 @@ def test_last_tokens_of_long_rows(dtype):
     assert torch.equal(y, want) and torch.equal(state, alone) and torch.equal(ya, yb) and torch.equal(ha, hb)
     with pytest.raises(L.Wkv7Error, match="SHAPE"):
         L.ssm_fwd(x, p["dt"], p["A"], b, p["c"])
+
+
+def test_millions_of_sequences():
+    """More than 2^21 sequences of one token: h = delta x b, y = (c b) delta x + D x."""
+    note("ssm 2^21 sequences")
+    N, C, S = 2 ** 21 + 5, 8, 16
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x, dt, b, c = (torch.randn(N, 1, *s, generator=gen, device=DEV).to(BF) for s in ((C,), (C,), (1, S), (1, S)))
+    A, D = -torch.ones(C, S, device=DEV), torch.ones(C, device=DEV)
+    cu = torch.arange(N + 1, dtype=torch.int32, device=DEV)
+    y, _, hT = L.ssm_fwd(x, dt, A, b, c, D, want_ckpt=False)
+    flat = lambda t: t.view(1, N, *t.shape[2:])  # noqa: E731
+    yp, _, hp = L.ssm_fwd(flat(x), flat(dt), A, flat(b), flat(c), D, cu_seqlens=cu, want_ckpt=False)
+    torch.cuda.synchronize()
+    # one token: delta is good to 8 E, its products to 2 more; y is a sum of S + 1 terms, of which the largest are a few times
+    # the result's size on average, and is rounded once
+    d = torch.nn.functional.softplus(dt.double())[:, 0]
+    want = (d * x[:, 0].double())[..., None] * b[:, 0].double()
+    err = ((hT.double() - want).norm() / want.norm()).item()
+    assert err <= 10 * E
+    del hT
+    want = (want * c[:, 0].double()).sum(-1) + x[:, 0].double()
+    err = ((y[:, 0].double() - want).norm() / want.norm()).item()
+    assert err <= half_step(BF) + 4 * (S + 10) * E
+    assert torch.equal(yp.view_as(y), y)

@@ -20,3 +20,13 @@ def test_row_distances():
         # past the check of shapes the missing output is what is wrong
         assert s(**{n: (1 << 24) + 8}, y=None) == ERR_ARG
         assert f(**{n: (1 << 24) + 8}) == ERR_SHAPE == s(**{n: 1 << 41}, y=None)
+
+
+def test_many_sequences():
+    """As many segments as a launch has threads for, fewer than 2^32 at 512 to a segment and 64 channels."""
+    lib = ssm._lib()
+    most = 2 ** 23 - 1
+    for size in (lib.ssm_fwd_workspace_bytes, lib.ssm_bwd_workspace_bytes):
+        assert size(most, 1, 64, 16, 1, 0, 0) > 0 == size(most + 1, 1, 64, 16, 1, 0, 0)
+        assert size(most // 64, 1, 4096, 16, 1, 0, 0) > 0 == size(most // 64 + 1, 1, 4096, 16, 1, 0, 0)
+        assert size(1, 15, 64, 16, 1, most, 1) > 0 == size(1, 15, 64, 16, 1, most + 1, 1)
