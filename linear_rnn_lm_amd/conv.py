@@ -162,18 +162,19 @@ def _make_autograd():
 
     class CONV(torch.autograd.Function):
         """Differentiable op: (x, weight, bias, h0, cu_seqlens, silu) -> (y, hT), gradients by
-        conv_bwd in the inputs' types."""
+        conv_bwd in the inputs' types.  weight and bias may be of two types; h0 has x's."""
 
         @staticmethod
         def forward(ctx, x, weight, bias=None, h0=None, cu_seqlens=None, silu=True):
             ctx.set_materialize_grads(False)               # a gradient that is not there costs nothing
-            x, weight = _rows(x), weight.contiguous()
-            tb, th = (None if t is None else t.dtype for t in (bias, h0))
-            bias = None if bias is None else bias.to(weight.dtype).contiguous()
-            h0 = None if h0 is None else h0.to(x.dtype).contiguous()
+            x, tw, tb = _rows(x), weight.dtype, None if bias is None else bias.dtype
+            wide = tw if tb is None else torch.promote_types(tw, tb)       # of two types the one that holds both
+            weight = weight.to(wide).contiguous()
+            bias = None if bias is None else bias.to(wide).contiguous()
+            h0 = None if h0 is None else h0.contiguous()
             y, hT = conv_fwd(x, weight, bias, h0, silu=silu, cu_seqlens=cu_seqlens)
             ctx.save_for_backward(x, weight, bias, h0, cu_seqlens)
-            ctx.silu, ctx.tb, ctx.th = silu, tb, th
+            ctx.silu, ctx.tw, ctx.tb, ctx.has_h0 = silu, tw, tb, h0 is not None
             return y, hT
 
         @staticmethod
@@ -183,9 +184,8 @@ def _make_autograd():
             dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _dense(dy.to(x.dtype))
             dhT = None if dhT is None else _dense(dhT.to(x.dtype))
             dx, dw, db, dh0 = conv_bwd(dy, x, weight, bias, h0, dhT, silu=ctx.silu, cu_seqlens=cu,
-                                       want_dh0=ctx.th is not None)
-            return (dx, dw.to(weight.dtype), None if ctx.tb is None else db.to(ctx.tb),
-                    None if ctx.th is None else dh0.to(ctx.th), None, None)
+                                       want_dh0=ctx.has_h0)
+            return dx, dw.to(ctx.tw), None if ctx.tb is None else db.to(ctx.tb), dh0, None, None
 
     return CONV
 

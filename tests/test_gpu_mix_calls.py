@@ -5,7 +5,7 @@ import torch
 
 import linear_rnn_lm_amd as L
 from tests.gpu_util import note
-from tests.mix_util import E, half_step, make_scan
+from tests.mix_util import E, conv_tol, half_step, make_conv, make_scan, ref_conv_grads, rel
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -126,3 +126,20 @@ def test_millions_of_sequences():
     err = ((y[:, 0].double() - want).norm() / want.norm()).item()
     assert err <= half_step(BF) + 4 * (S + 10) * E
     assert torch.equal(yp.view_as(y), y)
+
+
+@pytest.mark.parametrize("wd,bd", [(BF, F32), (F32, BF)])
+def test_convolution_with_weights_of_two_types(wd, bd):
+    """A bias of fp32 beside bf16 filters keeps its bits, and the other way; a state of another type than x's is refused."""
+    note(f"CONV {wd} {bd}")
+    p = make_conv(2, 21, 40, 4, F32, seed=5)
+    p["weight"], p["bias"] = p["weight"].to(wd), (p["bias"] + 1000 * E).to(bd)
+    wy, wh, want = ref_conv_grads(p)
+    leaves = {n: p[n].to(DEV).requires_grad_() for n in ("x", "weight", "bias", "h0")}
+    y, hT = L.CONV.apply(*leaves.values())
+    torch.autograd.backward([y, hT], [p["dy"].to(DEV), p["dhT"].to(DEV)])
+    assert rel(y, wy) <= conv_tol(4, F32) and rel(hT, wh) <= conv_tol(4, F32)
+    for (n, t), g in zip(leaves.items(), ("dx", "dweight", "dbias", "dh0")):
+        assert t.grad.dtype == p[n].dtype and rel(t.grad, want[g]) <= conv_tol(4, p[n].dtype, 42, True), n
+    with pytest.raises(ValueError, match="h0"):
+        L.CONV.apply(leaves["x"].to(BF), leaves["weight"], leaves["bias"], leaves["h0"])
