@@ -584,6 +584,27 @@ class _LazyOpOf:
         return getattr(self._op, name)
 
 
+class _NoGradients:
+    """What an op's forward sees as its context where gradients are off."""
+    needs_input_grad = ()
+
+    def set_materialize_grads(self, value):
+        pass
+
+    def save_for_backward(self, *tensors):
+        pass
+
+
+class _LazyOpOfEither(_LazyOpOf):
+    """An autograd op whose forward leaves what only a backward needs if one may follow: inside
+    forward gradients are always off, and parameters need theirs in a block without gradients too."""
+
+    def apply(self, *args):
+        if _torch_c().is_grad_enabled():
+            return self.__getattr__("apply")(*args)
+        return self.forward(_NoGradients(), *args)
+
+
 @functools.lru_cache(maxsize=None)
 def _types():
     """The two input types and their codes, and fp32."""

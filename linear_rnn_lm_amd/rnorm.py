@@ -26,7 +26,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import F32, _check_bytes, _dense, _launch, _LazyOpOf, _new_like, _ptr, _types, _where, lib
+from . import F32, _check_bytes, _dense, _launch, _LazyOpOfEither, _new_like, _ptr, _types, _where, lib
 from .ssm import _check_tensor
 
 _NORMS = {None: 0, "layer": 1, "rms": 2}
@@ -203,7 +203,8 @@ def _make_autograd():
                 ld = _uniform_ld(gate)
                 if ld is None or (align == 16 and (ld % 8 or gate.data_ptr() % 16)):
                     gate = fit(gate)
-            r, h, stats = rn_fwd(o, gate, res, weight=weight, bias=bias, scale=scale, weight2=weight2, bias2=bias2, **opt)
+            r, h, stats = rn_fwd(o, gate, res, weight=weight, bias=bias, scale=scale, weight2=weight2, bias2=bias2,
+                                 want_stats=any(ctx.needs_input_grad), **opt)
             ctx.save_for_backward(o, gate, res, weight, bias, scale, weight2, bias2, stats)
             ctx.opt = {k: opt[k] for k in ("groups", "norm", "norm2", "act") if k in opt}
             ctx.align, ctx.r, ctx.h = align, r.dtype, None if h is None else h.dtype
@@ -228,4 +229,4 @@ def _make_autograd():
     return RN
 
 
-RN = _LazyOpOf(_make_autograd)
+RN = _LazyOpOfEither(_make_autograd)

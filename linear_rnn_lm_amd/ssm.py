@@ -29,7 +29,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import (_check_bytes, _dense, _dense_on, _launch, _LazyOpOf, _new_like, _ptr, _row_ld, _rows, _types, _where,
+from . import (_check_bytes, _dense, _dense_on, _launch, _LazyOpOfEither, _new_like, _ptr, _row_ld, _rows, _types, _where,
                lib)
 from .gdr import _check_cu
 
@@ -245,4 +245,4 @@ def _make_autograd():
     return SSM
 
 
-SSM = _LazyOpOf(_make_autograd)
+SSM = _LazyOpOfEither(_make_autograd)

@@ -143,3 +143,29 @@ def test_convolution_with_weights_of_two_types(wd, bd):
         assert t.grad.dtype == p[n].dtype and rel(t.grad, want[g]) <= conv_tol(4, p[n].dtype, 42, True), n
     with pytest.raises(ValueError, match="h0"):
         L.CONV.apply(leaves["x"].to(BF), leaves["weight"], leaves["bias"], leaves["h0"])
+
+
+def test_without_gradients():
+    """SSM and RN in a block without gradients, their weights being parameters: the same outputs, no memory for a backward."""
+    note("SSM, RN without gradients")
+    B, T, C, S = 1, 4096, 512, 64
+    p = {n: None if t is None else t.to(DEV) for n, t in make_scan(B, T, C, S, 1, BF, seed=6, h0=False).items()}
+    p["A"].requires_grad_(), p["D"].requires_grad_()
+    scan = lambda: L.SSM.apply(*[p[n] for n in ("x", "dt", "A", "b", "c", "D", "z", "dt_bias")])  # noqa: E731
+    w = torch.ones(C, device=DEV, requires_grad=True)
+    norm = lambda y: L.RN.apply(y, p["z"], None, w, None, None, w, None, dict(norm="rms", norm2="rms"))  # noqa: E731
+    want = [t.detach() for t in (*scan(), *norm(p["x"]))]
+    with torch.no_grad():
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        got = scan()
+        used = torch.cuda.max_memory_allocated() - before
+        got = [*got, *norm(p["x"])]
+    lib, dims = L.ssm._lib(), (B, T, C, S, 1, 0, 0)
+    assert used < lib.ssm_ckpt_bytes(*dims) / 2
+    assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, want))
+    with torch.no_grad(), torch.enable_grad():
+        y, _ = scan()
+    y.backward(p["dy"])
+    assert torch.isfinite(p["A"].grad).all() and p["A"].grad.any()

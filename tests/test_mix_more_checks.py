@@ -1,7 +1,9 @@
 """More of what the selective scan, the short convolution and the block norm take and refuse, on the
 host (CPU only): made-up device addresses; every call fails a check, so nothing is launched."""
-import linear_rnn_lm_amd as L  # noqa: F401  (the binding sets the library's argument types)
-from linear_rnn_lm_amd import ssm
+import torch
+
+import linear_rnn_lm_amd as L
+from linear_rnn_lm_amd import rnorm, ssm
 from tests.test_abi import ERR_ARG, ERR_SHAPE, fake, needs_no_gpu
 from tests.test_mix_checks import call
 
@@ -30,3 +32,32 @@ def test_many_sequences():
         assert size(most, 1, 64, 16, 1, 0, 0) > 0 == size(most + 1, 1, 64, 16, 1, 0, 0)
         assert size(most // 64, 1, 4096, 16, 1, 0, 0) > 0 == size(most // 64 + 1, 1, 4096, 16, 1, 0, 0)
         assert size(1, 15, 64, 16, 1, most, 1) > 0 == size(1, 15, 64, 16, 1, most + 1, 1)
+
+
+def test_nothing_for_a_backward_without_gradients(monkeypatch):
+    """SSM's checkpoints and RN's statistics are asked for only where a backward may follow."""
+    asked = []
+
+    def scan(x, dt, A, *rest, want_ckpt, **kw):
+        asked.append(want_ckpt)
+        return x.clone(), torch.zeros(1), x.new_zeros(1, *A.shape)
+
+    def norm(o, *rest, want_stats, **kw):
+        asked.append(want_stats)
+        return o.clone(), None, torch.zeros(1)
+
+    monkeypatch.setattr(ssm, "ssm_fwd", scan)
+    monkeypatch.setattr(rnorm, "rn_fwd", norm)
+    x, A, b = torch.zeros(1, 3, 8), torch.zeros(8, 16), torch.zeros(1, 3, 1, 16)
+    param, w = A.clone().requires_grad_(), torch.ones(8, requires_grad=True)
+    for mode, want in ((torch.enable_grad, True), (torch.no_grad, False), (torch.inference_mode, False)):
+        asked.clear()
+        with mode():
+            y, hT = L.SSM.apply(x, x, param, b, b)
+            r, h = L.RN.apply(x[0], None, None, w)
+        assert asked == [want, want] and h is None
+        assert y.requires_grad == hT.requires_grad == r.requires_grad == want
+    asked.clear()
+    L.SSM.apply(x, x, A, b, b)                             # nothing has a gradient
+    L.RN.apply(x[0])
+    assert asked == [False, False]
