@@ -28,7 +28,7 @@
  *   every sequence are not read; their rows of y and of the token gradients stay as they were, or
  *   are set to zero with zero_outside.
  * - delta A should be at most 0; the states grow without bound otherwise.  A delta of 0
- *   passes the state on as it is.  A NaN or Inf in x, dt or z spoils its channel of its
+ *   passes the state on as it is, also where A is -infinity.  A NaN or Inf in x, dt or z spoils its channel of its
  *   sequence only, from its token on, in b or c every channel of the group; in the
  *   gradients what the formula lets it reach.
  * - Arithmetic, states and sums are fp32; sums of steps over a stretch of tokens 64 bits.

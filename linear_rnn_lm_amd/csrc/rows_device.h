@@ -3,6 +3,8 @@
 // the sequences of a call lie.
 #pragma once
 
+#include <float.h>
+
 #include "wkv7_device.h"
 
 namespace rows {
@@ -49,6 +51,13 @@ __device__ __forceinline__ float softplus(float v) {
     const float a = __builtin_fabsf(v), t = -kLog2e * a, e0 = exp2_f(t);
     const float e = fmaf(e0, __builtin_amdgcn_fmed3f(exp_rest(-a, t), -1.f, 1.f), e0), w = 1.f + e, r = e - (w - 1.f);
     return __builtin_fmaxf(v, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), r);
+}
+
+// log2(e) A, the lowest number in place of -infinity: a step of 0 (of a token behind the end of a sequence too) times it is
+// 0, so that it passes the state on, and any other step clears the state.
+__device__ __forceinline__ float rate_of(float A) {
+    const float a = kLog2e * A;
+    return a < -FLT_MAX ? -FLT_MAX : a;                    // a NaN stays
 }
 
 // A value that is the same for the whole wave, in scalar registers.

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64 * WN * WC, 2) void bwd_kernel(Args p, int blocks
     const int t_begin = used ? piece * p.seg : 0, t_end = used ? min(len, t_begin + p.seg) : 0;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-        A2[s] = on ? kLog2e * p.A[(int64_t)ch * S + n0 + s] : 0.f;
+        A2[s] = on ? rate_of(p.A[(int64_t)ch * S + n0 + s]) : 0.f;
         dA[s] = 0.f;
         gr[s] = used && on && p.dhT ? p.dhT[((int64_t)n * p.C + ch) * S + n0 + s] : 0.f;
     }

@@ -68,7 +68,7 @@ __global__ __launch_bounds__(64 * WN * WC, Ahead<NS>::waves) void fwd_kernel(Arg
     float A2[NS], h[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-        A2[s] = on ? kLog2e * p.A[(int64_t)ch * S + n0 + s] : 0.f;
+        A2[s] = on ? rate_of(p.A[(int64_t)ch * S + n0 + s]) : 0.f;
         h[s] = on && p.h0 ? p.h0[((int64_t)n * p.C + ch) * S + n0 + s] : 0.f;
     }
     if (p.split && on) fold_segments<NS>(p, first_slot(seqs, n, tok0, p.seg), 1, piece, ch, n0, A2, h);
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int block
     float A2[NS], h[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-        A2[s] = on ? kLog2e * p.A[(int64_t)ch * S + n0 + s] : 0.f;
+        A2[s] = on ? rate_of(p.A[(int64_t)ch * S + n0 + s]) : 0.f;
         h[s] = 0.f;
     }
     const D_ deal(tid, cb, p.C);

@@ -83,7 +83,9 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs p, int nsub) {
     float bias[K], Dv[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        if (on[k]) A2[k] = kLog2e * *reinterpret_cast<const f32x4*>(p.A + (int64_t)ch[k] * S + n0);
+        if (on[k]) A2[k] = *reinterpret_cast<const f32x4*>(p.A + (int64_t)ch[k] * S + n0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) A2[k][i] = rate_of(A2[k][i]);
         bias[k] = on[k] && p.dt_bias ? p.dt_bias[ch[k]] : 0.f;
         Dv[k] = on[k] && p.D ? p.D[ch[k]] : 0.f;
     }

@@ -5,7 +5,7 @@ import torch
 
 import linear_rnn_lm_amd as L
 from tests.gpu_util import note
-from tests.mix_util import E, conv_tol, half_step, make_conv, make_scan, ref_conv_grads, rel
+from tests.mix_util import E, GRADS, conv_tol, half_step, make_conv, make_scan, ref_conv_grads, ref_scan_grads, rel, scan_tol
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -169,3 +169,32 @@ def test_without_gradients():
         y, _ = scan()
     y.backward(p["dy"])
     assert torch.isfinite(p["A"].grad).all() and p["A"].grad.any()
+
+
+@pytest.mark.parametrize("B,T,C,S", [(2, 5, 24, 16), (1, 300, 40, 16), (3, 33, 40, 32), (1, 35, 33, 64)])
+def test_states_without_memory(B, T, C, S):
+    """A of -infinity clears a state at every step, as -1e30 does, and tokens behind a sequence's end do not touch it."""
+    note(f"ssm A -inf B{B} T{T} C{C} S{S}")
+    p = make_scan(B, T, C, S, 1, F32, seed=9)
+    p["A"][:, 0], p["A"][3] = -1e30, -1e30                 # every delta is above 1e-5: e^(delta A) is 0 in any precision
+    wy, wh, want = ref_scan_grads(p, dev=DEV)
+    p["A"][p["A"] < -1e29] = -float("inf")
+    d = {n: None if t is None else t.to(DEV) for n, t in p.items()}
+    ins = [d[n] for n in ("x", "dt", "A", "b", "c")]
+    y, ckpt, hT = L.ssm_fwd(*ins, d["D"], d["z"], d["h0"], dt_bias=d["dt_bias"])
+    got = dict(zip(GRADS, L.ssm_bwd(d["dy"], *ins, ckpt, d["D"], d["z"], d["dhT"], dt_bias=d["dt_bias"])))
+    state = d["h0"].clone()
+    ys = L.ssm_step(*ins, state, d["D"], d["z"], dt_bias=d["dt_bias"])
+    torch.cuda.synchronize()
+    for a, h in ((y, hT), (ys, state)):
+        assert rel(a, wy) <= scan_tol(T, S, F32) and rel(h, wh) <= scan_tol(T, S, F32)
+    for n in GRADS:
+        assert rel(got[n], want[n]) <= scan_tol(T, S, F32, B * T + C, True), n
+    # a step of exactly 0 keeps it
+    q = {n: d[n][:, :1].contiguous() for n in ("x", "dt", "b", "c")}
+    q["dt"].fill_(-float("inf"))
+    _, _, hT = L.ssm_fwd(q["x"], q["dt"], d["A"], q["b"], q["c"], h0=d["h0"], want_ckpt=False)
+    state = d["h0"].clone()
+    L.ssm_step(q["x"], q["dt"], d["A"], q["b"], q["c"], state)
+    torch.cuda.synchronize()
+    assert torch.equal(hT, d["h0"]) and torch.equal(state, d["h0"])
