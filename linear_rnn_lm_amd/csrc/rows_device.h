@@ -163,7 +163,7 @@ __device__ __forceinline__ bool by_length(const Seqs& s, int k, int piece_len, i
     int64_t tok0;
     int len = -1;
     if (lane < s.N) seq_span(s, lane, tok0, len);
-    const int mine = lane < s.N ? max(1, (len + piece_len - 1) / piece_len) : 0;
+    const int mine = lane < s.N ? max(1, pieces_dense(len, piece_len)) : 0;
     int before = 0;
     for (int j = 0; j < s.N; ++j) {
         const int l = __builtin_amdgcn_readlane(len, j), c = __builtin_amdgcn_readlane(mine, j);

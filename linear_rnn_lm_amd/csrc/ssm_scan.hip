@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64 * WN * WC, Ahead<NS>::waves) void fwd_kernel(Arg
     int64_t tok0;
     seq_span(seqs, n, tok0, len);
     n = uniform(n), piece = uniform(piece), len = uniform(len), tok0 = uniform(tok0);
-    const int t_begin = piece * p.seg, t_end = min(len, t_begin + p.seg);
+    const int t_begin = piece * p.seg, t_end = t_begin + min(len - t_begin, p.seg);    // below 2^31 as len is
 
     // scanning: channel and first state of this lane
     const int cl = wc * 16 + (lane & 15), g = lane >> 4, ch = cb * CH + cl, n0 = (wn * 4 + g) * NS;
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int block
     int64_t tok0;
     seq_span(seqs, n, tok0, len);
     n = uniform(n), piece = uniform(piece), len = uniform(len), tok0 = uniform(tok0);
-    const int t_begin = piece * p.seg, t_end = min(len, t_begin + p.seg);
+    const int t_begin = piece * p.seg, t_end = t_begin + min(len - t_begin, p.seg);    // below 2^31 as len is
     const int cl = wc * 16 + (lane & 15), g = lane >> 4, ch = cb * CH + cl, n0 = (wn * 4 + g) * NS;
     const bool on = ch < p.C;
     if (!BWD && p.h0_copy && piece == 0 && on) {

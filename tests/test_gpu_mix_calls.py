@@ -198,3 +198,26 @@ def test_states_without_memory(B, T, C, S):
     L.ssm_step(q["x"], q["dt"], d["A"], q["b"], q["c"], state)
     torch.cuda.synchronize()
     assert torch.equal(hT, d["h0"]) and torch.equal(state, d["h0"])
+
+
+def test_positions_near_2_to_31():
+    """As many tokens as positions of 32 bits have room for: the ends of segments lie below 2^31 as the sequence's does.  All
+    tokens are alike, so y has its limit everywhere but at a sequence's first tokens."""
+    note("ssm 2^31 tokens")
+    T, S = 2 ** 31 - 1100, 16
+    one, b = torch.ones(1, T, 1, dtype=BF, device=DEV), torch.ones(1, T, 1, S, dtype=BF, device=DEV)
+    A = -torch.ones(1, S, device=DEV)
+    y = torch.empty(1, T, 1, dtype=BF, device=DEV)
+    # h = e^-1 h + 1: 1 / (1 - 1 / e) from the 40th token on.  S times that is 25.31163, 580 E of itself from where bf16 rounds
+    # the other way (25.3125); the factor's 3 E and the update's 2 leave 5 E of h, the sum of S terms another 16.
+    h = 1 / (1 - torch.exp(torch.tensor(-1.0, dtype=torch.float64)))
+    want = (S * h).to(BF).item()
+    for cu in (None, [0, T - 5, T]):
+        y.fill_(float("nan"))
+        cut = None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV)
+        _, _, hT = L.ssm_fwd(one, one, A, b, b, softplus=False, cu_seqlens=cut, y=y, want_ckpt=False)
+        torch.cuda.synchronize()
+        end = T if cu is None else T - 5
+        assert (y[0, 40:end] == want).all() and (y[0, :40] <= want).all()
+        assert y[0, 0] == S and (cu is None or y[0, T - 5] == S)
+        assert rel(hT[0], h.expand(1, S)) <= scan_tol(40, S, F32)
