@@ -23,7 +23,7 @@
  *   centred values); outputs are rounded once.  NaN and Inf propagate within their part, and
  *   through norm2 within their row.
  * - Every pointer is a device pointer.  Where C is a multiple of 8, rows and weights are
- *   aligned to 16 bytes (and gate_ld is a multiple of 8), else to their values.
+ *   aligned to 16 bytes (each of gate's rows too), else to their values.
  * - Results do not vary from run to run: sums over the rows go through per-workgroup parts
  *   in a fixed order, without atomics.
  */

@@ -516,7 +516,7 @@ wkv7_status rn_fwd(int64_t rows, int C, int groups, rn_norm norm, rn_norm norm2,
     if ((gate != nullptr) != (act != RN_ONE) || (h != nullptr) != (norm2 != RN_NONE)) return WKV7_ERR_ARG;
     if (gate && (gate_ld < C || gate_ld > (int64_t(1) << 40) / rows)) return WKV7_ERR_SHAPE;
     const bool vec = C % 8 == 0;
-    if (vec && gate && gate_ld % 8) return WKV7_ERR_ALIGN;
+    if (vec && gate && gate_ld * esz(io_dtype) % 16) return WKV7_ERR_ALIGN;
     const int64_t n = rows * C, ob = esz(o_dtype), ib = esz(io_dtype), rb = esz(r_dtype), wb = esz(w_dtype);
     const int oa = vec ? 16 : (int)ob, ia = vec ? 16 : (int)ib, ra = vec ? 16 : (int)rb, wa = vec ? 16 : (int)wb;
     const abi::Buf bufs[] = {{o, n * ob, true, false, oa}, {gate, ((rows - 1) * gate_ld + C) * ib, false, false, ia},
@@ -555,7 +555,7 @@ wkv7_status rn_bwd(int64_t rows, int C, int groups, rn_norm norm, rn_norm norm2,
     if ((!dr && !dh) || (dh && norm2 == RN_NONE) || (dres && !res)) return WKV7_ERR_ARG;
     if (gate && (gate_ld < C || gate_ld > (int64_t(1) << 40) / rows)) return WKV7_ERR_SHAPE;
     const bool vec = C % 8 == 0;
-    if (vec && gate && gate_ld % 8) return WKV7_ERR_ALIGN;
+    if (vec && gate && gate_ld * esz(io_dtype) % 16) return WKV7_ERR_ALIGN;
     const int64_t n = rows * C, ob = esz(o_dtype), ib = esz(io_dtype), rb = esz(r_dtype), wb = esz(w_dtype);
     const int oa = vec ? 16 : (int)ob, ia = vec ? 16 : (int)ib, ra = vec ? 16 : (int)rb, wa = vec ? 16 : (int)wb;
     const int64_t need = dw ? (int64_t)rn_bwd_workspace_bytes(rows, C, groups) : 0;

@@ -201,7 +201,7 @@ def _make_autograd():
             o, res, weight, bias, scale, weight2, bias2 = map(fit, (o, res, weight, bias, scale, weight2, bias2))
             if gate is not None:
                 ld = _uniform_ld(gate)
-                if ld is None or (align == 16 and (ld % 8 or gate.data_ptr() % 16)):
+                if ld is None or (align == 16 and (ld * gate.element_size() % 16 or gate.data_ptr() % 16)):
                     gate = fit(gate)
             r, h, stats = rn_fwd(o, gate, res, weight=weight, bias=bias, scale=scale, weight2=weight2, bias2=bias2,
                                  want_stats=any(ctx.needs_input_grad), **opt)

@@ -221,3 +221,19 @@ def test_positions_near_2_to_31():
         assert (y[0, 40:end] == want).all() and (y[0, :40] <= want).all()
         assert y[0, 0] == S and (cu is None or y[0, T - 5] == S)
         assert rel(hT[0], h.expand(1, S)) <= scan_tol(40, S, F32)
+
+
+def test_gates_in_rows_of_fp32():
+    """A gate that is a slice of fp32 rows, each at a multiple of 16 bytes, their distance no multiple of eight values."""
+    note("rn fp32 gate slice")
+    gen = torch.Generator().manual_seed(4)
+    rows, C = 30, 64
+    o, res, dr, dh = (torch.randn(rows, C, generator=gen).to(DEV) for _ in range(4))
+    wide = torch.randn(rows, C + 20, generator=gen).to(DEV)
+    gate = wide[:, 4:4 + C]
+    assert gate.stride(0) % 8 and gate.data_ptr() % 16 == 0
+    kw = dict(norm="rms", norm2="rms")
+    got, want = (L.rn_fwd(o, g, res, **kw) for g in (gate, gate.contiguous()))
+    grads = [L.rn_bwd(dr, dh, o, g, res, want[2], **kw)[:3] for g in (gate, gate.contiguous())]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((*got, *grads[0]), (*want, *grads[1])))

@@ -4,7 +4,7 @@ import torch
 
 import linear_rnn_lm_amd as L
 from linear_rnn_lm_amd import rnorm, ssm
-from tests.test_abi import ERR_ARG, ERR_SHAPE, fake, needs_no_gpu
+from tests.test_abi import ERR_ALIGN, ERR_ARG, ERR_SHAPE, fake, needs_no_gpu
 from tests.test_mix_checks import call
 
 
@@ -61,3 +61,17 @@ def test_nothing_for_a_backward_without_gradients(monkeypatch):
     L.SSM.apply(x, x, A, b, b)                             # nothing has a gradient
     L.RN.apply(x[0])
     assert asked == [False, False]
+
+
+@needs_no_gpu
+def test_gate_rows_at_multiples_of_16_bytes():
+    lib = rnorm._lib()
+    kinds = dict(rows=4, C=128, G=2, n1=1, n2=2, act=1, o_t=0, io_t=1, r_t=1, w_t=0)
+    w = dict(w1=None, b1=None, sc=None, w2=None)
+    f = lambda **o: call(lib.rn_fwd, dict(**kinds, e1=1e-5, e2=1e-5, o=fake(0), g=fake(1), gl=128, res=fake(2), **w, b2=None,  # noqa: E731
+                                          r=None, h=fake(10), st=None), o)
+    g = lambda **o: call(lib.rn_bwd, dict(**kinds, dr=fake(12), dh=fake(13), o=fake(0), g=fake(1), gl=128, res=fake(2),  # noqa: E731
+                                          st=None, **w, do=fake(14), dg=fake(15), dres=None, dw=None, ws=None, wsb=0), o)
+    for c in (f, g):                                       # what is missing is found behind the rows' distance
+        assert c(io_t=0, r_t=0, gl=132) == c(gl=136) == ERR_ARG
+        assert c(io_t=0, r_t=0, gl=130) == c(gl=132) == ERR_ALIGN
