@@ -5,7 +5,11 @@ import torch
 
 import linear_rnn_lm_amd as L
 from tests.gpu_util import note
-from tests.mix_util import E, GRADS, conv_tol, half_step, make_conv, make_scan, ref_conv_grads, ref_scan_grads, rel, scan_tol
+from tests.mix_util import (E, GRADS, INS, conv_tol, half_step, make_conv, make_scan, ref_conv_grads, ref_scan, ref_scan_grads,
+                            rel, scan_tol)
+from tests.test_gpu_rnorm import check as check_rn
+from tests.test_gpu_rnorm import make as make_rn
+from tests.test_gpu_ssm import check as check_scan
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -237,3 +241,109 @@ def test_gates_in_rows_of_fp32():
     grads = [L.rn_bwd(dr, dh, o, g, res, want[2], **kw)[:3] for g in (gate, gate.contiguous())]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((*got, *grads[0]), (*want, *grads[1])))
+
+
+# ------------------------------------------------------------------ launches that the smaller tests do not reach
+def step_ref(p, pool, slots):
+    """Rows one after the other from the definition, on the GPU: y and the pool."""
+    pool = pool.double()
+    p = {n: None if t is None else t.to(DEV).double() for n, t in p.items()}
+    y = torch.zeros(p["x"].shape, dtype=torch.float64, device=DEV)
+    for r, s in enumerate(slots):
+        if 0 <= s < pool.shape[0]:
+            row = {n: p[n] if n in ("A", "D", "dt_bias") or p[n] is None else p[n][r:r + 1] for n in INS}
+            y[r:r + 1], h = ref_scan(dict(row, h0=pool[s:s + 1]))
+            pool[s] = h[0]
+    return y, pool
+
+
+MANY = [(300, 1, 449, 16, 1), (150, 1, 465, 32, 1), (140, 1, 247, 64, 1), (300, 2, 448, 16, 7), (140, 3, 256, 64, 4),
+        (160, 1, 448, 32, 7), (2048, 1, 5, 16, 1)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("B,T,C,S,G", MANY)
+def test_steps_of_many_rows(B, T, C, S, G, dtype):
+    """From 2048 workgroups on a wave has four times the channels: the last of them missing, several groups, several tokens."""
+    note(f"ssm step of many rows B{B} T{T} C{C} S{S} G{G} {dtype}")
+    assert B * -(-C * S // 1024) >= 2048
+    p = make_scan(B, T, C, S, G, dtype, seed=B + C)
+    d = {n: None if t is None else t.to(DEV) for n, t in p.items()}
+    state = d["h0"].clone()
+    y = L.ssm_step(d["x"], d["dt"], d["A"], d["b"], d["c"], state, d["D"], d["z"], dt_bias=d["dt_bias"])
+    plain = d["h0"].clone()                                # no z, D or bias; another pool for the results
+    out = torch.full_like(plain, 7.0)
+    y0 = L.ssm_step(d["x"], d["dt"], d["A"], d["b"], d["c"], plain, state_out=out)
+    torch.cuda.synchronize()
+    v = {n: d[n].double() for n in INS}
+    for (a, h), w in (((y, state), v), ((y0, out), dict(v, z=None, D=None, dt_bias=None))):
+        wy, wh = ref_scan(w)
+        assert rel(a, wy) <= scan_tol(T, S, dtype) and rel(h, wh) <= scan_tol(T, S, F32)
+    assert torch.equal(plain, d["h0"])
+
+
+@pytest.mark.parametrize("dtype,C,S,T", [(F32, 449, 16, 1), (BF, 247, 64, 2)])
+def test_steps_of_many_rows_in_a_pool(dtype, C, S, T):
+    """Slots in any order, padding whose inputs are NaN, repeated slots, all inputs slices at odd places; into the pool
+    and into another one."""
+    note(f"ssm step of many rows, slots C{C} S{S} {dtype}")
+    B, P = 300, 310
+    gen = torch.Generator().manual_seed(8)
+    p = make_scan(B, T, C, S, 1, dtype, seed=18)
+    slots = torch.randperm(P, generator=gen)[:B]
+    slots[17], slots[120], slots[299] = slots[3], slots[3], slots[200]
+    slots[50], slots[51], slots[298] = -1, P, 2 ** 31 - 1
+    for n in ("x", "dt", "b", "c", "z"):
+        p[n][50:52], p[n][298] = float("nan"), float("nan")
+    d = {n: None if t is None else t.to(DEV) for n, t in p.items()}
+    for n, off in (("x", 1), ("dt", 3), ("z", 5), ("b", 7), ("c", 1)):
+        t = d[n].flatten(2)
+        buf = torch.full((B, T, t.shape[2] + off + 2), float("nan"), dtype=dtype, device=DEV)
+        buf[..., off:off + t.shape[2]] = t
+        d[n] = buf[..., off:off + t.shape[2]].unflatten(-1, d[n].shape[2:])
+    pool = torch.randn(P, C, S, generator=gen).to(DEV)
+    wy, want = step_ref(p, pool, slots.tolist())
+    ids = slots.to(torch.int32).to(DEV)
+    nxt, before = torch.full_like(pool, 7.0), pool.clone()
+    step = lambda **kw: L.ssm_step(d["x"], d["dt"], d["A"], d["b"], d["c"], pool, d["D"], d["z"], dt_bias=d["dt_bias"],  # noqa: E731
+                                   slots=ids, **kw)
+    y = step(state_out=nxt)
+    torch.cuda.synchronize()
+    assert torch.equal(pool, before)
+    used = sorted({s for s in slots.tolist() if 0 <= s < P})
+    rest = [s for s in range(P) if s not in used]
+    assert rel(y, wy) <= scan_tol(3 * T, S, dtype) and (y[[50, 51, 298]] == 0).all()
+    assert rel(nxt[used], want[used]) <= scan_tol(3 * T, S, F32) and (nxt[rest] == 7).all()
+    y2 = step()
+    torch.cuda.synchronize()
+    assert torch.equal(y2, y) and torch.equal(pool[used], nxt[used]) and torch.equal(pool[rest], before[rest])
+
+
+@pytest.mark.parametrize("B,T,C,S,dtype", [(2, 130, 16801, 16, F32), (1, 129, 8501, 64, BF), (3, 150, 6001, 32, BF)])
+def test_gradients_in_two_segments(B, T, C, S, dtype):
+    """Between 2 and 3 waves per SIMD the gradient goes by two segments, the forward by one."""
+    note(f"ssm two segments B{B} T{T} C{C} S{S} {dtype}")
+    assert 2048 < B * -(-C // 16) * (S // 16) <= 3072
+    check_scan(make_scan(B, T, C, S, 1, dtype, seed=T), ref_on=DEV)
+
+
+@pytest.mark.parametrize("N,C,S,dtype", [(17, 4090, 16, BF), (17, 1024, 64, F32), (9, 4096, 16, F32)])
+def test_many_packed_sequences_in_quarters(N, C, S, dtype):
+    """Where packed sequences are enough to fill the chip only those of more than a quarter of all tokens are cut."""
+    note(f"ssm packed quarters N{N} C{C} S{S} {dtype}")
+    waves = N * -(-C // 16) * (S // 16)
+    assert waves > 2048 and (waves > 4096 or N == 9)
+    lens = [3, 0, 231, 1, 16, 17] + [5] * (N - 7) + [40]
+    cu = [2]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    check_scan(make_scan(1, cu[-1] + 4, C, S, 1, dtype, seed=N, N=N), cu=cu, ref_on=DEV)
+
+
+@pytest.mark.parametrize("rows,C,groups,od,iod,rd", [
+    (17001, 96, 1, F32, F32, F32), (9001, 500, 1, BF, BF, BF), (4003, 2048, 32, F32, BF, BF), (1201, 3001, 1, F32, F32, F32),
+    (1500, 8184, 1, BF, BF, F32)])
+def test_weights_of_norms_over_many_rows(rows, C, groups, od, iod, rd):
+    """More rows than the gradient has teams for twice: a team adds up several, and not all of them equally many."""
+    note(f"rn many rows {rows} x {C} {od} {iod} {rd}")
+    check_rn(make_rn(rows, C, od, iod, rd, F32, seed=C), groups, norm2="rms")
