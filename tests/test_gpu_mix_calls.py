@@ -347,3 +347,69 @@ def test_weights_of_norms_over_many_rows(rows, C, groups, od, iod, rd):
     """More rows than the gradient has teams for twice: a team adds up several, and not all of them equally many."""
     note(f"rn many rows {rows} x {C} {od} {iod} {rd}")
     check_rn(make_rn(rows, C, od, iod, rd, F32, seed=C), groups, norm2="rms")
+
+
+@pytest.mark.parametrize("B,T,C,S,G,dtype", [(1, 300, 40, 16, 1, BF), (2, 200, 128, 32, 2, F32), (1, 300, 70, 64, 1, BF)])
+def test_slices_in_several_segments(B, T, C, S, G, dtype):
+    """As slices at odd places of wider rows, what is not theirs being NaN, in sequences of several segments."""
+    note(f"ssm slices in segments B{B} T{T} C{C} S{S} {dtype}")
+    p = {n: None if t is None else t.to(DEV) for n, t in make_scan(B, T, C, S, G, dtype, seed=30).items()}
+    wide = dict(p)
+    for n, off in (("x", 1), ("dt", 3), ("z", 7), ("b", 5), ("c", 0)):
+        t = p[n].flatten(2)
+        buf = torch.full((B, T, t.shape[2] + off + 3), float("nan"), dtype=dtype, device=DEV)
+        buf[..., off:off + t.shape[2]] = t
+        wide[n] = buf[..., off:off + t.shape[2]].unflatten(-1, p[n].shape[2:])
+    got = []
+    for q in (p, wide):
+        ins = [q[n] for n in ("x", "dt", "A", "b", "c")]
+        y, ckpt, hT = L.ssm_fwd(*ins, q["D"], q["z"], q["h0"], dt_bias=q["dt_bias"])
+        got.append([y, hT, *L.ssm_bwd(q["dy"], *ins, ckpt, q["D"], q["z"], q["dhT"], dt_bias=q["dt_bias"])])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("C,dtype", [(1024, BF), (1029, BF), (1001, F32)])
+def test_convolution_of_slices_by_vectors(C, dtype):
+    """Vectors of channels at odd addresses: slices of wider rows, filters and biases in bf16 behind an odd value."""
+    note(f"conv slices by vectors C{C} {dtype}")
+    T, W = 9000, 4
+    p = {n: None if t is None else t.to(DEV) for n, t in make_conv(1, T, C, W, dtype, seed=31, wdtype=BF).items()}
+    odd = dict(p)
+    buf = torch.full((1, T, C + 5), float("nan"), dtype=dtype, device=DEV)
+    buf[..., 3:3 + C] = p["x"]
+    odd["x"] = buf[..., 3:3 + C]
+    for n in ("weight", "bias"):
+        flat = torch.full((p[n].numel() + 1,), float("nan"), dtype=BF, device=DEV)
+        flat[1:] = p[n].flatten()
+        odd[n] = flat[1:].view(p[n].shape)
+    got = []
+    for q in (p, odd):
+        y, hT = L.conv_fwd(q["x"], q["weight"], q["bias"], q["h0"])
+        got.append([y, hT, *L.conv_bwd(q["dy"], q["x"], q["weight"], q["bias"], q["h0"], q["dhT"])])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_broadcast_inputs_and_gradients():
+    """Inputs that are one value for many rows or channels, and gradients that are (a sum's): as their dense copies give."""
+    note("mix: broadcast")
+    B, T, C, S = 2, 21, 64, 16
+    p = {n: None if t is None else t.to(DEV) for n, t in make_scan(B, T, C, S, 1, F32, seed=32).items()}
+    thin = {"x": p["x"], "dt": p["dt"][:, :, :1], "b": p["b"][:, :1], "z": p["z"][:1], "A": p["A"][:1]}
+    full = {"x": (B, T, C), "dt": (B, T, C), "b": (B, T, 1, S), "z": (B, T, C), "A": (C, S)}
+    w, o = torch.randn(C, 4, generator=torch.Generator().manual_seed(1)).to(DEV), torch.ones(C, device=DEV)
+
+    def layer(dense):
+        leaves = {n: t.clone().requires_grad_() for n, t in thin.items()}
+        v = {n: t.expand(full[n]) for n, t in leaves.items()}
+        if dense:
+            v = {n: t.contiguous() for n, t in v.items()}
+        x, _ = L.CONV.apply(v["x"], w, None)
+        y, hT = L.SSM.apply(x, v["dt"], v["A"], v["b"], p["c"], o, v["z"])
+        r, h = L.RN.apply(y, v["z"], v["x"], o, None, None, o, None, dict(norm="rms", norm2="rms"))
+        (r.sum() + h.sum() + hT.sum()).backward()
+        return [r, h, *(t.grad for t in leaves.values())]
+
+    for a, b in zip(layer(False), layer(True)):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
