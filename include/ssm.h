@@ -31,7 +31,9 @@
  *   passes the state on as it is, also where A is -infinity.  A NaN or Inf in x, dt or z spoils its channel of its
  *   sequence only, from its token on, in b or c every channel of the group; in the
  *   gradients what the formula lets it reach.
- * - Arithmetic, states and sums are fp32; sums of steps over a stretch of tokens 64 bits.
+ * - Arithmetic, states and sums are fp32; sums of steps over a stretch of tokens 64 bits, of
+ *   sums of up to four neighbours in 32.  Steps and gates are good to 8 * 2^-24 of themselves, a gate
+ *   of bf16 rows to 2^-17.
  * - Checkpoints: the state entering every 16th token of a sequence.  A call has
  *   ssm_slots(...) of them: N * ceil(T / 16) dense, T / 16 + N packed.
  * - Every pointer is a device pointer aligned to its values (states, checkpoints and A: 16

@@ -1,5 +1,6 @@
-// abi_checks.h -- host-side argument checks of the gated delta rule's and the
-// layer norm's entry points: NULL, alignment and aliasing, before any launch.
+// abi_checks.h -- host-side argument checks of the entry points beside the recurrence's
+// (gated delta rule, layer norm, selective scan, short convolution, block norm): NULL,
+// alignment and aliasing, before any launch.
 #pragma once
 
 #include <stdint.h>

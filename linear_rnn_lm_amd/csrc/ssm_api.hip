@@ -79,8 +79,9 @@ wkv7_status shape(int B, int T, int C, int S, int G, int N, bool packed, Shape* 
     for (int back = 0; back < 2; ++back) {
         s->seg[back] = segment_of(s->N, T, C, S, packed, !back && s->halves, back);
         s->split[back] = s->seg[back] < T;
-        // the segments' sums alike, up to three waves per SIMD (backward of 4 x 4096 tokens of 4096 channels, as many: 244
-        // -> 186 us; forward of 16384, 3840 waves: 229 -> 245)
+        // the segments' sums alike, up to three waves per SIMD (backward of 10 x 2048 tokens of 4096 channels, 2560 waves: 1348
+        // -> 1280 us, of 12 x 2048 of 3500, 2628: 1527 -> 1466; but forward of 8 x 512 of 1024, 3584 waves: 42.8 -> 46.2, of
+        // 12 x 1024 of 768, 4032: 84 -> 88)
         s->halves_sums[back] = S == 16 && !packed && waves * ((T - 1) / s->seg[back]) <= 3 * 1024;
         const int64_t segs = slots_of(B, T, N, packed, s->seg[back]);
         // a launch takes fewer than 2^32 threads: at most 512 for each segment and channel block

@@ -9,7 +9,7 @@ namespace ssm {
 using namespace rows;
 
 // A long sequence is cut into segments that are scanned at once: a first launch finds what each
-// segment leaves of a zero state (L_j) and the sum of its steps (D_j, 64 bits, rounded once), and
+// segment leaves of a zero state (L_j) and the sum of its steps (D_j, of sums of up to four in 64 bits, rounded once), and
 // a segment's entering state is the fold h <- e^(D_j A) h + L_j over those before it; the
 // backward's entering gradient the same over those behind it.  `slot`: of the first one folded, `step`: 1 or -1.
 template <int NS>

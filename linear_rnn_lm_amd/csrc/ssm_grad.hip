@@ -14,8 +14,8 @@
 // Sums over workgroups (db, dc: one part per 64 channels, 32 with 64 states; dA, dD, ddt_bias: one per
 // segment) go through memory and a second launch, in a fixed order.
 //
-// Bound by vector instructions, 84 per wave and token: B4 T4096 C4096
-// S16 bf16 835 us, the vector units busy for 79 % of it at two waves per SIMD (all that 128 registers of a and
+// Bound by vector instructions, 86 per wave and token: B4 T4096 C4096
+// S16 bf16 825 us, the vector units busy for 82 % of it at two waves per SIMD (all that 128 registers of a and
 // a h_(t-1) leave); the sums of db and dc 24 us (5.5 TB/s).
 #include "column_sums.h"
 #include "ssm_device.h"

@@ -9,8 +9,10 @@
 // threads load x, dt, z, b, c, put delta, delta x, b and c into LDS as fp32, the waves scan,
 // and the threads that loaded z finish y.
 //
-// B4 T4096 C4096 S16 bf16, two states to a lane: 355 us, the vector units busy for 74 % of it; B1 T16384 in 16
-// segments: 200 us for their sums and 280, 92 %; 17 packed sequences, T8193 C2048 S64: 250 us, 93 %.
+// B4 T4096 C4096 S16 bf16, two states to a lane: 353 us, the vector units busy for 75 % of it; B1 T16384 in 16
+// segments: 190 us for their sums and 270, 95 and 93 %; 17 packed sequences, T8193 C2048 S64: 230 us, 95 %.  Four states of
+// 16 to a lane, with z, take all 128 registers of four waves per SIMD: bf16 spills a pair around the loop over blocks, fp32 six
+// registers, two of them read again once per block.
 #include "ssm_device.h"
 
 namespace ssm {
@@ -203,7 +205,8 @@ __global__ __launch_bounds__(64 * WN * WC, Ahead<NS>::waves) void fwd_kernel(Arg
 }
 
 // What a segment leaves of a zero state, forward (h <- a h + delta x b) or, for the backward,
-// in reverse (g <- a (g + c dy)), and the sum of its steps.  Five sixths of the forward's
+// in reverse (g <- a (g + c dy)), and the sum of its steps, a thread's neighbouring tokens (up to four) in
+// 32 bits, those sums in 64.  Five sixths of the forward's
 // instructions, without its outputs.
 template <typename InT, int NS, int WN, int WC, bool BWD, bool HZ>
 __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int blocks) {

@@ -216,7 +216,6 @@ def _make_autograd():
             o, gate, res, *ws, stats = ctx.saved_tensors
             if dr is None and dh is None:
                 return (None,) * 9
-            # given even where r has no gradient: it says the layer's type
             dr = None if dr is None else _dense(dr.to(ctx.r), ctx.align)
             dh = None if dh is None else _dense(dh.to(ctx.h), ctx.align)
             names = ("weight", "bias", "scale", "weight2", "bias2")

@@ -213,7 +213,7 @@ def _make_autograd():
     class SSM(torch.autograd.Function):
         """Differentiable op: (x, dt, A, b, c, D, z, dt_bias, h0, cu_seqlens, softplus) -> (y, hT),
         gradients by ssm_bwd in the inputs' types.  Rows that no packed sequence covers have
-        y = 0 and zero gradients."""
+        y = 0 and zero gradients.  Where gradients are off it leaves no checkpoints."""
 
         @staticmethod
         def forward(ctx, x, dt, A, b, c, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, softplus=True):
