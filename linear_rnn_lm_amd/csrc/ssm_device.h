@@ -31,6 +31,11 @@ __device__ __forceinline__ bool segment_of(const Args& p, const Seqs& seqs, int 
     return p.cu && p.N > 1 && p.N <= 64 ? by_length(seqs, k, p.seg, n, piece) : slot_piece(seqs, k, p.seg, n, piece);
 }
 
+// Where a segment ends: its start and length together may pass 2^31, where the sequence does not end.
+__device__ __forceinline__ int segment_end(int t_begin, int seg, int len) {
+    return (int)min((uint32_t)t_begin + (uint32_t)seg, (uint32_t)len);
+}
+
 // Token rows through buffer resources, so that a ragged end needs no branch: loads behind a
 // sequence's (segment's) end return 0 and stores there are dropped; lanes whose channel does not
 // exist have kNowhere for an offset.

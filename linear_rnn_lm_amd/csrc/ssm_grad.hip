@@ -55,7 +55,7 @@ __global__ __launch_bounds__(64 * WN * WC, 2) void bwd_kernel(Args p, int blocks
     const bool used = segment_of(p, seqs, slot, n, piece);
     if (used) seq_span(seqs, n, tok0, len);
     n = uniform(n), piece = uniform(piece), len = uniform(len), tok0 = uniform(tok0);
-    const int t_begin = used ? piece * p.seg : 0, t_end = used ? t_begin + min(len - t_begin, p.seg) : 0;
+    const int t_begin = used ? piece * p.seg : 0, t_end = used ? segment_end(t_begin, p.seg, len) : 0;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
         A2[s] = on ? rate_of(p.A[(int64_t)ch * S + n0 + s]) : 0.f;

@@ -11,8 +11,8 @@
 //
 // B4 T4096 C4096 S16 bf16, two states to a lane: 353 us, the vector units busy for 75 % of it; B1 T16384 in 16
 // segments: 190 us for their sums and 270, 95 and 93 %; 17 packed sequences, T8193 C2048 S64: 230 us, 95 %.  Four states of
-// 16 to a lane, with z, take all 128 registers of four waves per SIMD: bf16 spills a pair around the loop over blocks, fp32 six
-// registers, two of them read again once per block.
+// 16 to a lane take all 128 registers of four waves per SIMD: two to five of them are in scratch (20 bytes in bf16 with z) while the
+// loop over blocks runs, none within it.
 #include "ssm_device.h"
 
 namespace ssm {
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(64 * WN * WC, Ahead<NS>::waves) void fwd_kernel(Arg
     int64_t tok0;
     seq_span(seqs, n, tok0, len);
     n = uniform(n), piece = uniform(piece), len = uniform(len), tok0 = uniform(tok0);
-    const int t_begin = piece * p.seg, t_end = t_begin + min(len - t_begin, p.seg);    // below 2^31 as len is
+    const int t_begin = piece * p.seg, t_end = segment_end(t_begin, p.seg, len);
 
     // scanning: channel and first state of this lane
     const int cl = wc * 16 + (lane & 15), g = lane >> 4, ch = cb * CH + cl, n0 = (wn * 4 + g) * NS;
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int block
     int64_t tok0;
     seq_span(seqs, n, tok0, len);
     n = uniform(n), piece = uniform(piece), len = uniform(len), tok0 = uniform(tok0);
-    const int t_begin = piece * p.seg, t_end = t_begin + min(len - t_begin, p.seg);    // below 2^31 as len is
+    const int t_begin = piece * p.seg, t_end = segment_end(t_begin, p.seg, len);
     const int cl = wc * 16 + (lane & 15), g = lane >> 4, ch = cb * CH + cl, n0 = (wn * 4 + g) * NS;
     const bool on = ch < p.C;
     if (!BWD && p.h0_copy && piece == 0 && on) {
