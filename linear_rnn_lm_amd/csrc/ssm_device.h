@@ -167,12 +167,17 @@ __device__ __forceinline__ void get_lds(const float* p, float (&v)[LT]) {
         v[0] = *p;
     }
 }
-// softplus(v), or v.  Both are formed: a branch here would keep the scan's instructions from
+// softplus(v), or v, and its slope.  Both are formed: a branch here would keep the scan's instructions from
 // being mixed with these.
-__device__ __forceinline__ float step_of(bool soft, float v) {
-    float sp = softplus(v);
+__device__ __forceinline__ float step_of(bool soft, float v, float& slope) {
+    float sl, sp = softplus(v, sl);
     asm volatile("" : "+v"(sp));
+    slope = soft ? sl : 1.f;
     return soft ? sp : v;
+}
+__device__ __forceinline__ float step_of(bool soft, float v) {
+    float slope;
+    return step_of(soft, v, slope);
 }
 __device__ __forceinline__ f32x4 lds4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 

@@ -14,8 +14,8 @@
 // Sums over workgroups (db, dc: one part per 64 channels, 32 with 64 states; dA, dD, ddt_bias: one per
 // segment) go through memory and a second launch, in a fixed order.
 //
-// Bound by vector instructions, 86 per wave and token: B4 T4096 C4096
-// S16 bf16 825 us, the vector units busy for 82 % of it at two waves per SIMD (all that 128 registers of a and
+// Bound by vector instructions, 85 per wave and token: B4 T4096 C4096
+// S16 bf16 815 us, the vector units busy for 81 % of it at two waves per SIMD (all that 128 registers of a and
 // a h_(t-1) leave); the sums of db and dc 24 us (5.5 TB/s).
 #include "column_sums.h"
 #include "ssm_device.h"
@@ -108,13 +108,12 @@ __global__ __launch_bounds__(64 * WN * WC, 2) void bwd_kernel(Args p, int blocks
 #pragma unroll
             for (int i = 0; i < LT; ++i) {
                 xv[i] = widen(rx[i]);
-                const float v = widen(rd[i]) + bias, yv = widen(ry[i]), st = step_of(p.softplus, v);
+                const float v = widen(rd[i]) + bias, yv = widen(ry[i]), st = step_of(p.softplus, v, sl[i]);
                 d[i] = deal.lon && t0 + deal.lt + i < t_end ? st : 0.f;
                 u[i] = d[i] * xv[i];
-                sl[i] = p.softplus ? sigmoid(v) : 1.f;
                 dyv[i] = yv;
                 if (HZ) {
-                    const float zv = widen(rz[i]), sg = sigmoid(zv), zs = zv * sg;
+                    const float zv = widen(rz[i]), sg = sigmoid_for<InT>(zv), zs = zv * sg;
                     dyv[i] = yv * zs;
                     zf[i] = yv * fmaf(zs, 1.f - sg, sg);
                 }

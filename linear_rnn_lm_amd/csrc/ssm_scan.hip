@@ -10,7 +10,7 @@
 // and the threads that loaded z finish y.
 //
 // B4 T4096 C4096 S16 bf16, two states to a lane: 353 us, the vector units busy for 75 % of it; B1 T16384 in 16
-// segments: 190 us for their sums and 270, 95 and 93 %; 17 packed sequences, T8193 C2048 S64: 230 us, 95 %.  Four states of
+// segments: 190 us for their sums and 270, 95 and 92 %; 17 packed sequences, T8193 C2048 S64: 230 us, 93 %.  Four states of
 // 16 to a lane take all 128 registers of four waves per SIMD: two to five of them are in scratch (20 bytes in bf16 with z) while the
 // loop over blocks runs, none within it.
 #include "ssm_device.h"
@@ -280,7 +280,7 @@ __global__ __launch_bounds__(64 * WN * WC) void segment_kernel(Args p, int block
             u[i] = widen(ru[j][i]);
             if (HZ) {
                 const float zv = widen(rz[j][i]);
-                u[i] *= zv * sigmoid(zv);
+                u[i] *= zv * sigmoid_for<InT>(zv);
             }
             if (!BWD) u[i] *= d[i];
             sum += d[i];

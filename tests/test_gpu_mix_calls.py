@@ -413,3 +413,20 @@ def test_broadcast_inputs_and_gradients():
 
     for a, b in zip(layer(False), layer(True)):
         assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
+@pytest.mark.parametrize("lo,hi", SPANS)
+def test_slopes_keep_their_bits(lo, hi):
+    """The gradient of a raw step alone: one token, no decay, x = b = c = dy = 1, so ddt is S times the step's slope, of which S
+    and the sum are exact and one rounding is added."""
+    note(f"mix: slope {lo} {hi}")
+    v = spread(lo, hi, 1 << 16).float().view(1, 1, -1)
+    C = v.shape[2]
+    one, b = torch.ones(1, 1, C, device=DEV), torch.ones(1, 1, 1, 16, device=DEV)
+    ins = (one, v.to(DEV), torch.zeros(C, 16, device=DEV), b, b)
+    _, ckpt, _ = L.ssm_fwd(*ins)
+    ddt = L.ssm_bwd(one, *ins, ckpt)[1]
+    torch.cuda.synchronize()
+    want = 16 * torch.sigmoid(v.double())
+    err = ((ddt.double().cpu() - want).abs() / want).max().item()
+    assert err <= 9 * E, (lo, hi, err / E)
